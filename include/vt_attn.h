@@ -271,6 +271,91 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
                               void *workspace, size_t workspace_bytes,
                               const vt_attn_opts *opts, vt_stream_t stream);
 
+/*
+ * Token preparation: the per-head norm of Q and K and their rotation by the token's position, in one
+ * pass over the rows, with an optional append of K and V to a cache.  It produces the Q and K that the
+ * attention calls of this header read.
+ *
+ * For every token (b, s) and head h the row x[0..D) of Q or K becomes y[0..D):
+ *   n = x                                                        normalize = 0
+ *   n_j = w_j x_j / sqrt(mean_j(x_j^2) + eps)                    normalize != 0 (w = 1 when the weight is NULL)
+ *   angle_i = positions[pair_axis[i], b, s] * freqs[i],  i < R/2
+ *   (y_u, y_v) = (n_u cos(angle_i) - n_v sin(angle_i), n_u sin(angle_i) + n_v cos(angle_i))
+ *       with (u, v) = (i, i + R/2)   interleaved = 0
+ *            (u, v) = (2i, 2i + 1)   interleaved != 0
+ *   y_j = n_j for j >= R.
+ * Everything between x and y is fp32 (the angle is formed in fp64, so far positions keep their phase) and y is
+ * rounded once.  Several position axes (time, height, width of a video patch) need one row of `positions` each;
+ * pair_axis names the axis of every frequency pair, in any order.
+ *
+ * Append (kv_len not NULL): token s of sequence b belongs at cache row kv_len[b] - S + s, kv_len[b] being the
+ * sequence's length after these S tokens, so that the same array serves vt_attn_fwd_prefix.  The K row is
+ * written there in k_out [B,H_kv,cap,D] and the V row is copied there in v_out [B,H_kv,cap,D_v] (v may be NULL).
+ * A token whose row is negative is padding on the left: its K and V are not written (its Q is).  A row at or past
+ * `cap` is not written either and records VT_ERR_DEVICE_BOUNDS in the stream's status word.  No other row of the
+ * cache is read or written.
+ *
+ * Arguments, as a struct whose first field is its size.
+ *   q, k          [B,H,S,D] and [B,H_kv,S,D]; k may be NULL with H_kv = 0 (one tensor only)
+ *   q_out, k_out  as q and k, or (append) k_out the cache.  An output may be the same tensor as its input (same
+ *                 pointer and strides); it must not overlap any input or output in another way.
+ *   weights       [D] in the tensors' dtype, or NULL
+ *   freqs         fp32 [R/2]; R even, 2 <= R <= D
+ *   positions     int32, element strides pos_stride over (axis, b, s), 0 allowed (one row for the whole batch)
+ * Strides, dtypes, alignment and their errors are those of vt_attn_fwd_strided (16-byte rule; the stride of an
+ * index with one value is not looked at, and an append's K and V outputs count `cap` rows); D <= 256 and
+ * D_v <= 256, at most 4 axes.  eps must be finite and not negative.  B or S equal to 0 is a valid empty
+ * problem.
+ */
+#define VT_ROPE_MAX_AXES 4
+#define VT_ROPE_MAX_PAIRS 128
+typedef struct {
+    uint64_t struct_bytes; /* sizeof(vt_qk_rope_args) */
+    int64_t B, H, H_kv, S, D, R;
+    int32_t dtype; /* vt_dtype */
+    int32_t interleaved;
+    int32_t normalize;
+    int32_t axes;
+    float eps;
+    int32_t reserved; /* 0 */
+    const void *q, *k;
+    int64_t q_stride[3], k_stride[3];
+    const void *q_weight, *k_weight;
+    const float *freqs;
+    const int32_t *positions;
+    int64_t pos_stride[3];
+    void *q_out, *k_out;
+    int64_t q_out_stride[3], k_out_stride[3];
+    /* append (kv_len NULL: none, and the fields below are ignored) */
+    const int32_t *kv_len; /* [B] */
+    int64_t cap, D_v;
+    const void *v;
+    void *v_out;
+    int64_t v_stride[3], v_out_stride[3];
+    uint8_t pair_axis[VT_ROPE_MAX_PAIRS]; /* pair_axis[i] < axes for i < R/2 */
+} vt_qk_rope_args;
+
+vt_status vt_qk_rope_fwd(const vt_qk_rope_args *args, vt_stream_t stream);
+
+/*
+ * Gradients of vt_qk_rope_fwd (without the append).  With g the gradient of an output row, u its rotation by
+ * the opposite angles, r = 1 / sqrt(mean(x^2) + eps) and z = r x:
+ *   dw_j = sum over tokens and heads of u_j z_j,   dx = r (w u - z mean_j(w_j u_j z_j)),
+ * and dx = u when normalize is 0.  In `args`: q, k are the forward's inputs (not read, and may be NULL, when
+ * normalize is 0); q_out, k_out are dq and dk, written; kv_len must be NULL.  dq_out, dk_out are the gradients
+ * of the forward's outputs, with their strides; dq may be dq_out, or q (same pointer and strides), and dk the
+ * same way.  dq_weight, dk_weight: fp32 [D], written (each may be NULL), summed in an order that does not change from
+ * call to call.  The workspace (256-byte aligned, at least vt_qk_rope_bwd_workspace_size bytes) holds partial
+ * sums of the weight gradients; it is not used, and may be NULL, when normalize is 0 or both are NULL.
+ */
+vt_status vt_qk_rope_bwd(const vt_qk_rope_args *args, const void *dq_out, const int64_t dq_out_stride[3],
+                         const void *dk_out, const int64_t dk_out_stride[3], float *dq_weight, float *dk_weight,
+                         void *workspace, size_t workspace_bytes, vt_stream_t stream);
+
+/* Bytes of workspace vt_qk_rope_bwd needs for the weight gradients of rows of D elements (0 when D is outside
+ * 1..256).  Host-only arithmetic. */
+size_t vt_qk_rope_bwd_workspace_size(int64_t D);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *vt_status_str(vt_status status);
 

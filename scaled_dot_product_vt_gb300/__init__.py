@@ -9,7 +9,9 @@ raises.  PyTorch is used for device memory and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 from ._build import LIB, LIB_DEBUG, build  # noqa: F401
 
@@ -28,7 +30,8 @@ STATUS = {
 # Every symbol the header declares.
 EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_splitkv",
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
-           "vt_attn_fwd_general", "vt_status_str", "vt_last_device_status")
+           "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
+           "vt_status_str", "vt_last_device_status")
 
 
 class VtError(RuntimeError):
@@ -81,6 +84,12 @@ def load(path: str | None = None):
     lib.vt_attn_fwd_general.argtypes = [vp, st3, vp, st3, vp, st3, vp, st3, vp, i64, i64, i64, i64, i64, i64, i64, f,
                                         i, ctypes.POINTER(vt_attn_mask), i, vp, sz, ctypes.POINTER(vt_attn_opts), vp]
     lib.vt_attn_fwd_general.restype = i
+    lib.vt_qk_rope_fwd.argtypes = [ctypes.c_char_p, vp]
+    lib.vt_qk_rope_fwd.restype = i
+    lib.vt_qk_rope_bwd.argtypes = [ctypes.c_char_p, vp, st3, vp, st3, vp, vp, vp, sz, vp]
+    lib.vt_qk_rope_bwd.restype = i
+    lib.vt_qk_rope_bwd_workspace_size.argtypes = [i64]
+    lib.vt_qk_rope_bwd_workspace_size.restype = sz
     lib.vt_status_str.argtypes = [i]
     lib.vt_status_str.restype = ctypes.c_char_p
     lib.vt_last_device_status.argtypes = [vp]
@@ -154,6 +163,25 @@ def vt_attn_fwd_general(Q, q_stride, K, k_stride, V, v_stride, O, o_stride, lse,
                                       _stride3(o_stride), lse, B, H, H_kv, S_q, S_k, D_qk, D_v, scale, dtype,
                                       ctypes.byref(mask) if mask is not None else None, int(n_split), workspace,
                                       int(workspace_bytes), ctypes.byref(opts) if opts is not None else None, stream)
+
+
+# vt_qk_rope_args, packed in field order (every field is aligned without padding)
+_QK_ROPE_ARGS = struct.Struct("=Q6q4ifi2Q6q2QQQ3q2Q6qQ2q2Q6q128s")
+
+
+def vt_qk_rope_fwd(args: bytes, stream) -> int:
+    """The C entry point: ``args`` is a packed vt_qk_rope_args; returns the vt_status code."""
+    return load().vt_qk_rope_fwd(args, stream)
+
+
+def vt_qk_rope_bwd(args: bytes, dq_out, dq_out_stride, dk_out, dk_out_stride, dq_weight, dk_weight, workspace,
+                   workspace_bytes, stream) -> int:
+    return load().vt_qk_rope_bwd(args, dq_out, _stride3(dq_out_stride), dk_out, _stride3(dk_out_stride), dq_weight,
+                                 dk_weight, workspace, int(workspace_bytes), stream)
+
+
+def vt_qk_rope_bwd_workspace_size(D) -> int:
+    return int(load().vt_qk_rope_bwd_workspace_size(D))
 
 
 def vt_status_str(code: int) -> str:
@@ -282,3 +310,198 @@ def attn_fwd_general(q, k, v, scale: float | None = None, mask: str = "none", of
     if rc != 0:
         raise VtError(rc, "vt_attn_fwd_general")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- token preparation
+
+def _on_stream(fn):
+    """Run a wrapper on its ``stream=`` (a torch stream or a raw handle; None: the current stream of the first
+    tensor's device).  What the wrapper allocates is then allocated on that stream, and that device is current."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        if not first.is_cuda:
+            raise ValueError("the tensors must be CUDA tensors")
+        dev = first.device
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+
+    return call
+
+
+def _same_place(what, first, *tensors):
+    """Every tensor given (not None) lives on the first one's device."""
+    dev = first.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: all tensors must be on {dev}")
+
+
+def _bhsd(name, t, shape=None, dtype=None):
+    """(address, strides) of a [B, H, S, D] tensor with its last dimension contiguous."""
+    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
+        raise ValueError(f"{name} must be [B, H, S, D] with the last dimension contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr(), t.stride()[:3]
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axis_bytes(pair_axis, pairs: int, axes: int) -> bytes:
+    if pair_axis is None:
+        if axes != 1:
+            raise ValueError("pair_axis is required with more than one position axis")
+        pair_axis = (0,) * pairs
+    if len(pair_axis) != pairs or any(not 0 <= a < axes for a in pair_axis):
+        raise ValueError(f"pair_axis must name one of the {axes} axes for each of the {pairs} pairs")
+    return bytes(pair_axis).ljust(128, b"\0")
+
+
+def _rope_form(q, k, freqs, positions, pair_axis, q_weight, k_weight):
+    """The fields the two directions share: (dims, weights, freqs and positions, pair axes)."""
+    import torch
+    B, H, S, D = q.shape
+    if k is not None and (k.dim() != 4 or k.shape[0] != B or k.shape[2] != S or k.shape[3] != D):
+        raise ValueError("shape mismatch between q and k")
+    if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float32 vector")
+    pairs = freqs.shape[0]
+    if not 1 <= pairs <= 128:
+        raise ValueError("freqs must have 1 to 128 entries")
+    if positions.dtype != torch.int32:
+        raise TypeError(f"positions must be int32, got {positions.dtype}")
+    if positions.dim() == 2:
+        axes, pos_stride = 1, (0, *positions.stride())
+    elif positions.dim() == 3:
+        axes, pos_stride = positions.shape[0], positions.stride()
+    else:
+        raise ValueError("positions must be [B, S] or [axes, B, S]")
+    if positions.shape[-2:] != (B, S):
+        raise ValueError("positions must be [B, S] or [axes, B, S]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != q.dtype or w.shape != (D,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous vector of {D} elements of q's dtype")
+    if pair_axis is not None and not isinstance(pair_axis, tuple):
+        pair_axis = tuple(pair_axis)
+    return (B, H, k.shape[1] if k is not None else 0, S, D, 2 * pairs, axes,
+            q_weight.data_ptr() if q_weight is not None else 0, k_weight.data_ptr() if k_weight is not None else 0,
+            freqs.data_ptr(), positions.data_ptr(), pos_stride, _pair_axis_bytes(pair_axis, pairs, axes))
+
+
+_NO_TENSOR = (0, (0, 0, 0))
+
+
+def _new_rows(B, H, S, D, dtype, device):
+    """A new [B, H, S, D] tensor; rows that are no multiple of 16 bytes are padded to one (a view is returned)."""
+    import torch
+    step = 16 // dtype.itemsize
+    if D % step == 0:
+        return torch.empty((B, H, S, D), dtype=dtype, device=device)
+    return torch.empty((B, H, S, D + -D % step), dtype=dtype, device=device)[..., :D]
+
+
+@_on_stream
+def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False, eps: float | None = None,
+            q_weight=None, k_weight=None, q_out=None, k_out=None, kv_len=None, v=None, v_out=None):
+    """Norm (with ``eps``) and rotation of the rows of q [B,H,S,D] and k [B,H_kv,S,D] (or None) in one pass: see
+    vt_qk_rope_fwd in include/vt_attn.h.  Returns (q_out, k_out).
+
+    ``freqs`` (float32) holds the angle per position of each of the R/2 rotated pairs, ``positions`` (int32) is
+    [B,S] or [axes,B,S], and ``pair_axis`` names the axis of every pair.  ``eps=None`` leaves the norm out.
+    ``q_out=q`` and ``k_out=k`` work in place.  With ``kv_len`` (int32 [B]: the lengths after these tokens), k_out
+    is a cache [B,H_kv,cap,D] that K's rows are appended to, and v [B,H_kv,S,D_v] is appended to v_out.
+    ``stream`` may name another stream than the current one."""
+    import torch
+    (B, H, H_kv, S, D, R, axes, qw, kw, fr, pos, pos_st, axis) = _rope_form(q, k, freqs, positions, pair_axis,
+                                                                           q_weight, k_weight)
+    code = _dtype_code(q)
+    _same_place("qk_rope", q, k, freqs, positions, q_weight, k_weight, q_out, k_out, kv_len, v, v_out)
+    if q_out is None:
+        q_out = _new_rows(B, H, S, D, q.dtype, q.device)
+    pq, sq = _bhsd("q", q)
+    pqo, sqo = _bhsd("q_out", q_out, q.shape, q.dtype)
+    (pk, sk), (pko, sko), (pv, sv), (pvo, svo) = _NO_TENSOR, _NO_TENSOR, _NO_TENSOR, _NO_TENSOR
+    lens, cap, D_v = 0, 0, 0
+    if kv_len is not None:
+        if k is None or k_out is None or (v is None) != (v_out is None):
+            raise ValueError("an append needs k and its cache k_out, and v only with its cache v_out")
+        if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
+            raise ValueError("kv_len must be a contiguous int32 vector of B entries")
+        lens, cap = kv_len.data_ptr(), k_out.shape[2]
+        pko, sko = _bhsd("k_out", k_out, (B, H_kv, cap, D), q.dtype)
+        if v is not None:
+            D_v = v.shape[3]
+            pv, sv = _bhsd("v", v, (B, H_kv, S, D_v), q.dtype)
+            pvo, svo = _bhsd("v_out", v_out, (B, H_kv, cap, D_v), q.dtype)
+    elif v is not None or v_out is not None:
+        raise ValueError("v is appended with kv_len only")
+    elif k is not None:
+        if k_out is None:
+            k_out = _new_rows(B, H_kv, S, D, q.dtype, q.device)
+        pko, sko = _bhsd("k_out", k_out, k.shape, q.dtype)
+    if k is not None:
+        pk, sk = _bhsd("k", k, None, q.dtype)
+    args = _QK_ROPE_ARGS.pack(_QK_ROPE_ARGS.size, B, H, H_kv, S, D, R, code, bool(interleaved), eps is not None, axes,
+                              eps or 0.0, 0, pq, pk, *sq, *sk, qw, kw, fr, pos, *pos_st, pqo, pko, *sqo, *sko, lens,
+                              cap, D_v, pv, pvo, *sv, *svo, axis)
+    rc = load().vt_qk_rope_fwd(args, torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise VtError(rc, "vt_qk_rope_fwd")
+    return q_out, k_out
+
+
+@_on_stream
+def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=None, interleaved: bool = False,
+                eps: float | None = None, q_weight=None, k_weight=None, dq=None, dk=None, workspace=None):
+    """Gradients of ``qk_rope`` (without the append): see vt_qk_rope_bwd in include/vt_attn.h.  dq_out, dk_out are
+    the gradients of its outputs; q, k its inputs (needed with ``eps``).  Returns (dq, dk, dq_weight, dk_weight); the
+    weights' gradients are float32 [D], and None without ``eps`` (or, for K's, without dk_out).  ``dq=dq_out`` and
+    ``dk=dk_out`` work in place."""
+    import torch
+    (B, H, H_kv, S, D, R, axes, qw, kw, fr, pos, pos_st, axis) = _rope_form(dq_out, dk_out, freqs, positions, pair_axis,
+                                                                           q_weight, k_weight)
+    code = _dtype_code(dq_out)
+    _same_place("qk_rope_bwd", dq_out, dk_out, freqs, positions, q, k, q_weight, k_weight, dq, dk, workspace)
+    dt, dev = dq_out.dtype, dq_out.device
+    (pq, sq), (pk, sk), (pdk, sdk), (pgk, sgk) = _NO_TENSOR, _NO_TENSOR, _NO_TENSOR, _NO_TENSOR
+    if dq is None:
+        dq = _new_rows(B, H, S, D, dt, dev)
+    pgq, sgq = _bhsd("dq_out", dq_out)
+    pdq, sdq = _bhsd("dq", dq, dq_out.shape, dt)
+    if dk_out is not None:
+        if dk is None:
+            dk = _new_rows(B, H_kv, S, D, dt, dev)
+        pgk, sgk = _bhsd("dk_out", dk_out, None, dt)
+        pdk, sdk = _bhsd("dk", dk, dk_out.shape, dt)
+    dqw = dkw = None
+    ws_ptr, ws_bytes = None, 0
+    if eps is not None:
+        if q is None or (k is None) != (dk_out is None):
+            raise ValueError("the norm's gradients need the forward's inputs q and k")
+        pq, sq = _bhsd("q", q, dq_out.shape, dt)
+        dqw = torch.empty(D, dtype=torch.float32, device=dev)
+        if k is not None:
+            pk, sk = _bhsd("k", k, dk_out.shape, dt)
+            dkw = torch.empty(D, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(load().vt_qk_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    args = _QK_ROPE_ARGS.pack(_QK_ROPE_ARGS.size, B, H, H_kv, S, D, R, code, bool(interleaved), eps is not None, axes,
+                              eps or 0.0, 0, pq, pk, *sq, *sk, qw, kw, fr, pos, *pos_st, pdq, pdk, *sdq, *sdk, 0, 0, 0,
+                              0, 0, 0, 0, 0, 0, 0, 0, axis)
+    rc = vt_qk_rope_bwd(args, pgq, sgq, pgk, sgk, dqw.data_ptr() if dqw is not None else None,
+                        dkw.data_ptr() if dkw is not None else None, ws_ptr, ws_bytes,
+                        torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise VtError(rc, "vt_qk_rope_bwd")
+    return dq, dk, dqw, dkw

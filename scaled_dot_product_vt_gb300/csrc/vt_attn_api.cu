@@ -12,9 +12,8 @@
 #include <mutex>
 #include <type_traits>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/vt_attn.h"
+#include "vt_host.h"
 #include "vt_attn_bf16_2q.cuh"
 #include "vt_attn_f32_2q.cuh"
 #include "vt_attn_merge.cuh"
@@ -32,30 +31,8 @@ __device__ unsigned g_status[kStatusSlots];
 constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;  // 32 MiB
 static __device__ __align__(256) uint8_t g_noalloc_scratch[kNoAllocScratchBytes];
 
-namespace {
+// ---- shared host helpers (vt_host.h)
 
-// An NVTX range over one public call (named after the entry point), for profilers that record NVTX;
-// without one attached, push and pop return at once.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-constexpr int64_t kMaxD = 128;
-constexpr int64_t kMaxExtent = 0x7FFFFFFF;  // B and H (their product is bounded by the work-unit count)
-// S_q and S_k: the kernels form row and key indices a few tiles past an extent in 32-bit ints
-constexpr int64_t kMaxSeq = int64_t(1) << 30;
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
-constexpr int kSmemLimit = 232448;  // 227 KiB per CTA on sm_100-class parts
-
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi) bytes touched by a tensor's logical elements
-};
-
-// The bytes a tensor's logical elements touch; false when the extent arithmetic overflows (no such
-// tensor fits in an address space).  Extents and strides are positive here.
 bool span_of(const void *p, const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D, int elt, Span *out) {
     const int64_t n[3] = {B - 1, H - 1, S - 1};
     int64_t last = D - 1, t = 0, bytes = 0;
@@ -69,22 +46,23 @@ bool span_of(const void *p, const int64_t st[3], int64_t B, int64_t H, int64_t S
     return true;
 }
 
-// The LSE array: B * H * S_q floats from `lse`; false on overflow.
-bool lse_span(const float *lse, int64_t B, int64_t H, int64_t S_q, Span *out) {
-    int64_t n = 0;
-    if (__builtin_mul_overflow(B, H, &n) || __builtin_mul_overflow(n, S_q, &n) ||
-        __builtin_mul_overflow(n, int64_t(sizeof(float)), &n))
-        return false;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
-    if (static_cast<uint64_t>(n) > UINTPTR_MAX - lo) return false;
-    *out = {lo, lo + static_cast<uintptr_t>(n)};
+bool rows_disjoint(const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D) {
+    int64_t n[3] = {B, H, S}, s[3] = {st[0], st[1], st[2]};
+    for (int i = 0; i < 3; ++i)  // insertion sort by stride
+        for (int j = i; j > 0 && s[j] < s[j - 1]; --j) {
+            const int64_t ts = s[j], tn = n[j];
+            s[j] = s[j - 1]; n[j] = n[j - 1];
+            s[j - 1] = ts; n[j - 1] = tn;
+        }
+    int64_t span = D;  // elements covered by the dimensions taken so far, as one contiguous extent
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (s[i] < span) return false;
+        int64_t t = 0;
+        if (__builtin_mul_overflow(n[i] - 1, s[i], &t) || __builtin_add_overflow(span, t, &span)) return false;
+    }
     return true;
 }
-
-// Largest (b, h, s) stride in bytes that a TMA tensor map accepts is below 2^40.
-constexpr int64_t kMaxStrideBytes = int64_t(1) << 40;
-
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 bool env_check() {
     static const bool on = [] {
@@ -94,15 +72,7 @@ bool env_check() {
     return on;
 }
 
-// Per-device facts that do not change while the process runs, looked up once: the SM count, the L2
-// size and the device address of the status words.
-struct DeviceInfo {
-    bool ready = false;
-    int sms = 0;
-    long long l2_bytes = 0;
-    unsigned *status = nullptr;  // g_status on this device
-};
-constexpr int kMaxDevices = 64;
+namespace {
 std::mutex g_info_mu;
 DeviceInfo g_info[kMaxDevices];
 struct SmemGrant {
@@ -110,8 +80,10 @@ struct SmemGrant {
     int dev;
     int bytes;
 };
-SmemGrant g_grants[64];
+constexpr int kMaxGrants = 256;
+SmemGrant g_grants[kMaxGrants];
 int g_n_grants = 0;
+}  // namespace
 
 bool device_info(int dev, DeviceInfo *out) {
     if (dev < 0 || dev >= kMaxDevices) return false;
@@ -134,9 +106,11 @@ bool device_info(int dev, DeviceInfo *out) {
 // The status slot of a stream: the first kStatusSlots - 1 distinct stream handles seen get slots 1, 2, ...
 // in order of first use; later ones share slot 0.  Handles are process-wide, so one table serves every
 // device (each device has its own array of words).
+namespace {
 std::mutex g_slot_mu;
 cudaStream_t g_slot_stream[kStatusSlots];
 int g_n_slots = 1;
+}  // namespace
 
 int status_slot(cudaStream_t s) {
     std::lock_guard<std::mutex> lock(g_slot_mu);
@@ -160,11 +134,11 @@ bool ensure_smem(const void *kern, int dev, int bytes) {
             return true;
         }
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    if (g_n_grants < 64) g_grants[g_n_grants++] = {kern, dev, bytes};
+    if (g_n_grants < kMaxGrants) g_grants[g_n_grants++] = {kern, dev, bytes};
     return true;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -194,6 +168,20 @@ bool make_map(CUtensorMap *map, const void *ptr, const int64_t st[3], int64_t B,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+namespace {
+
+// The LSE array: B * H * S_q floats from `lse`; false on overflow.
+bool lse_span(const float *lse, int64_t B, int64_t H, int64_t S_q, Span *out) {
+    int64_t n = 0;
+    if (__builtin_mul_overflow(B, H, &n) || __builtin_mul_overflow(n, S_q, &n) ||
+        __builtin_mul_overflow(n, int64_t(sizeof(float)), &n))
+        return false;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
+    if (static_cast<uint64_t>(n) > UINTPTR_MAX - lo) return false;
+    *out = {lo, lo + static_cast<uintptr_t>(n)};
+    return true;
 }
 
 // Workspace of a split-KV call: partial outputs, then row maxima, row sums and row-sum corrections
@@ -504,6 +492,8 @@ void *noalloc_scratch(int dev) {
     return addr[dev];
 }
 
+}  // namespace
+
 // Wait for `stream`, then read and clear the status word of its slot on the current device.  The read and
 // the clear are ordered on `stream` itself, so no other stream is waited for.
 vt_status read_status(cudaStream_t stream) {
@@ -520,7 +510,6 @@ vt_status read_status(cudaStream_t stream) {
     return VT_OK;
 }
 
-}  // namespace
 }  // namespace vt
 
 extern "C" {
@@ -567,28 +556,6 @@ vt_status check_shape(const Problem &P, bool *empty) {
         return VT_ERR_UNSUPPORTED;
     if (B == 0 || H == 0 || S_q == 0) *empty = true;
     return VT_OK;
-}
-
-// True when no two logical elements of a [B, H, S, D] tensor with (b, h, s) strides st and unit stride
-// along D share an address: with the extents of size 1 left out and the rest taken in order of
-// increasing stride, each stride reaches past everything the smaller ones span.  This accepts every
-// nesting of the three indices ([B,H,S,D], [B,S,H,D], ...) without gaps or overlap, and any padding.
-bool rows_disjoint(const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D) {
-    int64_t n[3] = {B, H, S}, s[3] = {st[0], st[1], st[2]};
-    for (int i = 0; i < 3; ++i)  // insertion sort by stride
-        for (int j = i; j > 0 && s[j] < s[j - 1]; --j) {
-            const int64_t ts = s[j], tn = n[j];
-            s[j] = s[j - 1]; n[j] = n[j - 1];
-            s[j - 1] = ts; n[j - 1] = tn;
-        }
-    int64_t span = D;  // elements covered by the dimensions taken so far, as one contiguous extent
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        if (s[i] < span) return false;
-        int64_t t = 0;
-        if (__builtin_mul_overflow(n[i] - 1, s[i], &t) || __builtin_add_overflow(span, t, &span)) return false;
-    }
-    return true;
 }
 
 // The checks of include/vt_attn.h on pointers, strides and the memory they describe (after check_shape
