@@ -356,6 +356,62 @@ vt_status vt_qk_rope_bwd(const vt_qk_rope_args *args, const void *dq_out, const 
  * 1..256).  Host-only arithmetic. */
 size_t vt_qk_rope_bwd_workspace_size(int64_t D);
 
+/*
+ * Attention of a batch of sequences behind a prefix that all of them share, each with its own cache: decoding
+ * (S_q = 1), checking a few drafted tokens, or a chunk of a prompt.  K and V of the prefix are stored and read
+ * once for the batch, not once per sequence.
+ *
+ * Query (b, h, s) attends to every prefix row j < S_p of K_p[h_kv], V_p[h_kv] and to the rows
+ *   j <= kv_len[b] - S_q + s,  j >= 0
+ * of its own cache K_c[b, h_kv], V_c[b, h_kv], h_kv = h / (H / H_kv): the S_q queries are the last S_q tokens of
+ * the sequence's kv_len[b] cached ones (vt_qk_rope_fwd appends them), each seeing the tokens up to itself.
+ *   O = softmax(scale q . k) v over the union,  LSE = log(sum exp(scale q . k)) (natural log).
+ * A query with kv_len[b] - S_q + s < 0 sees the prefix alone; with no prefix either, O = 0 and LSE = -inf.
+ *
+ * Arguments, as a struct whose first field is its size.
+ *   q, o                 [B,H,S_q,D_qk] and [B,H,S_q,D_v]
+ *   k_prefix, v_prefix   [H_kv,S_p,D_qk] and [H_kv,S_p,D_v], strides (h_kv, s); not read when S_p = 0
+ *   k_cache, v_cache     [B,H_kv,S_c,D_qk] and [B,H_kv,S_c,D_v]; not read when S_c = 0.  Rows at or past kv_len[b]
+ *                        are not read, whatever they hold.
+ *   kv_len               int32 [B], 0 <= kv_len[b] <= S_c, read on the device (a captured call replays with new
+ *                        lengths); NULL: S_c for every sequence.  A length outside that range counts as the nearest
+ *                        one inside and records VT_ERR_DEVICE_BOUNDS in the stream's status word.
+ *   lse                  fp32 [B,H,S_q] or NULL
+ *   workspace            DEVICE scratch, 256-byte aligned, at least vt_attn_prefix_workspace_size bytes (may be
+ *                        NULL when that is 0).  Every call writes what it reads there; two calls that share it must
+ *                        not overlap on the GPU, replays of captured ones included.
+ * Element types: VT_BF16, and VT_F32 with products of two TF32 parts per operand (about 2^-21 of every factor is
+ * lost, against 2^-11 in the other fp32 calls of this header).  Sums and statistics are fp32.  A key that a query may
+ * not see but that another query of the same sequence does must be finite, as in the other calls.
+ * Strides, alignment and errors as for vt_attn_fwd_strided (the stride of an index with one value is not looked at);
+ * VT_ERR_INVALID_ARG also for H not a multiple of H_kv or a workspace that is too small, VT_ERR_UNSUPPORTED also for
+ * S_p + S_c or B * H * S_q above 2^30.  B, H or S_q equal to 0 is a valid empty problem.
+ */
+typedef struct {
+    uint64_t struct_bytes; /* sizeof(vt_attn_prefix_args) */
+    int64_t B, H, H_kv, S_q, S_p, S_c, D_qk, D_v;
+    int32_t dtype; /* vt_dtype */
+    float scale;
+    const void *q;
+    int64_t q_stride[3];
+    const void *k_prefix, *v_prefix;
+    int64_t kp_stride[2], vp_stride[2];
+    const void *k_cache, *v_cache;
+    int64_t kc_stride[3], vc_stride[3];
+    const int32_t *kv_len;
+    void *o;
+    int64_t o_stride[3];
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+} vt_attn_prefix_args;
+
+vt_status vt_attn_fwd_prefix(const vt_attn_prefix_args *args, vt_stream_t stream);
+
+/* Bytes of workspace vt_attn_fwd_prefix needs on the current device (0: none, or the call would be refused). */
+size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,
+                                     int64_t D_qk, int64_t D_v, vt_dtype dtype);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *vt_status_str(vt_status status);
 

@@ -31,6 +31,7 @@ STATUS = {
 EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_splitkv",
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
            "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
+           "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size",
            "vt_status_str", "vt_last_device_status")
 
 
@@ -90,6 +91,10 @@ def load(path: str | None = None):
     lib.vt_qk_rope_bwd.restype = i
     lib.vt_qk_rope_bwd_workspace_size.argtypes = [i64]
     lib.vt_qk_rope_bwd_workspace_size.restype = sz
+    lib.vt_attn_fwd_prefix.argtypes = [ctypes.c_char_p, vp]
+    lib.vt_attn_fwd_prefix.restype = i
+    lib.vt_attn_prefix_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i]
+    lib.vt_attn_prefix_workspace_size.restype = sz
     lib.vt_status_str.argtypes = [i]
     lib.vt_status_str.restype = ctypes.c_char_p
     lib.vt_last_device_status.argtypes = [vp]
@@ -182,6 +187,19 @@ def vt_qk_rope_bwd(args: bytes, dq_out, dq_out_stride, dk_out, dk_out_stride, dq
 
 def vt_qk_rope_bwd_workspace_size(D) -> int:
     return int(load().vt_qk_rope_bwd_workspace_size(D))
+
+
+# vt_attn_prefix_args, packed in field order (every field is aligned without padding)
+_ATTN_PREFIX_ARGS = struct.Struct("=Q8qifQ3q2Q4q2Q6q2Q3q3Q")
+
+
+def vt_attn_fwd_prefix(args: bytes, stream) -> int:
+    """The C entry point: ``args`` is a packed vt_attn_prefix_args; returns the vt_status code."""
+    return load().vt_attn_fwd_prefix(args, stream)
+
+
+def vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype) -> int:
+    return int(load().vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype))
 
 
 def vt_status_str(code: int) -> str:
@@ -505,3 +523,94 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
     if rc != 0:
         raise VtError(rc, "vt_qk_rope_bwd")
     return dq, dk, dqw, dkw
+
+
+# ---------------------------------------------------------------- attention behind a shared prefix
+
+def _kv(name, t, H_kv, S, D, dtype):
+    """(address, strides) of a prefix tensor [H_kv, S, D] with its last dimension contiguous."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [H_kv, S, D] with the last dimension contiguous")
+    if t.shape != (H_kv, S, D):
+        raise ValueError(f"{name} must have shape {(H_kv, S, D)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr(), t.stride()[:2]
+
+
+@_on_stream
+def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, scale: float | None = None,
+                    return_lse: bool = False, out=None, lse=None, workspace=None):
+    """Attention of q [B,H,S_q,D_qk] over a prefix that all sequences share, k_prefix [H_kv,S_p,D_qk] and v_prefix
+    [H_kv,S_p,D_v], and over each sequence's own cache, k_cache [B,H_kv,S_c,D_qk] and v_cache [B,H_kv,S_c,D_v], up to
+    its length kv_len (int32 [B], counting these S_q tokens; None: S_c): see vt_attn_fwd_prefix in include/vt_attn.h.
+    Prefix or cache may be None.  Returns O, or (O, LSE) with ``return_lse``.  ``workspace`` may be a preallocated
+    uint8 CUDA tensor of at least ``vt_attn_prefix_workspace_size`` bytes; ``stream`` may name another stream than the
+    current one."""
+    import torch
+    B, H, S_q, D_qk = q.shape
+    if (k_prefix is None) != (v_prefix is None) or (k_cache is None) != (v_cache is None):
+        raise ValueError("K and V of the prefix, and of the cache, come together")
+    if k_prefix is None and k_cache is None:
+        raise ValueError("a prefix or a cache is required")
+    some_k, some_v = (k_prefix, v_prefix) if k_prefix is not None else (k_cache, v_cache)
+    H_kv, D_v = some_k.shape[-3], some_v.shape[-1]
+    code, dt = _dtype_code(q), q.dtype
+    _same_place("attn_fwd_prefix", q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, workspace)
+    if scale is None:
+        scale = float(D_qk) ** -0.5
+    S_p = S_c = 0
+    pkp = pvp = pkc = pvc = lens = plse = 0
+    skp = svp = (0, 0)
+    skc = svc = (0, 0, 0)
+    pq, sq = _bhsd("q", q)
+    if k_prefix is not None:
+        S_p = k_prefix.shape[1]
+        pkp, skp = _kv("k_prefix", k_prefix, H_kv, S_p, D_qk, dt)
+        pvp, svp = _kv("v_prefix", v_prefix, H_kv, S_p, D_v, dt)
+    if k_cache is not None:
+        S_c = k_cache.shape[2]
+        pkc, skc = _bhsd("k_cache", k_cache, (B, H_kv, S_c, D_qk), dt)
+        pvc, svc = _bhsd("v_cache", v_cache, (B, H_kv, S_c, D_v), dt)
+    if kv_len is not None:
+        if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
+            raise ValueError("kv_len must be a contiguous int32 vector of B entries")
+        lens = kv_len.data_ptr()
+    if out is None:
+        out = _new_rows(B, H, S_q, D_v, dt, q.device)
+    po, so = _bhsd("out", out, (B, H, S_q, D_v), dt)
+    if return_lse and lse is None:
+        lse = torch.empty((B, H, S_q), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, S_q):
+            raise ValueError("lse must be a contiguous float32 [B, H, S_q] tensor")
+        plse = lse.data_ptr()
+    lib = load()
+    ws_ptr = ws_bytes = 0
+    if workspace is None:
+        need = lib.vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    args = _ATTN_PREFIX_ARGS.pack(_ATTN_PREFIX_ARGS.size, B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code, scale, pq, *sq,
+                                  pkp, pvp, *skp, *svp, pkc, pvc, *skc, *svc, lens, po, *so, plse, ws_ptr, ws_bytes)
+    rc = lib.vt_attn_fwd_prefix(args, torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise VtError(rc, "vt_attn_fwd_prefix")
+    return (out, lse) if return_lse else out
+
+
+def attn_prefix_step(q, k, v, freqs, positions, k_prefix, v_prefix, k_cache, v_cache, kv_len, *, pair_axis=None,
+                     interleaved: bool = False, eps: float | None = None, q_weight=None, k_weight=None,
+                     scale: float | None = None, return_lse: bool = False, out=None, lse=None, workspace=None,
+                     stream=None):
+    """One step of a batch behind a shared prefix, from the projections of its new tokens: norm and rotate q and k,
+    append k and v to the caches at the end of each sequence (``kv_len`` counts the new tokens already), and attend
+    to the prefix and to the caches.  ``qk_rope`` and ``attn_fwd_prefix`` in one call, with their arguments; q and k
+    are left as they are."""
+    q_rot, _ = qk_rope(q, k, freqs, positions, pair_axis=pair_axis, interleaved=interleaved, eps=eps,
+                       q_weight=q_weight, k_weight=k_weight, k_out=k_cache, kv_len=kv_len, v=v, v_out=v_cache,
+                       stream=stream)
+    return attn_fwd_prefix(q_rot, k_prefix, v_prefix, k_cache, v_cache, kv_len, scale=scale, return_lse=return_lse,
+                           out=out, lse=lse, workspace=workspace, stream=stream)

@@ -12,9 +12,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvt_attn.so")
 LIB_DEBUG = os.path.join(PKG, "libvt_attn_debug.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("vt_attn_api.cu", "vt_qk_rope_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("vt_attn_api.cu", "vt_qk_rope_api.cu", "vt_attn_prefix_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("vt_attn_f32_2q.cuh", "vt_attn_bf16_2q.cuh", "vt_attn_common.cuh", "vt_attn_merge.cuh",
-                                                  "vt_ptx.cuh", "vt_host.h", "vt_qk_rope.cuh")] + [
+                                                  "vt_ptx.cuh", "vt_host.h", "vt_qk_rope.cuh", "vt_attn_stream.cuh")] + [
     os.path.join(os.path.dirname(PKG), "include", "vt_attn.h")]
 
 NVCC_FLAGS = [

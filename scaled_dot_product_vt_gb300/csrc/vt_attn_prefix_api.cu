@@ -1,0 +1,282 @@
+// Host side of vt_attn_fwd_prefix: argument checks, the plan of a call, launches (contract in include/vt_attn.h).
+#include <cmath>
+#include <cstring>
+
+#include "vt_attn_stream.cuh"
+#include "vt_host.h"
+
+namespace vt {
+namespace prefix {
+namespace {
+
+using Args = vt_attn_prefix_args;
+
+// How a call runs: `shares` launches' worth of partial results of the prefix (0: the second launch reads the
+// prefix itself, for every sequence), then the caches.
+struct Plan {
+    int prefix_shares, prefix_cluster, cluster;
+    bool with_prefix;
+    size_t workspace;
+};
+
+struct Sizes {
+    int64_t G, per_b, rows, tiles_all, tiles_b;
+};
+
+vt_status check_shape(const Args &a, bool *empty) {
+    *empty = false;
+    if (a.struct_bytes != sizeof(Args)) return VT_ERR_INVALID_ARG;
+    if (a.dtype != VT_F32 && a.dtype != VT_BF16) return VT_ERR_INVALID_ARG;
+    if (a.B < 0 || a.H < 0 || a.S_q < 0 || a.S_p < 0 || a.S_c < 0 || a.D_qk <= 0 || a.D_v <= 0) return VT_ERR_INVALID_ARG;
+    if (a.H_kv < 1 || a.H % a.H_kv != 0 || !std::isfinite(a.scale)) return VT_ERR_INVALID_ARG;
+    if (a.D_qk > kMaxD || a.D_v > kMaxD || a.B > kMaxExtent || a.H > kMaxExtent || a.S_q > kMaxSeq) return VT_ERR_UNSUPPORTED;
+    if (a.S_p > kMaxSeq || a.S_c > kMaxSeq || a.S_p + a.S_c > kMaxSeq) return VT_ERR_UNSUPPORTED;
+    *empty = a.B == 0 || a.H == 0 || a.S_q == 0;
+    // rows are counted in 32 bits
+    int64_t n = 0;
+    if (__builtin_mul_overflow(a.B, a.H, &n) || __builtin_mul_overflow(n, a.S_q, &n) || n > kMaxSeq) return VT_ERR_UNSUPPORTED;
+    return VT_OK;
+}
+
+Sizes sizes_of(const Args &a) {
+    Sizes z;
+    z.G = a.H / a.H_kv;
+    z.per_b = a.S_q * z.G;
+    z.rows = a.B * a.H * a.S_q;
+    z.tiles_all = (a.B * z.per_b + st::kRowsTile - 1) / st::kRowsTile;
+    z.tiles_b = (z.per_b + st::kRowsTile - 1) / st::kRowsTile;
+    return z;
+}
+
+size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
+    return ((static_cast<size_t>(rows) * shares * (D_v + 3) * sizeof(float)) + 255) & ~size_t(255);
+}
+
+int cluster_for(int64_t units, int64_t keys, int sms) {
+    int c = 1;
+    // two CTAs per SM, and as long as every CTA keeps 64 keys (a block for each warp)
+    while (c < st::kMaxClusterCtas && units * c < 2LL * sms && keys >= 128LL * c) c *= 2;
+    return c;
+}
+
+Plan plan_of(const Args &a, int sms) {
+    const Sizes z = sizes_of(a);
+    Plan p{};
+    const int64_t kv_units = a.B * a.H_kv * z.tiles_b;
+    const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
+    // reading the prefix once per sequence and row tile costs no more than a launch when it is this small
+    const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
+    p.with_prefix = z.tiles_all >= a.B * z.tiles_b || again <= (int64_t(16) << 20);
+    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c, sms);
+    if (p.with_prefix || a.S_p == 0) {
+        p.with_prefix = true;
+        return p;
+    }
+    const int64_t units = a.H_kv * z.tiles_all;
+    p.prefix_cluster = cluster_for(units, a.S_p, sms);
+    int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
+    const int64_t most = a.S_p / (256LL * p.prefix_cluster);
+    if (shares > most) shares = most;
+    if (shares > kMaxSplit) shares = kMaxSplit;
+    p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
+    p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares);
+    return p;
+}
+
+// A tensor's checks (strides of an index with one value are not looked at).
+vt_status tensor(const void *p, const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D, int elt, bool out,
+                 Span *span) {
+    if (!p) return VT_ERR_INVALID_ARG;
+    const int64_t n[3] = {B, H, S};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] <= 0) return VT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p) % 16) return VT_ERR_MISALIGNED;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] >= kMaxStrideBytes / elt) return VT_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] * elt) % 16) return VT_ERR_MISALIGNED;
+    if (!span_of(p, st, B, H, S, D, elt, span)) return VT_ERR_INVALID_ARG;
+    if (out && !rows_disjoint(st, B, H, S, D)) return VT_ERR_INVALID_ARG;
+    return VT_OK;
+}
+
+#define VT_TRY(expr)                          \
+    do {                                      \
+        const vt_status vt_try_ = (expr);     \
+        if (vt_try_ != VT_OK) return vt_try_; \
+    } while (0)
+
+vt_status check_memory(const Args &a, const Plan &plan) {
+    const int elt = a.dtype == VT_BF16 ? 2 : 4;
+    Span in[6], out[3];
+    int n_in = 0, n_out = 0;
+    VT_TRY(tensor(a.q, a.q_stride, a.B, a.H, a.S_q, a.D_qk, elt, false, &in[n_in++]));
+    if (a.S_p > 0) {
+        const int64_t ks[3] = {1, a.kp_stride[0], a.kp_stride[1]}, vs[3] = {1, a.vp_stride[0], a.vp_stride[1]};
+        VT_TRY(tensor(a.k_prefix, ks, 1, a.H_kv, a.S_p, a.D_qk, elt, false, &in[n_in++]));
+        VT_TRY(tensor(a.v_prefix, vs, 1, a.H_kv, a.S_p, a.D_v, elt, false, &in[n_in++]));
+    }
+    if (a.S_c > 0) {
+        VT_TRY(tensor(a.k_cache, a.kc_stride, a.B, a.H_kv, a.S_c, a.D_qk, elt, false, &in[n_in++]));
+        VT_TRY(tensor(a.v_cache, a.vc_stride, a.B, a.H_kv, a.S_c, a.D_v, elt, false, &in[n_in++]));
+    }
+    if (a.kv_len) {
+        if (reinterpret_cast<uintptr_t>(a.kv_len) % 4) return VT_ERR_MISALIGNED;
+        if (!span_bytes(a.kv_len, a.B * 4, &in[n_in++])) return VT_ERR_INVALID_ARG;
+    }
+    VT_TRY(tensor(a.o, a.o_stride, a.B, a.H, a.S_q, a.D_v, elt, true, &out[n_out++]));
+    if (a.lse) {
+        if (reinterpret_cast<uintptr_t>(a.lse) % 4) return VT_ERR_INVALID_ARG;
+        if (!span_bytes(a.lse, a.B * a.H * a.S_q * 4, &out[n_out++])) return VT_ERR_INVALID_ARG;
+    }
+    if (plan.workspace) {
+        if (!a.workspace || a.workspace_bytes < plan.workspace) return VT_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(a.workspace) % 256) return VT_ERR_MISALIGNED;
+        if (!span_bytes(a.workspace, static_cast<int64_t>(plan.workspace), &out[n_out++])) return VT_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(out[i], in[j])) return VT_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return VT_ERR_INVALID_ARG;
+    }
+    return VT_OK;
+}
+
+st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *status) {
+    st::Params p{};
+    p.B = static_cast<int>(a.B);
+    p.H = static_cast<int>(a.H);
+    p.H_kv = static_cast<int>(a.H_kv);
+    p.G = static_cast<int>(z.G);
+    p.S_q = static_cast<int>(a.S_q);
+    p.S_p = static_cast<int>(a.S_p);
+    p.S_c = static_cast<int>(a.S_c);
+    p.D_qk = static_cast<int>(a.D_qk);
+    p.D_v = static_cast<int>(a.D_v);
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.Q = a.q;
+    p.Kp = a.k_prefix;
+    p.Vp = a.v_prefix;
+    p.Kc = a.k_cache;
+    p.Vc = a.v_cache;
+    p.q_sb = a.q_stride[0]; p.q_sh = a.q_stride[1]; p.q_ss = a.q_stride[2];
+    p.kp_sh = a.kp_stride[0]; p.kp_ss = a.kp_stride[1];
+    p.vp_sh = a.vp_stride[0]; p.vp_ss = a.vp_stride[1];
+    p.kc_sb = a.kc_stride[0]; p.kc_sh = a.kc_stride[1]; p.kc_ss = a.kc_stride[2];
+    p.vc_sb = a.vc_stride[0]; p.vc_sh = a.vc_stride[1]; p.vc_ss = a.vc_stride[2];
+    p.kv_len = a.S_c > 0 ? a.kv_len : nullptr;
+    p.rows = z.rows;
+    if (plan.workspace) {
+        const int64_t n = z.rows * plan.prefix_shares;
+        p.part_o = static_cast<float *>(a.workspace);
+        p.part_m = p.part_o + n * a.D_v;
+        p.part_l = p.part_m + n;
+        p.part_c = p.part_l + n;
+    }
+    p.O = a.o;
+    p.o_sb = a.o_stride[0]; p.o_sh = a.o_stride[1]; p.o_ss = a.o_stride[2];
+    p.lse = a.lse;
+    p.status = status;
+    return p;
+}
+
+using Kern = void (*)(const st::Params);
+
+template <typename T>
+Kern pick(const Args &a, int *smem) {
+    const bool k64 = a.D_qk <= 64, v64 = a.D_v <= 64;
+    if (k64 && v64) { *smem = st::Tile<T, 64, 64>::kSmem; return st::attn_stream_kernel<T, 64, 64>; }
+    if (k64) { *smem = st::Tile<T, 64, 128>::kSmem; return st::attn_stream_kernel<T, 64, 128>; }
+    if (v64) { *smem = st::Tile<T, 128, 64>::kSmem; return st::attn_stream_kernel<T, 128, 64>; }
+    *smem = st::Tile<T, 128, 128>::kSmem;
+    return st::attn_stream_kernel<T, 128, 128>;
+}
+
+vt_status launch_stream(const Args &a, const st::Params &p, int64_t units, int cluster, bool follows, int dev,
+                        cudaStream_t stream) {
+    int smem = 0;
+    const Kern kern = a.dtype == VT_BF16 ? pick<uint16_t>(a, &smem) : pick<float>(a, &smem);
+    if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
+    const int64_t ctas = units * cluster;
+    if (ctas > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(st::kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (follows) {  // start as the prefix's CTAs leave room; the kernel waits for them before it adds their results
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
+
+vt_status forward(const Args &a, cudaStream_t stream) {
+    bool empty = false;
+    VT_TRY(check_shape(a, &empty));
+    if (empty) return VT_OK;
+    int dev = 0;
+    DeviceInfo info;
+    const bool have = cudaGetDevice(&dev) == cudaSuccess && device_info(dev, &info);
+    const Plan plan = plan_of(a, have ? info.sms : 152);
+    VT_TRY(check_memory(a, plan));
+    if (!have) return VT_ERR_CUDA;
+    const Sizes z = sizes_of(a);
+    st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
+    if (plan.prefix_shares) {
+        p.all_rows = 1;
+        p.row_tiles = static_cast<int>(z.tiles_all);
+        p.shares = plan.prefix_shares;
+        p.cluster = plan.prefix_cluster;
+        VT_TRY(launch_stream(a, p, a.H_kv * z.tiles_all * p.shares, p.cluster, false, dev, stream));
+    }
+    p.all_rows = 0;
+    p.with_prefix = plan.with_prefix ? 1 : 0;
+    p.row_tiles = static_cast<int>(z.tiles_b);
+    p.shares = 1;
+    p.cluster = plan.cluster;
+    p.prior = plan.prefix_shares;
+    VT_TRY(launch_stream(a, p, a.B * a.H_kv * z.tiles_b, p.cluster, plan.prefix_shares > 0, dev, stream));
+    return env_check() ? read_status(stream) : VT_OK;
+}
+
+}  // namespace
+}  // namespace prefix
+}  // namespace vt
+
+extern "C" {
+
+vt_status vt_attn_fwd_prefix(const vt_attn_prefix_args *args, vt_stream_t stream) {
+    const vt::NvtxRange range("vt_attn_fwd_prefix");
+    if (!args) return VT_ERR_INVALID_ARG;
+    return vt::prefix::forward(*args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,
+                                     int64_t D_qk, int64_t D_v, vt_dtype dtype) {
+    vt_attn_prefix_args a{};
+    a.struct_bytes = sizeof a;
+    a.B = B; a.H = H; a.H_kv = H_kv; a.S_q = S_q; a.S_p = S_p; a.S_c = S_c; a.D_qk = D_qk; a.D_v = D_v;
+    a.dtype = dtype;
+    bool empty = false;
+    if (vt::prefix::check_shape(a, &empty) != VT_OK || empty) return 0;
+    int dev = 0;
+    vt::DeviceInfo info;
+    const bool have = cudaGetDevice(&dev) == cudaSuccess && vt::device_info(dev, &info);
+    return vt::prefix::plan_of(a, have ? info.sms : 152).workspace;
+}
+
+}  // extern "C"
