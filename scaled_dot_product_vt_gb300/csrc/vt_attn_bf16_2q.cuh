@@ -201,6 +201,31 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
     return true;
 }
 
+// Copy rows row0 .. row0 + 127 of head hk into a Q tile (128-byte swizzle: the 16-byte pieces of a row are permuted
+// by its low bits), zeros past the last row and past D_qk.  Called by the 128 threads of a softmax warpgroup; on
+// return the calling thread's pieces are visible to the tensor core.
+__device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int hk, const AttnParams &p) {
+    const int tid = threadIdx.x & 127;
+    const int pieces = p.q_chunks * 8;                 // 16-byte pieces of a row: 8 or 16
+    const int c = tid & (pieces - 1);
+    const int step = 128 / pieces;                     // rows the warpgroup copies at once
+    const int bytes = min(16, max(0, p.D_qk * 2 - c * 16));
+    const int per_seq = p.row_heads * p.row_tokens;
+    const uint32_t col = tile + (c >> 3) * kChunkBytes;
+#pragma unroll 8
+    for (int r = tid / pieces; r < kBM; r += step) {
+        const int f = row0 + r;
+        const bool in = f < p.S_q && bytes > 0;
+        const int b = in ? f / per_seq : 0, rest = in ? f - b * per_seq : 0;
+        const int s = rest / p.row_heads, g = rest - s * p.row_heads;
+        const uint16_t *src = static_cast<const uint16_t *>(p.Q) + b * p.q_sb +
+                              (static_cast<long long>(hk) * p.row_heads + g) * p.q_sh + s * p.q_ss + (in ? c * 8 : 0);
+        cp_async16(col + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? src : p.Q, in ? bytes : 0);
+    }
+    cp_async_wait_all();
+    fence_async_shared();
+}
+
 }  // namespace q2
 
 // KQ: MMA K-steps (16 bf16 each) of Q K^T, D_qk rounded up: 2, 4, 6 or 8.
@@ -210,7 +235,10 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
 // kEpiSplit: the partial results of a key-range share, for the split-KV merge kernel; kEpiPlainFast: O only,
 // 32-byte aligned rows and D_v a multiple of 16 (the common case, with no other store forms in the code).
 // FOLD: the scale is positive and folds into the exponent; otherwise the scores are scaled first.
-template <int KQ, bool RING, int EPI, bool FOLD>
+// GATHER: a tile's rows are those of several sequences and heads (AttnParams::row_heads), copied into the Q tiles by
+// the softmax warpgroups instead of TMA: no box covers them for every group size.  A launch of this form lets
+// the launch that follows it start early (griddepcontrol).
+template <int KQ, bool RING, int EPI, bool FOLD, bool GATHER = false>
 __global__ void __launch_bounds__(q2::kThreads, 1)
     attn_fwd_bf16_2q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
@@ -223,6 +251,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
     const int lane = threadIdx.x & 31;
 
     const int n_slots = p.stages;
+    if constexpr (GATHER) launch_dependents();
 
     // ---- shared memory: Q tile 0, Q tile 1, then `n_slots` equal K/V slots
     const uint32_t raw = smem_u32(smem_raw);
@@ -240,7 +269,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
             mbar_init(smem_u32(&ctl.full[s]), 1);
             mbar_init(smem_u32(&ctl.empty[s]), RING ? 2 : 1);
         }
-        mbar_init(smem_u32(&ctl.q_full), 1);
+        mbar_init(smem_u32(&ctl.q_full), GATHER ? 256 : 1);
         mbar_init(smem_u32(&ctl.q_empty), RING ? 2 : 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&ctl.s_full[t]), 1);
@@ -263,7 +292,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmQ);
+        if (!GATHER) tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
@@ -333,25 +362,27 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 mbar_arrive(smem_u32(&ctl.unit_full[k]));
                 if (u < 0) break;
                 if (U.n_kv == 0) continue;
-                // The unit's Q may only be loaded once the previous unit's last Q K^T has read the Q buffers;
-                // fetch it into L2 now, so that the load after that point is an L2 hit.
-                for (int t = 0; t < 2; ++t)
-                    if ((t ? U.es1 > U.as1 : U.es0 > U.as0))
-                        for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, U.r0 + t * kBM, U.h, U.b);
-                if (q_loads > 0) {  // the previous unit's last Q K^T has read Q
-                    ok = wait_bounded(smem_u32(&ctl.q_empty), (q_loads - 1) & 1, ctl.abort_flag, p);
-                    if (!ok) break;
+                if constexpr (!GATHER) {
+                    // The unit's Q may only be loaded once the previous unit's last Q K^T has read the Q buffers;
+                    // fetch it into L2 now, so that the load after that point is an L2 hit.
+                    for (int t = 0; t < 2; ++t)
+                        if ((t ? U.es1 > U.as1 : U.es0 > U.as0))
+                            for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, U.r0 + t * kBM, U.h, U.b);
+                    if (q_loads > 0) {  // the previous unit's last Q K^T has read Q
+                        ok = wait_bounded(smem_u32(&ctl.q_empty), (q_loads - 1) & 1, ctl.abort_flag, p);
+                        if (!ok) break;
+                    }
+                    const bool load0 = U.es0 > U.as0, load1 = U.es1 > U.as1;  // Q tiles with work
+                    mbar_arrive_expect_tx(smem_u32(&ctl.q_full), (int(load0) + int(load1)) * q_tile_bytes);
+                    if (load0)
+                        for (int c = 0; c < p.q_chunks; ++c)
+                            tma_load_4d(sQ0 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0, U.h, U.b);
+                    if (load1)
+                        for (int c = 0; c < p.q_chunks; ++c)
+                            tma_load_4d(sQ1 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0 + kBM, U.h,
+                                        U.b);
+                    ++q_loads;
                 }
-                const bool load0 = U.es0 > U.as0, load1 = U.es1 > U.as1;  // Q tiles with work
-                mbar_arrive_expect_tx(smem_u32(&ctl.q_full), (int(load0) + int(load1)) * q_tile_bytes);
-                if (load0)
-                    for (int c = 0; c < p.q_chunks; ++c)
-                        tma_load_4d(sQ0 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0, U.h, U.b);
-                if (load1)
-                    for (int c = 0; c < p.q_chunks; ++c)
-                        tma_load_4d(sQ1 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0 + kBM, U.h,
-                                    U.b);
-                ++q_loads;
                 for (int i = 0; i < 2 * U.n_kv; ++i) {
                     if (loads >= n_slots) {
                         ok = wait_bounded(smem_u32(&ctl.empty[s]), (empty_phase >> s) & 1u, ctl.abort_flag, p);
@@ -597,6 +628,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         uint32_t s_par = 0, o_par = 0;  // parities of the next scores and the next o_done of this tile
         uint32_t g = 0;                 // score ring: scores of this tile seen over the CTA's life
         uint32_t handed = 0;            // P hand-overs of this tile over the CTA's life
+        uint32_t gathered = 0;          // GATHER: Q tiles copied
         uint32_t pv_handed = 0, pv_seen = 0;  // score ring: P hand-overs, and P V completions consumed
         bool ok = true;
         // score ring: consume the completion of the oldest P V not yet consumed
@@ -618,6 +650,17 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
             const int key_lo = band_key_lo(p, q_row), key_hi = band_key_hi(p, q_row);
             const int mask_lo = band_key_lo(p, min(tile_row0 + kBM, p.S_q) - 1);
             const int mask_hi = band_key_hi(p, tile_row0);
+            if constexpr (GATHER) {
+                if (U.n_kv > 0) {
+                    if (gathered > 0)  // the previous unit's last Q K^T has read Q
+                        ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl.q_empty), (gathered - 1) & 1u,
+                                                                  ctl.abort_flag, p)) != 0;
+                    if (!ok) break;
+                    gather_rows(t ? sQ1 : sQ0, tile_row0, U.h, p);
+                    mbar_arrive(smem_u32(&ctl.q_full));
+                    ++gathered;
+                }
+            }
             float m_used = -INFINITY;  // reference max (log2 units) of O_t and l
             float l = 0.0f;
             float l_fix = 0.0f;        // bf16 rounding of each tile's largest P, relative to m_used

@@ -42,8 +42,11 @@ struct AttnParams {
     int o_vec32;                 // 1: O and its strides are 32-byte multiples (32-byte stores of O rows)
     const void *V;               // read by the fp32 V loader
     long long v_sb, v_sh, v_ss;
-    const void *Q;               // read by the fp32 kernel's softmax threads (Q goes to TMEM)
+    const void *Q;               // read by the fp32 kernel's softmax threads (Q goes to TMEM), and where rows are gathered
     long long q_sb, q_sh, q_ss;
+    // bf16, gathered rows: H counts key/value heads, B is 1, and row r of head h is query head
+    // h * row_heads + r % row_heads at position (r / row_heads) % row_tokens of sequence r / (row_heads * row_tokens)
+    int row_heads, row_tokens;
     // fp32 kernel: query tiles per work unit (1 or 2), and the CTAs of a thread-block cluster that share
     // one unit's key tiles and merge their results in distributed shared memory (1: no cluster)
     int tiles_per_unit;

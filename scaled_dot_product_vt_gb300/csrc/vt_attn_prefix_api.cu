@@ -2,6 +2,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "vt_attn_bf16_2q.cuh"
 #include "vt_attn_stream.cuh"
 #include "vt_host.h"
 
@@ -11,11 +12,12 @@ namespace {
 
 using Args = vt_attn_prefix_args;
 
-// How a call runs: `shares` launches' worth of partial results of the prefix (0: the second launch reads the
-// prefix itself, for every sequence), then the caches.
+// How a call runs.  With prefix_shares > 0 a first launch leaves that many partial results of the prefix in the
+// workspace, from the two-tile tcgen05 kernel (`tiles`) or from the key-streaming kernel; the second launch streams
+// the caches and adds them.  Otherwise one launch streams the prefix and the cache of every sequence.
 struct Plan {
+    bool tiles, with_prefix;
     int prefix_shares, prefix_cluster, cluster;
-    bool with_prefix;
     size_t workspace;
 };
 
@@ -48,6 +50,9 @@ Sizes sizes_of(const Args &a) {
     return z;
 }
 
+constexpr int64_t kTileRows = 32;                   // more rows per prefix key: the tcgen05 kernel
+constexpr int64_t kReadAgain = int64_t(16) << 20;  // bytes
+
 size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
     return ((static_cast<size_t>(rows) * shares * (D_v + 3) * sizeof(float)) + 255) & ~size_t(255);
 }
@@ -59,6 +64,24 @@ int cluster_for(int64_t units, int64_t keys, int sms) {
     return c;
 }
 
+// Shares of the prefix for the tcgen05 kernel: the count that its launch is expected to finish first with.  A unit
+// takes about 1.5 us per 128-key tile (two query tiles) and 4 us besides; a partial result is written and read.
+int tile_shares(int64_t blocks, int64_t S_p, int64_t rows, int64_t D_v, int sms) {
+    const int64_t tiles = (S_p + q2::kBN - 1) / q2::kBN;
+    int best = 1;
+    double best_us = 0.0;
+    for (int n = 1; n <= kMaxSplit && n <= tiles; ++n) {
+        const double waves = static_cast<double>((blocks * n + sms - 1) / sms);
+        const double us = waves * (1.5 * static_cast<double>((tiles + n - 1) / n) + 4.0) +
+                          static_cast<double>(rows) * n * (D_v + 3) * 8e-6 / 5.0;
+        if (n == 1 || us < best_us) {
+            best = n;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 Plan plan_of(const Args &a, int sms) {
     const Sizes z = sizes_of(a);
     Plan p{};
@@ -66,19 +89,25 @@ Plan plan_of(const Args &a, int sms) {
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
     // reading the prefix once per sequence and row tile costs no more than a launch when it is this small
     const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
-    p.with_prefix = z.tiles_all >= a.B * z.tiles_b || again <= (int64_t(16) << 20);
+    p.tiles = a.dtype == VT_BF16 && a.B * z.per_b > kTileRows;
+    p.with_prefix = again <= kReadAgain || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
     p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c, sms);
-    if (p.with_prefix || a.S_p == 0) {
-        p.with_prefix = true;
+    if (p.with_prefix) {
+        p.tiles = false;
         return p;
     }
-    const int64_t units = a.H_kv * z.tiles_all;
-    p.prefix_cluster = cluster_for(units, a.S_p, sms);
-    int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
-    const int64_t most = a.S_p / (256LL * p.prefix_cluster);
-    if (shares > most) shares = most;
-    if (shares > kMaxSplit) shares = kMaxSplit;
-    p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
+    if (p.tiles) {
+        const int64_t blocks = a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows);
+        p.prefix_shares = tile_shares(blocks, a.S_p, z.rows, a.D_v, sms);
+    } else {
+        const int64_t units = a.H_kv * z.tiles_all;
+        p.prefix_cluster = cluster_for(units, a.S_p, sms);
+        int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
+        const int64_t most = a.S_p / (256LL * p.prefix_cluster);
+        if (shares > most) shares = most;
+        if (shares > kMaxSplit) shares = kMaxSplit;
+        p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
+    }
     p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares);
     return p;
 }
@@ -224,6 +253,77 @@ vt_status launch_stream(const Args &a, const st::Params &p, int64_t units, int c
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
+// The prefix on the two-tile tcgen05 kernel: one sequence of B * S_q * G gathered rows per key/value head.
+vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st::Params &sp, const DeviceInfo &info,
+                       int dev, cudaStream_t stream) {
+    const int64_t row_k = (a.D_qk * 2 + 15) / 16 * 8, row_v = (a.D_v * 2 + 15) / 16 * 8;
+    auto map = [&](CUtensorMap *m, const void *ptr, const int64_t st[2], int64_t row, int64_t D) {
+        const int64_t ss = a.S_p > 1 ? st[1] : row, sh = a.H_kv > 1 ? st[0] : row;
+        const int64_t strides[3] = {row, sh, ss};
+        return make_map(m, ptr, strides, 1, a.H_kv, a.S_p, D, 2, q2::kBN);
+    };
+    CUtensorMap tk, tv;
+    if (!map(&tk, a.k_prefix, a.kp_stride, row_k, a.D_qk) || !map(&tv, a.v_prefix, a.vp_stride, row_v, a.D_v))
+        return VT_ERR_CUDA;
+    AttnParams p{};
+    p.B = 1;
+    p.H = sp.H_kv;
+    p.S_q = static_cast<int>(a.B * z.per_b);
+    p.S_k = sp.S_p;
+    p.D_qk = sp.D_qk;
+    p.D_v = sp.D_v;
+    p.n_qblocks = (p.S_q + q2::kRows - 1) / q2::kRows;
+    p.q_chunks = (p.D_qk + q2::kChunk - 1) / q2::kChunk;
+    p.v_chunks = (p.D_v + q2::kChunk - 1) / q2::kChunk;
+    p.n_pv = (p.D_v + 15) / 16 * 16;
+    p.band_lo = -kBandInf;
+    p.band_hi = kBandInf;
+    p.kv_group = 1;
+    p.scale_log2 = sp.scale_log2;
+    p.Q = sp.Q;
+    p.q_sb = sp.q_sb;
+    p.q_sh = sp.q_sh;
+    p.q_ss = sp.q_ss;
+    p.row_heads = sp.G;
+    p.row_tokens = sp.S_q;
+    p.tiles_per_unit = 2;
+    p.cluster = 1;
+    p.n_split = plan.prefix_shares;
+    p.part_o = sp.part_o;
+    p.part_m = sp.part_m;
+    p.part_l = sp.part_l;
+    p.part_c = sp.part_c;
+    p.timeout_ns = kDefaultTimeoutNs;
+    p.status = sp.status;
+    const int q_bytes = 2 * p.q_chunks * static_cast<int>(q2::kChunkBytes);
+    const int slot_bytes = (p.q_chunks > p.v_chunks ? p.q_chunks : p.v_chunks) * static_cast<int>(q2::kChunkBytes);
+    p.stages = (kSmemLimit - 1024 - static_cast<int>(sizeof(q2::Ctl)) - 256 - q_bytes) / slot_bytes;
+    if (p.stages > q2::kMaxSlots) p.stages = q2::kMaxSlots;
+    const int smem = 1024 + q_bytes + p.stages * slot_bytes;
+    // heads whose query blocks run at about the same time read K and V of the prefix from L2
+    const int64_t per_head = static_cast<int64_t>(p.n_qblocks) * p.n_split;
+    int64_t grp = (2LL * info.sms + per_head - 1) / per_head;
+    p.head_group = static_cast<int>(grp < 1 ? 1 : (grp > a.H_kv ? a.H_kv : grp));
+    const int64_t units = per_head * a.H_kv;
+    if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
+    p.n_units = static_cast<int>(units);
+    using TileKern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnParams);
+    const int ksteps = (p.D_qk + 15) / 16;
+    auto pick_k = [&](auto ring_c) -> TileKern {
+        constexpr bool R = decltype(ring_c)::value;
+        if (p.scale_log2 > 0.0f)
+            return ksteps <= 4   ? attn_fwd_bf16_2q_kernel<4, R, q2::kEpiSplit, true, true>
+                   : ksteps <= 6 ? attn_fwd_bf16_2q_kernel<6, R, q2::kEpiSplit, true, true>
+                                 : attn_fwd_bf16_2q_kernel<8, R, q2::kEpiSplit, true, true>;
+        return ksteps <= 4 ? attn_fwd_bf16_2q_kernel<4, R, q2::kEpiSplit, false, true>
+                           : attn_fwd_bf16_2q_kernel<8, R, q2::kEpiSplit, false, true>;
+    };
+    const TileKern kern = p.n_pv <= 64 ? pick_k(std::true_type{}) : pick_k(std::false_type{});
+    if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
+    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(tk, tk, tv, p);
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
+
 vt_status forward(const Args &a, cudaStream_t stream) {
     bool empty = false;
     VT_TRY(check_shape(a, &empty));
@@ -236,7 +336,9 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
-    if (plan.prefix_shares) {
+    if (plan.tiles) {
+        VT_TRY(launch_tiles(a, plan, z, p, info, dev, stream));
+    } else if (plan.prefix_shares) {
         p.all_rows = 1;
         p.row_tiles = static_cast<int>(z.tiles_all);
         p.shares = plan.prefix_shares;

@@ -51,14 +51,6 @@ struct Params {
     unsigned *status;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -81,11 +73,15 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x as hi + lo: hi keeps the 10 explicit mantissa bits of TF32, lo the rest (exact in fp32; its own TF32 part drops
-// below 2^-21 of x).
+// x as hi + lo, both rounded to TF32 (10 explicit mantissa bits): what hi + lo leaves out is below 2^-23 of x.
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-    hi = x & 0xFFFFE000u;
-    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+    hi = tf32_of(__uint_as_float(x));
+    lo = tf32_of(__uint_as_float(x) - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_3xtf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     uint32_t ah[4], al[4], bh[2], bl[2];
@@ -103,8 +99,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Shared memory of one warp: `stages` blocks of K [16][DQ] then V [16][DV], and after the loop over it the warp's
 // result: O [16][DV] fp32, then m, l, c [16].
@@ -208,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
         if (i < n_mine) load(first + warp + i * kWarps, i);
-        cp_commit();
+        cp_async_commit();
     }
 
     // ---- the rows' queries, in the layout of an MMA's A operand: rows lane / 4 and lane / 4 + 8
@@ -254,10 +248,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, c[2] = {0.f, 0.f};
 
     for (int it = 0; it < n_mine; ++it) {
-        cp_wait<kStages - 2>();
+        cp_async_wait<kStages - 2>();
         __syncwarp();
         if (it + kStages - 1 < n_mine) load(first + warp + (it + kStages - 1) * kWarps, (it + kStages - 1) % kStages);
-        cp_commit();
+        cp_async_commit();
         const int k0 = (first + warp + it * kWarps) * kKeys;
         const uint32_t sk = wbase + (it % kStages) * L::kStage, sv = sk + L::kBytesK;
 
@@ -362,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
             }
         }
     }
-    cp_wait<0>();
+    cp_async_wait<0>();
     __syncwarp();
 
     // ---- the warp's result

@@ -72,6 +72,30 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const void *tmap, int c0, int
                  : "memory");
 }
 
+// ---------------------------------------------------------------- asynchronous copies by threads
+
+// 16 bytes from global to shared memory: `bytes` (0 to 16) are read, the rest are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups this thread committed have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// This thread's writes to shared memory are visible to the asynchronous proxy (tensor core, TMA) afterwards.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---------------------------------------------------------------- programmatic dependent launch
+
+// The next launch of the stream may start before this one ends (it must wait for what it reads).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Every launch that this one was started ahead of has ended, and its writes are visible.
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {

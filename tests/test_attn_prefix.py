@@ -166,6 +166,9 @@ CASES = [
     ("bf16", 6, 4, 2, 1, 0, 3000, 128, 128),      # no prefix
     ("bf16", 6, 4, 2, 2, 640, 0, 128, 128),       # no cache
     ("bf16", 2, 3, 1, 2, 0, 9, 33, 20),
+    ("bf16", 33, 8, 1, 2, 1025, 9, 80, 128),      # three query tiles of gathered rows, the last one short
+    ("bf16", 160, 64, 8, 4, 300, 5, 64, 64),      # more blocks of gathered rows than SMs
+    ("bf16", 80, 64, 8, 8, 300, 8, 128, 128),
     ("f32", 1, 1, 1, 1, 1, 1, 4, 4),
     ("f32", 8, 8, 2, 1, 1000, 333, 72, 72),
     ("f32", 40, 8, 2, 1, 1500, 40, 128, 128),
@@ -213,8 +216,9 @@ def test_lengths_outside_the_cache_are_reported():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale", [0.0, -0.5, 3.0])
 def test_scales_and_peaked_rows(dtype, scale):
-    p = Problem(dtype, 20, 4, 1, 1, 1100, 60, 64, 64, seed=4, scale=scale, spread=2.0)
-    p.check(*p.run())
+    for B, D in ((20, 64), (90, 64), (90, 128)):  # streamed, and (bf16) on tiles of gathered rows
+        p = Problem(dtype, B, 4, 1, 1, 1100, 60, D, D, seed=4, scale=scale, spread=2.0)
+        p.check(*p.run())
 
 
 @gpu
