@@ -371,8 +371,8 @@ size_t vt_qk_rope_bwd_workspace_size(int64_t D);
  * Arguments, as a struct whose first field is its size.
  *   q, o                 [B,H,S_q,D_qk] and [B,H,S_q,D_v]
  *   k_prefix, v_prefix   [H_kv,S_p,D_qk] and [H_kv,S_p,D_v], strides (h_kv, s); not read when S_p = 0
- *   k_cache, v_cache     [B,H_kv,S_c,D_qk] and [B,H_kv,S_c,D_v]; not read when S_c = 0.  Rows at or past kv_len[b]
- *                        are not read, whatever they hold.
+ *   k_cache, v_cache     [B,H_kv,S_c,D_qk] and [B,H_kv,S_c,D_v]; not read when S_c = 0.  What the rows at
+ *                        or past kv_len[b] hold has no influence.
  *   kv_len               int32 [B], 0 <= kv_len[b] <= S_c, read on the device (a captured call replays with new
  *                        lengths); NULL: S_c for every sequence.  A length outside that range counts as the nearest
  *                        one inside and records VT_ERR_DEVICE_BOUNDS in the stream's status word.

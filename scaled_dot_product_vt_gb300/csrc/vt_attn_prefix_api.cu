@@ -185,15 +185,7 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     p.D_v = static_cast<int>(a.D_v);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.Q = a.q;
-    p.Kp = a.k_prefix;
-    p.Vp = a.v_prefix;
-    p.Kc = a.k_cache;
-    p.Vc = a.v_cache;
     p.q_sb = a.q_stride[0]; p.q_sh = a.q_stride[1]; p.q_ss = a.q_stride[2];
-    p.kp_sh = a.kp_stride[0]; p.kp_ss = a.kp_stride[1];
-    p.vp_sh = a.vp_stride[0]; p.vp_ss = a.vp_stride[1];
-    p.kc_sb = a.kc_stride[0]; p.kc_sh = a.kc_stride[1]; p.kc_ss = a.kc_stride[2];
-    p.vc_sb = a.vc_stride[0]; p.vc_sh = a.vc_stride[1]; p.vc_ss = a.vc_stride[2];
     p.kv_len = a.S_c > 0 ? a.kv_len : nullptr;
     p.rows = z.rows;
     if (plan.workspace) {
@@ -206,11 +198,35 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     p.O = a.o;
     p.o_sb = a.o_stride[0]; p.o_sh = a.o_stride[1]; p.o_ss = a.o_stride[2];
     p.lse = a.lse;
+    p.timeout_ns = kDefaultTimeoutNs;
     p.status = status;
     return p;
 }
 
-using Kern = void (*)(const st::Params);
+// A tensor map of a prefix or cache tensor, boxes of `rows` rows; strides of an index with one value are replaced.
+bool kv_map(CUtensorMap *map, const void *ptr, const int64_t st[3], int64_t B, int64_t H_kv, int64_t S, int64_t D,
+            int elt, int rows) {
+    const int64_t row = (D * elt + 15) / 16 * 16 / elt;
+    const int64_t strides[3] = {B > 1 ? st[0] : row, H_kv > 1 ? st[1] : row, S > 1 ? st[2] : row};
+    return make_map(map, ptr, strides, B, H_kv, S, D, elt, rows);
+}
+
+// The four maps with boxes of `rows` keys (an absent prefix or cache gets the other's: it is not read).
+bool kv_maps(const Args &a, int rows, st::Maps *m) {
+    const int elt = a.dtype == VT_BF16 ? 2 : 4;
+    const int64_t kp[3] = {0, a.kp_stride[0], a.kp_stride[1]}, vp[3] = {0, a.vp_stride[0], a.vp_stride[1]};
+    if (a.S_p > 0 && (!kv_map(&m->kp, a.k_prefix, kp, 1, a.H_kv, a.S_p, a.D_qk, elt, rows) ||
+                      !kv_map(&m->vp, a.v_prefix, vp, 1, a.H_kv, a.S_p, a.D_v, elt, rows)))
+        return false;
+    if (a.S_c > 0 && (!kv_map(&m->kc, a.k_cache, a.kc_stride, a.B, a.H_kv, a.S_c, a.D_qk, elt, rows) ||
+                      !kv_map(&m->vc, a.v_cache, a.vc_stride, a.B, a.H_kv, a.S_c, a.D_v, elt, rows)))
+        return false;
+    if (a.S_p == 0) m->kp = m->kc, m->vp = m->vc;
+    if (a.S_c == 0) m->kc = m->kp, m->vc = m->vp;
+    return true;
+}
+
+using Kern = void (*)(const st::Maps, const st::Params);
 
 template <typename T>
 Kern pick(const Args &a, int *smem) {
@@ -222,7 +238,7 @@ Kern pick(const Args &a, int *smem) {
     return st::attn_stream_kernel<T, 128, 128>;
 }
 
-vt_status launch_stream(const Args &a, const st::Params &p, int64_t units, int cluster, bool follows, int dev,
+vt_status launch_stream(const Args &a, const st::Maps &maps, const st::Params &p, int64_t units, int cluster, bool follows, int dev,
                         cudaStream_t stream) {
     int smem = 0;
     const Kern kern = a.dtype == VT_BF16 ? pick<uint16_t>(a, &smem) : pick<float>(a, &smem);
@@ -249,22 +265,15 @@ vt_status launch_stream(const Args &a, const st::Params &p, int64_t units, int c
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, maps, p) != cudaSuccess) return VT_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
 // The prefix on the two-tile tcgen05 kernel: one sequence of B * S_q * G gathered rows per key/value head.
 vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st::Params &sp, const DeviceInfo &info,
                        int dev, cudaStream_t stream) {
-    const int64_t row_k = (a.D_qk * 2 + 15) / 16 * 8, row_v = (a.D_v * 2 + 15) / 16 * 8;
-    auto map = [&](CUtensorMap *m, const void *ptr, const int64_t st[2], int64_t row, int64_t D) {
-        const int64_t ss = a.S_p > 1 ? st[1] : row, sh = a.H_kv > 1 ? st[0] : row;
-        const int64_t strides[3] = {row, sh, ss};
-        return make_map(m, ptr, strides, 1, a.H_kv, a.S_p, D, 2, q2::kBN);
-    };
-    CUtensorMap tk, tv;
-    if (!map(&tk, a.k_prefix, a.kp_stride, row_k, a.D_qk) || !map(&tv, a.v_prefix, a.vp_stride, row_v, a.D_v))
-        return VT_ERR_CUDA;
+    st::Maps m{};
+    if (!kv_maps(a, q2::kBN, &m)) return VT_ERR_CUDA;
     AttnParams p{};
     p.B = 1;
     p.H = sp.H_kv;
@@ -320,7 +329,7 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     };
     const TileKern kern = p.n_pv <= 64 ? pick_k(std::true_type{}) : pick_k(std::false_type{});
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
-    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(tk, tk, tv, p);
+    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(m.kp, m.kp, m.vp, p);
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
@@ -336,6 +345,8 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
+    st::Maps maps{};
+    if (!kv_maps(a, st::kKeys, &maps)) return VT_ERR_CUDA;
     if (plan.tiles) {
         VT_TRY(launch_tiles(a, plan, z, p, info, dev, stream));
     } else if (plan.prefix_shares) {
@@ -343,7 +354,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
         p.row_tiles = static_cast<int>(z.tiles_all);
         p.shares = plan.prefix_shares;
         p.cluster = plan.prefix_cluster;
-        VT_TRY(launch_stream(a, p, a.H_kv * z.tiles_all * p.shares, p.cluster, false, dev, stream));
+        VT_TRY(launch_stream(a, maps, p, a.H_kv * z.tiles_all * p.shares, p.cluster, false, dev, stream));
     }
     p.all_rows = 0;
     p.with_prefix = plan.with_prefix ? 1 : 0;
@@ -351,7 +362,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.shares = 1;
     p.cluster = plan.cluster;
     p.prior = plan.prefix_shares;
-    VT_TRY(launch_stream(a, p, a.B * a.H_kv * z.tiles_b, p.cluster, plan.prefix_shares > 0, dev, stream));
+    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b, p.cluster, plan.prefix_shares > 0, dev, stream));
     return env_check() ? read_status(stream) : VT_OK;
 }
 

@@ -6,9 +6,10 @@
 // rows per key the work is bound by the bytes of K and V (4 flops per row and byte against ~280 that the card
 // balances at), so everything serves the loads:
 //   - The unit's keys are cut over the CTAs of a cluster and over the grid's shares, and a CTA's keys over its
-//     four warps in blocks of 16.  Every warp runs its own ring of cp.async stages and its own online softmax, so
-//     the loop has no barrier; rows past the end are filled with zeros instead of being read (a cache row that
-//     holds NaN never meets a probability of 0).
+//     four warps in blocks of 16.  Every warp runs its own ring of TMA loads (one lane issues them; loads by all lanes
+//     spent more instructions on addresses than the products take) and its own online softmax, so the loop has no
+//     barrier between warps.  V rows past the end of a sequence are set to zero in shared memory: they may hold
+//     NaN, which a probability of 0 does not hide.
 //   - Products are mma.sync: 16 rows is a quarter of the smallest tcgen05 tile, and the tensor pipe is not what
 //     bounds this kernel.  bf16 with fp32 accumulation; fp32 operands as two TF32 parts each, three products
 //     (hi hi + hi lo + lo hi), which keeps 21 bits of every factor.
@@ -38,8 +39,8 @@ struct Params {
     int with_prefix;  // (all_rows = 0) the unit's keys start with the prefix
     int row_tiles, shares, cluster;
     float scale_log2;
-    const void *Q, *Kp, *Vp, *Kc, *Vc;
-    long long q_sb, q_sh, q_ss, kp_sh, kp_ss, vp_sh, vp_ss, kc_sb, kc_sh, kc_ss, vc_sb, vc_sh, vc_ss;
+    const void *Q;
+    long long q_sb, q_sh, q_ss;
     const int *kv_len;  // [B], or null: S_c
     // partial results: [share][rows], rows = H_kv * B * S_q * G indexed ((hk * B + b) * S_q + s) * G + g
     float *part_o, *part_m, *part_l, *part_c;
@@ -48,7 +49,13 @@ struct Params {
     void *O;
     long long o_sb, o_sh, o_ss;
     float *lse;
+    unsigned long long timeout_ns;
     unsigned *status;
+};
+
+// Tensor maps of the prefix and of the caches, boxes of 16 rows x 128 bytes with the 128-byte swizzle.
+struct Maps {
+    CUtensorMap kp, vp, kc, vc;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -100,29 +107,46 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// Shared memory of one warp: `stages` blocks of K [16][DQ] then V [16][DV], and after the loop over it the warp's
-// result: O [16][DV] fp32, then m, l, c [16].
+// Wait for the phase of `bar` with `parity`, giving up after the time limit (which the status word then records).
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, const Params &p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 63u) == 0 && globaltimer_ns() - t0 > p.timeout_ns) {
+            atomicOr(p.status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
+// Shared memory of one warp: `stages` blocks of K [DQ / 64][16][128 bytes] then V, and after the loop over it the
+// warp's result: O [16][DV] fp32, then m, l, c [16].  (fp32: 32 columns a piece.)
 template <typename T, int DQ, int DV>
 struct Tile {
     static constexpr int kElt = sizeof(T);
-    static constexpr uint32_t kRowK = DQ * kElt, kRowV = DV * kElt;
-    static constexpr uint32_t kBytesK = kKeys * kRowK;
-    static constexpr uint32_t kStage = kBytesK + kKeys * kRowV;
-    // three blocks in flight per warp at 8 KB a block and more, six below
-    static constexpr int kStages = kStage <= 4096 ? 6 : (kStage <= 8192 ? 3 : 3);
+    static constexpr int kCols = 128 / kElt;  // columns of a 128-byte piece
+    static constexpr uint32_t kPiece = kKeys * 128;
+    static constexpr uint32_t kBytesK = DQ / kCols * kPiece, kBytesV = DV / kCols * kPiece;
+    static constexpr uint32_t kStage = kBytesK + kBytesV;
+    // 24 KB a warp, which lets two CTAs share an SM (fp32 at full width: 48 KB, one CTA)
+    static constexpr int kStages = kStage <= 4096 ? 6 : (kStage <= 6144 ? 4 : 3);
     static constexpr uint32_t kWarpBytes = kStages * kStage;
-    static constexpr uint32_t kSmem = kWarps * kWarpBytes;
+    static constexpr uint32_t kSmem = 1024 + kWarps * kWarpBytes;  // pieces start on 1024 bytes
     static_assert(kRowsTile * DV * 4 + 3 * kRowsTile * 4 <= kWarpBytes, "a warp's result takes the place of its stages");
 };
 
 template <typename T, int DQ, int DV>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+    attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Tile<T, DQ, DV>;
     constexpr bool kBf = sizeof(T) == 2;
     constexpr int kStages = L::kStages;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kWarps][kStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = smem_u32(smem);
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const smem = smem_raw + (base - raw);
     const uint32_t wbase = base + warp * L::kWarpBytes;
 
     // the launch that adds this one's partial results may start; it waits for them where it needs them
@@ -145,65 +169,48 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
     const int f0 = rt * kRowsTile;
     const int n_rows = min(kRowsTile, group_rows - f0);
 
-    const int nP = (p.all_rows || p.with_prefix) ? p.S_p : 0;
     int len = 0;
     if (!p.all_rows) {
         len = p.kv_len ? p.kv_len[b] : p.S_c;
-        if (len < 0 || len > p.S_c) {  // a length outside the cache: as many keys as it has
+        if (len < 0 || len > p.S_c) {  // a length outside the cache counts as the nearest one inside
             if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
             len = len < 0 ? 0 : p.S_c;
         }
     }
-    // keys seen by row f (concatenated prefix and cache): those below limit(f)
-    auto limit = [&](int f) {
-        if (p.all_rows) return nP;
-        const int c = len - p.S_q + f / p.G + 1;
-        return nP + max(0, c);
-    };
-    const int total = limit(f0 + n_rows - 1), all_see = limit(f0);
-    const int blocks = (total + kKeys - 1) / kKeys;
+    // The key axis: the prefix's blocks, then the cache's.  Row f sees the prefix and the first own(f) cache rows.
+    const int nP = (p.all_rows || p.with_prefix) ? p.S_p : 0;
+    const int c0 = (nP + kKeys - 1) / kKeys * kKeys;  // where the cache starts on it
+    auto own = [&](int f) { return p.all_rows ? 0 : max(0, len - p.S_q + f / p.G + 1); };
+    const int own_last = own(f0 + n_rows - 1), own_first = own(f0);
+    const int blocks = (c0 + own_last + kKeys - 1) / kKeys;
     const int cuts = p.cluster * p.shares;
     const int per = (blocks + cuts - 1) / cuts;
     const int first = min(blocks, (share * p.cluster + rank) * per), last = min(blocks, first + per);
 
-    const T *kp = static_cast<const T *>(p.Kp) + hk * p.kp_sh, *vp = static_cast<const T *>(p.Vp) + hk * p.vp_sh;
-    const T *kc = static_cast<const T *>(p.Kc) + b * p.kc_sb + hk * p.kc_sh;
-    const T *vc = static_cast<const T *>(p.Vc) + b * p.vc_sb + hk * p.vc_sh;
-
-    // ---- loads: block i of the share into stage s, 16 bytes per lane and row; chunks of a row are permuted by
-    // the row's low bits, so that the reads below touch every bank once
+    // ---- loads: block blk into stage s, issued by one lane
     auto load = [&](int blk, int s) {
         const int k0 = blk * kKeys;
-        const uint32_t dk = wbase + s * L::kStage, dv = dk + L::kBytesK;
+        const uint32_t dk = wbase + s * L::kStage, dv = dk + L::kBytesK, bar = smem_u32(&full[warp][s]);
+        const bool pre = k0 < c0;
+        const CUtensorMap *mk = pre ? &maps.kp : &maps.kc, *mv = pre ? &maps.vp : &maps.vc;
+        const int row = pre ? k0 : k0 - c0, seq = pre ? 0 : b;
+        mbar_arrive_expect_tx(bar, L::kStage);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int D = half ? DV : DQ;
-            const int cpr = D * L::kElt / 16;  // chunks per row
-            const int used = (half ? p.D_v : p.D_qk) * L::kElt;
-            const T *pre = half ? vp : kp, *own = half ? vc : kc;
-            const long long pre_s = half ? p.vp_ss : p.kp_ss, own_s = half ? p.vc_ss : p.kc_ss;
-            const uint32_t d0 = half ? dv : dk;
+        for (int i = 0; i < DQ / L::kCols; ++i) tma_load_4d(dk + i * L::kPiece, mk, bar, i * L::kCols, row, hk, seq);
 #pragma unroll
-            for (int i = 0; i < kKeys * cpr / 32; ++i) {
-                const int idx = i * 32 + lane;
-                const int row = idx / cpr, c = idx % cpr;
-                const int key = k0 + row;
-                int bytes = min(16, used - c * 16);
-                if (key >= total || bytes < 0) bytes = 0;
-                const T *src = key < nP ? pre + key * pre_s : own + (key - nP) * own_s;
-                const int sw = kBf || !half ? (row & 7) : (row & 6);
-                const void *from = bytes > 0 ? reinterpret_cast<const uint8_t *>(src) + c * 16 : p.Q;
-                cp_async16(d0 + row * (D * L::kElt) + ((c ^ sw) << 4), from, bytes);
-            }
-        }
+        for (int i = 0; i < DV / L::kCols; ++i) tma_load_4d(dv + i * L::kPiece, mv, bar, i * L::kCols, row, hk, seq);
     };
 
     const int n_mine = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        if (i < n_mine) load(first + warp + i * kWarps, i);
-        cp_async_commit();
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+        fence_mbar_init();
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            if (i < n_mine) load(first + warp + i * kWarps, i);
     }
+    __syncwarp();
 
     // ---- the rows' queries, in the layout of an MMA's A operand: rows lane / 4 and lane / 4 + 8
     const int g8 = lane >> 2, t4 = lane & 3;
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
         qrow[r] = i < n_rows ? static_cast<const T *>(p.Q) + bb * p.q_sb + static_cast<long long>(hk * p.G + g) * p.q_sh +
                                    s * p.q_ss
                              : nullptr;
-        lim[r] = i < n_rows ? limit(f) : 0;
+        lim[r] = i < n_rows ? own(f) : 0;
     }
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks)
@@ -247,25 +254,43 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
         for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, c[2] = {0.f, 0.f};
 
+    bool ok = true;
+    int stage = 0, issued = min(n_mine, kStages - 1);
+    uint32_t parity = 0;
     for (int it = 0; it < n_mine; ++it) {
-        cp_async_wait<kStages - 2>();
-        __syncwarp();
-        if (it + kStages - 1 < n_mine) load(first + warp + (it + kStages - 1) * kWarps, (it + kStages - 1) % kStages);
-        cp_async_commit();
+        ok = __all_sync(0xffffffffu, wait_limited(smem_u32(&full[warp][stage]), parity, p)) != 0;
+        if (!ok) break;
+        if (issued < n_mine) {  // into the stage read last time (every lane has passed it)
+            if (lane == 0) load(first + warp + issued * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+            ++issued;
+        }
         const int k0 = (first + warp + it * kWarps) * kKeys;
-        const uint32_t sk = wbase + (it % kStages) * L::kStage, sv = sk + L::kBytesK;
+        const uint32_t sk = wbase + stage * L::kStage, sv = sk + L::kBytesK;
+        // keys of the block that exist
+        const int n_keys = k0 < c0 ? nP - k0 : c0 + own_last - k0;
+        if (k0 >= c0 && n_keys < kKeys) {  // the cache's last block (the prefix's is filled with zeros by the map)
+            constexpr int kUnits = static_cast<int>(L::kBytesV / 16);
+            for (int i = lane; i < kUnits; i += 32)
+                if (((i >> 3) & (kKeys - 1)) >= n_keys)
+                    *reinterpret_cast<uint4 *>(smem + (sv - base) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+        }
+        if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1u;
+        }
 
         // ---- scores of 16 rows x 16 keys: s[n] holds keys 8 n + 2 t4, + 1 of rows g8 (0, 1) and g8 + 8 (2, 3)
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         {
-            // lane 8 j + i addresses row i of matrix j: keys 0-7 and 8-15, chunks 2 ks and 2 ks + 1
+            // lane 8 j + i addresses row i of matrix j: keys 0-7 and 8-15, 16-byte columns 2 ks and 2 ks + 1
             const int key = (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t row = sk + key * L::kRowK;
-            const int odd = (lane >> 3) & 1;
+            const uint32_t row = sk + key * 128;
+            const uint32_t odd = (lane >> 3) & 1;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
                 uint32_t kb[4];
-                ldsm4(kb, row + (((2 * ks + odd) ^ (key & 7)) << 4));
+                ldsm4(kb, row + (ks >> 2) * L::kPiece + (((2 * (ks & 3) + odd) ^ (key & 7)) << 4));
                 if (kBf) {
                     mma_bf16(s[0], q[ks], kb[0], kb[1]);
                     mma_bf16(s[1], q[ks], kb[2], kb[3]);
@@ -279,12 +304,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
-        if (k0 + kKeys > all_see) {
+        if (k0 < c0 ? n_keys < kKeys : k0 + kKeys > c0 + own_first) {  // some row does not see every key
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (k0 + 8 * n + 2 * t4 + (i & 1) >= lim[i >> 1]) s[n][i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) {
+                    const int seen = k0 < c0 ? nP : c0 + lim[i >> 1];
+                    if (k0 + 8 * n + 2 * t4 + (i & 1) >= seen) s[n][i] = -INFINITY;
+                }
         }
 
         // ---- online softmax of the two rows
@@ -326,14 +353,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
         if (kBf) {
             const uint32_t a[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
                                    pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
-            // matrices: keys 0-7 and 8-15 of column chunk n, then of chunk n + 1
+            // matrices: keys 0-7 and 8-15 of 16-byte column n, then of column n + 1
             const int key = lane & 15;
-            const uint32_t row = sv + key * L::kRowV;
-            const int odd = lane >> 4;
+            const uint32_t row = sv + key * 128;
+            const uint32_t odd = lane >> 4;
 #pragma unroll
             for (int n = 0; n < DV / 8; n += 2) {
                 uint32_t vb[4];
-                ldsm4_t(vb, row + (((n + odd) ^ (key & 7)) << 4));
+                ldsm4_t(vb, row + (n >> 3) * L::kPiece + ((((n & 7) + odd) ^ (key & 7)) << 4));
                 mma_bf16(o[n], a, vb[0], vb[1]);
                 mma_bf16(o[n + 1], a, vb[2], vb[3]);
             }
@@ -345,18 +372,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
                 const uint32_t a[4] = {__float_as_uint(s[j][0]), __float_as_uint(s[j][2]), __float_as_uint(s[j][1]),
                                        __float_as_uint(s[j][3])};
                 const int key = 8 * j + 2 * t4;
-                const uint8_t *r0 = smem + (sv - base) + key * L::kRowV, *r1 = r0 + L::kRowV;
+                const uint8_t *r0 = smem + (sv - base) + key * 128, *r1 = r0 + 128;
 #pragma unroll
                 for (int n = 0; n < DV / 8; ++n) {
-                    const int col = n * 8 + g8;
-                    const uint32_t at = (((col >> 2) ^ (key & 6)) << 4) + (col & 3) * 4;
-                    mma_3xtf32(o[n], a, *reinterpret_cast<const uint32_t *>(r0 + at),
-                               *reinterpret_cast<const uint32_t *>(r1 + at));
+                    const int col = (n & 3) * 8 + g8;
+                    const uint32_t in = (n >> 2) * L::kPiece + (col & 3) * 4, unit = col >> 2;
+                    mma_3xtf32(o[n], a, *reinterpret_cast<const uint32_t *>(r0 + in + ((unit ^ (key & 7)) << 4)),
+                               *reinterpret_cast<const uint32_t *>(r1 + in + ((unit ^ ((key + 1) & 7)) << 4)));
                 }
             }
         }
+        __syncwarp();
     }
-    cp_async_wait<0>();
+    if (!ok && lane == 0) {  // gave up: the copies in flight land before their memory is used otherwise
+        for (int it = max(0, issued - kStages); it < issued; ++it)
+            wait_limited(smem_u32(&full[warp][it % kStages]), (it / kStages) & 1, p);
+    }
     __syncwarp();
 
     // ---- the warp's result
@@ -382,46 +413,83 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
     else __syncthreads();
     if (!p.all_rows) wait_prerequisites();  // (the whole grid waits, so that it ends after the prefix's launch)
 
-    // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row
+    // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row.  The sources of a
+    // row are the cluster's warps and the workspace's shares; every lane holds the weight of the sources that fall
+    // to it (lane, lane + 32, ...), then the sources' rows are added in order, eight loads at a time.
     constexpr int kCols = DV / 32;
+    constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxSplit;
+    constexpr int kPerLane = (kMaxSources + 31) / 32;
     const uint32_t o_off = base, m_off = base + kRowsTile * DV * 4;
+    const int n_smem = kWarps * p.cluster, n_src = n_smem + p.prior;
     for (int i = rank + p.cluster * warp; i < n_rows; i += p.cluster * kWarps) {
         const int f = f0 + i;
         const long long flat = static_cast<long long>(hk) * p.B * per_b + static_cast<long long>(b) * per_b + f;
-        float M = -INFINITY, Ls = 0.0f, Lo = 0.0f, acc[kCols];
+        auto warp_part = [&](uint32_t off, int src) {  // a warp's part of the cluster's shared memory
+            const uint32_t at = off + (src % kWarps) * L::kWarpBytes;
+            return p.cluster > 1 ? cluster_map(at, src / kWarps) : at;
+        };
+        float ms[kPerLane], ls[kPerLane], cs[kPerLane];
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            const int src = lane + 32 * k;
+            ms[k] = -INFINITY;
+            ls[k] = cs[k] = 0.0f;
+            if (src < n_smem) {
+                const uint32_t at = warp_part(m_off, src) + i * 4;
+                ms[k] = ld_cluster(at);
+                ls[k] = ld_cluster(at + kRowsTile * 4);
+                cs[k] = ld_cluster(at + 2 * kRowsTile * 4);
+            } else if (src < n_src) {
+                const long long at = (src - n_smem) * p.rows + flat;
+                ms[k] = p.part_m[at];
+                ls[k] = p.part_l[at];
+                cs[k] = p.part_c[at];
+            }
+        }
+        float M = ms[0];
+#pragma unroll
+        for (int k = 1; k < kPerLane; ++k) M = fmaxf(M, ms[k]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        float Ls = 0.0f, Lo = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            // the source's weight: 0 without keys (a sum that is NaN without a maximum stays NaN)
+            ms[k] = ms[k] == -INFINITY && ls[k] == 0.0f ? 0.0f : ex2(ms[k] - M);
+            Ls += ms[k] * ls[k];
+            Lo += ms[k] * (ls[k] + cs[k]);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) {
+            Ls += __shfl_xor_sync(0xffffffffu, Ls, x);
+            Lo += __shfl_xor_sync(0xffffffffu, Lo, x);
+        }
+        float acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
-        auto add = [&](float ms, float ls, float cs, const float (&v)[kCols]) {
-            if (ms == -INFINITY) return;  // no key there
-            const float Mn = fmaxf(M, ms);
-            const float a = M == -INFINITY ? 0.0f : ex2(M - Mn), w = ex2(ms - Mn);
-            Ls = Ls * a + w * ls;
-            Lo = Lo * a + w * (ls + cs);
+        constexpr int kAtOnce = 8;
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) acc[k] = acc[k] * a + w * v[k];
-            M = Mn;
-        };
-        for (int r = 0; r < p.cluster; ++r)
+        for (int k = 0; k < kPerLane; ++k)
+            for (int s0 = 0; s0 < 32 && s0 + 32 * k < n_src; s0 += kAtOnce) {
+                float v[kAtOnce][kCols], w[kAtOnce];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const uint32_t at = w * L::kWarpBytes;
-                const uint32_t mo = p.cluster > 1 ? cluster_map(m_off + at, r) : m_off + at;
-                const uint32_t oo = p.cluster > 1 ? cluster_map(o_off + at, r) : o_off + at;
-                float v[kCols];
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int src = s0 + j + 32 * k;
+                    w[j] = __shfl_sync(0xffffffffu, ms[k], s0 + j);
+                    const bool in = src < n_src && w[j] != 0.0f;  // (a source without weight may hold anything)
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) v[k] = ld_cluster(oo + (i * DV + lane + 32 * k) * 4);
-                add(ld_cluster(mo + i * 4), ld_cluster(mo + (kRowsTile + i) * 4), ld_cluster(mo + (2 * kRowsTile + i) * 4), v);
+                    for (int x = 0; x < kCols; ++x) {
+                        const int col = lane + 32 * x;
+                        v[j][x] = 0.0f;
+                        if (in && src < n_smem) v[j][x] = ld_cluster(warp_part(o_off, src) + (i * DV + col) * 4);
+                        else if (in && col < p.D_v) v[j][x] = p.part_o[((src - n_smem) * p.rows + flat) * p.D_v + col];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                    for (int x = 0; x < kCols; ++x) acc[x] = fmaf(w[j], v[j][x], acc[x]);
             }
-        for (int r = 0; r < p.prior; ++r) {
-            const long long at = r * p.rows + flat;
-            float v[kCols];
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                const int col = lane + 32 * k;
-                v[k] = col < p.D_v ? p.part_o[at * p.D_v + col] : 0.0f;
-            }
-            add(p.part_m[at], p.part_l[at], p.part_c[at], v);
-        }
         if (p.all_rows) {
             const long long at = share * p.rows + flat;
 #pragma unroll
@@ -435,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
         } else {
             const int s = f / p.G, g = f - s * p.G;
             const int h = hk * p.G + g;
-            const float inv = Ls > 0.0f ? 1.0f / Lo : 0.0f;  // a row without keys is 0
+            const float inv = Ls == 0.0f ? 0.0f : 1.0f / Lo;  // a row without keys is 0
             T *orow = static_cast<T *>(p.O) + b * p.o_sb + h * p.o_sh + s * p.o_ss;
 #pragma unroll
             for (int k = 0; k < kCols; ++k) {
@@ -449,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) attn_stream_
                 }
             }
             if (p.lse && lane == 0)
-                p.lse[(static_cast<long long>(b) * p.H + h) * p.S_q + s] = lse_from(M, Ls);
+                p.lse[(static_cast<long long>(b) * p.H + h) * p.S_q + s] =
+                    Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
         }
     }
     if (p.cluster > 1) cluster_sync();  // the other CTAs have read this one's results

@@ -103,7 +103,7 @@ class Problem:
         self.vc, self.vc64 = self.tensor(B, H_kv, S_c, D_v)
         self.lens = np.asarray(self.rng.integers(0, S_c + 1, B) if lens is None else lens)
         self.kv_len = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
-        for b, n in enumerate(self.lens):  # nothing reads what lies behind a sequence
+        for b, n in enumerate(self.lens):  # what lies behind a sequence has no influence
             self.kc[b, :, max(n, 0):] = beyond
             self.vc[b, :, max(n, 0):] = beyond
 
