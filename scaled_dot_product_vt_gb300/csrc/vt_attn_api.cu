@@ -194,10 +194,10 @@ SplitLayout split_layout(int64_t B, int64_t H, int64_t S_q, int64_t D_v, int n_s
     auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
     SplitLayout L{};
     uint64_t rows = 0, per = 0, o_bytes = 0;
-    if (B <= 0 || H <= 0 || S_q <= 0 || D_v <= 0 || n_split <= 0 ||
+    if (B <= 0 || H <= 0 || S_q <= 0 || D_v <= 0 || D_v > (int64_t(1) << 40) || n_split <= 0 ||
         __builtin_mul_overflow(uint64_t(B), uint64_t(H), &rows) || __builtin_mul_overflow(rows, uint64_t(S_q), &rows) ||
         __builtin_mul_overflow(rows, uint64_t(n_split) * sizeof(float), &per) ||
-        __builtin_mul_overflow(per, uint64_t(D_v), &o_bytes) || o_bytes > (uint64_t(1) << 60) ||
+        __builtin_mul_overflow(per, uint64_t(partial_ld(D_v)), &o_bytes) || o_bytes > (uint64_t(1) << 60) ||
         per > (uint64_t(1) << 60))
         return L;
     L.o_off = 0;
@@ -248,6 +248,7 @@ vt_status merge(const AttnParams &p, const Problem &P, cudaStream_t stream) {
     mp.S_q = static_cast<int>(P.S_q);
     mp.D_v = static_cast<int>(P.D_v);
     mp.n_split = p.n_split;
+    mp.part_ld = p.part_ld;
     mp.o_sb = P.os[0];
     mp.o_sh = P.os[1];
     mp.o_ss = P.os[2];
@@ -329,6 +330,7 @@ vt_status launch(const Problem &P, const vt_attn_opts *opts, int n_split, void *
         const SplitLayout L = split_layout(B, H, S_q, D_v, n_split);
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         p.part_o = reinterpret_cast<float *>(ws + L.o_off);
+        p.part_ld = static_cast<int>(partial_ld(D_v));
         p.part_m = reinterpret_cast<float *>(ws + L.m_off);
         p.part_l = reinterpret_cast<float *>(ws + L.l_off);
         p.part_c = reinterpret_cast<float *>(ws + L.c_off);

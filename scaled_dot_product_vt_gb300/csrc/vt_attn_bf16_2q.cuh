@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 // key tile for this query tile writes the empty partial (m = -inf, l = 0, O = 0).
                 const long long row_lin = (static_cast<long long>(U.b) * p.H + U.h) * p.S_q + q_row;
                 const long long part = static_cast<long long>(U.split) * p.B * p.H * p.S_q + row_lin;
-                float *orow = p.part_o + part * p.D_v;
+                float *orow = p.part_o + part * p.part_ld;
                 if (n_my > 0) tc_fence_after();
                 for (int cc = 0; cc < p.n_pv; cc += 16) {
                     uint32_t o[16];

@@ -20,6 +20,8 @@ constexpr unsigned kStatusBounds = 2u;
 
 enum : int { kF32 = 0, kBF16 = 1 };
 
+__host__ __device__ constexpr long long partial_ld(long long D_v) { return (D_v + 7) / 8 * 8; }
+
 struct AttnParams {
     int B, H, S_q, S_k, D_qk, D_v;
     int n_qblocks;    // query blocks per (b, h): ceil(S_q / rows per block)
@@ -57,6 +59,7 @@ struct AttnParams {
     // as the bf16 values P V used, indexed [split][(b*H + h)*S_q + i].
     int n_split;
     float *part_o;
+    int part_ld;      // floats from one partial O row to the next: D_v rounded up to 8, so rows take 32-byte stores
     float *part_m;
     float *part_l;
     float *part_c;

@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(f2::kThreads, 1)
         // ------------------------------------------------------------ partial result for the merge kernel
         if (row_active && live) {
             const long long part = static_cast<long long>(U.share) * p.B * p.H * p.S_q + lse_idx;
-            float *prow = p.part_o + part * p.D_v;
+            float *prow = p.part_o + part * p.part_ld;
             for (int cc = 0; cc < p.D_v; cc += 16) {
                 float v[16];
                 load_o(cc, v);

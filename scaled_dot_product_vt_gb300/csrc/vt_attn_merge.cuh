@@ -24,6 +24,7 @@ struct MergeParams {
     float *lse;      // nullptr, or one natural-log log-sum-exp per row
     long long rows;  // B * H * S_q
     int H, S_q, D_v, n_split;
+    int part_ld;  // floats between partial O rows
     long long o_sb, o_sh, o_ss;
 };
 
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(32 * kMergeRowsPerBlock)
             ms[u] = in ? mp.part_m[idx] : -INFINITY;
             ls[u] = in ? mp.part_l[idx] : 0.0f;
             cs[u] = in ? mp.part_c[idx] : 0.0f;
-            const float *po = mp.part_o + idx * mp.D_v;
+            const float *po = mp.part_o + idx * mp.part_ld;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int col = lane + 32 * c;

@@ -54,7 +54,7 @@ constexpr int64_t kTileRows = 32;                   // more rows per prefix key:
 constexpr int64_t kReadAgain = int64_t(16) << 20;  // bytes
 
 size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
-    return ((static_cast<size_t>(rows) * shares * (D_v + 3) * sizeof(float)) + 255) & ~size_t(255);
+    return ((static_cast<size_t>(rows) * shares * (partial_ld(D_v) + 3) * sizeof(float)) + 255) & ~size_t(255);
 }
 
 int cluster_for(int64_t units, int64_t keys, int sms) {
@@ -191,7 +191,8 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     if (plan.workspace) {
         const int64_t n = z.rows * plan.prefix_shares;
         p.part_o = static_cast<float *>(a.workspace);
-        p.part_m = p.part_o + n * a.D_v;
+        p.part_ld = static_cast<int>(partial_ld(a.D_v));
+        p.part_m = p.part_o + n * p.part_ld;
         p.part_l = p.part_m + n;
         p.part_c = p.part_l + n;
     }
@@ -299,6 +300,7 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.cluster = 1;
     p.n_split = plan.prefix_shares;
     p.part_o = sp.part_o;
+    p.part_ld = sp.part_ld;
     p.part_m = sp.part_m;
     p.part_l = sp.part_l;
     p.part_c = sp.part_c;

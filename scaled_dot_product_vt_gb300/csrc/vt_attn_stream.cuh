@@ -45,6 +45,7 @@ struct Params {
     // partial results: [share][rows], rows = H_kv * B * S_q * G indexed ((hk * B + b) * S_q + s) * G + g
     float *part_o, *part_m, *part_l, *part_c;
     long long rows;
+    int part_ld;  // floats between partial O rows
     int prior;  // shares in the workspace to add (all_rows = 0)
     void *O;
     long long o_sb, o_sh, o_ss;
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
                         const int col = lane + 32 * x;
                         v[j][x] = 0.0f;
                         if (in && src < n_smem) v[j][x] = ld_cluster(warp_part(o_off, src) + (i * DV + col) * 4);
-                        else if (in && col < p.D_v) v[j][x] = p.part_o[((src - n_smem) * p.rows + flat) * p.D_v + col];
+                        else if (in && col < p.D_v) v[j][x] = p.part_o[((src - n_smem) * p.rows + flat) * p.part_ld + col];
                     }
                 }
 #pragma unroll
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             const long long at = share * p.rows + flat;
 #pragma unroll
             for (int k = 0; k < kCols; ++k)
-                if (lane + 32 * k < p.D_v) p.part_o[at * p.D_v + lane + 32 * k] = acc[k];
+                if (lane + 32 * k < p.D_v) p.part_o[at * p.part_ld + lane + 32 * k] = acc[k];
             if (lane == 0) {
                 p.part_m[at] = M;
                 p.part_l[at] = Ls;
