@@ -378,7 +378,7 @@ vt_status launch(const Problem &P, const vt_attn_opts *opts, int n_split, void *
         // kernel variants: K-steps of Q K^T, the score ring, the epilogue (O in any layout with the log-sum-exp;
         // partial outputs for a split-KV merge; O alone in 32-byte rows of whole 16-column groups), and a positive
         // scale folded into the exponent
-        using Kern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnParams);
+        using Kern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnParams);
         auto pick = [&](auto ring_c, auto epi_c, auto fold_c) -> Kern {
             constexpr bool R = decltype(ring_c)::value, F = decltype(fold_c)::value;
             constexpr int E = decltype(epi_c)::value;
@@ -407,7 +407,7 @@ vt_status launch(const Problem &P, const vt_attn_opts *opts, int n_split, void *
                                         : (ring ? pick(T_{}, Plain{}, F_{}) : pick(F_{}, Plain{}, F_{}));
         }
         if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
-        kern<<<grid, q2::kThreads, smem, stream>>>(tq, tk, tv, p);
+        kern<<<grid, q2::kThreads, smem, stream>>>(tq, tk, tv, tv, p);
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
         if (n_split > 1) return merge<2>(p, P, stream);
         return VT_OK;

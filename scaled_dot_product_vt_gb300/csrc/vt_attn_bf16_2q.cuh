@@ -61,6 +61,7 @@ constexpr int kRegsControl = 72;    // warpgroup 0 after setmaxnreg
 constexpr int kRegsSoftmax = 216;   // softmax warpgroups after setmaxnreg
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split exceeds the launch");
 constexpr int kMaxSlots = 6;
+constexpr int kRowsPlain = 0, kRowsAll = 1, kRowsSeq = 2;  // what a tile's rows are (the kernel's ROWS)
 constexpr int kEpiPlain = 0, kEpiSplit = 1, kEpiPlainFast = 2;  // epilogue variants (the kernel's EPI)
 constexpr int kUnitRing = 4;        // unit indices in flight between the producer and the other roles
 constexpr int kUnitReaders = 1 + 8;  // the MMA warp and one lane of each softmax warp (one more MMA warp with the score ring)
@@ -82,6 +83,7 @@ struct Unit {
     int b, h, hk, r0;
     int j0, n_kv;             // the share's first key tile and its number of key tiles
     int as0, es0, as1, es1;   // key tiles [as_t, es_t) of the share that query tile t needs
+    int len;                  // kRowsSeq: cached tokens of the sequence
 };
 
 struct Ctl {
@@ -107,10 +109,17 @@ struct Ctl {
 };
 
 
+// kRowsSeq: the keys of its own cache that row r of a sequence with `len` cached tokens sees.
+__device__ __forceinline__ int own_keys(const AttnParams &p, int len, int r) {
+    return max(0, len - p.row_tokens + r / p.row_heads + 1);
+}
+
 // Units run over groups of `head_group` heads; inside a group, the heaviest query blocks first
 // when work grows with the block index; the shares of one block are adjacent.
+template <int ROWS>
 __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     Unit U;
+    U.len = 0;
     const int split = u % p.n_split;
     U.u = u;
     U.split = split;
@@ -127,6 +136,14 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     U.b = bh / p.H;
     U.hk = U.h / p.kv_group;
     U.r0 = qb * kRows;
+    if constexpr (ROWS == kRowsSeq) {
+        int len = p.kv_len ? p.kv_len[U.b] : p.cache_keys;
+        if (len < 0 || len > p.cache_keys) {  // a length outside the cache counts as the nearest one inside
+            atomicOr(p.status, kStatusBounds);
+            len = len < 0 ? 0 : p.cache_keys;
+        }
+        U.len = len;
+    }
     // The union of both query tiles' key-tile ranges is contiguous (tile 1's first key never lies
     // past tile 0's last); it is cut into n_split contiguous shares.
     int a[2], e[2];
@@ -136,6 +153,9 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
         if (first >= p.S_q) {
             a[t] = 0;
             e[t] = 0;
+        } else if constexpr (ROWS == kRowsSeq) {
+            a[t] = 0;
+            e[t] = p.prefix_tiles + (own_keys(p, U.len, min(first + kBM, p.S_q) - 1) + kBN - 1) / kBN;
         } else {
             band_tiles(p, first, min(first + kBM, p.S_q) - 1, kBN, &a[t], &e[t]);
         }
@@ -177,6 +197,7 @@ __device__ __forceinline__ bool unit_valid(const AttnParams &p, const Unit &U) {
 // The n-th unit this CTA works on, as the producer decoded and published it (u = -1: no more
 // units); false on abort.  Called by a whole warp: lane 0 waits for the ring entry and releases it,
 // every lane copies the unit (the producer decodes ahead, so readers spend no time on it).
+template <int ROWS>
 __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const AttnParams &p, int lane) {
     const int k = n % kUnitRing;
     bool ok = true;
@@ -196,34 +217,54 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
     out->es0 = src->es0;
     out->as1 = src->as1;
     out->es1 = src->es1;
+    if (ROWS == kRowsSeq) out->len = src->len;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_empty[k]));
     return true;
 }
 
-// Copy rows row0 .. row0 + 127 of head hk into a Q tile (128-byte swizzle: the 16-byte pieces of a row are permuted
-// by its low bits), zeros past the last row and past D_qk.  Called by the 128 threads of a softmax warpgroup; on
-// return the calling thread's pieces are visible to the tensor core.
-__device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int hk, const AttnParams &p) {
-    const int tid = threadIdx.x & 127;
-    const int pieces = p.q_chunks * 8;                 // 16-byte pieces of a row: 8 or 16
-    const int c = tid & (pieces - 1);
-    const int step = 128 / pieces;                     // rows the warpgroup copies at once
+// Copy rows row0 .. row0 + 127 of key/value head hk (of sequence b, kRowsSeq) into a Q tile (128-byte swizzle: the
+// 16-byte pieces of a row are permuted by its low bits), zeros past the last row and past D_qk.  Called by the 128
+// threads of a softmax warpgroup; on return the calling thread's pieces are visible to the tensor core.  Each lane
+// finds the address of one of its warp's 32 rows; 8 or 16 lanes then copy a row together.
+template <int ROWS>
+__device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int b, int hk, const AttnParams &p) {
+    const int lane = threadIdx.x & 31, first = threadIdx.x & 96;
+    const int f = row0 + first + lane;
+    unsigned long long src = 0;
+    if (f < p.S_q) {
+        const int token = f / p.row_heads, g = f - token * p.row_heads;
+        const int bb = ROWS == kRowsAll ? token / p.row_tokens : b;
+        const int s = ROWS == kRowsAll ? token - bb * p.row_tokens : token;
+        src = reinterpret_cast<unsigned long long>(static_cast<const uint16_t *>(p.Q) + bb * p.q_sb +
+                                                   (static_cast<long long>(hk) * p.row_heads + g) * p.q_sh + s * p.q_ss);
+    }
+    const int pieces = p.q_chunks * 8;  // 16-byte pieces of a row: 8 or 16
+    const int c = lane & (pieces - 1), step = 32 / pieces;
     const int bytes = min(16, max(0, p.D_qk * 2 - c * 16));
-    const int per_seq = p.row_heads * p.row_tokens;
     const uint32_t col = tile + (c >> 3) * kChunkBytes;
-#pragma unroll 8
-    for (int r = tid / pieces; r < kBM; r += step) {
-        const int f = row0 + r;
-        const bool in = f < p.S_q && bytes > 0;
-        const int b = in ? f / per_seq : 0, rest = in ? f - b * per_seq : 0;
-        const int s = rest / p.row_heads, g = rest - s * p.row_heads;
-        const uint16_t *src = static_cast<const uint16_t *>(p.Q) + b * p.q_sb +
-                              (static_cast<long long>(hk) * p.row_heads + g) * p.q_sh + s * p.q_ss + (in ? c * 8 : 0);
-        cp_async16(col + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? src : p.Q, in ? bytes : 0);
+#pragma unroll 4
+    for (int i = lane / pieces; i < 32; i += step) {
+        const unsigned long long at = __shfl_sync(0xffffffffu, src, i);
+        const int r = first + i;
+        const bool in = at != 0 && bytes > 0;
+        cp_async16(col + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   in ? reinterpret_cast<const void *>(at + c * 16) : p.Q, in ? bytes : 0);
     }
     cp_async_wait_all();
     fence_async_shared();
+}
+
+// kRowsSeq: zero the V rows of key tile j that lie past the sequence's end (the whole warp): they may hold NaN, which
+// a probability of 0 does not hide.  The tensor core sees the zeros afterwards.
+__device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int j, int lane, const AttnParams &p) {
+    const int n = U.len - (U.j0 + j - p.prefix_tiles) * kBN;  // rows of the tile that exist
+    if (U.j0 + j < p.prefix_tiles || n >= kBN) return;
+    for (int c = 0; c < p.v_chunks; ++c)
+        for (int i = n * 8 + lane; i < kBN * 8; i += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot + c * kChunkBytes + i * 16), "r"(0) : "memory");
+    fence_async_shared();
+    __syncwarp();
 }
 
 }  // namespace q2
@@ -235,15 +276,20 @@ __device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int hk, con
 // kEpiSplit: the partial results of a key-range share, for the split-KV merge kernel; kEpiPlainFast: O only,
 // 32-byte aligned rows and D_v a multiple of 16 (the common case, with no other store forms in the code).
 // FOLD: the scale is positive and folds into the exponent; otherwise the scores are scaled first.
-// GATHER: a tile's rows are those of several sequences and heads (AttnParams::row_heads), copied into the Q tiles by
-// the softmax warpgroups instead of TMA: no box covers them for every group size.  A launch of this form lets
-// the launch that follows it start early (griddepcontrol).
-template <int KQ, bool RING, int EPI, bool FOLD, bool GATHER = false>
+// ROWS: what a tile's rows are.  kRowsPlain: consecutive queries of one head, loaded by TMA.  The other two take the
+// queries of all the heads that share a key/value head as rows (AttnParams::row_heads), so that a few queries per
+// sequence still fill a tile; no TMA box covers them for every group size, so the softmax warpgroups copy them.
+// kRowsAll: rows of all sequences, over keys that all of them see; the launch that follows may start early
+// (griddepcontrol).  kRowsSeq: rows of one sequence, over a shared prefix and then the sequence's own cache (tmK, tmV
+// and tmQ, tmV2), causal in the cache.
+template <int KQ, bool RING, int EPI, bool FOLD, int ROWS = q2::kRowsPlain>
 __global__ void __launch_bounds__(q2::kThreads, 1)
     attn_fwd_bf16_2q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                            const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV2,
+                            const AttnParams p) {
     using namespace q2;
     constexpr int BN = kBN;
+    constexpr bool GATHER = ROWS != kRowsPlain;
     __shared__ Ctl ctl;
     extern __shared__ uint8_t smem_raw[];
 
@@ -251,7 +297,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
     const int lane = threadIdx.x & 31;
 
     const int n_slots = p.stages;
-    if constexpr (GATHER) launch_dependents();
+    if constexpr (ROWS == kRowsAll) launch_dependents();
 
     // ---- shared memory: Q tile 0, Q tile 1, then `n_slots` equal K/V slots
     const uint32_t raw = smem_u32(smem_raw);
@@ -340,11 +386,11 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 if (u >= p.n_units) u = -1;
                 Unit U;
                 if (u >= 0) {
-                    U = decode_unit(p, u);
+                    U = decode_unit<ROWS>(p, u);
                     if (!VT_DEV_CHECK(!(p.flags & kFlagTestBounds) && unit_valid(p, U), ctl.abort_flag, p)) break;
                 } else {
                     U.u = -1;
-                    U.split = U.b = U.h = U.hk = U.r0 = U.j0 = U.n_kv = U.as0 = U.es0 = U.as1 = U.es1 = 0;
+                    U.split = U.b = U.h = U.hk = U.r0 = U.j0 = U.n_kv = U.as0 = U.es0 = U.as1 = U.es1 = U.len = 0;
                 }
                 volatile Unit *dst_u = &ctl.unit[k];
                 dst_u->u = U.u;
@@ -359,6 +405,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 dst_u->es0 = U.es0;
                 dst_u->as1 = U.as1;
                 dst_u->es1 = U.es1;
+                if (ROWS == kRowsSeq) dst_u->len = U.len;
                 mbar_arrive(smem_u32(&ctl.unit_full[k]));
                 if (u < 0) break;
                 if (U.n_kv == 0) continue;
@@ -396,14 +443,21 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         ok = false;
                         break;
                     }
+                    // kRowsSeq: the prefix's tiles, then those of the sequence's cache
+                    const int tile = U.j0 + j;
+                    const bool own = ROWS == kRowsSeq && tile >= p.prefix_tiles;
+                    const int key = (own ? tile - p.prefix_tiles : tile) * BN;
+                    const int seq = ROWS == kRowsSeq && !own ? 0 : U.b;
                     if ((i & 1) == 0) {
+                        const CUtensorMap *m = own ? &tmQ : &tmK;
                         mbar_arrive_expect_tx(bar, k_bytes);
                         for (int c = 0; c < p.q_chunks; ++c)
-                            tma_load_4d(dst + c * kChunkBytes, &tmK, bar, c * kChunk, (U.j0 + j) * BN, U.hk, U.b);
+                            tma_load_4d(dst + c * kChunkBytes, m, bar, c * kChunk, key, U.hk, seq);
                     } else {
+                        const CUtensorMap *m = own ? &tmV2 : &tmV;
                         mbar_arrive_expect_tx(bar, v_bytes);
                         for (int c = 0; c < p.v_chunks; ++c)
-                            tma_load_4d(dst + c * kChunkBytes, &tmV, bar, c * kChunk, (U.j0 + j) * BN, U.hk, U.b);
+                            tma_load_4d(dst + c * kChunkBytes, m, bar, c * kChunk, key, U.hk, seq);
                     }
                     ++loads;
                     if (++s == n_slots) s = 0;
@@ -488,7 +542,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 uint32_t g = 0, cur = 0, nxt = 0, c = 0, h = 0, sr_par = 0;
                 for (int n = 0; ok; ++n) {
                     Unit U;
-                    if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+                    if (!(ok = next_unit<ROWS>(ctl, n, &U, p, lane)) || U.u < 0) break;
                     const int n_kv = U.n_kv;
                     if (n_kv == 0) continue;
                     const int as = tm ? U.as1 : U.as0, es = tm ? U.es1 : U.es0;
@@ -526,6 +580,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             mma_commit_lead(smem_u32(&ctl.empty[kn]), lead);
                         }
                         if (!(ok = wait_full(vs))) break;
+                        if constexpr (ROWS == kRowsSeq) clear_past_end(sSlot0 + vs * slot_bytes, U, j, lane, p);
                         if (act(j)) {
                             if (!(ok = wait1(smem_u32(&ctl.p_full[tm][h & 1u]), (h >> 1) & 1u))) break;
                             ++h;
@@ -542,7 +597,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
             } else {
             for (int n = 0; ok; ++n) {
                 Unit U;
-                if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+                if (!(ok = next_unit<ROWS>(ctl, n, &U, p, lane)) || U.u < 0) break;
                 const int n_kv = U.n_kv;
                 if (n_kv == 0) continue;
                 const int as0 = U.as0, es0 = U.es0, as1 = U.as1, es1 = U.es1;
@@ -571,6 +626,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     const int kn = vs + 1 == n_slots ? 0 : vs + 1;  // slot of K_{j+1} (or the next unit's K_0)
                     const bool more = j + 1 < n_kv;
                     if (!(ok = wait_full(vs))) break;
+                    if constexpr (ROWS == kRowsSeq) clear_past_end(sSlot0 + vs * slot_bytes, U, j, lane, p);
                     const uint32_t v_lo = v_lo0 + vs * slot_step;
                     const uint32_t kn_lo = k_lo0 + kn * slot_step;
                     if (act0(j)) {
@@ -640,23 +696,30 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
 
         for (int n = 0; ok; ++n) {
             Unit U;
-            if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+            if (!(ok = next_unit<ROWS>(ctl, n, &U, p, lane)) || U.u < 0) break;
             const int tile_row0 = U.r0 + t * kBM;
             const int q_row = tile_row0 + row;
             const int as_my = t ? U.as1 : U.as0;
             const int n_my = (t ? U.es1 : U.es0) - as_my;
             // this row's allowed keys [key_lo, key_hi); a key tile starting below mask_lo or ending past
             // mask_hi cuts some row's range and is masked (the same decision for the whole warpgroup)
-            const int key_lo = band_key_lo(p, q_row), key_hi = band_key_hi(p, q_row);
-            const int mask_lo = band_key_lo(p, min(tile_row0 + kBM, p.S_q) - 1);
-            const int mask_hi = band_key_hi(p, tile_row0);
+            int key_lo, key_hi, mask_lo, mask_hi;
+            if constexpr (ROWS == kRowsSeq) {  // in the cache's tiles; in the prefix's, prefix_keys (below)
+                key_lo = mask_lo = 0;
+                key_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(q_row, p.S_q - 1));
+                mask_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(tile_row0, p.S_q - 1));
+            } else {
+                key_lo = band_key_lo(p, q_row), key_hi = band_key_hi(p, q_row);
+                mask_lo = band_key_lo(p, min(tile_row0 + kBM, p.S_q) - 1);
+                mask_hi = band_key_hi(p, tile_row0);
+            }
             if constexpr (GATHER) {
                 if (U.n_kv > 0) {
                     if (gathered > 0)  // the previous unit's last Q K^T has read Q
                         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl.q_empty), (gathered - 1) & 1u,
                                                                   ctl.abort_flag, p)) != 0;
                     if (!ok) break;
-                    gather_rows(t ? sQ1 : sQ0, tile_row0, U.h, p);
+                    gather_rows<ROWS>(t ? sQ1 : sQ0, tile_row0, U.b, U.h, p);
                     mbar_arrive(smem_u32(&ctl.q_full));
                     ++gathered;
                 }
@@ -689,7 +752,15 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     for (int k = 0; k < BN; ++k) s[k] *= p.scale_log2;
                 }
                 const int k0 = (U.j0 + as_my + j) * BN;
-                if (k0 < mask_lo || k0 + BN > mask_hi) {
+                if constexpr (ROWS == kRowsSeq) {
+                    const bool pre = k0 < p.prefix_tiles * BN;
+                    const int hi = pre ? p.prefix_keys : key_hi;
+                    if (k0 + BN > (pre ? p.prefix_keys : mask_hi)) {
+                        #pragma unroll
+                        for (int k = 0; k < BN; ++k)
+                            if (k0 + k >= hi) s[k] = -INFINITY;
+                    }
+                } else if (k0 < mask_lo || k0 + BN > mask_hi) {
                     #pragma unroll
                     for (int k = 0; k < BN; ++k)
                         if (k0 + k < key_lo || k0 + k >= key_hi) s[k] = -INFINITY;
@@ -789,10 +860,13 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 // ------------------------------------------------------------ epilogue: O = O_t / l
                 // A row with no allowed key (l = 0, or no key tile at all) is written as 0.
                 if (n_my > 0) tc_fence_after();
-                const float inv_l = l > 0.0f ? 1.0f / (l + l_fix) : 0.0f;
+                const float inv_l = (ROWS == kRowsSeq ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
+                // kRowsSeq: row q_row is query head U.h * row_heads + g at position s
+                const int s_row = ROWS == kRowsSeq ? q_row / p.row_heads : q_row;
+                const int h_row = ROWS == kRowsSeq ? U.h * p.row_heads + q_row - s_row * p.row_heads : U.h;
                 uint8_t *orow = reinterpret_cast<uint8_t *>(p.O) +
-                                (static_cast<long long>(U.b) * p.o_sb + static_cast<long long>(U.h) * p.o_sh +
-                                 static_cast<long long>(q_row) * p.o_ss) * 2;
+                                (static_cast<long long>(U.b) * p.o_sb + static_cast<long long>(h_row) * p.o_sh +
+                                 static_cast<long long>(s_row) * p.o_ss) * 2;
                 for (int cc = 0; cc < p.n_pv; cc += 16) {
                     uint32_t o[16];
                     if (n_my > 0) {
@@ -824,8 +898,13 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             if (cc + k < p.D_v) dst[k] = static_cast<uint16_t>((w[k >> 1] >> ((k & 1) * 16)) & 0xFFFFu);
                     }
                 }
-                if (EPI == kEpiPlain && p.lse && row_ok)
-                    p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + q_row] = lse_from(m_used, l);
+                if (EPI == kEpiPlain && p.lse && row_ok) {
+                    if constexpr (ROWS == kRowsSeq)
+                        p.lse[(static_cast<long long>(U.b) * p.H * p.row_heads + h_row) * p.row_tokens + s_row] =
+                            l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+                    else
+                        p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + q_row] = lse_from(m_used, l);
+                }
             } else if (ok && EPI == kEpiSplit) {
                 // ------------------------------------------------------------ epilogue: partial O, m, l
                 // Unnormalised O_t with its reference max m (log2 units) and sum l; a share with no
@@ -834,6 +913,11 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 const long long part = static_cast<long long>(U.split) * p.B * p.H * p.S_q + row_lin;
                 float *orow = p.part_o + part * p.part_ld;
                 if (n_my > 0) tc_fence_after();
+                // Two lanes store their two rows together, 64 bytes of one and then of the other: a warp's store then
+                // touches 16 lines, where a row per lane would touch 32 (the store unit takes a line a cycle).
+                const bool odd = lane & 1;
+                const bool row_ok_e = q_row - (odd ? 1 : 0) < p.S_q, row_ok_o = q_row + (odd ? 0 : 1) < p.S_q;
+                float *pair = orow - (odd ? p.part_ld : 0) + (odd ? 8 : 0);  // the even row, this lane's 8 columns
                 for (int cc = 0; cc < p.n_pv; cc += 16) {
                     uint32_t o[16];
                     if (n_my > 0) {
@@ -843,14 +927,16 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = 0u;
                     }
-                    if (!row_ok) continue;
-                    if (cc + 16 <= p.D_v) {
-                        float4 *dst = reinterpret_cast<float4 *>(orow + cc);
+                    if (cc + 16 <= p.part_ld) {
+                        uint32_t mine[8], other[8];
                         #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                    } else {
+                        for (int k = 0; k < 8; ++k) {
+                            mine[k] = odd ? o[8 + k] : o[k];
+                            other[k] = __shfl_xor_sync(0xffffffffu, odd ? o[k] : o[8 + k], 1);
+                        }
+                        if (row_ok_e) st_global_v8(pair + cc, odd ? other : mine);
+                        if (row_ok_o) st_global_v8(pair + p.part_ld + cc, odd ? mine : other);
+                    } else if (row_ok) {
                         #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             if (cc + k < p.D_v) orow[cc + k] = __uint_as_float(o[k]);

@@ -46,9 +46,12 @@ struct AttnParams {
     long long v_sb, v_sh, v_ss;
     const void *Q;               // read by the fp32 kernel's softmax threads (Q goes to TMEM), and where rows are gathered
     long long q_sb, q_sh, q_ss;
-    // bf16, gathered rows: H counts key/value heads, B is 1, and row r of head h is query head
-    // h * row_heads + r % row_heads at position (r / row_heads) % row_tokens of sequence r / (row_heads * row_tokens)
+    // bf16, gathered rows (kRowsAll, kRowsSeq of the kernel): H counts key/value heads, and the query rows of head h
+    // are (b, s, g) or, with kRowsSeq, (s, g) of sequence b in this order: query head h * row_heads + g at position s
     int row_heads, row_tokens;
+    // kRowsSeq: the key axis is the prefix's tiles (prefix_keys keys), then the tiles of the sequence's cache
+    int prefix_tiles, prefix_keys, cache_keys;
+    const int *kv_len;  // cached tokens per sequence, or null: cache_keys
     // fp32 kernel: query tiles per work unit (1 or 2), and the CTAs of a thread-block cluster that share
     // one unit's key tiles and merge their results in distributed shared memory (1: no cluster)
     int tiles_per_unit;

@@ -14,9 +14,10 @@ using Args = vt_attn_prefix_args;
 
 // How a call runs.  With prefix_shares > 0 a first launch leaves that many partial results of the prefix in the
 // workspace, from the two-tile tcgen05 kernel (`tiles`) or from the key-streaming kernel; the second launch streams
-// the caches and adds them.  Otherwise one launch streams the prefix and the cache of every sequence.
+// the caches and adds them.  Otherwise one launch streams the prefix and the cache of every sequence, or
+// (`seq_tiles`: many rows per sequence) takes them on the tcgen05 kernel.
 struct Plan {
-    bool tiles, with_prefix;
+    bool tiles, seq_tiles, with_prefix;
     int prefix_shares, prefix_cluster, cluster;
     size_t workspace;
 };
@@ -51,6 +52,7 @@ Sizes sizes_of(const Args &a) {
 }
 
 constexpr int64_t kTileRows = 32;                   // more rows per prefix key: the tcgen05 kernel
+constexpr int64_t kSeqTileRows = 64;                // more rows per sequence and key/value head: the tcgen05 kernel for all keys
 constexpr int64_t kReadAgain = int64_t(16) << 20;  // bytes
 
 size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
@@ -70,7 +72,7 @@ int tile_shares(int64_t blocks, int64_t S_p, int64_t rows, int64_t D_v, int sms)
     const int64_t tiles = (S_p + q2::kBN - 1) / q2::kBN;
     int best = 1;
     double best_us = 0.0;
-    for (int n = 1; n <= kMaxSplit && n <= tiles; ++n) {
+    for (int n = 1; n <= st::kMaxShares && n <= tiles; ++n) {
         const double waves = static_cast<double>((blocks * n + sms - 1) / sms);
         const double us = waves * (1.5 * static_cast<double>((tiles + n - 1) / n) + 4.0) +
                           static_cast<double>(rows) * n * (D_v + 3) * 8e-6 / 5.0;
@@ -89,6 +91,8 @@ Plan plan_of(const Args &a, int sms) {
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
     // reading the prefix once per sequence and row tile costs no more than a launch when it is this small
     const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
+    p.seq_tiles = a.dtype == VT_BF16 && z.per_b > kSeqTileRows;
+    if (p.seq_tiles) return p;
     p.tiles = a.dtype == VT_BF16 && a.B * z.per_b > kTileRows;
     p.with_prefix = again <= kReadAgain || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
     p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c, sms);
@@ -105,7 +109,7 @@ Plan plan_of(const Args &a, int sms) {
         int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
         const int64_t most = a.S_p / (256LL * p.prefix_cluster);
         if (shares > most) shares = most;
-        if (shares > kMaxSplit) shares = kMaxSplit;
+        if (shares > st::kMaxShares) shares = st::kMaxShares;
         p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
     }
     p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares);
@@ -270,16 +274,38 @@ vt_status launch_stream(const Args &a, const st::Maps &maps, const st::Params &p
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
-// The prefix on the two-tile tcgen05 kernel: one sequence of B * S_q * G gathered rows per key/value head.
-vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st::Params &sp, const DeviceInfo &info,
-                       int dev, cudaStream_t stream) {
+using TileKern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnParams);
+
+template <int EPI, int ROWS>
+TileKern pick_tiles(const AttnParams &p) {
+    const int ksteps = (p.D_qk + 15) / 16;
+    auto pick = [&](auto ring_c) -> TileKern {
+        constexpr bool R = decltype(ring_c)::value;
+        if (p.scale_log2 > 0.0f)
+            return ksteps <= 4   ? attn_fwd_bf16_2q_kernel<4, R, EPI, true, ROWS>
+                   : ksteps <= 6 ? attn_fwd_bf16_2q_kernel<6, R, EPI, true, ROWS>
+                                 : attn_fwd_bf16_2q_kernel<8, R, EPI, true, ROWS>;
+        return ksteps <= 4 ? attn_fwd_bf16_2q_kernel<4, R, EPI, false, ROWS>
+                           : attn_fwd_bf16_2q_kernel<8, R, EPI, false, ROWS>;
+    };
+    return p.n_pv <= 64 ? pick(std::true_type{}) : pick(std::false_type{});
+}
+
+// The two-tile tcgen05 kernel on gathered rows: the prefix for the rows of all sequences (partial results), or
+// (`seq`) the prefix and the cache for the rows of each sequence (the whole answer).
+vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st::Params &sp, bool seq,
+                       const DeviceInfo &info, int dev, cudaStream_t stream) {
     st::Maps m{};
     if (!kv_maps(a, q2::kBN, &m)) return VT_ERR_CUDA;
     AttnParams p{};
-    p.B = 1;
+    p.B = seq ? sp.B : 1;
     p.H = sp.H_kv;
-    p.S_q = static_cast<int>(a.B * z.per_b);
-    p.S_k = sp.S_p;
+    p.S_q = static_cast<int>(seq ? z.per_b : a.B * z.per_b);
+    p.prefix_tiles = (sp.S_p + q2::kBN - 1) / q2::kBN;
+    p.prefix_keys = sp.S_p;
+    p.cache_keys = sp.S_c;
+    p.kv_len = sp.kv_len;
+    p.S_k = seq ? (p.prefix_tiles + (sp.S_c + q2::kBN - 1) / q2::kBN) * q2::kBN : sp.S_p;
     p.D_qk = sp.D_qk;
     p.D_v = sp.D_v;
     p.n_qblocks = (p.S_q + q2::kRows - 1) / q2::kRows;
@@ -288,6 +314,7 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.n_pv = (p.D_v + 15) / 16 * 16;
     p.band_lo = -kBandInf;
     p.band_hi = kBandInf;
+    p.reverse_q = seq ? 1 : 0;
     p.kv_group = 1;
     p.scale_log2 = sp.scale_log2;
     p.Q = sp.Q;
@@ -296,9 +323,16 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.q_ss = sp.q_ss;
     p.row_heads = sp.G;
     p.row_tokens = sp.S_q;
+    p.O = sp.O;
+    p.o_sb = sp.o_sb;
+    p.o_sh = sp.o_sh;
+    p.o_ss = sp.o_ss;
+    p.o_vec32 = reinterpret_cast<uintptr_t>(sp.O) % 32 == 0 && (sp.B < 2 || sp.o_sb % 16 == 0) &&
+                (sp.H < 2 || sp.o_sh % 16 == 0) && (sp.S_q < 2 || sp.o_ss % 16 == 0);
+    p.lse = sp.lse;
     p.tiles_per_unit = 2;
     p.cluster = 1;
-    p.n_split = plan.prefix_shares;
+    p.n_split = seq ? 1 : plan.prefix_shares;
     p.part_o = sp.part_o;
     p.part_ld = sp.part_ld;
     p.part_m = sp.part_m;
@@ -311,27 +345,17 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.stages = (kSmemLimit - 1024 - static_cast<int>(sizeof(q2::Ctl)) - 256 - q_bytes) / slot_bytes;
     if (p.stages > q2::kMaxSlots) p.stages = q2::kMaxSlots;
     const int smem = 1024 + q_bytes + p.stages * slot_bytes;
-    // heads whose query blocks run at about the same time read K and V of the prefix from L2
+    // heads whose query blocks run at about the same time read K and V from L2
+    const int64_t heads = static_cast<int64_t>(p.B) * p.H;
     const int64_t per_head = static_cast<int64_t>(p.n_qblocks) * p.n_split;
-    int64_t grp = (2LL * info.sms + per_head - 1) / per_head;
-    p.head_group = static_cast<int>(grp < 1 ? 1 : (grp > a.H_kv ? a.H_kv : grp));
-    const int64_t units = per_head * a.H_kv;
+    const int64_t grp = (2LL * info.sms + per_head - 1) / per_head;
+    p.head_group = static_cast<int>(grp < 1 ? 1 : (grp > heads ? heads : grp));
+    const int64_t units = per_head * heads;
     if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
     p.n_units = static_cast<int>(units);
-    using TileKern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnParams);
-    const int ksteps = (p.D_qk + 15) / 16;
-    auto pick_k = [&](auto ring_c) -> TileKern {
-        constexpr bool R = decltype(ring_c)::value;
-        if (p.scale_log2 > 0.0f)
-            return ksteps <= 4   ? attn_fwd_bf16_2q_kernel<4, R, q2::kEpiSplit, true, true>
-                   : ksteps <= 6 ? attn_fwd_bf16_2q_kernel<6, R, q2::kEpiSplit, true, true>
-                                 : attn_fwd_bf16_2q_kernel<8, R, q2::kEpiSplit, true, true>;
-        return ksteps <= 4 ? attn_fwd_bf16_2q_kernel<4, R, q2::kEpiSplit, false, true>
-                           : attn_fwd_bf16_2q_kernel<8, R, q2::kEpiSplit, false, true>;
-    };
-    const TileKern kern = p.n_pv <= 64 ? pick_k(std::true_type{}) : pick_k(std::false_type{});
+    const TileKern kern = seq ? pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p) : pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p);
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
-    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(m.kp, m.kp, m.vp, p);
+    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(m.kc, m.kp, m.vp, m.vc, p);
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
@@ -347,10 +371,14 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
+    if (plan.seq_tiles) {
+        VT_TRY(launch_tiles(a, plan, z, p, true, info, dev, stream));
+        return env_check() ? read_status(stream) : VT_OK;
+    }
     st::Maps maps{};
     if (!kv_maps(a, st::kKeys, &maps)) return VT_ERR_CUDA;
     if (plan.tiles) {
-        VT_TRY(launch_tiles(a, plan, z, p, info, dev, stream));
+        VT_TRY(launch_tiles(a, plan, z, p, false, info, dev, stream));
     } else if (plan.prefix_shares) {
         p.all_rows = 1;
         p.row_tiles = static_cast<int>(z.tiles_all);

@@ -31,6 +31,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;
 constexpr int kKeys = 16;        // keys per block of a warp
 constexpr int kMaxClusterCtas = 8;
+constexpr int kMaxShares = 32;   // partial results of the prefix, at most
+constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares;
+static_assert(kMaxSources == 64, "a lane holds the weights of two sources");
 constexpr float kTau = 8.0f;     // the reference max moves when the running max exceeds it by 2^8 (see kTau of vt_attn_bf16_2q.cuh)
 
 struct Params {
@@ -107,6 +110,18 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+template <typename V>
+__device__ __forceinline__ V ld_cluster_vec(uint32_t addr) {
+    V v;
+    if constexpr (sizeof(V) == 16)
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 
 // Wait for the phase of `bar` with `parity`, giving up after the time limit (which the status word then records).
 __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, const Params &p) {
@@ -121,24 +136,27 @@ __device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity, cons
     }
 }
 
-// Shared memory of one warp: `stages` blocks of K [DQ / 64][16][128 bytes] then V, and after the loop over it the
-// warp's result: O [16][DV] fp32, then m, l, c [16].  (fp32: 32 columns a piece.)
+// Shared memory: each warp's `stages` blocks of K [pieces of 128 bytes][16 keys] then V, which its result takes the
+// place of after the loop (O [16][DV + 8] fp32, then m, l, c [16]); then the queries, as pieces of 16 rows.
 template <typename T, int DQ, int DV>
 struct Tile {
     static constexpr int kElt = sizeof(T);
     static constexpr int kCols = 128 / kElt;  // columns of a 128-byte piece
     static constexpr uint32_t kPiece = kKeys * 128;
-    static constexpr uint32_t kBytesK = DQ / kCols * kPiece, kBytesV = DV / kCols * kPiece;
+    static constexpr uint32_t kBytesK = DQ / kCols * kPiece, kBytesV = DV / kCols * kPiece, kBytesQ = kBytesK;
     static constexpr uint32_t kStage = kBytesK + kBytesV;
-    // 24 KB a warp, which lets two CTAs share an SM (fp32 at full width: 48 KB, one CTA)
-    static constexpr int kStages = kStage <= 4096 ? 6 : (kStage <= 6144 ? 4 : 3);
+    // 16 KB a warp, so that three CTAs share an SM and one's start and end hide behind the others' loads
+    // (fp32 at full width: 32 KB, one CTA)
+    static constexpr int kStages = kStage <= 4096 ? 4 : (kStage <= 6144 ? 3 : 2);
     static constexpr uint32_t kWarpBytes = kStages * kStage;
-    static constexpr uint32_t kSmem = 1024 + kWarps * kWarpBytes;  // pieces start on 1024 bytes
-    static_assert(kRowsTile * DV * 4 + 3 * kRowsTile * 4 <= kWarpBytes, "a warp's result takes the place of its stages");
+    static constexpr uint32_t kQ = kWarps * kWarpBytes;
+    static constexpr uint32_t kSmem = 1024 + kQ + kBytesQ;  // pieces start on 1024 bytes
+    static constexpr int kLdO = DV + 8;  // floats between result rows: eight rows' stores fall into different banks
+    static_assert(kRowsTile * kLdO * 4 + 3 * kRowsTile * 4 <= kWarpBytes, "a warp's result takes the place of its stages");
 };
 
 template <typename T, int DQ, int DV>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
     attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Tile<T, DQ, DV>;
     constexpr bool kBf = sizeof(T) == 2;
@@ -154,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     if (p.all_rows) launch_dependents();
 
     // ---- the unit: 16 rows, and the keys of this CTA's share of them
-    const int rank = static_cast<int>(blockIdx.x) % p.cluster;
-    long long u = blockIdx.x / p.cluster;
+    unsigned u = blockIdx.x / p.cluster;
+    const int rank = static_cast<int>(blockIdx.x - u * p.cluster);
     int share = 0;
     if (p.all_rows) {
         share = static_cast<int>(u % p.shares);
@@ -163,12 +181,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     }
     const int rt = static_cast<int>(u % p.row_tiles);
     u /= p.row_tiles;
-    const int hk = static_cast<int>(u % p.H_kv);
     const int b = static_cast<int>(u / p.H_kv);  // 0 with all_rows
+    const int hk = static_cast<int>(u) - b * p.H_kv;
     const int per_b = p.S_q * p.G;
     const int group_rows = p.all_rows ? p.B * per_b : per_b;
     const int f0 = rt * kRowsTile;
     const int n_rows = min(kRowsTile, group_rows - f0);
+
+    // the queries on their way to shared memory: 16 bytes per thread and step, swizzled as the keys are, zeros past
+    // the last row and past D_qk
+    {
+        constexpr int kUnitsRow = DQ * L::kElt / 16;
+        for (int i = threadIdx.x; i < kRowsTile * kUnitsRow; i += kThreads) {
+            const int r = i / kUnitsRow, c = i % kUnitsRow;
+            const int f = f0 + r;
+            const int bytes = r < n_rows ? min(16, max(0, p.D_qk * L::kElt - c * 16)) : 0;
+            const void *src = p.Q;
+            if (bytes > 0) {
+                const int bb = p.all_rows ? f / per_b : b;
+                const int fs = p.all_rows ? f - bb * per_b : f;
+                const int s = fs / p.G, g = fs - s * p.G;
+                src = static_cast<const T *>(p.Q) + bb * p.q_sb + static_cast<long long>(hk * p.G + g) * p.q_sh +
+                      s * p.q_ss + c * (16 / L::kElt);
+            }
+            cp_async16(base + L::kQ + (c >> 3) * L::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, bytes);
+        }
+        cp_async_commit();
+    }
 
     int len = 0;
     if (!p.all_rows) {
@@ -211,42 +250,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         for (int i = 0; i < kStages - 1; ++i)
             if (i < n_mine) load(first + warp + i * kWarps, i);
     }
-    __syncwarp();
+    cp_async_wait<0>();
+    __syncthreads();
 
-    // ---- the rows' queries, in the layout of an MMA's A operand: rows lane / 4 and lane / 4 + 8
+    // ---- the queries in the layout of an MMA's A operand: this thread's rows are lane / 4 and lane / 4 + 8
     const int g8 = lane >> 2, t4 = lane & 3;
     constexpr int kSteps = kBf ? DQ / 16 : DQ / 8;
     uint32_t q[kSteps][4];
-    const T *qrow[2];
-    int lim[2];
+    {
+        // matrices: rows 0-7 and 8-15 of 16-byte column 2 ks, then of column 2 ks + 1
+        const int r = lane & 15;
+        const uint32_t row = base + L::kQ + r * 128, odd = lane >> 4;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int i = g8 + 8 * r;
-        const int f = f0 + (i < n_rows ? i : 0);
-        const int bb = p.all_rows ? f / per_b : b;
-        const int fs = p.all_rows ? f - bb * per_b : f;
-        const int s = fs / p.G, g = fs - s * p.G;
-        qrow[r] = i < n_rows ? static_cast<const T *>(p.Q) + bb * p.q_sb + static_cast<long long>(hk * p.G + g) * p.q_sh +
-                                   s * p.q_ss
-                             : nullptr;
-        lim[r] = i < n_rows ? own(f) : 0;
+        for (int ks = 0; ks < kSteps; ++ks)
+            ldsm4(q[ks], row + (ks >> 2) * L::kPiece + (((2 * (ks & 3) + odd) ^ (r & 7)) << 4));
     }
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const T *row = qrow[j & 1];
-            if (kBf) {
-                const int d = ks * 16 + (j >> 1) * 8 + t4 * 2;
-                uint32_t v = 0;
-                if (row && d + 1 < p.D_qk) v = *reinterpret_cast<const uint32_t *>(row + d);
-                else if (row && d < p.D_qk) v = *reinterpret_cast<const uint16_t *>(row + d);
-                q[ks][j] = v;
-            } else {
-                const int d = ks * 8 + (j >> 1) * 4 + t4;
-                q[ks][j] = row && d < p.D_qk ? *reinterpret_cast<const uint32_t *>(row + d) : 0u;
-            }
-        }
+    const int lim[2] = {g8 < n_rows ? own(f0 + g8) : 0, g8 + 8 < n_rows ? own(f0 + g8 + 8) : 0};
 
     float o[DV / 8][4];
 #pragma unroll
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 
     // ---- the warp's result
     float *wo = reinterpret_cast<float *>(smem + warp * L::kWarpBytes);
-    float *wm = wo + kRowsTile * DV;
+    float *wm = wo + kRowsTile * L::kLdO;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
 #pragma unroll
@@ -408,20 +427,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         }
 #pragma unroll
         for (int n = 0; n < DV / 8; ++n)
-            *reinterpret_cast<float2 *>(wo + (g8 + 8 * r) * DV + n * 8 + 2 * t4) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+            *reinterpret_cast<float2 *>(wo + (g8 + 8 * r) * L::kLdO + n * 8 + 2 * t4) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
     }
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
     if (!p.all_rows) wait_prerequisites();  // (the whole grid waits, so that it ends after the prefix's launch)
 
     // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row.  The sources of a
-    // row are the cluster's warps and the workspace's shares; every lane holds the weight of the sources that fall
-    // to it (lane, lane + 32, ...), then the sources' rows are added in order, eight loads at a time.
+    // row are the cluster's warps and the workspace's shares; every lane holds the weights of sources lane and
+    // lane + 32, then the sources' rows are added in order, eight loads at a time, DV / 32 columns per lane.
     constexpr int kCols = DV / 32;
-    constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxSplit;
-    constexpr int kPerLane = (kMaxSources + 31) / 32;
-    const uint32_t o_off = base, m_off = base + kRowsTile * DV * 4;
+    using VecC = typename std::conditional<kCols == 4, float4, float2>::type;
+    const uint32_t o_off = base, m_off = base + kRowsTile * L::kLdO * 4;
     const int n_smem = kWarps * p.cluster, n_src = n_smem + p.prior;
+    const int col = lane * kCols;
+#pragma unroll 1
     for (int i = rank + p.cluster * warp; i < n_rows; i += p.cluster * kWarps) {
         const int f = f0 + i;
         const long long flat = static_cast<long long>(hk) * p.B * per_b + static_cast<long long>(b) * per_b + f;
@@ -429,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             const uint32_t at = off + (src % kWarps) * L::kWarpBytes;
             return p.cluster > 1 ? cluster_map(at, src / kWarps) : at;
         };
-        float ms[kPerLane], ls[kPerLane], cs[kPerLane];
+        float ms[kMaxSources / 32], ls[kMaxSources / 32], cs[kMaxSources / 32];
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
+        for (int k = 0; k < kMaxSources / 32; ++k) {
             const int src = lane + 32 * k;
             ms[k] = -INFINITY;
             ls[k] = cs[k] = 0.0f;
@@ -449,12 +469,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         }
         float M = ms[0];
 #pragma unroll
-        for (int k = 1; k < kPerLane; ++k) M = fmaxf(M, ms[k]);
+        for (int k = 1; k < kMaxSources / 32; ++k) M = fmaxf(M, ms[k]);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
         float Ls = 0.0f, Lo = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
+        for (int k = 0; k < kMaxSources / 32; ++k) {
             // the source's weight: 0 without keys (a sum that is NaN without a maximum stays NaN)
             ms[k] = ms[k] == -INFINITY && ls[k] == 0.0f ? 0.0f : ex2(ms[k] - M);
             Ls += ms[k] * ls[k];
@@ -469,33 +489,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
         constexpr int kAtOnce = 8;
+#pragma unroll 1
+        for (int s0 = 0; s0 < n_src; s0 += kAtOnce) {
+            VecC v[kAtOnce];
+            float w[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k)
-            for (int s0 = 0; s0 < 32 && s0 + 32 * k < n_src; s0 += kAtOnce) {
-                float v[kAtOnce][kCols], w[kAtOnce];
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const int src = s0 + j + 32 * k;
-                    w[j] = __shfl_sync(0xffffffffu, ms[k], s0 + j);
-                    const bool in = src < n_src && w[j] != 0.0f;  // (a source without weight may hold anything)
-#pragma unroll
-                    for (int x = 0; x < kCols; ++x) {
-                        const int col = lane + 32 * x;
-                        v[j][x] = 0.0f;
-                        if (in && src < n_smem) v[j][x] = ld_cluster(warp_part(o_off, src) + (i * DV + col) * 4);
-                        else if (in && col < p.D_v) v[j][x] = p.part_o[((src - n_smem) * p.rows + flat) * p.part_ld + col];
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-                    for (int x = 0; x < kCols; ++x) acc[x] = fmaf(w[j], v[j][x], acc[x]);
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int src = s0 + j;
+                w[j] = __shfl_sync(0xffffffffu, s0 < 32 ? ms[0] : ms[1], src & 31);
+                v[j] = VecC{};
+                if (w[j] == 0.0f) continue;  // (a source without weight, or none at all)
+                if (src < n_smem) v[j] = ld_cluster_vec<VecC>(warp_part(o_off, src) + (i * L::kLdO + col) * 4);
+                else if (col < p.part_ld)
+                    v[j] = *reinterpret_cast<const VecC *>(p.part_o + ((src - n_smem) * p.rows + flat) * p.part_ld + col);
             }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                for (int x = 0; x < kCols; ++x)
+                    acc[x] = fmaf(w[j], reinterpret_cast<const float *>(&v[j])[x], acc[x]);
+        }
         if (p.all_rows) {
             const long long at = share * p.rows + flat;
-#pragma unroll
-            for (int k = 0; k < kCols; ++k)
-                if (lane + 32 * k < p.D_v) p.part_o[at * p.part_ld + lane + 32 * k] = acc[k];
+            if (col < p.part_ld)
+                *reinterpret_cast<VecC *>(p.part_o + at * p.part_ld + col) = *reinterpret_cast<const VecC *>(acc);
             if (lane == 0) {
                 p.part_m[at] = M;
                 p.part_l[at] = Ls;
@@ -505,16 +522,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             const int s = f / p.G, g = f - s * p.G;
             const int h = hk * p.G + g;
             const float inv = Ls == 0.0f ? 0.0f : 1.0f / Lo;  // a row without keys is 0
-            T *orow = static_cast<T *>(p.O) + b * p.o_sb + h * p.o_sh + s * p.o_ss;
+            T *orow = static_cast<T *>(p.O) + b * p.o_sb + h * p.o_sh + s * p.o_ss + col;
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                const int col = lane + 32 * k;
-                if (col >= p.D_v) continue;
-                const float v = acc[k] * inv;
+            for (int k = 0; k < kCols; ++k) acc[k] *= inv;
+            if (col + kCols <= p.D_v) {  // rows start on 16 bytes
                 if constexpr (kBf) {
-                    reinterpret_cast<uint16_t *>(orow)[col] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+#pragma unroll
+                    for (int k = 0; k < kCols; k += 2)
+                        *reinterpret_cast<uint32_t *>(orow + k) = pack_bf16x2(acc[k], acc[k + 1]);
                 } else {
-                    reinterpret_cast<float *>(orow)[col] = v;
+                    *reinterpret_cast<VecC *>(orow) = *reinterpret_cast<const VecC *>(acc);
+                }
+            } else {
+                for (int k = 0; k < kCols && col + k < p.D_v; ++k) {
+                    if constexpr (kBf) {
+                        reinterpret_cast<uint16_t *>(orow)[k] = static_cast<uint16_t>(pack_bf16x2(acc[k], 0.0f) & 0xFFFFu);
+                    } else {
+                        reinterpret_cast<float *>(orow)[k] = acc[k];
+                    }
                 }
             }
             if (p.lse && lane == 0)

@@ -169,6 +169,11 @@ CASES = [
     ("bf16", 33, 8, 1, 2, 1025, 9, 80, 128),      # three query tiles of gathered rows, the last one short
     ("bf16", 160, 64, 8, 4, 300, 5, 64, 64),      # more blocks of gathered rows than SMs
     ("bf16", 80, 64, 8, 8, 300, 8, 128, 128),
+    ("bf16", 3, 8, 2, 100, 129, 300, 128, 128),   # chunks: the rows of a sequence fill tiles of their own
+    ("bf16", 2, 4, 1, 70, 0, 200, 96, 64),
+    ("bf16", 5, 8, 1, 33, 1000, 0, 128, 72),
+    ("bf16", 40, 6, 2, 90, 70, 91, 40, 128),      # more of them than SMs
+    ("bf16", 70, 4, 2, 1, 1000, 37, 64, 33),      # an odd value width in the shares
     ("f32", 1, 1, 1, 1, 1, 1, 4, 4),
     ("f32", 8, 8, 2, 1, 1000, 333, 72, 72),
     ("f32", 40, 8, 2, 1, 1500, 40, 128, 128),
@@ -188,12 +193,12 @@ def test_against_the_definition(case, tokens_first):
 
 
 @gpu
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype,S_q,D_v", [("bf16", 3, 64), ("f32", 3, 64), ("bf16", 70, 64), ("bf16", 70, 128)])
 @pytest.mark.parametrize("S_p", [0, 5, 600])
-def test_lengths_at_their_ends(dtype, S_p):
+def test_lengths_at_their_ends(dtype, S_q, D_v, S_p):
     # empty, one token, fewer than the queries, a block of keys and its neighbours, full
-    lens = [0, 1, 2, 3, 15, 16, 17, 63, 64, 65, 127, 128, 129]
-    p = Problem(dtype, len(lens), 4, 2, 3, S_p, 129, 64, 64, lens=lens, seed=2)
+    lens = [0, 1, 2, 3, 15, 16, 17, 63, 64, 65, 69, 70, 71, 127, 128, 129]
+    p = Problem(dtype, len(lens), 4, 2, S_q, S_p, 129, 64, D_v, lens=lens, seed=2)
     p.check(*p.run())
     p.lens[:] = 129
     o, lse = vt.attn_fwd_prefix(p.q, p.kp, p.vp, p.kc.nan_to_num(0.0), p.vc.nan_to_num(0.0), None, scale=p.scale,
@@ -204,8 +209,9 @@ def test_lengths_at_their_ends(dtype, S_p):
 
 
 @gpu
-def test_lengths_outside_the_cache_are_reported():
-    p = Problem("bf16", 3, 4, 2, 1, 50, 20, 64, 64, lens=[-5, 20, 20], seed=3)
+@pytest.mark.parametrize("S_q", [1, 64])
+def test_lengths_outside_the_cache_are_reported(S_q):
+    p = Problem("bf16", 3, 4, 2, S_q, 50, 20, 64, 64, lens=[-5, 20, 20], seed=3)
     p.kv_len[2] = 1 << 20
     p.check(*p.run())
     assert vt.vt_last_device_status() == 6
@@ -216,9 +222,22 @@ def test_lengths_outside_the_cache_are_reported():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale", [0.0, -0.5, 3.0])
 def test_scales_and_peaked_rows(dtype, scale):
-    for B, D in ((20, 64), (90, 64), (90, 128)):  # streamed, and (bf16) on tiles of gathered rows
-        p = Problem(dtype, B, 4, 1, 1, 1100, 60, D, D, seed=4, scale=scale, spread=2.0)
+    # streamed, and (bf16) on tiles of gathered rows
+    for B, S_q, D in ((20, 1, 64), (90, 1, 64), (90, 1, 128), (2, 50, 64), (2, 50, 128)):
+        p = Problem(dtype, B, 4, 1, S_q, 1100, 60, D, D, seed=4, scale=scale, spread=2.0)
         p.check(*p.run())
+
+
+@gpu
+@pytest.mark.parametrize("B,S_q,S_p", [(3, 1, 100), (90, 1, 1100), (2, 70, 300)])
+def test_nan_stays_in_its_row(B, S_q, S_p):
+    p = Problem("bf16", B, 4, 2, S_q, S_p, 80, 64, 64, lens=[80] * B, seed=11)
+    want = [t.clone() for t in p.run()]
+    p.q[1, 2, S_q - 1, 5] = float("nan")
+    o, lse = p.run()
+    assert p.torch.isnan(o[1, 2, S_q - 1]).all() and p.torch.isnan(lse[1, 2, S_q - 1])
+    o[1, 2, S_q - 1], lse[1, 2, S_q - 1] = want[0][1, 2, S_q - 1], want[1][1, 2, S_q - 1]
+    assert p.torch.equal(o, want[0]) and p.torch.equal(lse, want[1])
 
 
 @gpu
