@@ -449,6 +449,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
             const uint32_t at = off + (src % kWarps) * L::kWarpBytes;
             return p.cluster > 1 ? cluster_map(at, src / kWarps) : at;
         };
+        constexpr int kAtOnce = 8;
+        VecC v[kAtOnce];
+        auto load_rows = [&](int s0) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int src = s0 + j;
+                v[j] = VecC{};
+                if (src < n_smem) v[j] = ld_cluster_vec<VecC>(warp_part(o_off, src) + (i * L::kLdO + col) * 4);
+                else if (src < n_src && col < p.part_ld)
+                    v[j] = *reinterpret_cast<const VecC *>(p.part_o + ((src - n_smem) * p.rows + flat) * p.part_ld + col);
+            }
+        };
+        load_rows(0);  // on their way while the weights are formed
         float ms[kMaxSources / 32], ls[kMaxSources / 32], cs[kMaxSources / 32];
 #pragma unroll
         for (int k = 0; k < kMaxSources / 32; ++k) {
@@ -488,26 +501,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
         float acc[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
-        constexpr int kAtOnce = 8;
 #pragma unroll 1
         for (int s0 = 0; s0 < n_src; s0 += kAtOnce) {
-            VecC v[kAtOnce];
-            float w[kAtOnce];
+            if (s0 > 0) load_rows(s0);
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
-                const int src = s0 + j;
-                w[j] = __shfl_sync(0xffffffffu, s0 < 32 ? ms[0] : ms[1], src & 31);
-                v[j] = VecC{};
-                if (w[j] == 0.0f) continue;  // (a source without weight, or none at all)
-                if (src < n_smem) v[j] = ld_cluster_vec<VecC>(warp_part(o_off, src) + (i * L::kLdO + col) * 4);
-                else if (col < p.part_ld)
-                    v[j] = *reinterpret_cast<const VecC *>(p.part_o + ((src - n_smem) * p.rows + flat) * p.part_ld + col);
-            }
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j)
+                const float w = __shfl_sync(0xffffffffu, s0 < 32 ? ms[0] : ms[1], (s0 + j) & 31);
 #pragma unroll
                 for (int x = 0; x < kCols; ++x)
-                    acc[x] = fmaf(w[j], reinterpret_cast<const float *>(&v[j])[x], acc[x]);
+                    acc[x] = fmaf(w, reinterpret_cast<const float *>(&v[j])[x], acc[x]);
+            }
         }
         if (p.all_rows) {
             const long long at = share * p.rows + flat;
