@@ -311,27 +311,26 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
 #define VT_ROPE_MAX_PAIRS 128
 typedef struct {
     uint64_t struct_bytes; /* sizeof(vt_qk_rope_args) */
+    const void *q, *k;
+    const void *q_weight, *k_weight;
+    const float *freqs;
+    const int32_t *positions;
+    void *q_out, *k_out;
+    const int32_t *kv_len; /* [B]; NULL: no append, and v, v_out, cap and D_v are ignored */
+    const void *v;
+    void *v_out;
     int64_t B, H, H_kv, S, D, R;
+    int64_t cap, D_v;
     int32_t dtype; /* vt_dtype */
     int32_t interleaved;
     int32_t normalize;
     int32_t axes;
     float eps;
     int32_t reserved; /* 0 */
-    const void *q, *k;
     int64_t q_stride[3], k_stride[3];
-    const void *q_weight, *k_weight;
-    const float *freqs;
-    const int32_t *positions;
-    int64_t pos_stride[3];
-    void *q_out, *k_out;
     int64_t q_out_stride[3], k_out_stride[3];
-    /* append (kv_len NULL: none, and the fields below are ignored) */
-    const int32_t *kv_len; /* [B] */
-    int64_t cap, D_v;
-    const void *v;
-    void *v_out;
     int64_t v_stride[3], v_out_stride[3];
+    int64_t pos_stride[3];
     uint8_t pair_axis[VT_ROPE_MAX_PAIRS]; /* pair_axis[i] < axes for i < R/2 */
 } vt_qk_rope_args;
 
@@ -389,21 +388,21 @@ size_t vt_qk_rope_bwd_workspace_size(int64_t D);
  */
 typedef struct {
     uint64_t struct_bytes; /* sizeof(vt_attn_prefix_args) */
-    int64_t B, H, H_kv, S_q, S_p, S_c, D_qk, D_v;
-    int32_t dtype; /* vt_dtype */
-    float scale;
     const void *q;
-    int64_t q_stride[3];
     const void *k_prefix, *v_prefix;
-    int64_t kp_stride[2], vp_stride[2];
     const void *k_cache, *v_cache;
-    int64_t kc_stride[3], vc_stride[3];
     const int32_t *kv_len;
     void *o;
-    int64_t o_stride[3];
     float *lse;
     void *workspace;
     size_t workspace_bytes;
+    int64_t B, H, H_kv, S_q, S_p, S_c, D_qk, D_v;
+    int32_t dtype; /* vt_dtype */
+    float scale;
+    int64_t q_stride[3];
+    int64_t kp_stride[2], vp_stride[2];
+    int64_t kc_stride[3], vc_stride[3];
+    int64_t o_stride[3];
 } vt_attn_prefix_args;
 
 vt_status vt_attn_fwd_prefix(const vt_attn_prefix_args *args, vt_stream_t stream);

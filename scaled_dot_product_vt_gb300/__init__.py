@@ -170,8 +170,10 @@ def vt_attn_fwd_general(Q, q_stride, K, k_stride, V, v_stride, O, o_stride, lse,
                                       int(workspace_bytes), ctypes.byref(opts) if opts is not None else None, stream)
 
 
-# vt_qk_rope_args, packed in field order (every field is aligned without padding)
-_QK_ROPE_ARGS = struct.Struct("=Q6q4ifi2Q6q2QQQ3q2Q6qQ2q2Q6q128s")
+# vt_qk_rope_args in field order (every field is aligned without padding): its size and the addresses, then the rest
+_QK_ROPE_PTRS = struct.Struct("=12Q")
+_QK_ROPE_REST = struct.Struct("=8q4ifi21q128s")
+_QK_ROPE_BYTES = _QK_ROPE_PTRS.size + _QK_ROPE_REST.size
 
 
 def vt_qk_rope_fwd(args: bytes, stream) -> int:
@@ -189,8 +191,11 @@ def vt_qk_rope_bwd_workspace_size(D) -> int:
     return int(load().vt_qk_rope_bwd_workspace_size(D))
 
 
-# vt_attn_prefix_args, packed in field order (every field is aligned without padding)
-_ATTN_PREFIX_ARGS = struct.Struct("=Q8qifQ3q2Q4q2Q6q2Q3q3Q")
+# vt_attn_prefix_args in field order (every field is aligned without padding): its size, the addresses and the
+# workspace's size, then the rest
+_ATTN_PREFIX_PTRS = struct.Struct("=11Q")
+_ATTN_PREFIX_REST = struct.Struct("=8qif16q")
+_ATTN_PREFIX_BYTES = _ATTN_PREFIX_PTRS.size + _ATTN_PREFIX_REST.size
 
 
 def vt_attn_fwd_prefix(args: bytes, stream) -> int:
@@ -332,49 +337,79 @@ def attn_fwd_general(q, k, v, scale: float | None = None, mask: str = "none", of
 
 # ---------------------------------------------------------------- token preparation
 
-def _on_stream(fn):
-    """Run a wrapper on its ``stream=`` (a torch stream or a raw handle; None: the current stream of the first
-    tensor's device).  What the wrapper allocates is then allocated on that stream, and that device is current."""
+# The wrappers below check a call and pack the fixed part of its arguments once per combination of shapes, strides,
+# types and options (the functions under lru_cache, which see no address), and add the addresses per call.
 
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        import torch
-        if not first.is_cuda:
-            raise ValueError("the tensors must be CUDA tensors")
-        dev = first.device
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-
-    return call
+def _elsewhere(fn, first, stream, args, kw):
+    """Run a wrapper on another stream (a torch stream or a raw handle) or for tensors of another device than the
+    current one: what it allocates is then allocated on that stream, and that device is current."""
+    import torch
+    if not first.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return fn(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
-def _same_place(what, first, *tensors):
-    """Every tensor given (not None) lives on the first one's device."""
-    dev = first.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: all tensors must be on {dev}")
+def _here(t) -> bool:
+    """The tensor is on the current device."""
+    import torch
+    return t.is_cuda and t.get_device() == torch.cuda.current_device()
 
 
-def _bhsd(name, t, shape=None, dtype=None):
-    """(address, strides) of a [B, H, S, D] tensor with its last dimension contiguous."""
-    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
-        raise ValueError(f"{name} must be [B, H, S, D] with the last dimension contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr(), t.stride()[:3]
+def _meta(t):
+    """What the checks need to know of a tensor (None: absent)."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-@functools.lru_cache(maxsize=64)
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _check(name, meta, dev, dtype, shape=None, dims=4):
+    """Strides of a tensor of `dims` indices whose last one is contiguous, without the last."""
+    t_shape, stride, t_dtype, t_dev = meta
+    if t_dev != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    if len(t_shape) != dims or (stride[-1] != 1 and t_shape[-1] != 1):
+        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
+    if shape is not None and tuple(t_shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t_shape)}")
+    if t_dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t_dtype}")
+    return stride[:-1]
+
+
+def _check_vector(name, meta, dev, dtype, n):
+    shape, stride, t_dtype, t_dev = meta
+    if t_dev != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    if t_dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t_dtype}")
+    if len(shape) != 1 or (n is not None and shape[0] != n) or (shape[0] > 1 and stride[0] != 1):
+        raise ValueError(f"{name} must be a contiguous vector" + (f" of {n} elements" if n is not None else ""))
+
+
+def _new_rows(shape, dtype, device):
+    """A new [B, H, S, D] tensor; rows that are no multiple of 16 bytes are padded to one (a view is returned)."""
+    import torch
+    over = shape[3] % (16 // dtype.itemsize)
+    if over == 0:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty((*shape[:3], shape[3] - over + 16 // dtype.itemsize), dtype=dtype, device=device)[..., :shape[3]]
+
+
+def _new_strides(shape, dtype):
+    """Strides of _new_rows(shape, dtype)."""
+    step = 16 // dtype.itemsize
+    row = (shape[3] + step - 1) // step * step
+    return (shape[1] * shape[2] * row, shape[2] * row, row)
+
+
 def _pair_axis_bytes(pair_axis, pairs: int, axes: int) -> bytes:
     if pair_axis is None:
         if axes != 1:
@@ -385,141 +420,149 @@ def _pair_axis_bytes(pair_axis, pairs: int, axes: int) -> bytes:
     return bytes(pair_axis).ljust(128, b"\0")
 
 
-def _rope_form(q, k, freqs, positions, pair_axis, q_weight, k_weight):
-    """The fields the two directions share: (dims, weights, freqs and positions, pair axes)."""
+_NO3 = (0, 0, 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_plan(q, k, freqs, positions, q_weight, k_weight, q_out, k_out, kv_len, v, v_out, pair_axis, interleaved, eps):
+    """Checks of a qk_rope call from its tensors' metadata; the packed fixed part of its arguments."""
     import torch
-    B, H, S, D = q.shape
-    if k is not None and (k.dim() != 4 or k.shape[0] != B or k.shape[2] != S or k.shape[3] != D):
-        raise ValueError("shape mismatch between q and k")
-    if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous float32 vector")
-    pairs = freqs.shape[0]
+    q_shape, _, dt, dev = q
+    code = VT_BF16 if dt == torch.bfloat16 else VT_F32 if dt == torch.float32 else None
+    if code is None:
+        raise TypeError(f"qk_rope supports bfloat16 and float32 tensors, got {dt}")
+    sq = _check("q", q, dev, dt)
+    B, H, S, D = q_shape
+    _check_vector("freqs", freqs, dev, torch.float32, None)
+    pairs = freqs[0][0]
     if not 1 <= pairs <= 128:
         raise ValueError("freqs must have 1 to 128 entries")
-    if positions.dtype != torch.int32:
-        raise TypeError(f"positions must be int32, got {positions.dtype}")
-    if positions.dim() == 2:
-        axes, pos_stride = 1, (0, *positions.stride())
-    elif positions.dim() == 3:
-        axes, pos_stride = positions.shape[0], positions.stride()
-    else:
+    if positions[3] != dev or positions[2] != torch.int32:
+        raise TypeError("positions must be int32, on the device of the other tensors")
+    p_shape, p_stride = positions[0], positions[1]
+    if len(p_shape) not in (2, 3) or tuple(p_shape[-2:]) != (B, S):
         raise ValueError("positions must be [B, S] or [axes, B, S]")
-    if positions.shape[-2:] != (B, S):
-        raise ValueError("positions must be [B, S] or [axes, B, S]")
+    axes, pos_st = (1, (0, *p_stride)) if len(p_shape) == 2 else (p_shape[0], p_stride)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != q.dtype or w.shape != (D,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous vector of {D} elements of q's dtype")
-    if pair_axis is not None and not isinstance(pair_axis, tuple):
-        pair_axis = tuple(pair_axis)
-    return (B, H, k.shape[1] if k is not None else 0, S, D, 2 * pairs, axes,
-            q_weight.data_ptr() if q_weight is not None else 0, k_weight.data_ptr() if k_weight is not None else 0,
-            freqs.data_ptr(), positions.data_ptr(), pos_stride, _pair_axis_bytes(pair_axis, pairs, axes))
+        if w is not None:
+            _check_vector(name, w, dev, dt, D)
+    sqo = _check("q_out", q_out, dev, dt, q_shape) if q_out is not None else _new_strides(q_shape, dt)
+    sk = sko = sv = svo = _NO3
+    H_kv = cap = D_v = 0
+    if k is not None:
+        sk = _check("k", k, dev, dt)
+        H_kv = k[0][1]
+        if tuple(k[0]) != (B, H_kv, S, D):
+            raise ValueError("shape mismatch between q and k")
+    if kv_len is not None:
+        if k is None or k_out is None or (v is None) != (v_out is None):
+            raise ValueError("an append needs k and its cache k_out, and v only with its cache v_out")
+        _check_vector("kv_len", kv_len, dev, torch.int32, B)
+        cap = k_out[0][2] if len(k_out[0]) == 4 else 0
+        sko = _check("k_out", k_out, dev, dt, (B, H_kv, cap, D))
+        if v is not None:
+            D_v = v[0][3] if len(v[0]) == 4 else 0
+            sv = _check("v", v, dev, dt, (B, H_kv, S, D_v))
+            svo = _check("v_out", v_out, dev, dt, (B, H_kv, cap, D_v))
+    elif v is not None or v_out is not None:
+        raise ValueError("v is appended with kv_len only")
+    elif k is not None:
+        sko = _check("k_out", k_out, dev, dt, k[0]) if k_out is not None else _new_strides(k[0], dt)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    return _QK_ROPE_REST.pack(B, H, H_kv, S, D, 2 * pairs, cap, D_v, code, interleaved, eps is not None, axes,
+                              eps or 0.0, 0, *sq, *sk, *sqo, *sko, *sv, *svo, *pos_st,
+                              _pair_axis_bytes(pair_axis, pairs, axes))
 
 
-_NO_TENSOR = (0, (0, 0, 0))
-
-
-def _new_rows(B, H, S, D, dtype, device):
-    """A new [B, H, S, D] tensor; rows that are no multiple of 16 bytes are padded to one (a view is returned)."""
-    import torch
-    step = 16 // dtype.itemsize
-    if D % step == 0:
-        return torch.empty((B, H, S, D), dtype=dtype, device=device)
-    return torch.empty((B, H, S, D + -D % step), dtype=dtype, device=device)[..., :D]
-
-
-@_on_stream
 def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False, eps: float | None = None,
-            q_weight=None, k_weight=None, q_out=None, k_out=None, kv_len=None, v=None, v_out=None):
+            q_weight=None, k_weight=None, q_out=None, k_out=None, kv_len=None, v=None, v_out=None, stream=None):
     """Norm (with ``eps``) and rotation of the rows of q [B,H,S,D] and k [B,H_kv,S,D] (or None) in one pass: see
     vt_qk_rope_fwd in include/vt_attn.h.  Returns (q_out, k_out).
 
     ``freqs`` (float32) holds the angle per position of each of the R/2 rotated pairs, ``positions`` (int32) is
-    [B,S] or [axes,B,S], and ``pair_axis`` names the axis of every pair.  ``eps=None`` leaves the norm out.
+    [B,S] or [axes,B,S], and ``pair_axis`` (a tuple) names the axis of every pair.  ``eps=None`` leaves the norm out.
     ``q_out=q`` and ``k_out=k`` work in place.  With ``kv_len`` (int32 [B]: the lengths after these tokens), k_out
     is a cache [B,H_kv,cap,D] that K's rows are appended to, and v [B,H_kv,S,D_v] is appended to v_out.
     ``stream`` may name another stream than the current one."""
+    if stream is not None or not _here(q):
+        return _elsewhere(qk_rope, q, stream, (q, k, freqs, positions), dict(
+            pair_axis=pair_axis, interleaved=interleaved, eps=eps, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+            k_out=k_out, kv_len=kv_len, v=v, v_out=v_out))
     import torch
-    (B, H, H_kv, S, D, R, axes, qw, kw, fr, pos, pos_st, axis) = _rope_form(q, k, freqs, positions, pair_axis,
-                                                                           q_weight, k_weight)
-    code = _dtype_code(q)
-    _same_place("qk_rope", q, k, freqs, positions, q_weight, k_weight, q_out, k_out, kv_len, v, v_out)
+    if pair_axis is not None and type(pair_axis) is not tuple:
+        pair_axis = tuple(pair_axis)
+    rest = _rope_plan(_meta(q), _meta(k), _meta(freqs), _meta(positions), _meta(q_weight), _meta(k_weight),
+                      _meta(q_out), _meta(k_out), _meta(kv_len), _meta(v), _meta(v_out), pair_axis, bool(interleaved),
+                      eps)
     if q_out is None:
-        q_out = _new_rows(B, H, S, D, q.dtype, q.device)
-    pq, sq = _bhsd("q", q)
-    pqo, sqo = _bhsd("q_out", q_out, q.shape, q.dtype)
-    (pk, sk), (pko, sko), (pv, sv), (pvo, svo) = _NO_TENSOR, _NO_TENSOR, _NO_TENSOR, _NO_TENSOR
-    lens, cap, D_v = 0, 0, 0
-    if kv_len is not None:
-        if k is None or k_out is None or (v is None) != (v_out is None):
-            raise ValueError("an append needs k and its cache k_out, and v only with its cache v_out")
-        if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
-            raise ValueError("kv_len must be a contiguous int32 vector of B entries")
-        lens, cap = kv_len.data_ptr(), k_out.shape[2]
-        pko, sko = _bhsd("k_out", k_out, (B, H_kv, cap, D), q.dtype)
-        if v is not None:
-            D_v = v.shape[3]
-            pv, sv = _bhsd("v", v, (B, H_kv, S, D_v), q.dtype)
-            pvo, svo = _bhsd("v_out", v_out, (B, H_kv, cap, D_v), q.dtype)
-    elif v is not None or v_out is not None:
-        raise ValueError("v is appended with kv_len only")
-    elif k is not None:
-        if k_out is None:
-            k_out = _new_rows(B, H_kv, S, D, q.dtype, q.device)
-        pko, sko = _bhsd("k_out", k_out, k.shape, q.dtype)
-    if k is not None:
-        pk, sk = _bhsd("k", k, None, q.dtype)
-    args = _QK_ROPE_ARGS.pack(_QK_ROPE_ARGS.size, B, H, H_kv, S, D, R, code, bool(interleaved), eps is not None, axes,
-                              eps or 0.0, 0, pq, pk, *sq, *sk, qw, kw, fr, pos, *pos_st, pqo, pko, *sqo, *sko, lens,
-                              cap, D_v, pv, pvo, *sv, *svo, axis)
-    rc = load().vt_qk_rope_fwd(args, torch.cuda.current_stream().cuda_stream)
+        q_out = _new_rows(q.shape, q.dtype, q.device)
+    if k_out is None and k is not None:
+        k_out = _new_rows(k.shape, q.dtype, q.device)
+    args = _QK_ROPE_PTRS.pack(_QK_ROPE_BYTES, q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), freqs.data_ptr(),
+                              positions.data_ptr(), q_out.data_ptr(), _ptr(k_out), _ptr(kv_len), _ptr(v),
+                              _ptr(v_out)) + rest
+    rc = load().vt_qk_rope_fwd(args, torch._C._cuda_getCurrentRawStream(q.get_device()))
     if rc != 0:
         raise VtError(rc, "vt_qk_rope_fwd")
     return q_out, k_out
 
 
-@_on_stream
+@functools.lru_cache(maxsize=1024)
+def _rope_bwd_plan(gq, gk, freqs, positions, q, k, q_weight, k_weight, dq, dk, pair_axis, interleaved, eps):
+    """Checks of a qk_rope_bwd call from its tensors' metadata: (packed fixed part of its arguments, strides of dq_out,
+    strides of dk_out)."""
+    if eps is not None and (q is None or (k is None) != (gk is None)):
+        raise ValueError("the norm's gradients need the forward's inputs q and k")
+    # the forward's fields, with dq and dk for its outputs
+    x, y = (q, k) if eps is not None else (gq, gk)
+    if q is not None and tuple(q[0]) != tuple(gq[0]) or k is not None and (gk is None or tuple(k[0]) != tuple(gk[0])):
+        raise ValueError("q and k must have the shapes of dq_out and dk_out")
+    rest = _rope_plan(x, y, freqs, positions, q_weight, k_weight, dq, dk, None, None, None, pair_axis, interleaved, eps)
+    dt, dev = x[2], x[3]
+    sgq = _check("dq_out", gq, dev, dt)
+    sgk = _check("dk_out", gk, dev, dt) if gk is not None else None
+    c3 = ctypes.c_int64 * 3
+    return rest, c3(*sgq), c3(*sgk) if sgk is not None else None
+
+
 def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=None, interleaved: bool = False,
-                eps: float | None = None, q_weight=None, k_weight=None, dq=None, dk=None, workspace=None):
+                eps: float | None = None, q_weight=None, k_weight=None, dq=None, dk=None, workspace=None, stream=None):
     """Gradients of ``qk_rope`` (without the append): see vt_qk_rope_bwd in include/vt_attn.h.  dq_out, dk_out are
     the gradients of its outputs; q, k its inputs (needed with ``eps``).  Returns (dq, dk, dq_weight, dk_weight); the
     weights' gradients are float32 [D], and None without ``eps`` (or, for K's, without dk_out).  ``dq=dq_out`` and
-    ``dk=dk_out`` work in place."""
+    ``dk=dk_out`` work in place.  ``workspace`` may be a preallocated uint8 CUDA tensor of at least
+    ``vt_qk_rope_bwd_workspace_size`` bytes, ``stream`` another stream than the current one."""
+    if stream is not None or not _here(dq_out):
+        return _elsewhere(qk_rope_bwd, dq_out, stream, (dq_out, dk_out, freqs, positions), dict(
+            q=q, k=k, pair_axis=pair_axis, interleaved=interleaved, eps=eps, q_weight=q_weight, k_weight=k_weight,
+            dq=dq, dk=dk, workspace=workspace))
     import torch
-    (B, H, H_kv, S, D, R, axes, qw, kw, fr, pos, pos_st, axis) = _rope_form(dq_out, dk_out, freqs, positions, pair_axis,
-                                                                           q_weight, k_weight)
-    code = _dtype_code(dq_out)
-    _same_place("qk_rope_bwd", dq_out, dk_out, freqs, positions, q, k, q_weight, k_weight, dq, dk, workspace)
+    if pair_axis is not None and type(pair_axis) is not tuple:
+        pair_axis = tuple(pair_axis)
+    rest, sgq, sgk = _rope_bwd_plan(_meta(dq_out), _meta(dk_out), _meta(freqs), _meta(positions), _meta(q), _meta(k),
+                                    _meta(q_weight), _meta(k_weight), _meta(dq), _meta(dk), pair_axis,
+                                    bool(interleaved), eps)
     dt, dev = dq_out.dtype, dq_out.device
-    (pq, sq), (pk, sk), (pdk, sdk), (pgk, sgk) = _NO_TENSOR, _NO_TENSOR, _NO_TENSOR, _NO_TENSOR
     if dq is None:
-        dq = _new_rows(B, H, S, D, dt, dev)
-    pgq, sgq = _bhsd("dq_out", dq_out)
-    pdq, sdq = _bhsd("dq", dq, dq_out.shape, dt)
-    if dk_out is not None:
-        if dk is None:
-            dk = _new_rows(B, H_kv, S, D, dt, dev)
-        pgk, sgk = _bhsd("dk_out", dk_out, None, dt)
-        pdk, sdk = _bhsd("dk", dk, dk_out.shape, dt)
+        dq = _new_rows(dq_out.shape, dt, dev)
+    if dk is None and dk_out is not None:
+        dk = _new_rows(dk_out.shape, dt, dev)
     dqw = dkw = None
-    ws_ptr, ws_bytes = None, 0
+    ws_bytes = 0
+    lib = load()
     if eps is not None:
-        if q is None or (k is None) != (dk_out is None):
-            raise ValueError("the norm's gradients need the forward's inputs q and k")
-        pq, sq = _bhsd("q", q, dq_out.shape, dt)
+        D = dq_out.shape[3]
         dqw = torch.empty(D, dtype=torch.float32, device=dev)
-        if k is not None:
-            pk, sk = _bhsd("k", k, dk_out.shape, dt)
+        if dk_out is not None:
             dkw = torch.empty(D, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = torch.empty(load().vt_qk_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    args = _QK_ROPE_ARGS.pack(_QK_ROPE_ARGS.size, B, H, H_kv, S, D, R, code, bool(interleaved), eps is not None, axes,
-                              eps or 0.0, 0, pq, pk, *sq, *sk, qw, kw, fr, pos, *pos_st, pdq, pdk, *sdq, *sdk, 0, 0, 0,
-                              0, 0, 0, 0, 0, 0, 0, 0, axis)
-    rc = vt_qk_rope_bwd(args, pgq, sgq, pgk, sgk, dqw.data_ptr() if dqw is not None else None,
-                        dkw.data_ptr() if dkw is not None else None, ws_ptr, ws_bytes,
-                        torch.cuda.current_stream().cuda_stream)
+            workspace = torch.empty(lib.vt_qk_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    args = _QK_ROPE_PTRS.pack(_QK_ROPE_BYTES, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), freqs.data_ptr(),
+                              positions.data_ptr(), dq.data_ptr(), _ptr(dk), 0, 0, 0) + rest
+    rc = lib.vt_qk_rope_bwd(args, dq_out.data_ptr(), sgq, _ptr(dk_out), sgk, _ptr(dqw), _ptr(dkw), _ptr(workspace),
+                            ws_bytes, torch._C._cuda_getCurrentRawStream(dq_out.get_device()))
     if rc != 0:
         raise VtError(rc, "vt_qk_rope_bwd")
     return dq, dk, dqw, dkw
@@ -527,75 +570,75 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
 
 # ---------------------------------------------------------------- attention behind a shared prefix
 
-def _kv(name, t, H_kv, S, D, dtype):
-    """(address, strides) of a prefix tensor [H_kv, S, D] with its last dimension contiguous."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-        raise ValueError(f"{name} must be [H_kv, S, D] with the last dimension contiguous")
-    if t.shape != (H_kv, S, D):
-        raise ValueError(f"{name} must have shape {(H_kv, S, D)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr(), t.stride()[:2]
-
-
-@_on_stream
-def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, scale: float | None = None,
-                    return_lse: bool = False, out=None, lse=None, workspace=None):
-    """Attention of q [B,H,S_q,D_qk] over a prefix that all sequences share, k_prefix [H_kv,S_p,D_qk] and v_prefix
-    [H_kv,S_p,D_v], and over each sequence's own cache, k_cache [B,H_kv,S_c,D_qk] and v_cache [B,H_kv,S_c,D_v], up to
-    its length kv_len (int32 [B], counting these S_q tokens; None: S_c): see vt_attn_fwd_prefix in include/vt_attn.h.
-    Prefix or cache may be None.  Returns O, or (O, LSE) with ``return_lse``.  ``workspace`` may be a preallocated
-    uint8 CUDA tensor of at least ``vt_attn_prefix_workspace_size`` bytes; ``stream`` may name another stream than the
-    current one."""
+@functools.lru_cache(maxsize=1024)
+def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, scale):
+    """Checks of an attn_fwd_prefix call from its tensors' metadata: (packed fixed part of its arguments, shape of O,
+    bytes of workspace)."""
     import torch
-    B, H, S_q, D_qk = q.shape
+    q_shape, _, dt, dev = q
+    code = VT_BF16 if dt == torch.bfloat16 else VT_F32 if dt == torch.float32 else None
+    if code is None:
+        raise TypeError(f"attn_fwd_prefix supports bfloat16 and float32 tensors, got {dt}")
     if (k_prefix is None) != (v_prefix is None) or (k_cache is None) != (v_cache is None):
         raise ValueError("K and V of the prefix, and of the cache, come together")
     if k_prefix is None and k_cache is None:
         raise ValueError("a prefix or a cache is required")
+    sq = _check("q", q, dev, dt)
+    B, H, S_q, D_qk = q_shape
     some_k, some_v = (k_prefix, v_prefix) if k_prefix is not None else (k_cache, v_cache)
-    H_kv, D_v = some_k.shape[-3], some_v.shape[-1]
-    code, dt = _dtype_code(q), q.dtype
-    _same_place("attn_fwd_prefix", q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, workspace)
+    if len(some_k[0]) < 3 or len(some_v[0]) < 3:
+        raise ValueError("the prefix is [H_kv, S, D] and the cache [B, H_kv, S, D]")
+    H_kv, D_v = some_k[0][-3], some_v[0][-1]
+    S_p = S_c = 0
+    skp = svp = (0, 0)
+    skc = svc = _NO3
+    if k_prefix is not None:
+        S_p = k_prefix[0][-2]
+        skp = _check("k_prefix", k_prefix, dev, dt, (H_kv, S_p, D_qk), 3)
+        svp = _check("v_prefix", v_prefix, dev, dt, (H_kv, S_p, D_v), 3)
+    if k_cache is not None:
+        S_c = k_cache[0][-2]
+        skc = _check("k_cache", k_cache, dev, dt, (B, H_kv, S_c, D_qk))
+        svc = _check("v_cache", v_cache, dev, dt, (B, H_kv, S_c, D_v))
+    if kv_len is not None:
+        _check_vector("kv_len", kv_len, dev, torch.int32, B)
+    o_shape = (B, H, S_q, D_v)
+    so = _check("out", out, dev, dt, o_shape) if out is not None else _new_strides(o_shape, dt)
+    if lse is not None and (lse[3] != dev or lse[2] != torch.float32 or tuple(lse[0]) != (B, H, S_q) or any(
+            n > 1 and st != want for n, st, want in zip(lse[0], lse[1], (H * S_q, S_q, 1)))):
+        raise ValueError("lse must be a contiguous float32 [B, H, S_q] tensor on the device of the other tensors")
     if scale is None:
         scale = float(D_qk) ** -0.5
-    S_p = S_c = 0
-    pkp = pvp = pkc = pvc = lens = plse = 0
-    skp = svp = (0, 0)
-    skc = svc = (0, 0, 0)
-    pq, sq = _bhsd("q", q)
-    if k_prefix is not None:
-        S_p = k_prefix.shape[1]
-        pkp, skp = _kv("k_prefix", k_prefix, H_kv, S_p, D_qk, dt)
-        pvp, svp = _kv("v_prefix", v_prefix, H_kv, S_p, D_v, dt)
-    if k_cache is not None:
-        S_c = k_cache.shape[2]
-        pkc, skc = _bhsd("k_cache", k_cache, (B, H_kv, S_c, D_qk), dt)
-        pvc, svc = _bhsd("v_cache", v_cache, (B, H_kv, S_c, D_v), dt)
-    if kv_len is not None:
-        if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
-            raise ValueError("kv_len must be a contiguous int32 vector of B entries")
-        lens = kv_len.data_ptr()
+    need = vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code)
+    rest = _ATTN_PREFIX_REST.pack(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code, scale, *sq, *skp, *svp, *skc, *svc, *so)
+    return rest, o_shape, need
+
+
+def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, scale: float | None = None,
+                    return_lse: bool = False, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q [B,H,S_q,D_qk] over a prefix that all sequences share, k_prefix [H_kv,S_p,D_qk] and v_prefix
+    [H_kv,S_p,D_v], and over each sequence's own cache, k_cache [B,H_kv,S_c,D_qk] and v_cache [B,H_kv,S_c,D_v], up to
+    its length kv_len (int32 [B], counting these S_q tokens; None: S_c): see vt_attn_fwd_prefix in include/vt_attn.h.
+    Prefix or cache may be None.  Returns O, or (O, LSE) with ``return_lse``.  ``workspace`` may be a preallocated
+    uint8 CUDA tensor of at least ``vt_attn_prefix_workspace_size`` bytes, ``stream`` another stream than the
+    current one."""
+    if stream is not None or not _here(q):
+        return _elsewhere(attn_fwd_prefix, q, stream, (q, k_prefix, v_prefix, k_cache, v_cache, kv_len), dict(
+            scale=scale, return_lse=return_lse, out=out, lse=lse, workspace=workspace))
+    import torch
+    rest, o_shape, need = _prefix_plan(_meta(q), _meta(k_prefix), _meta(v_prefix), _meta(k_cache), _meta(v_cache),
+                                       _meta(kv_len), _meta(out), _meta(lse), scale)
+    dev = q.device
     if out is None:
-        out = _new_rows(B, H, S_q, D_v, dt, q.device)
-    po, so = _bhsd("out", out, (B, H, S_q, D_v), dt)
+        out = _new_rows(o_shape, q.dtype, dev)
     if return_lse and lse is None:
-        lse = torch.empty((B, H, S_q), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, S_q):
-            raise ValueError("lse must be a contiguous float32 [B, H, S_q] tensor")
-        plse = lse.data_ptr()
-    lib = load()
-    ws_ptr = ws_bytes = 0
-    if workspace is None:
-        need = lib.vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    args = _ATTN_PREFIX_ARGS.pack(_ATTN_PREFIX_ARGS.size, B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code, scale, pq, *sq,
-                                  pkp, pvp, *skp, *svp, pkc, pvc, *skc, *svc, lens, po, *so, plse, ws_ptr, ws_bytes)
-    rc = lib.vt_attn_fwd_prefix(args, torch.cuda.current_stream().cuda_stream)
+        lse = torch.empty(o_shape[:3], dtype=torch.float32, device=dev)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    args = _ATTN_PREFIX_PTRS.pack(_ATTN_PREFIX_BYTES, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(kv_len), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size()) + rest
+    rc = load().vt_attn_fwd_prefix(args, torch._C._cuda_getCurrentRawStream(q.get_device()))
     if rc != 0:
         raise VtError(rc, "vt_attn_fwd_prefix")
     return (out, lse) if return_lse else out

@@ -6,9 +6,13 @@
 //     elements they pair with, so a rotation needs no other thread and the norm's mean is a shuffle over tpr
 //     lanes.  A thread keeps its token and its columns for every head it works on, so the cosines and sines
 //     of its pairs live in registers.
-//   - A block owns `tok` consecutive tokens (about one angle per thread) and walks over their heads.  The
-//     angles are formed once per token and pair, in fp64 and reduced to (-1, 1] half turns before they are
-//     rounded to fp32: fp32 products lose the phase of positions beyond a few thousand.
+//   - A block owns `tok` consecutive tokens (about one angle per thread) and walks over their heads, Q's and then
+//     K's, with the next rows' loads in flight while it works on the current ones (kAhead rows a thread): one row per
+//     thread keeps too few bytes in flight to cover the memory's latency.
+//   - Angles are formed once per token and pair as 64-bit fixed-point fractions of a turn: the position times the
+//     frequency in turns, whose overflow is the reduction by whole turns.  fp32 products lose the phase of
+//     positions beyond a few thousand, and fp64 ones keep the (slow) fp64 pipe busy for longer than the loads take
+//     when few heads share a token.
 //   - VEC is 16 bytes when R and D allow it, else 8 bytes or single elements.
 #pragma once
 
@@ -22,7 +26,8 @@ namespace rope {
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
 constexpr int kMaxD = 256;
-constexpr int kBwdMaxBlocks = 608;  // blocks of a backward launch: 4 per SM, each leaves one partial weight gradient
+constexpr int kBwdMaxBlocks = 608;  // blocks of a backward launch, each leaves one partial weight gradient
+constexpr int kAhead = 2;           // rows a thread has in flight besides the current one
 
 struct Params {
     int B, H, H_kv, S, D, half;  // half = R / 2
@@ -37,7 +42,8 @@ struct Params {
     long long y_st[2][3];
     const void *g[2];            // backward: gradients of the outputs
     long long g_st[2][3];
-    float *part[2];              // backward: partial weight gradients [blocks][D], or null
+    float *part[2];              // backward: partial weight gradients [blocks of the tensor][D], or null
+    int blocks_q;                // backward: the first blocks work on Q, the others on K
     const float *freqs;
     const int *pos;
     long long pos_st[3];
@@ -51,25 +57,52 @@ struct Params {
     uint8_t axis[kMaxPairs];
 };
 
-template <typename T>
-struct Cvt;
-template <>
-struct Cvt<float> {
-    __device__ static float in(float x) { return x; }
-    __device__ static float out(float x) { return x; }
-};
 struct bf16 {
     uint16_t u;
 };
-template <>
-struct Cvt<bf16> {
-    __device__ static float in(bf16 x) { return __uint_as_float(static_cast<uint32_t>(x.u) << 16); }
-    __device__ static bf16 out(float x) { return {static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xFFFFu)}; }
-};
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
-    T e[N];
+// A run of VEC elements as 32-bit words (single bf16 elements in the low half of one).
+template <typename T, int VEC>
+struct Run {
+    static constexpr int kBytes = VEC * sizeof(T), kWords = kBytes < 4 ? 1 : kBytes / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (kBytes == 16) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (kBytes == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kBytes == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t *>(p) = w[0];
+        else *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+    // elements i and i + 1 (i even; with VEC = 1 the first alone)
+    __device__ __forceinline__ void set2(int i, float a, float b) {
+        if constexpr (sizeof(T) == 4) {
+            w[i] = __float_as_uint(a);
+            if constexpr (VEC > 1) w[i + 1] = __float_as_uint(b);
+        } else {
+            w[i >> 1] = pack_bf16x2(a, b);
+        }
+    }
 };
 
 // The 2 VEC elements of chunk c: the two runs of VEC elements they occupy start at first() and second(), and
@@ -94,64 +127,75 @@ struct Chunk {
     __device__ int pair() const { return INTER ? a / 2 : a; }
 };
 
+// A chunk as it lies in memory.
+template <typename T, int VEC>
+struct Raw {
+    Run<T, VEC> lo, hi;
+};
+template <typename T, int VEC, bool INTER>
+__device__ __forceinline__ void load_raw(Raw<T, VEC> &r, const T *row, const Chunk<VEC, INTER> &ch, int D) {
+    r.lo.load(row + ch.a);
+    if (VEC > 1 || ch.b < D) r.hi.load(row + ch.b);  // (in single elements an odd D ends inside a chunk)
+    else r.hi.zero();
+}
 // x[i] and x[VEC + i] are the members of pair i for i < VEC.
 template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void load_chunk(const T *row, const Chunk<VEC, INTER> &ch, int D, float (&x)[2 * VEC]) {
-    Vec<T, VEC> lo, hi;
-    if (VEC == 1) {  // single elements: an odd D ends inside a chunk
-        lo.e[0] = row[ch.a];
-        hi.e[0] = ch.b < D ? row[ch.b] : T{};
-    } else {
-        lo = *reinterpret_cast<const Vec<T, VEC> *>(row + ch.a);
-        hi = *reinterpret_cast<const Vec<T, VEC> *>(row + ch.b);
-    }
+__device__ __forceinline__ void unpack(const Raw<T, VEC> &r, float (&x)[2 * VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         if (INTER) {
-            x[i] = Cvt<T>::in(2 * i < VEC ? lo.e[2 * i] : hi.e[2 * i - VEC]);
-            x[VEC + i] = Cvt<T>::in(2 * i + 1 < VEC ? lo.e[2 * i + 1] : hi.e[2 * i + 1 - VEC]);
+            x[i] = 2 * i < VEC ? r.lo.get(2 * i) : r.hi.get(2 * i - VEC);
+            x[VEC + i] = 2 * i + 1 < VEC ? r.lo.get(2 * i + 1) : r.hi.get(2 * i + 1 - VEC);
         } else {
-            x[i] = Cvt<T>::in(lo.e[i]);
-            x[VEC + i] = Cvt<T>::in(hi.e[i]);
+            x[i] = r.lo.get(i);
+            x[VEC + i] = r.hi.get(i);
         }
     }
 }
-
 template <typename T, int VEC, bool INTER>
 __device__ __forceinline__ void store_chunk(T *row, const Chunk<VEC, INTER> &ch, int D, const float (&x)[2 * VEC]) {
-    Vec<T, VEC> lo, hi;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        if (INTER) {
-            (2 * i < VEC ? lo.e[2 * i] : hi.e[2 * i - VEC]) = Cvt<T>::out(x[i]);
-            (2 * i + 1 < VEC ? lo.e[2 * i + 1] : hi.e[2 * i + 1 - VEC]) = Cvt<T>::out(x[VEC + i]);
-        } else {
-            lo.e[i] = Cvt<T>::out(x[i]);
-            hi.e[i] = Cvt<T>::out(x[VEC + i]);
-        }
-    }
-    if (VEC == 1) {
-        row[ch.a] = lo.e[0];
-        if (ch.b < D) row[ch.b] = hi.e[0];
+    Run<T, VEC> lo, hi;
+    if constexpr (VEC == 1) {
+        lo.set2(0, x[0], 0.0f);
+        hi.set2(0, x[1], 0.0f);
+        lo.store(row + ch.a);
+        if (ch.b < D) hi.store(row + ch.b);
     } else {
-        *reinterpret_cast<Vec<T, VEC> *>(row + ch.a) = lo;
-        *reinterpret_cast<Vec<T, VEC> *>(row + ch.b) = hi;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            if (INTER) {
+                lo.set2(i, x[i / 2], x[VEC + i / 2]);
+                hi.set2(i, x[VEC / 2 + i / 2], x[VEC + VEC / 2 + i / 2]);
+            } else {
+                lo.set2(i, x[i], x[i + 1]);
+                hi.set2(i, x[VEC + i], x[VEC + i + 1]);
+            }
+        }
+        lo.store(row + ch.a);
+        hi.store(row + ch.b);
     }
 }
 
-// cos and sin of every (token, pair) of the block's tokens, [tok][half].
-__device__ __forceinline__ void block_angles(const Params &p, long long t0, float2 *cs) {
+// The frequency of pair j as a fraction of a turn per position, in units of 2^-64 turns.
+__device__ __forceinline__ unsigned long long turns_of(const Params &p, int j) {
+    const double t = static_cast<double>(p.freqs[j]) * 0.15915494309189533577;  // 1 / (2 pi)
+    return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+
+// cos and sin of every (token, pair) of the block's tokens, [tok][half]; `turns` holds turns_of every pair.
+__device__ __forceinline__ void block_angles(const Params &p, long long t0, const unsigned long long *turns, float2 *cs) {
     const int n = p.tok * p.half;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const int tl = i / p.half, j = i - tl * p.half;
         const long long t = t0 + tl;
         if (t >= p.tokens) continue;
-        const long long b = t / p.S, s = t - b * p.S;
+        const int b = static_cast<int>(t / p.S), s = static_cast<int>(t - static_cast<long long>(b) * p.S);
         const int pos = p.pos[p.axis[j] * p.pos_st[0] + b * p.pos_st[1] + s * p.pos_st[2]];
-        double turn = static_cast<double>(pos) * static_cast<double>(p.freqs[j]) * 0.31830988618379067154;
-        turn -= 2.0 * rint(0.5 * turn);
+        // the product modulo 2^64 is the angle modulo a turn; its high word, read as signed, is in half turns
+        const unsigned long long phase = turns[j] * static_cast<unsigned long long>(static_cast<long long>(pos));
+        const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
         float sn, cn;
-        sincospif(static_cast<float>(turn), &sn, &cn);
+        sincospif(half_turns, &sn, &cn);
         cs[i] = make_float2(cn, sn);
     }
 }
@@ -164,12 +208,10 @@ __device__ __forceinline__ float row_sum(float v, int tpr) {
 
 // NC: chunks per thread (4 covers D = 256 in single elements).
 template <typename T, int VEC, int NC, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(const Params p) {
-    extern __shared__ float2 cs[];
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 1) fwd_kernel(const __grid_constant__ Params p) {
+    extern __shared__ float2 cs[];  // [tok][half], then turns_of every pair
+    unsigned long long *turns = reinterpret_cast<unsigned long long *>(cs + p.tok * p.half);
     const long long t0 = static_cast<long long>(blockIdx.x) * p.tok;
-    block_angles(p, t0, cs);
-    __syncthreads();
-
     const int per_head = p.tpr * p.tok;
     const int hs = threadIdx.x / per_head;
     const int r = threadIdx.x - hs * per_head;
@@ -177,8 +219,35 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Params p) {
     const long long t = t0 + tl;
     // (threads without a row take part in the shuffles of the norm)
     const bool live = hs < p.heads && t < p.tokens;
-    const long long b = live ? t / p.S : 0, s = live ? t - b * p.S : 0;
+    const int b = live ? static_cast<int>(t / p.S) : 0;
+    const int s = live ? static_cast<int>(t - static_cast<long long>(b) * p.S) : 0;
+    const int all_heads = p.H + p.H_kv;
 
+    const T *q0 = static_cast<const T *>(p.x[0]) + b * p.x_st[0][0] + s * p.x_st[0][2];
+    const T *k0 = static_cast<const T *>(p.x[1]) + b * p.x_st[1][0] + s * p.x_st[1][2];
+    // row h of this token: Q's heads, then K's
+    auto load_row = [&](int h, Raw<T, VEC> (&raw)[NC]) {
+        const bool on = live && h < all_heads;
+        const T *row = h < p.H ? q0 + h * p.x_st[0][1] : k0 + (h - p.H) * p.x_st[1][1];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (on && lane_c + c * p.tpr < p.chunks) {
+                load_raw<T, VEC, INTER>(raw[c], row, Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D);
+            } else {
+                raw[c].lo.zero();
+                raw[c].hi.zero();
+            }
+        }
+    };
+    constexpr int kDepth = NC == 1 ? kAhead : 1;
+    Raw<T, VEC> ahead[kDepth][NC];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load_row(hs + i * p.heads, ahead[i]);
+
+    for (int j = threadIdx.x; j < p.half; j += kThreads) turns[j] = turns_of(p, j);
+    __syncthreads();
+    block_angles(p, t0, turns, cs);
+    __syncthreads();
     float2 ang[NC][VEC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -196,61 +265,53 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Params p) {
         write_kv = row_kv >= 0 && row_kv < p.cap;
         if (row_kv >= p.cap && lane_c == 0 && hs == 0) atomicOr(p.status, kStatusBounds);
     }
+    T *qo = static_cast<T *>(p.y[0]) + b * p.y_st[0][0] + s * p.y_st[0][2];
+    T *ko = static_cast<T *>(p.y[1]) + b * p.y_st[1][0] + row_kv * p.y_st[1][2];
 
+    for (int h0 = 0; h0 < all_heads; h0 += p.heads) {
+        const int h = h0 + hs;
+        const bool is_q = h < p.H;
+        float x[NC][2 * VEC];
+        float ss = 0.0f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const int heads = which ? p.H_kv : p.H;
-        const T *x0 = static_cast<const T *>(p.x[which]) + b * p.x_st[which][0] + s * p.x_st[which][2];
-        T *y0 = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + (which ? row_kv : s) * p.y_st[which][2];
-        float w[NC][2 * VEC];
-        if (NORM) {
-            const T *wp = static_cast<const T *>(p.w[which]);
+        for (int c = 0; c < NC; ++c) {
+            unpack<T, VEC, INTER>(ahead[0][c], x[c]);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const bool in = lane_c + c * p.tpr < p.chunks;
-                const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                if (wp && in) {
-                    load_chunk<T, VEC, INTER>(wp, ch, p.D, w[c]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) w[c][i] = 1.0f;
-                }
-            }
+            for (int i = 0; i < 2 * VEC; ++i) ss = fmaf(x[c][i], x[c][i], ss);
         }
-        for (int h0 = 0; h0 < heads; h0 += p.heads) {
-            const int h = h0 + hs;
-            const bool on = live && h < heads;
-            float x[NC][2 * VEC];
-            float ss = 0.0f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                if (on && lane_c + c * p.tpr < p.chunks) {
-                    load_chunk<T, VEC, INTER>(x0 + h * p.x_st[which][1], ch, p.D, x[c]);
-                } else {
+        for (int i = 0; i + 1 < kDepth; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[c][i] = 0.0f;
+            for (int c = 0; c < NC; ++c) ahead[i][c] = ahead[i + 1][c];
+        load_row(h + kDepth * p.heads, ahead[kDepth - 1]);
+        float rs = 1.0f;
+        if (NORM) rs = rsqrtf(row_sum(ss, p.tpr) / static_cast<float>(p.D) + p.eps);
+        if (!(live && h < all_heads && (is_q || write_kv))) continue;
+        T *row = is_q ? qo + h * p.y_st[0][1] : ko + (h - p.H) * p.y_st[1][1];
+        const T *wp = static_cast<const T *>(is_q ? p.w[0] : p.w[1]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (lane_c + c * p.tpr >= p.chunks) continue;
+            const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
+            if (NORM) {
+                if (wp) {
+                    Raw<T, VEC> raw;
+                    float w[2 * VEC];
+                    load_raw<T, VEC, INTER>(raw, wp, ch, p.D);
+                    unpack<T, VEC, INTER>(raw, w);
+#pragma unroll
+                    for (int i = 0; i < 2 * VEC; ++i) x[c][i] *= w[i];
                 }
 #pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) ss = fmaf(x[c][i], x[c][i], ss);
+                for (int i = 0; i < 2 * VEC; ++i) x[c][i] *= rs;
             }
-            float rs = 1.0f;
-            if (NORM) rs = rsqrtf(row_sum(ss, p.tpr) / static_cast<float>(p.D) + p.eps);
-            if (!(which ? on && write_kv : on)) continue;
+            float y[2 * VEC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                if (lane_c + c * p.tpr >= p.chunks) continue;
-                const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                float y[2 * VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float u = NORM ? x[c][i] * rs * w[c][i] : x[c][i];
-                    const float v = NORM ? x[c][VEC + i] * rs * w[c][VEC + i] : x[c][VEC + i];
-                    y[i] = u * ang[c][i].x - v * ang[c][i].y;
-                    y[VEC + i] = u * ang[c][i].y + v * ang[c][i].x;
-                }
-                store_chunk<T, VEC, INTER>(y0 + h * p.y_st[which][1], ch, p.D, y);
+            for (int i = 0; i < VEC; ++i) {
+                y[i] = x[c][i] * ang[c][i].x - x[c][VEC + i] * ang[c][i].y;
+                y[VEC + i] = x[c][i] * ang[c][i].y + x[c][VEC + i] * ang[c][i].x;
             }
+            store_chunk<T, VEC, INTER>(row, ch, p.D, y);
         }
     }
 
@@ -263,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Params p) {
                 const T *src = v0 + h * p.v_st[1] + e;
                 T *dst = o0 + h * p.vo_st[1] + e;
                 if (e + N <= p.D_v) {
-                    *reinterpret_cast<Vec<T, N> *>(dst) = *reinterpret_cast<const Vec<T, N> *>(src);
+                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
                 } else {
                     for (int i = 0; i < p.D_v - e; ++i) dst[i] = src[i];
                 }
@@ -271,35 +332,65 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const Params p) {
     }
 }
 
-// Backward: dx from the gradient's inverse rotation; each block leaves its sum of u z per column (see
-// include/vt_attn.h) in part[which][block], summed in a fixed order.
+// Backward: dx from the gradient's inverse rotation; a block works on Q or on K, so that one set of weight-gradient
+// sums lives in its registers, and leaves its sum of u z per column (see include/vt_attn.h) in its part[], summed in
+// a fixed order.  Both means of a row, of x^2 and of w u x, are taken in one pass of shuffles.
 template <typename T, int VEC, int NC, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const Params p) {
-    extern __shared__ float2 cs[];  // [tok][half], then (weight gradients) float [kThreads / tpr][D] over it
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __grid_constant__ Params p) {
+    extern __shared__ float2 cs[];  // [tok][half], turns_of every pair; then (weight gradients) float [kThreads / tpr][D]
+    unsigned long long *turns = reinterpret_cast<unsigned long long *>(cs + p.tok * p.half);
+    if (NORM) launch_dependents();  // the launch that adds the blocks' sums waits for them
+    const int which = blockIdx.x >= static_cast<unsigned>(p.blocks_q);
+    const int block = static_cast<int>(blockIdx.x) - (which ? p.blocks_q : 0);
+    const int n_blocks = which ? static_cast<int>(gridDim.x) - p.blocks_q : p.blocks_q;
+    const int heads = which ? p.H_kv : p.H;
     const int per_head = p.tpr * p.tok;
     const int hs = threadIdx.x / per_head;
     const int r = threadIdx.x - hs * per_head;
     const int tl = r / p.tpr, lane_c = r - tl * p.tpr;
+    const T *x_base = static_cast<const T *>(p.x[which]), *g_base = static_cast<const T *>(p.g[which]);
+    T *y_base = static_cast<T *>(p.y[which]);
+    const T *wp = static_cast<const T *>(p.w[which]);
 
-    float dw[2][NC][2 * VEC];
+    for (int j = threadIdx.x; j < p.half; j += kThreads) turns[j] = turns_of(p, j);
+    float dw[NC][2 * VEC];
     if (NORM) {
 #pragma unroll
-        for (int which = 0; which < 2; ++which)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) dw[which][c][i] = 0.0f;
+            for (int i = 0; i < 2 * VEC; ++i) dw[c][i] = 0.0f;
     }
 
-    const long long blocks = (p.tokens + p.tok - 1) / p.tok;
-    for (long long tb = blockIdx.x; tb < blocks; tb += gridDim.x) {
-        const long long t0 = tb * p.tok;
-        __syncthreads();  // the previous tokens' angles have been read
-        block_angles(p, t0, cs);
-        __syncthreads();
-        const long long t = t0 + tl;
+    const long long groups = (p.tokens + p.tok - 1) / p.tok;
+    for (long long tb = block; tb < groups; tb += n_blocks) {
+        const long long t = tb * p.tok + tl;
         const bool live = hs < p.heads && t < p.tokens;
-        const long long b = live ? t / p.S : 0, s = live ? t - b * p.S : 0;
+        const int b = live ? static_cast<int>(t / p.S) : 0;
+        const int s = live ? static_cast<int>(t - static_cast<long long>(b) * p.S) : 0;
+        const T *x0 = x_base + b * p.x_st[which][0] + s * p.x_st[which][2];
+        const T *g0 = g_base + b * p.g_st[which][0] + s * p.g_st[which][2];
+        T *y0 = y_base + b * p.y_st[which][0] + s * p.y_st[which][2];
+        Raw<T, VEC> g_next[NC], x_next[NC];
+        auto load_row = [&](int h) {
+            const bool on = live && h < heads;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if (on && lane_c + c * p.tpr < p.chunks) {
+                    const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
+                    load_raw<T, VEC, INTER>(g_next[c], g0 + h * p.g_st[which][1], ch, p.D);
+                    if (NORM) load_raw<T, VEC, INTER>(x_next[c], x0 + h * p.x_st[which][1], ch, p.D);
+                } else {
+                    g_next[c].lo.zero();
+                    g_next[c].hi.zero();
+                    x_next[c].lo.zero();
+                    x_next[c].hi.zero();
+                }
+            }
+        };
+        load_row(hs);
+        __syncthreads();  // the frequencies are there, and the previous tokens' angles have been read
+        block_angles(p, tb * p.tok, turns, cs);
+        __syncthreads();
         float2 ang[NC][VEC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -308,126 +399,115 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Params p) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) ang[c][i] = in ? cs[tl * p.half + ch.pair() + i] : make_float2(1.0f, 0.0f);
         }
+        for (int h0 = 0; h0 < heads; h0 += p.heads) {
+            const int h = h0 + hs;
+            float u[NC][2 * VEC], x[NC][2 * VEC], w[NC][2 * VEC];
+            float ss = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const int heads = which ? p.H_kv : p.H;
-            const T *x0 = static_cast<const T *>(p.x[which]) + b * p.x_st[which][0] + s * p.x_st[which][2];
-            const T *g0 = static_cast<const T *>(p.g[which]) + b * p.g_st[which][0] + s * p.g_st[which][2];
-            T *y0 = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + s * p.y_st[which][2];
-            const T *wp = static_cast<const T *>(p.w[which]);
-            for (int h0 = 0; h0 < heads; h0 += p.heads) {
-                const int h = h0 + hs;
-                const bool on = live && h < heads;
-                float u[NC][2 * VEC], x[NC][2 * VEC];
-                float ss = 0.0f;
+            for (int c = 0; c < NC; ++c) {
+                float g[2 * VEC];
+                unpack<T, VEC, INTER>(g_next[c], g);
+                if (NORM) unpack<T, VEC, INTER>(x_next[c], x[c]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    u[c][i] = g[i] * ang[c][i].x + g[VEC + i] * ang[c][i].y;
+                    u[c][VEC + i] = g[VEC + i] * ang[c][i].x - g[i] * ang[c][i].y;
+                }
+            }
+            load_row(h + p.heads);
+            if (NORM) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                    float g[2 * VEC];
-                    const bool in = on && lane_c + c * p.tpr < p.chunks;
-                    if (in) {
-                        load_chunk<T, VEC, INTER>(g0 + h * p.g_st[which][1], ch, p.D, g);
-                        if (NORM) load_chunk<T, VEC, INTER>(x0 + h * p.x_st[which][1], ch, p.D, x[c]);
+#pragma unroll
+                    for (int i = 0; i < 2 * VEC; ++i) w[c][i] = 1.0f;
+                    if (wp && lane_c + c * p.tpr < p.chunks) {
+                        Raw<T, VEC> raw;
+                        load_raw<T, VEC, INTER>(raw, wp, Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D);
+                        unpack<T, VEC, INTER>(raw, w[c]);
                     }
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        u[c][i] = in ? g[i] * ang[c][i].x + g[VEC + i] * ang[c][i].y : 0.0f;
-                        u[c][VEC + i] = in ? g[VEC + i] * ang[c][i].x - g[i] * ang[c][i].y : 0.0f;
-                    }
-                    if (NORM) {
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; ++i) {
-                            x[c][i] = in ? x[c][i] : 0.0f;
-                            ss = fmaf(x[c][i], x[c][i], ss);
-                        }
+                    for (int i = 0; i < 2 * VEC; ++i) {
+                        ss = fmaf(x[c][i], x[c][i], ss);
+                        dot = fmaf(w[c][i] * u[c][i], x[c][i], dot);
                     }
                 }
-                if (NORM) {
-                    const float rs = rsqrtf(row_sum(ss, p.tpr) / static_cast<float>(p.D) + p.eps);
-                    float dot = 0.0f;
+                for (int o = p.tpr >> 1; o > 0; o >>= 1) {
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                }
+                const float rs = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+                const float mean = dot * rs / static_cast<float>(p.D);  // of w u z
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                        const bool in = lane_c + c * p.tpr < p.chunks;
-                        float w[2 * VEC];
-                        if (wp && in) {
-                            load_chunk<T, VEC, INTER>(wp, ch, p.D, w);
-                        } else {
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
-                            for (int i = 0; i < 2 * VEC; ++i) w[i] = 1.0f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; ++i) {
-                            x[c][i] *= rs;  // z
-                            dw[which][c][i] = fmaf(u[c][i], x[c][i], dw[which][c][i]);
-                            u[c][i] *= w[i];
-                            dot = fmaf(u[c][i], x[c][i], dot);
-                        }
+                    for (int i = 0; i < 2 * VEC; ++i) {
+                        const float z = x[c][i] * rs;
+                        dw[c][i] = fmaf(u[c][i], z, dw[c][i]);
+                        u[c][i] = rs * (w[c][i] * u[c][i] - z * mean);
                     }
-                    const float mean = row_sum(dot, p.tpr) / static_cast<float>(p.D);
+            }
+            if (!(live && h < heads)) continue;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; ++i) u[c][i] = rs * (u[c][i] - x[c][i] * mean);
-                }
-                if (!on) continue;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (lane_c + c * p.tpr >= p.chunks) continue;
-                    const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                    store_chunk<T, VEC, INTER>(y0 + h * p.y_st[which][1], ch, p.D, u[c]);
-                }
+            for (int c = 0; c < NC; ++c) {
+                if (lane_c + c * p.tpr >= p.chunks) continue;
+                store_chunk<T, VEC, INTER>(y0 + h * p.y_st[which][1], Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D, u[c]);
             }
         }
     }
 
-    if (!NORM) return;
+    if (!NORM || !p.part[which]) return;
     // the block's sums: rows of the block (same columns, other tokens and heads) are added in order
     float *sm = reinterpret_cast<float *>(cs);
     const int rows = kThreads / p.tpr;
     const int row = threadIdx.x / p.tpr;
+    __syncthreads();
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (!p.part[which]) continue;
-        __syncthreads();
+    for (int c = 0; c < NC; ++c) {
+        if (lane_c + c * p.tpr >= p.chunks) continue;
+        const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (lane_c + c * p.tpr >= p.chunks) continue;
-            const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int lo = INTER ? ch.a + 2 * i : ch.a + i, hi = INTER ? lo + 1 : ch.b + i;
-                sm[row * p.D + lo] = dw[which][c][i];
-                if (hi < p.D) sm[row * p.D + hi] = dw[which][c][VEC + i];
-            }
+        for (int i = 0; i < VEC; ++i) {
+            const int lo = INTER ? ch.a + 2 * i : ch.a + i, hi = INTER ? lo + 1 : ch.b + i;
+            sm[row * p.D + lo] = dw[c][i];
+            if (hi < p.D) sm[row * p.D + hi] = dw[c][VEC + i];
         }
-        __syncthreads();
-        for (int d = threadIdx.x; d < p.D; d += kThreads) {
-            float acc = 0.0f;
-            for (int k = 0; k < rows; ++k) acc += sm[k * p.D + d];
-            p.part[which][static_cast<long long>(blockIdx.x) * p.D + d] = acc;
-        }
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.D; d += kThreads) {
+        float acc = 0.0f;
+        for (int k = 0; k < rows; ++k) acc += sm[k * p.D + d];
+        p.part[which][static_cast<long long>(block) * p.D + d] = acc;
     }
 }
 
-// Sum of the blocks' partial weight gradients, 32 columns of one tensor per block: 32 rows of threads take
-// every 32nd partial, then the rows are added in order.
-__global__ void __launch_bounds__(1024) bwd_weights_kernel(const float *part_q, const float *part_k, float *dwq,
-                                                           float *dwk, int n, int D) {
-    __shared__ float sm[32][33];
+// Sum of the blocks' partial weight gradients, 8 columns of one tensor per block: 64 rows of 8 threads take every
+// 64th partial with all their loads in flight, then the rows are added in order.
+constexpr int kSumRows = 64;
+__global__ void __launch_bounds__(8 * kSumRows) bwd_weights_kernel(const float *part_q, const float *part_k, float *dwq,
+                                                                   float *dwk, int n_q, int n_k, int D) {
+    __shared__ float sm[kSumRows][9];
     const float *part = blockIdx.y ? part_k : part_q;
     float *dw = blockIdx.y ? dwk : dwq;
+    const int n = blockIdx.y ? n_k : n_q;
+    const int lane = threadIdx.x & 7, row = threadIdx.x >> 3;
+    const int d = blockIdx.x * 8 + lane;
+    wait_prerequisites();
     if (!dw) return;
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + lane;
+    float v[(kBwdMaxBlocks + kSumRows - 1) / kSumRows];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof v / sizeof v[0]); ++i) {
+        const int k = row + i * kSumRows;
+        v[i] = d < D && k < n ? part[static_cast<long long>(k) * D + d] : 0.0f;
+    }
     float acc = 0.0f;
-    if (d < D)
-        for (int k = row; k < n; k += 32) acc += part[static_cast<long long>(k) * D + d];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof v / sizeof v[0]); ++i) acc += v[i];
     sm[row][lane] = acc;
     __syncthreads();
     if (row == 0 && d < D) {
         float sum = 0.0f;
-        for (int k = 0; k < 32; ++k) sum += sm[k][lane];
+#pragma unroll 16
+        for (int k = 0; k < kSumRows; ++k) sum += sm[k][lane];
         dw[d] = sum;
     }
 }

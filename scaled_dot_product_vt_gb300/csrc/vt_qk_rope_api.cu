@@ -173,7 +173,7 @@ Params common_params(const Args &a, const Shape &sh, int sms) {
     return p;
 }
 
-using Kern = void (*)(const Params);
+using Kern = void (*)(const Params);  // (the kernels take it as a grid constant)
 
 template <typename T, int VEC, int NC, bool BWD>
 Kern pick_form(bool inter, bool norm) {
@@ -244,7 +244,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.status = info.status + status_slot(stream);
     const long long blocks = (p.tokens + p.tok - 1) / p.tok;
     if (blocks > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
-    pick<false>(a, sh)<<<static_cast<unsigned>(blocks), kThreads, p.tok * p.half * sizeof(float2), stream>>>(p);
+    pick<false>(a, sh)<<<static_cast<unsigned>(blocks), kThreads, (p.tok + 1) * p.half * sizeof(float2), stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
     return env_check() ? read_status(stream) : VT_OK;
 }
@@ -303,21 +303,39 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
         p.g_st[0][i] = a.H > 0 ? gq_st[i] : 0;
         p.g_st[1][i] = a.H_kv > 0 ? gk_st[i] : 0;
     }
-    const long long want = (p.tokens + p.tok - 1) / p.tok;
-    const int blocks = static_cast<int>(want < kBwdMaxBlocks ? want : kBwdMaxBlocks);
+    // blocks for Q and for K in proportion to their rows, two per SM in all (they fit at once)
+    const long long groups = (p.tokens + p.tok - 1) / p.tok;
+    const int most = 2 * info.sms < kBwdMaxBlocks ? 2 * info.sms : kBwdMaxBlocks;
+    auto share = [&](long long heads) -> int {
+        if (heads == 0) return 0;
+        const long long n = (most * heads + p.H + p.H_kv - 1) / (p.H + p.H_kv);
+        return static_cast<int>(groups < n ? groups : n);
+    };
+    const int n_q = share(p.H), n_k = share(p.H_kv);
+    p.blocks_q = n_q;
     float *part = static_cast<float *>(ws);
     p.part[0] = dwq ? part : nullptr;
-    p.part[1] = dwk ? part + static_cast<long long>(blocks) * p.D : nullptr;
-    size_t smem = p.tok * p.half * sizeof(float2);
+    p.part[1] = dwk ? part + static_cast<long long>(kBwdMaxBlocks) * p.D : nullptr;
+    size_t smem = (p.tok + 1) * p.half * sizeof(float2);
     const size_t sums = norm ? static_cast<size_t>(kThreads / p.tpr) * p.D * sizeof(float) : 0;
     if (sums > smem) smem = sums;
-    pick<true>(a, sh)<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+    pick<true>(a, sh)<<<static_cast<unsigned>(n_q + n_k), kThreads, smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
-    if (weights) {
-        bwd_weights_kernel<<<dim3((p.D + 31) / 32, 2), 1024, 0, stream>>>(p.part[0], p.part[1], dwq, dwk, blocks, p.D);
-        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
-    }
-    return VT_OK;
+    if (!weights) return VT_OK;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((p.D + 7) / 8, 2);
+    cfg.blockDim = dim3(8 * kSumRows);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float *part_q = p.part[0], *part_k = p.part[1];
+    const int D = p.D;
+    if (cudaLaunchKernelEx(&cfg, bwd_weights_kernel, part_q, part_k, dwq, dwk, n_q, n_k, D) != cudaSuccess)
+        return VT_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
 }  // namespace

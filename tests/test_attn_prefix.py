@@ -21,15 +21,15 @@ A = 1 << 24  # fake, aligned, distinct "device" addresses: never dereferenced on
 # ---------------------------------------------------------------- refusals (no GPU)
 
 def pack(**kw):
-    f = dict(size=vt._ATTN_PREFIX_ARGS.size, B=2, H=4, H_kv=2, S_q=3, S_p=40, S_c=24, D_qk=16, D_v=8, dtype=vt.VT_BF16,
+    f = dict(size=vt._ATTN_PREFIX_BYTES, B=2, H=4, H_kv=2, S_q=3, S_p=40, S_c=24, D_qk=16, D_v=8, dtype=vt.VT_BF16,
              scale=0.25, q=A, qs=(192, 48, 16), kp=2 * A, vp=3 * A, kps=(640, 16), vps=(320, 8), kc=4 * A, vc=5 * A,
              kcs=(768, 384, 16), vcs=(384, 192, 8), lens=6 * A, o=7 * A, os=(96, 24, 8), lse=8 * A, ws=9 * A,
              wsb=1 << 23)
     f.update(kw)
-    return vt._ATTN_PREFIX_ARGS.pack(f["size"], f["B"], f["H"], f["H_kv"], f["S_q"], f["S_p"], f["S_c"], f["D_qk"],
-                                     f["D_v"], f["dtype"], f["scale"], f["q"], *f["qs"], f["kp"], f["vp"], *f["kps"],
-                                     *f["vps"], f["kc"], f["vc"], *f["kcs"], *f["vcs"], f["lens"], f["o"], *f["os"],
-                                     f["lse"], f["ws"], f["wsb"])
+    return vt._ATTN_PREFIX_PTRS.pack(f["size"], f["q"], f["kp"], f["vp"], f["kc"], f["vc"], f["lens"], f["o"], f["lse"],
+                                     f["ws"], f["wsb"]) + vt._ATTN_PREFIX_REST.pack(
+        f["B"], f["H"], f["H_kv"], f["S_q"], f["S_p"], f["S_c"], f["D_qk"], f["D_v"], f["dtype"], f["scale"], *f["qs"],
+        *f["kps"], *f["vps"], *f["kcs"], *f["vcs"], *f["os"])
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -24,16 +24,16 @@ A = 1 << 24  # fake, aligned, distinct "device" addresses: never dereferenced on
 
 def pack(**kw):
     """A valid two-head call, with fields replaced."""
-    f = dict(size=vt._QK_ROPE_ARGS.size, B=2, H=2, H_kv=1, S=4, D=16, R=16, dtype=vt.VT_BF16, inter=0, norm=1, axes=1,
+    f = dict(size=vt._QK_ROPE_BYTES, B=2, H=2, H_kv=1, S=4, D=16, R=16, dtype=vt.VT_BF16, inter=0, norm=1, axes=1,
              eps=1e-6, reserved=0, q=A, k=2 * A, qs=(128, 64, 16), ks=(64, 64, 16), qw=3 * A, kw=4 * A, freqs=5 * A,
              pos=6 * A, ps=(8, 4, 1), qo=7 * A, ko=8 * A, qos=(128, 64, 16), kos=(64, 64, 16), lens=0, cap=0, D_v=0,
              v=0, vo=0, vs=(0, 0, 0), vos=(0, 0, 0), axis=bytes(128))
     f.update(kw)
-    return vt._QK_ROPE_ARGS.pack(f["size"], f["B"], f["H"], f["H_kv"], f["S"], f["D"], f["R"], f["dtype"], f["inter"],
-                                 f["norm"], f["axes"], f["eps"], f["reserved"], f["q"], f["k"], *f["qs"], *f["ks"],
-                                 f["qw"], f["kw"], f["freqs"], f["pos"], *f["ps"], f["qo"], f["ko"], *f["qos"],
-                                 *f["kos"], f["lens"], f["cap"], f["D_v"], f["v"], f["vo"], *f["vs"], *f["vos"],
-                                 f["axis"])
+    return vt._QK_ROPE_PTRS.pack(f["size"], f["q"], f["k"], f["qw"], f["kw"], f["freqs"], f["pos"], f["qo"], f["ko"],
+                                 f["lens"], f["v"], f["vo"]) + vt._QK_ROPE_REST.pack(
+        f["B"], f["H"], f["H_kv"], f["S"], f["D"], f["R"], f["cap"], f["D_v"], f["dtype"], f["inter"], f["norm"],
+        f["axes"], f["eps"], f["reserved"], *f["qs"], *f["ks"], *f["qos"], *f["kos"], *f["vs"], *f["vos"], *f["ps"],
+        f["axis"])
 
 
 def bwd(**kw):
