@@ -304,7 +304,7 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
  *   positions     int32, element strides pos_stride over (axis, b, s), 0 allowed (one row for the whole batch)
  * Strides, dtypes, alignment and their errors are those of vt_attn_fwd_strided (16-byte rule; the stride of an
  * index with one value is not looked at, and an append's K and V outputs count `cap` rows); D <= 256 and
- * D_v <= 256, at most 4 axes.  eps must be finite and not negative.  B or S equal to 0 is a valid empty
+ * D_v <= 256, at most 4 axes, B * S at most 2^30.  eps must be finite and not negative.  B or S equal to 0 is a valid empty
  * problem.
  */
 #define VT_ROPE_MAX_AXES 4

@@ -6,9 +6,10 @@
 //     elements they pair with, so a rotation needs no other thread and the norm's mean is a shuffle over tpr
 //     lanes.  A thread keeps its token and its columns for every head it works on, so the cosines and sines
 //     of its pairs live in registers.
-//   - A block owns `tok` consecutive tokens (about one angle per thread) and walks over their heads, Q's and then
-//     K's, with the next rows' loads in flight while it works on the current ones (kAhead rows a thread): one row per
-//     thread keeps too few bytes in flight to cover the memory's latency.
+//   - A block walks over groups of `tok` consecutive tokens (about one angle per thread) and their heads, Q's and then
+//     K's.  The rows come through a ring in shared memory that every thread fills and reads for itself (cp.async, no
+//     barrier), several rows ahead and across groups: bytes in flight are what this kernel lives on, and registers
+//     hold too few of them.
 //   - Angles are formed once per token and pair as 64-bit fixed-point fractions of a turn: the position times the
 //     frequency in turns, whose overflow is the reduction by whole turns.  fp32 products lose the phase of
 //     positions beyond a few thousand, and fp64 ones keep the (slow) fp64 pipe busy for longer than the loads take
@@ -26,14 +27,14 @@ namespace rope {
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
 constexpr int kMaxD = 256;
+constexpr int kAhead = 6, kAheadBwd = 4;  // rows a thread has under way (32 bytes each, the backward's 64)
 constexpr int kBwdMaxBlocks = 608;  // blocks of a backward launch, each leaves one partial weight gradient
-constexpr int kAhead = 2;           // rows a thread has in flight besides the current one
 
 struct Params {
     int B, H, H_kv, S, D, half;  // half = R / 2
     int tpr, tok, heads;         // threads per row, tokens per block, heads a block works on at once
     int chunks;                  // chunks of 2 VEC elements in a row
-    long long tokens;            // B * S
+    unsigned tokens;             // B * S
     float eps;
     const void *x[2];            // q, k
     long long x_st[2][3];
@@ -90,6 +91,16 @@ struct Run {
         else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t *>(p) = w[0];
         else *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
     }
+    // a copy of the run on its way to shared memory, and from there
+    __device__ static __forceinline__ void fetch(uint32_t dst, const T *p) {
+        if constexpr (kBytes == 16)
+            cp_async16(dst, p, 16);
+        else if constexpr (kBytes >= 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(kBytes) : "memory");
+        else
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(*reinterpret_cast<const uint16_t *>(p)) : "memory");
+    }
+    __device__ __forceinline__ void take(const uint8_t *staged) { load(reinterpret_cast<const T *>(staged)); }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
@@ -123,58 +134,99 @@ struct Chunk {
             b = turn ? a + p.half : a + VEC;
         }
     }
-    // pair index of the chunk's first pair
-    __device__ int pair() const { return INTER ? a / 2 : a; }
 };
 
 // A chunk as it lies in memory.
 template <typename T, int VEC>
 struct Raw {
     Run<T, VEC> lo, hi;
+
+    __device__ __forceinline__ void zero() {
+        lo.zero();
+        hi.zero();
+    }
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void load_raw(Raw<T, VEC> &r, const T *row, int a, int b, int D) {
+    r.lo.load(row + a);
+    if (VEC > 1 || b < D) r.hi.load(row + b);  // (in single elements an odd D ends inside a chunk)
+}
+
+// The ring: `kRuns` runs of a row per thread and stage, each thread's side by side with its neighbours'.
+template <typename T, int VEC, int kRuns, int kStages>
+struct Ring {
+    static constexpr int kBytes = Run<T, VEC>::kBytes;
+    static constexpr int kStage = kRuns * kThreads * kBytes;
+    uint8_t *mine;
+    uint32_t mine_s;
+    int put = 0, got = 0;  // stages to fill and to read next
+
+    __device__ Ring(uint8_t *smem) : mine(smem + threadIdx.x * kBytes), mine_s(smem_u32(smem) + threadIdx.x * kBytes) {}
+    __device__ __forceinline__ void fetch(int run, const T *p) {
+        Run<T, VEC>::fetch(mine_s + put * kStage + run * kThreads * kBytes, p);
+    }
+    __device__ __forceinline__ void pushed() {
+        cp_async_commit();
+        if (++put == kStages) put = 0;
+    }
+    __device__ __forceinline__ void take(int run, Run<T, VEC> &r) const {
+        r.take(mine + got * kStage + run * kThreads * kBytes);
+    }
+    __device__ __forceinline__ void popped() {
+        if (++got == kStages) got = 0;
+    }
+};
+
+// The chunk's pairs two by two, for arithmetic on both at once: a[j], b[j] hold the first and the second members of
+// pairs 2 j and 2 j + 1 (VEC = 1: of its one pair, and 0).
+template <int VEC>
+struct Pairs {
+    static constexpr int kN = VEC > 1 ? VEC / 2 : 1;
+    float2 a[kN], b[kN];
 };
 template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void load_raw(Raw<T, VEC> &r, const T *row, const Chunk<VEC, INTER> &ch, int D) {
-    r.lo.load(row + ch.a);
-    if (VEC > 1 || ch.b < D) r.hi.load(row + ch.b);  // (in single elements an odd D ends inside a chunk)
-    else r.hi.zero();
-}
-// x[i] and x[VEC + i] are the members of pair i for i < VEC.
-template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void unpack(const Raw<T, VEC> &r, float (&x)[2 * VEC]) {
+__device__ __forceinline__ void unpack(const Raw<T, VEC> &r, Pairs<VEC> &x) {
+    if constexpr (VEC == 1) {
+        x.a[0] = make_float2(r.lo.get(0), 0.0f);
+        x.b[0] = make_float2(r.hi.get(0), 0.0f);
+    } else {
+        auto at = [&](int i) { return i < VEC ? r.lo.get(i) : r.hi.get(i - VEC); };  // the chunk's elements in order
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        if (INTER) {
-            x[i] = 2 * i < VEC ? r.lo.get(2 * i) : r.hi.get(2 * i - VEC);
-            x[VEC + i] = 2 * i + 1 < VEC ? r.lo.get(2 * i + 1) : r.hi.get(2 * i + 1 - VEC);
-        } else {
-            x[i] = r.lo.get(i);
-            x[VEC + i] = r.hi.get(i);
+        for (int j = 0; j < VEC / 2; ++j) {
+            x.a[j] = INTER ? make_float2(at(4 * j), at(4 * j + 2)) : make_float2(at(2 * j), at(2 * j + 1));
+            x.b[j] = INTER ? make_float2(at(4 * j + 1), at(4 * j + 3)) : make_float2(at(VEC + 2 * j), at(VEC + 2 * j + 1));
         }
     }
 }
 template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void store_chunk(T *row, const Chunk<VEC, INTER> &ch, int D, const float (&x)[2 * VEC]) {
+__device__ __forceinline__ void store_raw(T *row, int a, int b, int D, const Pairs<VEC> &x) {
     Run<T, VEC> lo, hi;
     if constexpr (VEC == 1) {
-        lo.set2(0, x[0], 0.0f);
-        hi.set2(0, x[1], 0.0f);
-        lo.store(row + ch.a);
-        if (ch.b < D) hi.store(row + ch.b);
+        lo.set2(0, x.a[0].x, 0.0f);
+        hi.set2(0, x.b[0].x, 0.0f);
+        lo.store(row + a);
+        if (b < D) hi.store(row + b);
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) {
+        for (int j = 0; j < VEC / 2; ++j) {
             if (INTER) {
-                lo.set2(i, x[i / 2], x[VEC + i / 2]);
-                hi.set2(i, x[VEC / 2 + i / 2], x[VEC + VEC / 2 + i / 2]);
+                Run<T, VEC> &run = 4 * j < VEC ? lo : hi;
+                run.set2(4 * j % VEC, x.a[j].x, x.b[j].x);
+                run.set2(4 * j % VEC + 2, x.a[j].y, x.b[j].y);
             } else {
-                lo.set2(i, x[i], x[i + 1]);
-                hi.set2(i, x[VEC + i], x[VEC + i + 1]);
+                lo.set2(2 * j, x.a[j].x, x.a[j].y);
+                hi.set2(2 * j, x.b[j].x, x.b[j].y);
             }
         }
-        lo.store(row + ch.a);
-        hi.store(row + ch.b);
+        lo.store(row + a);
+        hi.store(row + b);
     }
 }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // The frequency of pair j as a fraction of a turn per position, in units of 2^-64 turns.
 __device__ __forceinline__ unsigned long long turns_of(const Params &p, int j) {
@@ -182,21 +234,81 @@ __device__ __forceinline__ unsigned long long turns_of(const Params &p, int j) {
     return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
 }
 
-// cos and sin of every (token, pair) of the block's tokens, [tok][half]; `turns` holds turns_of every pair.
-__device__ __forceinline__ void block_angles(const Params &p, long long t0, const unsigned long long *turns, float2 *cs) {
-    const int n = p.tok * p.half;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int tl = i / p.half, j = i - tl * p.half;
-        const long long t = t0 + tl;
-        if (t >= p.tokens) continue;
-        const int b = static_cast<int>(t / p.S), s = static_cast<int>(t - static_cast<long long>(b) * p.S);
-        const int pos = p.pos[p.axis[j] * p.pos_st[0] + b * p.pos_st[1] + s * p.pos_st[2]];
+// The tokens t0 .. t0 + tok - 1 of a block, t0 moving on by `step` tokens at a time without a division.
+struct Walk {
+    unsigned t0, b0, s0, step, step_b, step_s;
+
+    __device__ Walk(const Params &p, unsigned first, unsigned step_) : t0(first), step(step_) {
+        b0 = t0 / p.S;
+        s0 = t0 - b0 * p.S;
+        step_b = step / p.S;
+        step_s = step - step_b * p.S;
+    }
+    __device__ __forceinline__ void next(const Params &p) {
+        t0 += step;
+        b0 += step_b;
+        s0 += step_s;
+        if (s0 >= static_cast<unsigned>(p.S)) {
+            s0 -= p.S;
+            ++b0;
+        }
+    }
+    // sequence and position in it of token t0 + i
+    __device__ __forceinline__ void at(const Params &p, int i, unsigned &b, unsigned &s) const {
+        b = b0;
+        s = s0 + i;
+        while (s >= static_cast<unsigned>(p.S)) {
+            s -= p.S;
+            ++b;
+        }
+    }
+};
+
+// One angle per thread (tok * half <= kThreads): thread i forms that of token i / half and pair i % half.
+struct Angle {
+    int tl, j, slot;
+    bool on;
+    long long pos_off;
+    unsigned long long turn;
+
+    // A chunk's `vec` angles lie `half / vec` apart, so that neighbouring threads read neighbouring ones.
+    __device__ Angle(const Params &p, int vec) {
+        tl = threadIdx.x / p.half;
+        j = threadIdx.x - tl * p.half;
+        slot = tl * p.half + j % vec * (p.half / vec) + j / vec;
+        on = tl < p.tok;
+        pos_off = on ? p.axis[j] * p.pos_st[0] : 0;
+        turn = on ? turns_of(p, j) : 0;
+    }
+    __device__ __forceinline__ int position(const Params &p, const Walk &w) const {
+        if (!on || w.t0 + tl >= p.tokens) return 0;
+        unsigned b, s;
+        w.at(p, tl, b, s);
+        return p.pos[pos_off + b * p.pos_st[1] + s * p.pos_st[2]];
+    }
+    // cos and sin into cs[token][pair]
+    __device__ __forceinline__ void form(int pos, float2 *cs) const {
         // the product modulo 2^64 is the angle modulo a turn; its high word, read as signed, is in half turns
-        const unsigned long long phase = turns[j] * static_cast<unsigned long long>(static_cast<long long>(pos));
+        const unsigned long long phase = turn * static_cast<unsigned long long>(static_cast<long long>(pos));
         const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
         float sn, cn;
         sincospif(half_turns, &sn, &cn);
-        cs[i] = make_float2(cn, sn);
+        if (on) cs[slot] = make_float2(cn, sn);
+    }
+};
+
+// cos and sin of the pairs of a chunk (1 and 0 where nothing is rotated), `step` = half / VEC.
+template <int VEC>
+__device__ __forceinline__ void chunk_angles(int chunk, bool in, const float2 *cs, int step, Pairs<VEC> &ang) {
+#pragma unroll
+    for (int j = 0; j < Pairs<VEC>::kN; ++j) {
+        ang.a[j] = both(1.0f);
+        ang.b[j] = both(0.0f);
+        if (in) {
+            const float2 p0 = cs[chunk + 2 * j * step], p1 = VEC > 1 ? cs[chunk + (2 * j + 1) * step] : p0;
+            ang.a[j] = make_float2(p0.x, p1.x);
+            ang.b[j] = make_float2(p0.y, p1.y);
+        }
     }
 }
 
@@ -208,128 +320,193 @@ __device__ __forceinline__ float row_sum(float v, int tpr) {
 
 // NC: chunks per thread (4 covers D = 256 in single elements).
 template <typename T, int VEC, int NC, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 1) fwd_kernel(const __grid_constant__ Params p) {
-    extern __shared__ float2 cs[];  // [tok][half], then turns_of every pair
-    unsigned long long *turns = reinterpret_cast<unsigned long long *>(cs + p.tok * p.half);
-    const long long t0 = static_cast<long long>(blockIdx.x) * p.tok;
+__global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __grid_constant__ Params p) {
+    using P = Pairs<VEC>;
+    __shared__ float2 cs[2][kThreads];  // [tok][half] of this group of tokens and of the next
+    extern __shared__ __align__(16) uint8_t ring_mem[];
+    Ring<T, VEC, 2 * NC, kAhead> ring(ring_mem);
     const int per_head = p.tpr * p.tok;
     const int hs = threadIdx.x / per_head;
     const int r = threadIdx.x - hs * per_head;
     const int tl = r / p.tpr, lane_c = r - tl * p.tpr;
-    const long long t = t0 + tl;
-    // (threads without a row take part in the shuffles of the norm)
-    const bool live = hs < p.heads && t < p.tokens;
-    const int b = live ? static_cast<int>(t / p.S) : 0;
-    const int s = live ? static_cast<int>(t - static_cast<long long>(b) * p.S) : 0;
-    const int all_heads = p.H + p.H_kv;
-
-    const T *q0 = static_cast<const T *>(p.x[0]) + b * p.x_st[0][0] + s * p.x_st[0][2];
-    const T *k0 = static_cast<const T *>(p.x[1]) + b * p.x_st[1][0] + s * p.x_st[1][2];
-    // row h of this token: Q's heads, then K's
-    auto load_row = [&](int h, Raw<T, VEC> (&raw)[NC]) {
-        const bool on = live && h < all_heads;
-        const T *row = h < p.H ? q0 + h * p.x_st[0][1] : k0 + (h - p.H) * p.x_st[1][1];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (on && lane_c + c * p.tpr < p.chunks) {
-                load_raw<T, VEC, INTER>(raw[c], row, Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D);
-            } else {
-                raw[c].lo.zero();
-                raw[c].hi.zero();
-            }
-        }
-    };
-    constexpr int kDepth = NC == 1 ? kAhead : 1;
-    Raw<T, VEC> ahead[kDepth][NC];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) load_row(hs + i * p.heads, ahead[i]);
-
-    for (int j = threadIdx.x; j < p.half; j += kThreads) turns[j] = turns_of(p, j);
-    __syncthreads();
-    block_angles(p, t0, turns, cs);
-    __syncthreads();
-    float2 ang[NC][VEC];
+    const Angle angle(p, VEC);
+    int at_a[NC], at_b[NC];  // where this thread's runs start in a row
+    bool has[NC], turn[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-        const bool in = live && lane_c + c * p.tpr < p.chunks && ch.turn;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ang[c][i] = in ? cs[tl * p.half + ch.pair() + i] : make_float2(1.0f, 0.0f);
+        has[c] = lane_c + c * p.tpr < p.chunks;
+        turn[c] = has[c] && ch.turn;
+        at_a[c] = ch.a;
+        at_b[c] = ch.b;
     }
+    const float inv_d = 1.0f / static_cast<float>(p.D), eps = p.eps;
+    // (copies: the loop's asm statements would have every use of p read again)
+    const int tpr = p.tpr, D = p.D, tokens = static_cast<int>(p.tokens), step_cs = p.half / VEC;
+    const long long q_step = p.heads * p.x_st[0][1], k_step = p.heads * p.x_st[1][1];
+    // A token's rows in rounds: round i takes heads hs + i * p.heads of Q, then the K rounds those of K; the rounds
+    // are the same for every thread of the block (the norm shuffles), some threads have no row in the last ones.
+    const int rounds_q = (p.H + p.heads - 1) / p.heads, rounds = rounds_q + (p.H_kv + p.heads - 1) / p.heads;
+    const int rows_q = hs < p.H ? (p.H - hs + p.heads - 1) / p.heads : 0;
+    const int rows_k = hs < p.H_kv ? (p.H_kv - hs + p.heads - 1) / p.heads : 0;
 
-    // the cache row of this token's K and V: written when 0 <= row < cap
-    long long row_kv = s;
-    bool write_kv = live;
-    if (p.kv_len) {
-        row_kv = live ? static_cast<long long>(p.kv_len[b]) - p.S + s : -1;
-        write_kv = row_kv >= 0 && row_kv < p.cap;
-        if (row_kv >= p.cap && lane_c == 0 && hs == 0) atomicOr(p.status, kStatusBounds);
-    }
-    T *qo = static_cast<T *>(p.y[0]) + b * p.y_st[0][0] + s * p.y_st[0][2];
-    T *ko = static_cast<T *>(p.y[1]) + b * p.y_st[1][0] + row_kv * p.y_st[1][2];
+    const bool row_thread = hs < p.heads;
 
-    for (int h0 = 0; h0 < all_heads; h0 += p.heads) {
-        const int h = h0 + hs;
-        const bool is_q = h < p.H;
-        float x[NC][2 * VEC];
-        float ss = 0.0f;
+    // ---- the loads' own walk over groups and rounds, kAhead rows in front
+    Walk ahead(p, blockIdx.x * p.tok, gridDim.x * p.tok);
+    int ahead_i = 0;
+    bool ahead_live = false;
+    const T *ahead_q = nullptr, *ahead_k = nullptr;
+    auto ahead_group = [&]() {
+        ahead_live = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
+        if (!ahead_live) return;
+        unsigned b, s;
+        ahead.at(p, tl, b, s);
+        ahead_q = static_cast<const T *>(p.x[0]) + b * p.x_st[0][0] + s * p.x_st[0][2] + hs * p.x_st[0][1];
+        ahead_k = static_cast<const T *>(p.x[1]) + b * p.x_st[1][0] + s * p.x_st[1][2] + hs * p.x_st[1][1];
+    };
+    auto fetch = [&]() {
+        const bool k = ahead_i >= rounds_q;
+        const T *row = k ? ahead_k : ahead_q;
+        if (ahead_live && ahead_i < (k ? rounds_q + rows_k : rows_q)) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            unpack<T, VEC, INTER>(ahead[0][c], x[c]);
-#pragma unroll
-            for (int i = 0; i < 2 * VEC; ++i) ss = fmaf(x[c][i], x[c][i], ss);
+            for (int c = 0; c < NC; ++c)
+                if (has[c]) {
+                    ring.fetch(2 * c, row + at_a[c]);
+                    if (VEC > 1 || at_b[c] < D) ring.fetch(2 * c + 1, row + at_b[c]);
+                }
         }
+        ring.pushed();
+        if (k) ahead_k = row + k_step;
+        else ahead_q = row + q_step;
+        if (++ahead_i == rounds) {
+            ahead_i = 0;
+            ahead.next(p);
+            ahead_group();
+        }
+    };
+    Walk walk = ahead;
+    ahead_group();
+    int pos_next = angle.position(p, walk);
+#pragma unroll 1
+    for (int i = 0; i < kAhead - 1; ++i) fetch();
+    angle.form(pos_next, cs[0]);
+    Walk after = walk;
+    after.next(p);
+    pos_next = after.t0 < p.tokens ? angle.position(p, after) : 0;
+
+    for (int group = 0; walk.t0 < p.tokens; walk.next(p), ++group) {
+        __syncthreads();  // this group's angles are there, and the previous group's have been read
+        if (after.t0 < p.tokens) {
+            angle.form(pos_next, cs[(group + 1) & 1]);
+            after.next(p);
+            if (after.t0 < p.tokens) pos_next = angle.position(p, after);
+        }
+        // (threads without a row take part in the shuffles of the norm)
+        const bool live = hs < p.heads && walk.t0 + tl < p.tokens;
+        unsigned b = 0, s = 0;
+        if (live) walk.at(p, tl, b, s);
+        // the cache row of this token's K and V: written when 0 <= row < cap
+        long long row_kv = s;
+        bool write_kv = live;
+        if (p.kv_len) {
+            row_kv = live ? static_cast<long long>(p.kv_len[b]) - p.S + s : -1;
+            write_kv = row_kv >= 0 && row_kv < p.cap;
+            if (row_kv >= p.cap && lane_c == 0 && hs == 0) atomicOr(p.status, kStatusBounds);
+        }
+
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const int n = which ? rounds - rounds_q : rounds_q;
+            const int mine = which ? (write_kv ? rows_k : 0) : (live ? rows_q : 0);  // rows to write
+            T *dst = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + (which ? row_kv : s) * p.y_st[which][2] +
+                     hs * p.y_st[which][1];
+            const long long y_step = p.heads * p.y_st[which][1];
+            // y_a = a (w_a cos) - b (w_b sin), y_b = a (w_a sin) + b (w_b cos): the weights go into the coefficients
+            P ac_bs[NC], as_bc[NC];
+            const T *wp = static_cast<const T *>(p.w[which]);
 #pragma unroll
-        for (int i = 0; i + 1 < kDepth; ++i)
+            for (int c = 0; c < NC; ++c) {
+                P ang, w;
+                chunk_angles<VEC>(lane_c + c * tpr, live && turn[c], cs[group & 1] + tl * p.half, step_cs, ang);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) ahead[i][c] = ahead[i + 1][c];
-        load_row(h + kDepth * p.heads, ahead[kDepth - 1]);
-        float rs = 1.0f;
-        if (NORM) rs = rsqrtf(row_sum(ss, p.tpr) / static_cast<float>(p.D) + p.eps);
-        if (!(live && h < all_heads && (is_q || write_kv))) continue;
-        T *row = is_q ? qo + h * p.y_st[0][1] : ko + (h - p.H) * p.y_st[1][1];
-        const T *wp = static_cast<const T *>(is_q ? p.w[0] : p.w[1]);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (lane_c + c * p.tpr >= p.chunks) continue;
-            const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-            if (NORM) {
-                if (wp) {
+                for (int j = 0; j < P::kN; ++j) w.a[j] = w.b[j] = both(1.0f);
+                if (NORM && wp && has[c]) {
                     Raw<T, VEC> raw;
-                    float w[2 * VEC];
-                    load_raw<T, VEC, INTER>(raw, wp, ch, p.D);
+                    raw.zero();
+                    load_raw<T, VEC>(raw, wp, at_a[c], at_b[c], p.D);
                     unpack<T, VEC, INTER>(raw, w);
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[c][i] *= w[i];
                 }
 #pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) x[c][i] *= rs;
+                for (int j = 0; j < P::kN; ++j) {
+                    ac_bs[c].a[j] = NORM ? mul2(w.a[j], ang.a[j]) : ang.a[j];
+                    ac_bs[c].b[j] = NORM ? mul2(w.b[j], neg2(ang.b[j])) : neg2(ang.b[j]);
+                    as_bc[c].a[j] = NORM ? mul2(w.a[j], ang.b[j]) : ang.b[j];
+                    as_bc[c].b[j] = NORM ? mul2(w.b[j], ang.a[j]) : ang.a[j];
+                }
             }
-            float y[2 * VEC];
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                fetch();
+                cp_async_wait<kAhead - 1>();
+                P x[NC];
+                float2 ss = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                y[i] = x[c][i] * ang[c][i].x - x[c][VEC + i] * ang[c][i].y;
-                y[VEC + i] = x[c][i] * ang[c][i].y + x[c][VEC + i] * ang[c][i].x;
+                for (int c = 0; c < NC; ++c) {
+                    Raw<T, VEC> raw;
+                    ring.take(2 * c, raw.lo);
+                    ring.take(2 * c + 1, raw.hi);
+                    if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
+                    unpack<T, VEC, INTER>(raw, x[c]);
+                    if (NORM && has[c]) {
+#pragma unroll
+                        for (int j = 0; j < P::kN; ++j) ss = fma2(x[c].a[j], x[c].a[j], fma2(x[c].b[j], x[c].b[j], ss));
+                    }
+                }
+                ring.popped();
+                if (NORM) {
+                    const float2 rs = both(rsqrtf(row_sum(ss.x + ss.y, tpr) * inv_d + eps));
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int j = 0; j < P::kN; ++j) {
+                            x[c].a[j] = mul2(x[c].a[j], rs);
+                            x[c].b[j] = mul2(x[c].b[j], rs);
+                        }
+                }
+                if (i < mine) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        P y;
+#pragma unroll
+                        for (int j = 0; j < P::kN; ++j) {
+                            y.a[j] = fma2(x[c].a[j], ac_bs[c].a[j], mul2(x[c].b[j], ac_bs[c].b[j]));
+                            y.b[j] = fma2(x[c].a[j], as_bc[c].a[j], mul2(x[c].b[j], as_bc[c].b[j]));
+                        }
+                        if (has[c]) store_raw<T, VEC, INTER>(dst, at_a[c], at_b[c], D, y);
+                    }
+                }
+                dst += y_step;
             }
-            store_chunk<T, VEC, INTER>(row, ch, p.D, y);
+        }
+
+        if (p.kv_len && p.v && write_kv) {  // V rows are copied, 16 bytes at a time (rows start on 16 bytes)
+            constexpr int N = 16 / sizeof(T);
+            const T *v0 = static_cast<const T *>(p.v) + b * p.v_st[0] + s * p.v_st[2];
+            T *o0 = static_cast<T *>(p.v_out) + b * p.vo_st[0] + row_kv * p.vo_st[2];
+            for (int h = hs; h < p.H_kv; h += p.heads)
+                for (int e = lane_c * N; e < p.D_v; e += p.tpr * N) {
+                    const T *from = v0 + h * p.v_st[1] + e;
+                    T *to = o0 + h * p.vo_st[1] + e;
+                    if (e + N <= p.D_v) {
+                        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+                    } else {
+                        for (int i = 0; i < p.D_v - e; ++i) to[i] = from[i];
+                    }
+                }
         }
     }
-
-    if (p.kv_len && p.v && write_kv) {  // V rows are copied, 16 bytes at a time (rows start on 16 bytes)
-        constexpr int N = 16 / sizeof(T);
-        const T *v0 = static_cast<const T *>(p.v) + b * p.v_st[0] + s * p.v_st[2];
-        T *o0 = static_cast<T *>(p.v_out) + b * p.vo_st[0] + row_kv * p.vo_st[2];
-        for (int h = hs; h < p.H_kv; h += p.heads)
-            for (int e = lane_c * N; e < p.D_v; e += p.tpr * N) {
-                const T *src = v0 + h * p.v_st[1] + e;
-                T *dst = o0 + h * p.vo_st[1] + e;
-                if (e + N <= p.D_v) {
-                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
-                } else {
-                    for (int i = 0; i < p.D_v - e; ++i) dst[i] = src[i];
-                }
-            }
-    }
+    cp_async_wait<0>();
 }
 
 // Backward: dx from the gradient's inverse rotation; a block works on Q or on K, so that one set of weight-gradient
@@ -337,139 +514,200 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 1) fwd_kernel(const __
 // a fixed order.  Both means of a row, of x^2 and of w u x, are taken in one pass of shuffles.
 template <typename T, int VEC, int NC, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __grid_constant__ Params p) {
-    extern __shared__ float2 cs[];  // [tok][half], turns_of every pair; then (weight gradients) float [kThreads / tpr][D]
-    unsigned long long *turns = reinterpret_cast<unsigned long long *>(cs + p.tok * p.half);
+    using P = Pairs<VEC>;
+    constexpr int kRuns = (NORM ? 4 : 2) * NC;
+    __shared__ float2 cs[2][kThreads];  // [tok][half] of this group of tokens and of the next
+    // the ring, and after the loop the weight gradients: float [kThreads / tpr][D]
+    extern __shared__ __align__(16) uint8_t ring_mem[];
+    Ring<T, VEC, kRuns, kAheadBwd> ring(ring_mem);
     if (NORM) launch_dependents();  // the launch that adds the blocks' sums waits for them
     const int which = blockIdx.x >= static_cast<unsigned>(p.blocks_q);
-    const int block = static_cast<int>(blockIdx.x) - (which ? p.blocks_q : 0);
-    const int n_blocks = which ? static_cast<int>(gridDim.x) - p.blocks_q : p.blocks_q;
+    const unsigned block = blockIdx.x - (which ? p.blocks_q : 0);
+    const unsigned n_blocks = which ? gridDim.x - p.blocks_q : p.blocks_q;
     const int heads = which ? p.H_kv : p.H;
     const int per_head = p.tpr * p.tok;
     const int hs = threadIdx.x / per_head;
     const int r = threadIdx.x - hs * per_head;
     const int tl = r / p.tpr, lane_c = r - tl * p.tpr;
-    const T *x_base = static_cast<const T *>(p.x[which]), *g_base = static_cast<const T *>(p.g[which]);
-    T *y_base = static_cast<T *>(p.y[which]);
+    const Angle angle(p, VEC);
+    int at_a[NC], at_b[NC];
+    bool has[NC], turn[NC];
+    P w[NC], dw[NC];
     const T *wp = static_cast<const T *>(p.w[which]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
+        has[c] = lane_c + c * p.tpr < p.chunks;
+        turn[c] = has[c] && ch.turn;
+        at_a[c] = ch.a;
+        at_b[c] = ch.b;
+        if (NORM) {
+#pragma unroll
+            for (int j = 0; j < P::kN; ++j) {
+                w[c].a[j] = w[c].b[j] = both(1.0f);
+                dw[c].a[j] = dw[c].b[j] = both(0.0f);
+            }
+            if (wp && has[c]) {
+                Raw<T, VEC> raw;
+                raw.zero();
+                load_raw<T, VEC>(raw, wp, at_a[c], at_b[c], p.D);
+                unpack<T, VEC, INTER>(raw, w[c]);
+            }
+        }
+    }
+    const int rounds = (heads + p.heads - 1) / p.heads;  // the same for the whole block: the norm shuffles
+    const int rows_of = hs < heads ? (heads - hs + p.heads - 1) / p.heads : 0;
+    const float inv_d = 1.0f / static_cast<float>(p.D), eps = p.eps;
+    // (copies: the loop's asm statements would have every use of p read again)
+    const int tpr = p.tpr, D = p.D, tokens = static_cast<int>(p.tokens), step_cs = p.half / VEC;
+    const long long g_step = p.heads * p.g_st[which][1], x_step = p.heads * p.x_st[which][1];
+    const long long y_step = p.heads * p.y_st[which][1];
+    const bool row_thread = hs < p.heads;
 
-    for (int j = threadIdx.x; j < p.half; j += kThreads) turns[j] = turns_of(p, j);
-    float dw[NC][2 * VEC];
-    if (NORM) {
+    // ---- the loads' own walk, kAheadBwd rows in front
+    Walk ahead(p, block * p.tok, n_blocks * p.tok);
+    int ahead_i = 0;
+    bool ahead_live = false;
+    const T *ahead_g = nullptr, *ahead_x = nullptr;
+    auto ahead_group = [&]() {
+        ahead_live = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
+        if (!ahead_live) return;
+        unsigned b, s;
+        ahead.at(p, tl, b, s);
+        ahead_g = static_cast<const T *>(p.g[which]) + b * p.g_st[which][0] + s * p.g_st[which][2] + hs * p.g_st[which][1];
+        ahead_x = static_cast<const T *>(p.x[which]) + b * p.x_st[which][0] + s * p.x_st[which][2] + hs * p.x_st[which][1];
+    };
+    auto fetch = [&]() {
+        if (ahead_live && ahead_i < rows_of) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (has[c]) {
+                    const bool two = VEC > 1 || at_b[c] < D;
+                    ring.fetch(2 * c, ahead_g + at_a[c]);
+                    if (two) ring.fetch(2 * c + 1, ahead_g + at_b[c]);
+                    if (NORM) {
+                        ring.fetch(2 * (NC + c), ahead_x + at_a[c]);
+                        if (two) ring.fetch(2 * (NC + c) + 1, ahead_x + at_b[c]);
+                    }
+                }
+        }
+        ring.pushed();
+        ahead_g += g_step;
+        if (NORM) ahead_x += x_step;
+        if (++ahead_i == rounds) {
+            ahead_i = 0;
+            ahead.next(p);
+            ahead_group();
+        }
+    };
+    Walk walk = ahead;
+    ahead_group();
+    int pos_next = angle.position(p, walk);
+#pragma unroll 1
+    for (int i = 0; i < kAheadBwd - 1; ++i) fetch();
+    angle.form(pos_next, cs[0]);
+    Walk after = walk;
+    after.next(p);
+    pos_next = after.t0 < p.tokens ? angle.position(p, after) : 0;
+
+    for (int group = 0; walk.t0 < p.tokens; walk.next(p), ++group) {
+        __syncthreads();  // this group's angles are there, and the previous group's have been read
+        if (after.t0 < p.tokens) {
+            angle.form(pos_next, cs[(group + 1) & 1]);
+            after.next(p);
+            if (after.t0 < p.tokens) pos_next = angle.position(p, after);
+        }
+        const bool live = hs < p.heads && walk.t0 + tl < p.tokens;
+        unsigned b = 0, s = 0;
+        if (live) walk.at(p, tl, b, s);
+        T *y = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + s * p.y_st[which][2] + hs * p.y_st[which][1];
+        const int mine = live ? rows_of : 0;  // rows to write
+        P ang[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 2 * VEC; ++i) dw[c][i] = 0.0f;
-    }
-
-    const long long groups = (p.tokens + p.tok - 1) / p.tok;
-    for (long long tb = block; tb < groups; tb += n_blocks) {
-        const long long t = tb * p.tok + tl;
-        const bool live = hs < p.heads && t < p.tokens;
-        const int b = live ? static_cast<int>(t / p.S) : 0;
-        const int s = live ? static_cast<int>(t - static_cast<long long>(b) * p.S) : 0;
-        const T *x0 = x_base + b * p.x_st[which][0] + s * p.x_st[which][2];
-        const T *g0 = g_base + b * p.g_st[which][0] + s * p.g_st[which][2];
-        T *y0 = y_base + b * p.y_st[which][0] + s * p.y_st[which][2];
-        Raw<T, VEC> g_next[NC], x_next[NC];
-        auto load_row = [&](int h) {
-            const bool on = live && h < heads;
+            chunk_angles<VEC>(lane_c + c * tpr, live && turn[c], cs[group & 1] + tl * p.half, step_cs, ang[c]);
+#pragma unroll 1
+        for (int i = 0; i < rounds; ++i) {
+            fetch();
+            cp_async_wait<kAheadBwd - 1>();
+            P u[NC], z[NC];
+            float2 ss = both(0.0f), dot = both(0.0f);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                if (on && lane_c + c * p.tpr < p.chunks) {
-                    const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-                    load_raw<T, VEC, INTER>(g_next[c], g0 + h * p.g_st[which][1], ch, p.D);
-                    if (NORM) load_raw<T, VEC, INTER>(x_next[c], x0 + h * p.x_st[which][1], ch, p.D);
-                } else {
-                    g_next[c].lo.zero();
-                    g_next[c].hi.zero();
-                    x_next[c].lo.zero();
-                    x_next[c].hi.zero();
+                Raw<T, VEC> raw;
+                P gv;
+                ring.take(2 * c, raw.lo);
+                ring.take(2 * c + 1, raw.hi);
+                if (i >= mine || !has[c]) raw.zero();  // no row: nothing may come of what the ring holds
+                if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
+                unpack<T, VEC, INTER>(raw, gv);
+                if (NORM) {
+                    ring.take(2 * (NC + c), raw.lo);
+                    ring.take(2 * (NC + c) + 1, raw.hi);
+                    if (i >= mine || !has[c]) raw.zero();
+                    if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
+                    unpack<T, VEC, INTER>(raw, z[c]);
+                }
+#pragma unroll
+                for (int j = 0; j < P::kN; ++j) {
+                    u[c].a[j] = fma2(gv.a[j], ang[c].a[j], mul2(gv.b[j], ang[c].b[j]));
+                    u[c].b[j] = fma2(gv.b[j], ang[c].a[j], mul2(gv.a[j], neg2(ang[c].b[j])));
                 }
             }
-        };
-        load_row(hs);
-        __syncthreads();  // the frequencies are there, and the previous tokens' angles have been read
-        block_angles(p, tb * p.tok, turns, cs);
-        __syncthreads();
-        float2 ang[NC][VEC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
-            const bool in = live && lane_c + c * p.tpr < p.chunks && ch.turn;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) ang[c][i] = in ? cs[tl * p.half + ch.pair() + i] : make_float2(1.0f, 0.0f);
-        }
-        for (int h0 = 0; h0 < heads; h0 += p.heads) {
-            const int h = h0 + hs;
-            float u[NC][2 * VEC], x[NC][2 * VEC], w[NC][2 * VEC];
-            float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                float g[2 * VEC];
-                unpack<T, VEC, INTER>(g_next[c], g);
-                if (NORM) unpack<T, VEC, INTER>(x_next[c], x[c]);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    u[c][i] = g[i] * ang[c][i].x + g[VEC + i] * ang[c][i].y;
-                    u[c][VEC + i] = g[VEC + i] * ang[c][i].x - g[i] * ang[c][i].y;
-                }
-            }
-            load_row(h + p.heads);
+            ring.popped();
             if (NORM) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) w[c][i] = 1.0f;
-                    if (wp && lane_c + c * p.tpr < p.chunks) {
-                        Raw<T, VEC> raw;
-                        load_raw<T, VEC, INTER>(raw, wp, Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D);
-                        unpack<T, VEC, INTER>(raw, w[c]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) {
-                        ss = fmaf(x[c][i], x[c][i], ss);
-                        dot = fmaf(w[c][i] * u[c][i], x[c][i], dot);
-                    }
-                }
-                for (int o = p.tpr >> 1; o > 0; o >>= 1) {
-                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                }
-                const float rs = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
-                const float mean = dot * rs / static_cast<float>(p.D);  // of w u z
+                // dx = rs w u - x rs^3 mean(w u x),  dw += u x rs
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) {
-                        const float z = x[c][i] * rs;
-                        dw[c][i] = fmaf(u[c][i], z, dw[c][i]);
-                        u[c][i] = rs * (w[c][i] * u[c][i] - z * mean);
+                    for (int j = 0; j < P::kN; ++j) {
+                        ss = fma2(z[c].a[j], z[c].a[j], fma2(z[c].b[j], z[c].b[j], ss));
+                        dot = fma2(mul2(w[c].a[j], u[c].a[j]), z[c].a[j],
+                                   fma2(mul2(w[c].b[j], u[c].b[j]), z[c].b[j], dot));
                     }
-            }
-            if (!(live && h < heads)) continue;
+                float s1 = ss.x + ss.y, d1 = dot.x + dot.y;
+                for (int o = tpr >> 1; o > 0; o >>= 1) {
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+                }
+                const float rs = rsqrtf(s1 * inv_d + eps);
+                const float2 rs2 = both(rs), m2 = both(-rs * rs * rs * d1 * inv_d);
+                if (i < mine) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                if (lane_c + c * p.tpr >= p.chunks) continue;
-                store_chunk<T, VEC, INTER>(y0 + h * p.y_st[which][1], Chunk<VEC, INTER>(p, lane_c + c * p.tpr), p.D, u[c]);
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int j = 0; j < P::kN; ++j) {
+                            dw[c].a[j] = fma2(mul2(u[c].a[j], rs2), z[c].a[j], dw[c].a[j]);
+                            dw[c].b[j] = fma2(mul2(u[c].b[j], rs2), z[c].b[j], dw[c].b[j]);
+                            u[c].a[j] = fma2(mul2(rs2, w[c].a[j]), u[c].a[j], mul2(m2, z[c].a[j]));
+                            u[c].b[j] = fma2(mul2(rs2, w[c].b[j]), u[c].b[j], mul2(m2, z[c].b[j]));
+                        }
+                }
             }
+            if (i < mine) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (has[c]) store_raw<T, VEC, INTER>(y, at_a[c], at_b[c], D, u[c]);
+            }
+            y += y_step;
         }
     }
+    cp_async_wait<0>();
 
     if (!NORM || !p.part[which]) return;
     // the block's sums: rows of the block (same columns, other tokens and heads) are added in order
-    float *sm = reinterpret_cast<float *>(cs);
+    float *sm = reinterpret_cast<float *>(ring_mem);
     const int rows = kThreads / p.tpr;
     const int row = threadIdx.x / p.tpr;
-    __syncthreads();
+    __syncthreads();  // every thread is done with the ring
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        if (lane_c + c * p.tpr >= p.chunks) continue;
-        const Chunk<VEC, INTER> ch(p, lane_c + c * p.tpr);
+        if (!has[c]) continue;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int lo = INTER ? ch.a + 2 * i : ch.a + i, hi = INTER ? lo + 1 : ch.b + i;
-            sm[row * p.D + lo] = dw[c][i];
-            if (hi < p.D) sm[row * p.D + hi] = dw[c][VEC + i];
+            const int lo = INTER ? at_a[c] + 2 * i : at_a[c] + i, hi = INTER ? lo + 1 : at_b[c] + i;
+            sm[row * p.D + lo] = i & 1 ? dw[c].a[i / 2].y : dw[c].a[i / 2].x;
+            if (hi < p.D) sm[row * p.D + hi] = i & 1 ? dw[c].b[i / 2].y : dw[c].b[i / 2].x;
         }
     }
     __syncthreads();

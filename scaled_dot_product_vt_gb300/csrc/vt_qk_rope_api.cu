@@ -57,6 +57,8 @@ vt_status check_shape(const Args &a, bool *empty) {
         return VT_ERR_UNSUPPORTED;
     for (int64_t i = 0; i < a.R / 2; ++i)
         if (a.pair_axis[i] >= a.axes) return VT_ERR_INVALID_ARG;
+    // tokens, and the next group's past the last one, are counted in 32 bits (B < 2^31 and S <= 2^30 here)
+    if (a.B * a.S > kMaxSeq) return VT_ERR_UNSUPPORTED;
     *empty = a.B == 0 || a.S == 0 || (a.H == 0 && a.H_kv == 0);
     return VT_OK;
 }
@@ -145,12 +147,12 @@ Params common_params(const Args &a, const Shape &sh, int sms) {
     const int lanes = (p.chunks + sh.nc - 1) / sh.nc;
     // the norm's shuffles want a power of two; without it a row takes exactly the threads it needs
     p.tpr = a.normalize ? pow2_at_least(lanes) : lanes;
-    p.tokens = a.B * a.S;
-    // about one angle per thread, while every SM still has a few blocks
+    p.tokens = static_cast<unsigned>(a.B * a.S);
+    // at most one angle per thread, while every SM still has a few blocks
     int tok = kThreads / p.half;
     if (tok > 8) tok = 8;
     if (tok > kThreads / p.tpr) tok = kThreads / p.tpr;
-    while (tok > 1 && p.tokens / tok < 4LL * sms) tok /= 2;
+    while (tok > 1 && a.B * a.S / tok < 4LL * sms) tok /= 2;
     p.tok = tok < 1 ? 1 : tok;
     p.heads = kThreads / (p.tpr * p.tok);
     p.eps = a.eps;
@@ -173,20 +175,28 @@ Params common_params(const Args &a, const Shape &sh, int sms) {
     return p;
 }
 
-using Kern = void (*)(const Params);  // (the kernels take it as a grid constant)
+// A kernel variant and the shared memory of its ring.
+struct Variant {
+    void (*kern)(const Params);
+    int smem;
+};
 
 template <typename T, int VEC, int NC, bool BWD>
-Kern pick_form(bool inter, bool norm) {
-    if constexpr (BWD)
-        return inter ? (norm ? bwd_kernel<T, VEC, NC, true, true> : bwd_kernel<T, VEC, NC, true, false>)
-                     : (norm ? bwd_kernel<T, VEC, NC, false, true> : bwd_kernel<T, VEC, NC, false, false>);
-    else
-        return inter ? (norm ? fwd_kernel<T, VEC, NC, true, true> : fwd_kernel<T, VEC, NC, true, false>)
-                     : (norm ? fwd_kernel<T, VEC, NC, false, true> : fwd_kernel<T, VEC, NC, false, false>);
+Variant pick_form(bool inter, bool norm) {
+    if constexpr (BWD) {
+        const int smem = norm ? kAheadBwd * Ring<T, VEC, 4 * NC, kAheadBwd>::kStage : kAheadBwd * Ring<T, VEC, 2 * NC, kAheadBwd>::kStage;
+        return {inter ? (norm ? bwd_kernel<T, VEC, NC, true, true> : bwd_kernel<T, VEC, NC, true, false>)
+                      : (norm ? bwd_kernel<T, VEC, NC, false, true> : bwd_kernel<T, VEC, NC, false, false>),
+                smem};
+    } else {
+        return {inter ? (norm ? fwd_kernel<T, VEC, NC, true, true> : fwd_kernel<T, VEC, NC, true, false>)
+                      : (norm ? fwd_kernel<T, VEC, NC, false, true> : fwd_kernel<T, VEC, NC, false, false>),
+                kAhead * Ring<T, VEC, 2 * NC, kAhead>::kStage};
+    }
 }
 
 template <bool BWD>
-Kern pick(const Args &a, const Shape &sh) {
+Variant pick(const Args &a, const Shape &sh) {
     const bool in = a.interleaved != 0, no = a.normalize != 0;
     if (a.dtype == VT_BF16) {
         if (sh.vec == 8) return pick_form<bf16, 8, 1, BWD>(in, no);
@@ -197,9 +207,14 @@ Kern pick(const Args &a, const Shape &sh) {
     return sh.nc == 1 ? pick_form<float, 1, 1, BWD>(in, no) : pick_form<float, 1, 4, BWD>(in, no);
 }
 
-vt_status device_of(DeviceInfo *info) {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && device_info(dev, info) ? VT_OK : VT_ERR_CUDA;
+vt_status launch(const Variant &v, int smem, unsigned blocks, const Params &p, int dev, cudaStream_t stream) {
+    if (!ensure_smem(reinterpret_cast<const void *>(v.kern), dev, smem)) return VT_ERR_CUDA;
+    v.kern<<<blocks, kThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
+
+vt_status device_of(int *dev, DeviceInfo *info) {
+    return cudaGetDevice(dev) == cudaSuccess && device_info(*dev, info) ? VT_OK : VT_ERR_CUDA;
 }
 
 vt_status forward(const Args &a, cudaStream_t stream) {
@@ -228,8 +243,9 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     // Q and (without an append) K may be rotated in place
     if (!outputs_clear(ps, a.q, append ? nullptr : a.k)) return VT_ERR_INVALID_ARG;
 
+    int dev = 0;
     DeviceInfo info;
-    VT_TRY(device_of(&info));
+    VT_TRY(device_of(&dev, &info));
     const Shape sh = shape_of(a, elt);
     Params p = common_params(a, sh, info.sms);
     p.kv_len = a.kv_len;
@@ -242,10 +258,10 @@ vt_status forward(const Args &a, cudaStream_t stream) {
         p.vo_st[i] = a.v_out_stride[i];
     }
     p.status = info.status + status_slot(stream);
-    const long long blocks = (p.tokens + p.tok - 1) / p.tok;
-    if (blocks > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
-    pick<false>(a, sh)<<<static_cast<unsigned>(blocks), kThreads, (p.tok + 1) * p.half * sizeof(float2), stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    const int64_t groups = (a.B * a.S + p.tok - 1) / p.tok, most = 3LL * info.sms;
+    const unsigned blocks = static_cast<unsigned>(groups < most ? groups : most);
+    const Variant v = pick<false>(a, sh);
+    VT_TRY(launch(v, v.smem, blocks, p, dev, stream));
     return env_check() ? read_status(stream) : VT_OK;
 }
 
@@ -293,8 +309,9 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
         return VT_OK;
     }
 
+    int dev = 0;
     DeviceInfo info;
-    VT_TRY(device_of(&info));
+    VT_TRY(device_of(&dev, &info));
     const Shape sh = shape_of(a, elt);
     Params p = common_params(a, sh, info.sms);
     p.g[0] = gq;
@@ -304,23 +321,21 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
         p.g_st[1][i] = a.H_kv > 0 ? gk_st[i] : 0;
     }
     // blocks for Q and for K in proportion to their rows, two per SM in all (they fit at once)
-    const long long groups = (p.tokens + p.tok - 1) / p.tok;
+    const int64_t groups = (a.B * a.S + p.tok - 1) / p.tok;
     const int most = 2 * info.sms < kBwdMaxBlocks ? 2 * info.sms : kBwdMaxBlocks;
-    auto share = [&](long long heads) -> int {
-        if (heads == 0) return 0;
-        const long long n = (most * heads + p.H + p.H_kv - 1) / (p.H + p.H_kv);
-        return static_cast<int>(groups < n ? groups : n);
-    };
-    const int n_q = share(p.H), n_k = share(p.H_kv);
+    int n_k = p.H == 0 ? most : (p.H_kv == 0 ? 0 : static_cast<int>(static_cast<long long>(most) * p.H_kv / (p.H + p.H_kv)));
+    if (p.H_kv > 0 && n_k < 1) n_k = 1;
+    if (p.H > 0 && n_k >= most) n_k = most - 1;
+    int n_q = p.H > 0 ? most - n_k : 0;
+    if (n_q > groups) n_q = static_cast<int>(groups);
+    if (n_k > groups) n_k = static_cast<int>(groups);
     p.blocks_q = n_q;
     float *part = static_cast<float *>(ws);
     p.part[0] = dwq ? part : nullptr;
     p.part[1] = dwk ? part + static_cast<long long>(kBwdMaxBlocks) * p.D : nullptr;
-    size_t smem = (p.tok + 1) * p.half * sizeof(float2);
-    const size_t sums = norm ? static_cast<size_t>(kThreads / p.tpr) * p.D * sizeof(float) : 0;
-    if (sums > smem) smem = sums;
-    pick<true>(a, sh)<<<static_cast<unsigned>(n_q + n_k), kThreads, smem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    const Variant v = pick<true>(a, sh);
+    const int sums = norm ? kThreads / p.tpr * p.D * static_cast<int>(sizeof(float)) : 0;
+    VT_TRY(launch(v, v.smem > sums ? v.smem : sums, static_cast<unsigned>(n_q + n_k), p, dev, stream));
     if (!weights) return VT_OK;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.D + 7) / 8, 2);
