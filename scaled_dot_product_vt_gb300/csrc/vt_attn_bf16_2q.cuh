@@ -116,12 +116,31 @@ __device__ __forceinline__ int own_keys(const AttnParams &p, int len, int r) {
 
 // Units run over groups of `head_group` heads; inside a group, the heaviest query blocks first
 // when work grows with the block index; the shares of one block are adjacent.
+// Gathered rows are launched by key/value head, then sequence (kRowsSeq), query block and share, so that the units in
+// flight read few heads' keys: share, sequence, head and query block of unit u.
+template <int ROWS>
+__device__ __forceinline__ void gathered_unit(const AttnParams &p, unsigned u, int *split, int *b, int *h, int *qb) {
+    const unsigned item = p.n_split > 1 ? u / p.n_split : u;
+    *split = static_cast<int>(u - item * p.n_split);
+    const unsigned slice = p.n_qblocks > 1 ? item / p.n_qblocks : item;
+    *qb = static_cast<int>(item - slice * p.n_qblocks);
+    *h = static_cast<int>(ROWS == kRowsSeq ? slice / p.B : slice);
+    *b = static_cast<int>(ROWS == kRowsSeq ? slice - *h * p.B : 0);
+    if (ROWS == kRowsSeq) *qb = p.n_qblocks - 1 - *qb;  // (later blocks see more of the cache)
+}
+
 template <int ROWS>
 __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     Unit U;
     U.len = 0;
-    const int split = u % p.n_split;
     U.u = u;
+    if constexpr (ROWS != kRowsPlain) {
+        int qb;
+        gathered_unit<ROWS>(p, u, &U.split, &U.b, &U.h, &qb);
+        U.hk = U.h;
+        U.r0 = qb * kRows;
+    } else {
+    const int split = u % p.n_split;
     U.split = split;
     const int item = u / p.n_split;
     const int BH = p.B * p.H;
@@ -136,6 +155,8 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     U.b = bh / p.H;
     U.hk = U.h / p.kv_group;
     U.r0 = qb * kRows;
+    }
+    const int split = U.split;
     if constexpr (ROWS == kRowsSeq) {
         int len = p.kv_len ? p.kv_len[U.b] : p.cache_keys;
         if (len < 0 || len > p.cache_keys) {  // a length outside the cache counts as the nearest one inside
@@ -225,8 +246,8 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
 
 // Copy rows row0 .. row0 + 127 of key/value head hk (of sequence b, kRowsSeq) into a Q tile (128-byte swizzle: the
 // 16-byte pieces of a row are permuted by its low bits), zeros past the last row and past D_qk.  Called by the 128
-// threads of a softmax warpgroup; on return the calling thread's pieces are visible to the tensor core.  Each lane
-// finds the address of one of its warp's 32 rows; 8 or 16 lanes then copy a row together.
+// threads of a softmax warpgroup, and followed by gather_done.  Each lane finds the address of one of its warp's 32 rows;
+// 8 or 16 lanes then copy a row together.
 template <int ROWS>
 __device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int b, int hk, const AttnParams &p) {
     const int lane = threadIdx.x & 31, first = threadIdx.x & 96;
@@ -251,6 +272,9 @@ __device__ __forceinline__ void gather_rows(uint32_t tile, int row0, int b, int 
         cp_async16(col + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                    in ? reinterpret_cast<const void *>(at + c * 16) : p.Q, in ? bytes : 0);
     }
+}
+// The pieces this thread copied have landed, and the tensor core sees them.
+__device__ __forceinline__ void gather_done() {
     cp_async_wait_all();
     fence_async_shared();
 }
@@ -308,6 +332,17 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
     const uint32_t slot_bytes = max(k_bytes, v_bytes);
     const uint32_t sQ0 = base, sQ1 = base + q_tile_bytes;
     const uint32_t sSlot0 = base + 2 * q_tile_bytes;
+
+    // The first unit's rows start on their way before anything else, ahead of the keys: behind them they would wait
+    // for the slots' 160 KB of every SM (6.4 us from a cold start).
+    if constexpr (GATHER) {
+        if (warp >= 4) {
+            int split, b, h, qb;
+            gathered_unit<ROWS>(p, blockIdx.x, &split, &b, &h, &qb);
+            const int t = (warp - 4) >> 2;
+            gather_rows<ROWS>(t ? sQ1 : sQ0, qb * kRows + t * kBM, b, h, p);
+        }
+    }
 
     if (threadIdx.x == 0) {
         // with the score ring each query tile has its own MMA warp, and both release every slot and Q
@@ -714,12 +749,16 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 mask_hi = band_key_hi(p, tile_row0);
             }
             if constexpr (GATHER) {
+                if (n == 0) gather_done();  // copied at the start
                 if (U.n_kv > 0) {
                     if (gathered > 0)  // the previous unit's last Q K^T has read Q
                         ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl.q_empty), (gathered - 1) & 1u,
                                                                   ctl.abort_flag, p)) != 0;
                     if (!ok) break;
-                    gather_rows<ROWS>(t ? sQ1 : sQ0, tile_row0, U.b, U.h, p);
+                    if (n > 0) {
+                        gather_rows<ROWS>(t ? sQ1 : sQ0, tile_row0, U.b, U.h, p);
+                        gather_done();
+                    }
                     mbar_arrive(smem_u32(&ctl.q_full));
                     ++gathered;
                 }

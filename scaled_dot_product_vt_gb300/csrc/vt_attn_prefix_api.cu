@@ -314,7 +314,6 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.n_pv = (p.D_v + 15) / 16 * 16;
     p.band_lo = -kBandInf;
     p.band_hi = kBandInf;
-    p.reverse_q = seq ? 1 : 0;
     p.kv_group = 1;
     p.scale_log2 = sp.scale_log2;
     p.Q = sp.Q;
@@ -345,11 +344,9 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.stages = (kSmemLimit - 1024 - static_cast<int>(sizeof(q2::Ctl)) - 256 - q_bytes) / slot_bytes;
     if (p.stages > q2::kMaxSlots) p.stages = q2::kMaxSlots;
     const int smem = 1024 + q_bytes + p.stages * slot_bytes;
-    // heads whose query blocks run at about the same time read K and V from L2
     const int64_t heads = static_cast<int64_t>(p.B) * p.H;
     const int64_t per_head = static_cast<int64_t>(p.n_qblocks) * p.n_split;
-    const int64_t grp = (2LL * info.sms + per_head - 1) / per_head;
-    p.head_group = static_cast<int>(grp < 1 ? 1 : (grp > heads ? heads : grp));
+    p.head_group = 1;
     const int64_t units = per_head * heads;
     if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
     p.n_units = static_cast<int>(units);

@@ -188,6 +188,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
     const int f0 = rt * kRowsTile;
     const int n_rows = min(kRowsTile, group_rows - f0);
 
+    int len = p.all_rows ? 0 : (p.kv_len ? p.kv_len[b] : p.S_c);  // (asked for first: the keys wait for it)
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(p.all_rows ? &maps.kp : &maps.kc);
+        tma_prefetch_desc(p.all_rows ? &maps.vp : &maps.vc);
+    }
     // the queries on their way to shared memory: 16 bytes per thread and step, swizzled as the keys are, zeros past
     // the last row and past D_qk
     {
@@ -209,9 +214,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
         cp_async_commit();
     }
 
-    int len = 0;
     if (!p.all_rows) {
-        len = p.kv_len ? p.kv_len[b] : p.S_c;
         if (len < 0 || len > p.S_c) {  // a length outside the cache counts as the nearest one inside
             if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
             len = len < 0 ? 0 : p.S_c;

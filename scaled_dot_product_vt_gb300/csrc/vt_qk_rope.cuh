@@ -159,22 +159,20 @@ struct Ring {
     static constexpr int kStage = kRuns * kThreads * kBytes;
     uint8_t *mine;
     uint32_t mine_s;
-    int put = 0, got = 0;  // stages to fill and to read next
+    int put = 0, got = 0;  // byte offsets of the stages to fill and to read next
 
     __device__ Ring(uint8_t *smem) : mine(smem + threadIdx.x * kBytes), mine_s(smem_u32(smem) + threadIdx.x * kBytes) {}
     __device__ __forceinline__ void fetch(int run, const T *p) {
-        Run<T, VEC>::fetch(mine_s + put * kStage + run * kThreads * kBytes, p);
+        Run<T, VEC>::fetch(mine_s + put + run * kThreads * kBytes, p);
     }
     __device__ __forceinline__ void pushed() {
         cp_async_commit();
-        if (++put == kStages) put = 0;
+        put = put == (kStages - 1) * kStage ? 0 : put + kStage;
     }
     __device__ __forceinline__ void take(int run, Run<T, VEC> &r) const {
-        r.take(mine + got * kStage + run * kThreads * kBytes);
+        r.take(mine + got + run * kThreads * kBytes);
     }
-    __device__ __forceinline__ void popped() {
-        if (++got == kStages) got = 0;
-    }
+    __device__ __forceinline__ void popped() { got = got == (kStages - 1) * kStage ? 0 : got + kStage; }
 };
 
 // The chunk's pairs two by two, for arithmetic on both at once: a[j], b[j] hold the first and the second members of
@@ -343,50 +341,50 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
     const float inv_d = 1.0f / static_cast<float>(p.D), eps = p.eps;
     // (copies: the loop's asm statements would have every use of p read again)
     const int tpr = p.tpr, D = p.D, tokens = static_cast<int>(p.tokens), step_cs = p.half / VEC;
-    const long long q_step = p.heads * p.x_st[0][1], k_step = p.heads * p.x_st[1][1];
     // A token's rows in rounds: round i takes heads hs + i * p.heads of Q, then the K rounds those of K; the rounds
     // are the same for every thread of the block (the norm shuffles), some threads have no row in the last ones.
     const int rounds_q = (p.H + p.heads - 1) / p.heads, rounds = rounds_q + (p.H_kv + p.heads - 1) / p.heads;
     const int rows_q = hs < p.H ? (p.H - hs + p.heads - 1) / p.heads : 0;
     const int rows_k = hs < p.H_kv ? (p.H_kv - hs + p.heads - 1) / p.heads : 0;
 
-    const bool row_thread = hs < p.heads;
+    const bool row_thread = hs < p.heads && has[0];
 
-    // ---- the loads' own walk over groups and rounds, kAhead rows in front
+    // ---- the loads' own walk over groups, tensors and rounds, kAhead rows in front
     Walk ahead(p, blockIdx.x * p.tok, gridDim.x * p.tok);
-    int ahead_i = 0;
-    bool ahead_live = false;
-    const T *ahead_q = nullptr, *ahead_k = nullptr;
-    auto ahead_group = [&]() {
-        ahead_live = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
-        if (!ahead_live) return;
-        unsigned b, s;
-        ahead.at(p, tl, b, s);
-        ahead_q = static_cast<const T *>(p.x[0]) + b * p.x_st[0][0] + s * p.x_st[0][2] + hs * p.x_st[0][1];
-        ahead_k = static_cast<const T *>(p.x[1]) + b * p.x_st[1][0] + s * p.x_st[1][2] + hs * p.x_st[1][1];
+    int ahead_which = 1, ahead_rounds = 0, ahead_rows = 0;  // tensor, its rounds left, this thread's rows left
+    long long ahead_step = 0;
+    const T *ahead_at = nullptr;
+    auto ahead_next = [&](bool move) {  // on to the next tensor with rounds: K after Q, the next group's Q after K
+        do {
+            ahead_which ^= 1;
+            if (ahead_which == 0 && move) ahead.next(p);
+            move = true;
+            ahead_rounds = ahead_which ? rounds - rounds_q : rounds_q;
+        } while (ahead_rounds == 0);
+        const int w = ahead_which;
+        unsigned b = 0, s = 0;
+        const bool in = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
+        if (in) ahead.at(p, tl, b, s);
+        ahead_rows = in ? (w ? rows_k : rows_q) : 0;
+        ahead_step = p.heads * p.x_st[w][1];
+        ahead_at = static_cast<const T *>(p.x[w]) + b * p.x_st[w][0] + s * p.x_st[w][2] + hs * p.x_st[w][1];
     };
     auto fetch = [&]() {
-        const bool k = ahead_i >= rounds_q;
-        const T *row = k ? ahead_k : ahead_q;
-        if (ahead_live && ahead_i < (k ? rounds_q + rows_k : rows_q)) {
+        if (ahead_rows > 0) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                if (has[c]) {
-                    ring.fetch(2 * c, row + at_a[c]);
-                    if (VEC > 1 || at_b[c] < D) ring.fetch(2 * c + 1, row + at_b[c]);
+                if (NC == 1 || has[c]) {
+                    ring.fetch(2 * c, ahead_at + at_a[c]);
+                    if (VEC > 1 || at_b[c] < D) ring.fetch(2 * c + 1, ahead_at + at_b[c]);
                 }
         }
         ring.pushed();
-        if (k) ahead_k = row + k_step;
-        else ahead_q = row + q_step;
-        if (++ahead_i == rounds) {
-            ahead_i = 0;
-            ahead.next(p);
-            ahead_group();
-        }
+        --ahead_rows;
+        ahead_at += ahead_step;
+        if (--ahead_rounds == 0) ahead_next(true);
     };
     Walk walk = ahead;
-    ahead_group();
+    ahead_next(false);
     int pos_next = angle.position(p, walk);
 #pragma unroll 1
     for (int i = 0; i < kAhead - 1; ++i) fetch();
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
             if (after.t0 < p.tokens) pos_next = angle.position(p, after);
         }
         // (threads without a row take part in the shuffles of the norm)
-        const bool live = hs < p.heads && walk.t0 + tl < p.tokens;
+        const bool live = hs < p.heads && static_cast<int>(walk.t0 + tl) < tokens;
         unsigned b = 0, s = 0;
         if (live) walk.at(p, tl, b, s);
         // the cache row of this token's K and V: written when 0 <= row < cap
@@ -418,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             const int n = which ? rounds - rounds_q : rounds_q;
-            const int mine = which ? (write_kv ? rows_k : 0) : (live ? rows_q : 0);  // rows to write
+            const int mine = has[0] ? (which ? (write_kv ? rows_k : 0) : (live ? rows_q : 0)) : 0;  // rows to write
             T *dst = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + (which ? row_kv : s) * p.y_st[which][2] +
                      hs * p.y_st[which][1];
             const long long y_step = p.heads * p.y_st[which][1];
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
                             y.a[j] = fma2(x[c].a[j], ac_bs[c].a[j], mul2(x[c].b[j], ac_bs[c].b[j]));
                             y.b[j] = fma2(x[c].a[j], as_bc[c].a[j], mul2(x[c].b[j], as_bc[c].b[j]));
                         }
-                        if (has[c]) store_raw<T, VEC, INTER>(dst, at_a[c], at_b[c], D, y);
+                        if (NC == 1 || has[c]) store_raw<T, VEC, INTER>(dst, at_a[c], at_b[c], D, y);
                     }
                 }
                 dst += y_step;
@@ -562,26 +560,26 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
     const int tpr = p.tpr, D = p.D, tokens = static_cast<int>(p.tokens), step_cs = p.half / VEC;
     const long long g_step = p.heads * p.g_st[which][1], x_step = p.heads * p.x_st[which][1];
     const long long y_step = p.heads * p.y_st[which][1];
-    const bool row_thread = hs < p.heads;
+    const bool row_thread = hs < p.heads && has[0];
 
     // ---- the loads' own walk, kAheadBwd rows in front
     Walk ahead(p, block * p.tok, n_blocks * p.tok);
-    int ahead_i = 0;
-    bool ahead_live = false;
+    int ahead_rounds = 0, ahead_rows = 0;  // rounds left in the group, this thread's rows left
     const T *ahead_g = nullptr, *ahead_x = nullptr;
     auto ahead_group = [&]() {
-        ahead_live = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
-        if (!ahead_live) return;
-        unsigned b, s;
-        ahead.at(p, tl, b, s);
+        unsigned b = 0, s = 0;
+        const bool in = row_thread && static_cast<int>(ahead.t0 + tl) < tokens;
+        if (in) ahead.at(p, tl, b, s);
+        ahead_rounds = rounds;
+        ahead_rows = in ? rows_of : 0;
         ahead_g = static_cast<const T *>(p.g[which]) + b * p.g_st[which][0] + s * p.g_st[which][2] + hs * p.g_st[which][1];
         ahead_x = static_cast<const T *>(p.x[which]) + b * p.x_st[which][0] + s * p.x_st[which][2] + hs * p.x_st[which][1];
     };
     auto fetch = [&]() {
-        if (ahead_live && ahead_i < rows_of) {
+        if (ahead_rows > 0) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                if (has[c]) {
+                if (NC == 1 || has[c]) {
                     const bool two = VEC > 1 || at_b[c] < D;
                     ring.fetch(2 * c, ahead_g + at_a[c]);
                     if (two) ring.fetch(2 * c + 1, ahead_g + at_b[c]);
@@ -592,10 +590,10 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
                 }
         }
         ring.pushed();
+        --ahead_rows;
         ahead_g += g_step;
         if (NORM) ahead_x += x_step;
-        if (++ahead_i == rounds) {
-            ahead_i = 0;
+        if (--ahead_rounds == 0) {
             ahead.next(p);
             ahead_group();
         }
@@ -617,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
             after.next(p);
             if (after.t0 < p.tokens) pos_next = angle.position(p, after);
         }
-        const bool live = hs < p.heads && walk.t0 + tl < p.tokens;
+        const bool live = row_thread && static_cast<int>(walk.t0 + tl) < tokens;
         unsigned b = 0, s = 0;
         if (live) walk.at(p, tl, b, s);
         T *y = static_cast<T *>(p.y[which]) + b * p.y_st[which][0] + s * p.y_st[which][2] + hs * p.y_st[which][1];
@@ -638,13 +636,13 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
                 P gv;
                 ring.take(2 * c, raw.lo);
                 ring.take(2 * c + 1, raw.hi);
-                if (i >= mine || !has[c]) raw.zero();  // no row: nothing may come of what the ring holds
+                if (i >= mine || (NC > 1 && !has[c])) raw.zero();  // no row: nothing may come of what the ring holds
                 if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
                 unpack<T, VEC, INTER>(raw, gv);
                 if (NORM) {
                     ring.take(2 * (NC + c), raw.lo);
                     ring.take(2 * (NC + c) + 1, raw.hi);
-                    if (i >= mine || !has[c]) raw.zero();
+                    if (i >= mine || (NC > 1 && !has[c])) raw.zero();
                     if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
                     unpack<T, VEC, INTER>(raw, z[c]);
                 }
@@ -687,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
             if (i < mine) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    if (has[c]) store_raw<T, VEC, INTER>(y, at_a[c], at_b[c], D, u[c]);
+                    if (NC == 1 || has[c]) store_raw<T, VEC, INTER>(y, at_a[c], at_b[c], D, u[c]);
             }
             y += y_step;
         }

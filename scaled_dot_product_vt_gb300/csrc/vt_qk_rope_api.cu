@@ -320,13 +320,16 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
         p.g_st[0][i] = a.H > 0 ? gq_st[i] : 0;
         p.g_st[1][i] = a.H_kv > 0 ? gk_st[i] : 0;
     }
-    // blocks for Q and for K in proportion to their rows, two per SM in all (they fit at once)
+    // Two blocks per SM in all (they fit at once), for Q and for K in proportion to what a group of tokens costs them:
+    // its rounds of rows, and about two rounds' time for its angles and addresses.
     const int64_t groups = (a.B * a.S + p.tok - 1) / p.tok;
     const int most = 2 * info.sms < kBwdMaxBlocks ? 2 * info.sms : kBwdMaxBlocks;
-    int n_k = p.H == 0 ? most : (p.H_kv == 0 ? 0 : static_cast<int>(static_cast<long long>(most) * p.H_kv / (p.H + p.H_kv)));
+    const int cost_q = p.H > 0 ? (p.H + p.heads - 1) / p.heads + 2 : 0;
+    const int cost_k = p.H_kv > 0 ? (p.H_kv + p.heads - 1) / p.heads + 2 : 0;
+    int n_k = static_cast<int>(static_cast<int64_t>(most) * cost_k / (cost_q + cost_k));
     if (p.H_kv > 0 && n_k < 1) n_k = 1;
-    if (p.H > 0 && n_k >= most) n_k = most - 1;
-    int n_q = p.H > 0 ? most - n_k : 0;
+    if (p.H > 0 && n_k > most - 1) n_k = most - 1;
+    int n_q = most - n_k;
     if (n_q > groups) n_q = static_cast<int>(groups);
     if (n_k > groups) n_k = static_cast<int>(groups);
     p.blocks_q = n_q;
