@@ -51,31 +51,45 @@ Sizes sizes_of(const Args &a) {
     return z;
 }
 
-constexpr int64_t kTileRows = 32;                   // more rows per prefix key: the tcgen05 kernel
-constexpr int64_t kSeqTileRows = 64;                // more rows per sequence and key/value head: the tcgen05 kernel for all keys
-constexpr int64_t kReadAgain = int64_t(16) << 20;  // bytes
+// More rows that share the prefix's keys than this take the tcgen05 kernel (bf16): 37 rows of 32 heads over 8191 keys,
+// 52 us against 74 us streamed; with 64 rows of 8 heads over 2048 keys the two are level (59 us).
+constexpr int64_t kTileRows = 32;
+// More rows per sequence and key/value head than this take it for all their keys.
+constexpr int64_t kSeqTileRows = 64;
+// Bytes of the prefix that the streaming launch may read again, once per sequence and row tile, to spare a launch
+// (4 sequences of 16 rows over 333 keys: 6.6 us against 9 us).  fp32 multiplies three times as much, and gains
+// from the prefix's own launch earlier (8 sequences over 1000 keys: 12.8 us against 19.7 us).
+constexpr int64_t kReadAgainBf16 = int64_t(16) << 20, kReadAgainF32 = int64_t(2) << 20;
 
 size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
     return ((static_cast<size_t>(rows) * shares * (partial_ld(D_v) + 3) * sizeof(float)) + 255) & ~size_t(255);
 }
 
-int cluster_for(int64_t units, int64_t keys, int sms) {
+// CTAs of a cluster that share a unit's keys: two CTAs per SM in all, as long as every CTA keeps about 96 keys (four
+// drafted tokens over 256 keys: 46 us with 2, 53 us with 4).  The fp32 kernel fills an SM per CTA, and clusters of 8
+// then wait for room (26 us against 20 us with 4).
+int cluster_for(int64_t units, int64_t keys, bool f32, int sms) {
     int c = 1;
-    // two CTAs per SM, and as long as every CTA keeps 64 keys (a block for each warp)
-    while (c < st::kMaxClusterCtas && units * c < 2LL * sms && keys >= 128LL * c) c *= 2;
+    const int most = f32 ? 4 : st::kMaxClusterCtas;
+    while (c < most && units * c < 2LL * sms && keys >= 2 * 96LL * c) c *= 2;
     return c;
 }
 
-// Shares of the prefix for the tcgen05 kernel: the count that its launch is expected to finish first with.  A unit
-// takes about 1.5 us per 128-key tile (two query tiles) and 4 us besides; a partial result is written and read.
-int tile_shares(int64_t blocks, int64_t S_p, int64_t rows, int64_t D_v, int sms) {
-    const int64_t tiles = (S_p + q2::kBN - 1) / q2::kBN;
+// Shares of the prefix for the tcgen05 kernel.  A unit takes about 1.6 us per 128-key tile (two query tiles) and 8 us
+// besides; its launch runs beside the streaming one, whose CTAs wait for it at their end, so it should be done well
+// before them, without spending more of the SMs than that needs.
+int tile_shares(const Args &a, const Sizes &z, int sms) {
+    const int64_t tiles = (a.S_p + q2::kBN - 1) / q2::kBN;
+    const int64_t blocks = a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows);
+    // the streaming launch, with caches half full, at 6 bytes per ns
+    const double stream_us = static_cast<double>(a.B * a.H_kv) * (a.S_c / 2) * (a.D_qk + a.D_v) * 2.0 / 6e6;
     int best = 1;
     double best_us = 0.0;
     for (int n = 1; n <= st::kMaxShares && n <= tiles; ++n) {
-        const double waves = static_cast<double>((blocks * n + sms - 1) / sms);
-        const double us = waves * (1.5 * static_cast<double>((tiles + n - 1) / n) + 4.0) +
-                          static_cast<double>(rows) * n * (D_v + 3) * 8e-6 / 5.0;
+        const double unit_us = 8.0 + 1.6 * static_cast<double>((tiles + n - 1) / n);
+        const double latency = static_cast<double>((blocks * n + sms - 1) / sms) * unit_us;
+        const double machine = static_cast<double>(blocks * n) * unit_us / sms + stream_us + 0.1 * n;
+        const double us = latency / 0.45 > machine ? latency / 0.45 : machine;
         if (n == 1 || us < best_us) {
             best = n;
             best_us = us;
@@ -89,25 +103,24 @@ Plan plan_of(const Args &a, int sms) {
     Plan p{};
     const int64_t kv_units = a.B * a.H_kv * z.tiles_b;
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
-    // reading the prefix once per sequence and row tile costs no more than a launch when it is this small
     const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
-    p.seq_tiles = a.dtype == VT_BF16 && z.per_b > kSeqTileRows;
+    const bool f32 = a.dtype == VT_F32;
+    p.seq_tiles = !f32 && z.per_b > kSeqTileRows;
     if (p.seq_tiles) return p;
-    p.tiles = a.dtype == VT_BF16 && a.B * z.per_b > kTileRows;
-    p.with_prefix = again <= kReadAgain || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
-    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c, sms);
+    p.tiles = !f32 && a.B * z.per_b > kTileRows;
+    p.with_prefix = again <= (f32 ? kReadAgainF32 : kReadAgainBf16) || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
+    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, f32, sms);
     if (p.with_prefix) {
         p.tiles = false;
         return p;
     }
     if (p.tiles) {
-        const int64_t blocks = a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows);
-        p.prefix_shares = tile_shares(blocks, a.S_p, z.rows, a.D_v, sms);
+        p.prefix_shares = tile_shares(a, z, sms);
     } else {
         const int64_t units = a.H_kv * z.tiles_all;
-        p.prefix_cluster = cluster_for(units, a.S_p, sms);
+        p.prefix_cluster = cluster_for(units, a.S_p, f32, sms);
         int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
-        const int64_t most = a.S_p / (256LL * p.prefix_cluster);
+        const int64_t most = a.S_p / ((f32 ? 64LL : 256LL) * p.prefix_cluster);
         if (shares > most) shares = most;
         if (shares > st::kMaxShares) shares = st::kMaxShares;
         p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
