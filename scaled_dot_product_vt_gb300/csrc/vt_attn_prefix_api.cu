@@ -16,8 +16,9 @@ using Args = vt_attn_prefix_args;
 // workspace, from the two-tile tcgen05 kernel (`tiles`) or from the key-streaming kernel; the second launch streams
 // the caches and adds them.  Otherwise one launch streams the prefix and the cache of every sequence, or
 // (`seq_tiles`: many rows per sequence) takes them on the tcgen05 kernel.
+// (`merge`: the streaming launch leaves its results in the workspace too, and a third one adds them.)
 struct Plan {
-    bool tiles, seq_tiles, with_prefix;
+    bool tiles, seq_tiles, with_prefix, merge;
     int prefix_shares, prefix_cluster, cluster;
     size_t workspace;
 };
@@ -65,31 +66,32 @@ size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
     return ((static_cast<size_t>(rows) * shares * (partial_ld(D_v) + 3) * sizeof(float)) + 255) & ~size_t(255);
 }
 
-// CTAs of a cluster that share a unit's keys: two CTAs per SM in all, as long as every CTA keeps about 96 keys (four
-// drafted tokens over 256 keys: 46 us with 2, 53 us with 4).  The fp32 kernel fills an SM per CTA, and clusters of 8
-// then wait for room (26 us against 20 us with 4).
-int cluster_for(int64_t units, int64_t keys, bool f32, int sms) {
+// CTAs of a cluster that share a unit's keys: two CTAs per SM in all, as long as every CTA keeps `least` keys.  The
+// fp32 kernel fills an SM per CTA, and clusters of 8 then wait for room (26 us against 20 us with 4).
+int cluster_for(int64_t units, int64_t keys, int64_t least, bool f32, int sms) {
     int c = 1;
     const int most = f32 ? 4 : st::kMaxClusterCtas;
-    while (c < most && units * c < 2LL * sms && keys >= 2 * 96LL * c) c *= 2;
+    while (c < most && units * c < 2LL * sms && keys >= 2 * least * c) c *= 2;
     return c;
 }
 
-// Shares of the prefix for the tcgen05 kernel.  A unit takes about 1.6 us per 128-key tile (two query tiles) and 8 us
-// besides; its launch runs beside the streaming one, whose CTAs wait for it at their end, so it should be done well
-// before them, without spending more of the SMs than that needs.
-int tile_shares(const Args &a, const Sizes &z, int sms) {
-    const int64_t tiles = (a.S_p + q2::kBN - 1) / q2::kBN;
-    const int64_t blocks = a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows);
-    // the streaming launch, with caches half full, at 6 bytes per ns
-    const double stream_us = static_cast<double>(a.B * a.H_kv) * (a.S_c / 2) * (a.D_qk + a.D_v) * 2.0 / 6e6;
+// Shares of the prefix for the tcgen05 kernel.  A unit takes 1.6 us per 128-key tile (1 us when its rows fill one query
+// tile only) and 8 us besides; a streaming CTA takes 4.8 us besides its keys' time at 6 bytes per ns for all, three on
+// an SM.  The two launches run beside each other: the first should be done when both are, without more overhead
+// than that needs.
+int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
+    const int64_t tiles = (a.S_p + q2::kBN - 1) / q2::kBN, rows = a.B * z.per_b;
+    const int64_t blocks = a.H_kv * ((rows + q2::kRows - 1) / q2::kRows);
+    const double tile_us = rows > kBM ? 1.6 : 1.0;
+    const double stream_us = static_cast<double>(a.B * a.H_kv) * (a.S_c / 2) * (a.D_qk + a.D_v) * 2.0 / 6e6 +
+                             static_cast<double>(a.B * a.H_kv * z.tiles_b * cluster) * 4.8 / (3.0 * sms);
     int best = 1;
     double best_us = 0.0;
     for (int n = 1; n <= st::kMaxShares && n <= tiles; ++n) {
-        const double unit_us = 8.0 + 1.6 * static_cast<double>((tiles + n - 1) / n);
+        const double unit_us = 8.0 + tile_us * static_cast<double>((tiles + n - 1) / n);
         const double latency = static_cast<double>((blocks * n + sms - 1) / sms) * unit_us;
-        const double machine = static_cast<double>(blocks * n) * unit_us / sms + stream_us + 0.1 * n;
-        const double us = latency / 0.45 > machine ? latency / 0.45 : machine;
+        const double machine = static_cast<double>(blocks * n) * unit_us / sms + stream_us;
+        const double us = (latency > machine ? latency : machine) + 0.1 * n;
         if (n == 1 || us < best_us) {
             best = n;
             best_us = us;
@@ -109,23 +111,31 @@ Plan plan_of(const Args &a, int sms) {
     if (p.seq_tiles) return p;
     p.tiles = !f32 && a.B * z.per_b > kTileRows;
     p.with_prefix = again <= (f32 ? kReadAgainF32 : kReadAgainBf16) || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
-    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, f32, sms);
+    // keys a CTA should keep: with one launch latency counts (16 rows over 460 keys: 6.6 us with 4 CTAs, 7.1 us with
+    // 2), beside the tcgen05 kernel overhead does (256 keys: 38 us with 1, 43 us with 2); fp32 is bound by its products
+    const int64_t least = f32 ? 32 : (p.with_prefix || !p.tiles ? 96 : 192);
+    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, least, f32, sms);
     if (p.with_prefix) {
         p.tiles = false;
         return p;
     }
     if (p.tiles) {
-        p.prefix_shares = tile_shares(a, z, sms);
+        p.prefix_shares = tile_shares(a, z, p.cluster, sms);
     } else {
         const int64_t units = a.H_kv * z.tiles_all;
-        p.prefix_cluster = cluster_for(units, a.S_p, f32, sms);
+        p.prefix_cluster = cluster_for(units, a.S_p, f32 ? 32 : 96, f32, sms);
         int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
         const int64_t most = a.S_p / ((f32 ? 64LL : 256LL) * p.prefix_cluster);
         if (shares > most) shares = most;
         if (shares > st::kMaxShares) shares = st::kMaxShares;
         p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
     }
-    p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares);
+    // Streaming CTAs wait for the prefix's shares only where every CTA of both launches has room at once.
+    const int64_t per_sm = f32 ? 1 : 3;
+    const int64_t first = p.tiles ? per_sm * a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows) * p.prefix_shares
+                                  : a.H_kv * z.tiles_all * p.prefix_shares * p.prefix_cluster;
+    p.merge = first + kv_units * p.cluster > per_sm * sms;
+    p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares + (p.merge ? 1 : 0));
     return p;
 }
 
@@ -206,7 +216,7 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     p.kv_len = a.S_c > 0 ? a.kv_len : nullptr;
     p.rows = z.rows;
     if (plan.workspace) {
-        const int64_t n = z.rows * plan.prefix_shares;
+        const int64_t n = z.rows * (plan.prefix_shares + (plan.merge ? 1 : 0));
         p.part_o = static_cast<float *>(a.workspace);
         p.part_ld = static_cast<int>(partial_ld(a.D_v));
         p.part_m = p.part_o + n * p.part_ld;
@@ -391,6 +401,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
         VT_TRY(launch_tiles(a, plan, z, p, false, info, dev, stream));
     } else if (plan.prefix_shares) {
         p.all_rows = 1;
+        p.partial = 1;
         p.row_tiles = static_cast<int>(z.tiles_all);
         p.shares = plan.prefix_shares;
         p.cluster = plan.prefix_cluster;
@@ -401,8 +412,20 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.row_tiles = static_cast<int>(z.tiles_b);
     p.shares = 1;
     p.cluster = plan.cluster;
-    p.prior = plan.prefix_shares;
+    p.partial = plan.merge ? 1 : 0;
+    p.share0 = plan.merge ? plan.prefix_shares : 0;
+    p.prior = plan.merge ? 0 : plan.prefix_shares;
     VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b, p.cluster, plan.prefix_shares > 0, dev, stream));
+    if (plan.merge) {
+        p.prior = plan.prefix_shares + 1;
+        const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
+        // (an ordinary launch: it starts when both of the others have ended)
+        const bool bf = a.dtype == VT_BF16;
+        void (*kern)(const st::Params) = a.D_v <= 64 ? (bf ? st::attn_shares_kernel<uint16_t, 64> : st::attn_shares_kernel<float, 64>)
+                                                     : (bf ? st::attn_shares_kernel<uint16_t, 128> : st::attn_shares_kernel<float, 128>);
+        kern<<<blocks, 32 * st::kMergeWarps, 0, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    }
     return env_check() ? read_status(stream) : VT_OK;
 }
 

@@ -14,9 +14,10 @@
 //     bounds this kernel.  bf16 with fp32 accumulation; fp32 operands as two TF32 parts each, three products
 //     (hi hi + hi lo + lo hi), which keeps 21 bits of every factor.
 //   - At the end the warps of the cluster leave (max, sum, unnormalised O) in shared memory; each CTA combines its
-//     share of the rows over all of them through distributed shared memory, adds partial results of the prefix
-//     that an earlier launch left in the workspace, and writes O.  No merge launch and no atomics: the order of
-//     every sum is fixed.
+//     share of the rows over all of them through distributed shared memory.  Then either it adds the partial results of
+//     the prefix that an earlier launch leaves in the workspace and writes O, or (more CTAs than fit at once: those that
+//     wait for the earlier launch would keep the others out) it leaves one there itself and attn_shares_kernel adds
+//     them all.  No atomics: the order of every sum is fixed.
 #pragma once
 
 #include <type_traits>
@@ -31,8 +32,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;
 constexpr int kKeys = 16;        // keys per block of a warp
 constexpr int kMaxClusterCtas = 8;
-constexpr int kMaxShares = 32;   // partial results of the prefix, at most
-constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares;
+constexpr int kMaxShares = 31;   // partial results of the prefix, at most (and one of the caches)
+constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares + 1;
 static_assert(kMaxSources == 64, "a lane holds the weights of two sources");
 constexpr float kTau = 8.0f;     // the reference max moves when the running max exceeds it by 2^8 (see kTau of vt_attn_bf16_2q.cuh)
 
@@ -49,7 +50,8 @@ struct Params {
     float *part_o, *part_m, *part_l, *part_c;
     long long rows;
     int part_ld;  // floats between partial O rows
-    int prior;  // shares in the workspace to add (all_rows = 0)
+    int partial, share0;  // 1: write a partial result, to share0 and on; 0: write O
+    int prior;            // shares in the workspace to add (partial = 0)
     void *O;
     long long o_sb, o_sh, o_ss;
     float *lse;
@@ -154,6 +156,128 @@ struct Tile {
     static constexpr int kLdO = DV + 8;  // floats between result rows: eight rows' stores fall into different banks
     static_assert(kRowsTile * kLdO * 4 + 3 * kRowsTile * 4 <= kWarpBytes, "a warp's result takes the place of its stages");
 };
+
+// One row's answer from its sources (partial results), by one warp: every lane holds the weights of sources lane and
+// lane + 32 and sums DV / 32 columns over the sources in order, eight loads at a time.
+template <typename T, int DV>
+struct Combine {
+    static constexpr int kCols = DV / 32;
+    using Vec = typename std::conditional<kCols == 4, float4, float2>::type;
+    float M, Ls, Lo;   // max (log2 units), sum, and the sum as P V weighed it
+    float acc[kCols];
+    int col;
+
+    __device__ __forceinline__ Vec vec() const {
+        if constexpr (kCols == 4) return make_float4(acc[0], acc[1], acc[2], acc[3]);
+        else return make_float2(acc[0], acc[1]);
+    }
+
+    // row(src, col, v) loads a source's columns, stats(src, m, l, fix) its statistics
+    template <typename Row, typename Stats>
+    __device__ __forceinline__ void run(int lane, int n_src, Row row, Stats stats) {
+        constexpr int kAtOnce = 8, kPer = kMaxSources / 32;
+        col = lane * kCols;
+        Vec v[kAtOnce];
+        auto load_rows = [&](int s0) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                v[j] = Vec{};
+                if (s0 + j < n_src) row(s0 + j, col, v[j]);
+            }
+        };
+        load_rows(0);  // on their way while the weights are formed
+        float ms[kPer], ls[kPer], cs[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            ms[k] = -INFINITY;
+            ls[k] = cs[k] = 0.0f;
+            if (lane + 32 * k < n_src) stats(lane + 32 * k, ms[k], ls[k], cs[k]);
+        }
+        M = ms[0];
+#pragma unroll
+        for (int k = 1; k < kPer; ++k) M = fmaxf(M, ms[k]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        Ls = Lo = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            // the source's weight: 0 without keys (a sum that is NaN without a maximum stays NaN)
+            ms[k] = ms[k] == -INFINITY && ls[k] == 0.0f ? 0.0f : ex2(ms[k] - M);
+            Ls += ms[k] * ls[k];
+            Lo += ms[k] * (ls[k] + cs[k]);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) {
+            Ls += __shfl_xor_sync(0xffffffffu, Ls, x);
+            Lo += __shfl_xor_sync(0xffffffffu, Lo, x);
+        }
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+#pragma unroll 1
+        for (int s0 = 0; s0 < n_src; s0 += kAtOnce) {
+            if (s0 > 0) load_rows(s0);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const float w = __shfl_sync(0xffffffffu, s0 < 32 ? ms[0] : ms[1], (s0 + j) & 31);
+#pragma unroll
+                for (int x = 0; x < kCols; ++x) acc[x] = fmaf(w, reinterpret_cast<const float *>(&v[j])[x], acc[x]);
+            }
+        }
+    }
+
+    // O and LSE of row f of sequence b
+    __device__ __forceinline__ void store(const Params &p, int lane, int b, int hk, int f) {
+        const int s = f / p.G, h = hk * p.G + f - s * p.G;
+        const float inv = Ls == 0.0f ? 0.0f : 1.0f / Lo;  // a row without keys is 0
+        T *orow = static_cast<T *>(p.O) + b * p.o_sb + h * p.o_sh + s * p.o_ss + col;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] *= inv;
+        if (col + kCols <= p.D_v) {  // rows start on 16 bytes
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int k = 0; k < kCols; k += 2)
+                    *reinterpret_cast<uint32_t *>(orow + k) = pack_bf16x2(acc[k], acc[k + 1]);
+            } else {
+                *reinterpret_cast<Vec *>(orow) = vec();
+            }
+        } else {
+            for (int k = 0; k < kCols && col + k < p.D_v; ++k) {
+                if constexpr (sizeof(T) == 2)
+                    reinterpret_cast<uint16_t *>(orow)[k] = static_cast<uint16_t>(pack_bf16x2(acc[k], 0.0f) & 0xFFFFu);
+                else
+                    reinterpret_cast<float *>(orow)[k] = acc[k];
+            }
+        }
+        if (p.lse && lane == 0)
+            p.lse[(static_cast<long long>(b) * p.H + h) * p.S_q + s] =
+                Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
+    }
+};
+
+// The workspace's shares of every row combined into O: one warp per row.
+constexpr int kMergeWarps = 4;
+template <typename T, int DV>
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __grid_constant__ Params p) {
+    using C = Combine<T, DV>;
+    const int lane = threadIdx.x & 31;
+    const long long flat = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    if (flat >= p.rows) return;
+    C c;
+    c.run(
+        lane, p.prior,
+        [&](int src, int col, typename C::Vec &v) {
+            if (col < p.part_ld)
+                v = *reinterpret_cast<const typename C::Vec *>(p.part_o + (src * p.rows + flat) * p.part_ld + col);
+        },
+        [&](int src, float &m, float &l, float &fix) {
+            const long long at = src * p.rows + flat;
+            m = p.part_m[at];
+            l = p.part_l[at];
+            fix = p.part_c[at];
+        });
+    const int per_b = p.S_q * p.G, seq = static_cast<int>(flat) / per_b, hk = seq / p.B;  // rows stay below 2^30
+    c.store(p, lane, seq - hk * p.B, hk, static_cast<int>(flat) - seq * per_b);
+}
 
 template <typename T, int DQ, int DV>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
@@ -434,16 +558,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
     }
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
-    if (!p.all_rows) wait_prerequisites();  // (the whole grid waits, so that it ends after the prefix's launch)
+    if (p.prior) wait_prerequisites();  // (the whole grid waits, so that it ends after the prefix's launch)
 
-    // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row.  The sources of a
-    // row are the cluster's warps and the workspace's shares; every lane holds the weights of sources lane and
-    // lane + 32, then the sources' rows are added in order, eight loads at a time, DV / 32 columns per lane.
-    constexpr int kCols = DV / 32;
-    using VecC = typename std::conditional<kCols == 4, float4, float2>::type;
+    // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row, over the cluster's warps
+    // and the workspace's shares
+    using C = Combine<T, DV>;
     const uint32_t o_off = base, m_off = base + kRowsTile * L::kLdO * 4;
     const int n_smem = kWarps * p.cluster, n_src = n_smem + p.prior;
-    const int col = lane * kCols;
 #pragma unroll 1
     for (int i = rank + p.cluster * warp; i < n_rows; i += p.cluster * kWarps) {
         const int f = f0 + i;
@@ -452,105 +573,38 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
             const uint32_t at = off + (src % kWarps) * L::kWarpBytes;
             return p.cluster > 1 ? cluster_map(at, src / kWarps) : at;
         };
-        constexpr int kAtOnce = 8;
-        VecC v[kAtOnce];
-        auto load_rows = [&](int s0) {
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const int src = s0 + j;
-                v[j] = VecC{};
-                if (src < n_smem) v[j] = ld_cluster_vec<VecC>(warp_part(o_off, src) + (i * L::kLdO + col) * 4);
-                else if (src < n_src && col < p.part_ld)
-                    v[j] = *reinterpret_cast<const VecC *>(p.part_o + ((src - n_smem) * p.rows + flat) * p.part_ld + col);
-            }
-        };
-        load_rows(0);  // on their way while the weights are formed
-        float ms[kMaxSources / 32], ls[kMaxSources / 32], cs[kMaxSources / 32];
-#pragma unroll
-        for (int k = 0; k < kMaxSources / 32; ++k) {
-            const int src = lane + 32 * k;
-            ms[k] = -INFINITY;
-            ls[k] = cs[k] = 0.0f;
-            if (src < n_smem) {
-                const uint32_t at = warp_part(m_off, src) + i * 4;
-                ms[k] = ld_cluster(at);
-                ls[k] = ld_cluster(at + kRowsTile * 4);
-                cs[k] = ld_cluster(at + 2 * kRowsTile * 4);
-            } else if (src < n_src) {
-                const long long at = (src - n_smem) * p.rows + flat;
-                ms[k] = p.part_m[at];
-                ls[k] = p.part_l[at];
-                cs[k] = p.part_c[at];
-            }
-        }
-        float M = ms[0];
-#pragma unroll
-        for (int k = 1; k < kMaxSources / 32; ++k) M = fmaxf(M, ms[k]);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        float Ls = 0.0f, Lo = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMaxSources / 32; ++k) {
-            // the source's weight: 0 without keys (a sum that is NaN without a maximum stays NaN)
-            ms[k] = ms[k] == -INFINITY && ls[k] == 0.0f ? 0.0f : ex2(ms[k] - M);
-            Ls += ms[k] * ls[k];
-            Lo += ms[k] * (ls[k] + cs[k]);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) {
-            Ls += __shfl_xor_sync(0xffffffffu, Ls, x);
-            Lo += __shfl_xor_sync(0xffffffffu, Lo, x);
-        }
-        float acc[kCols];
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
-#pragma unroll 1
-        for (int s0 = 0; s0 < n_src; s0 += kAtOnce) {
-            if (s0 > 0) load_rows(s0);
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const float w = __shfl_sync(0xffffffffu, s0 < 32 ? ms[0] : ms[1], (s0 + j) & 31);
-#pragma unroll
-                for (int x = 0; x < kCols; ++x)
-                    acc[x] = fmaf(w, reinterpret_cast<const float *>(&v[j])[x], acc[x]);
-            }
-        }
-        if (p.all_rows) {
-            const long long at = share * p.rows + flat;
-            if (col < p.part_ld)
-                *reinterpret_cast<VecC *>(p.part_o + at * p.part_ld + col) = *reinterpret_cast<const VecC *>(acc);
+        C c;
+        c.run(
+            lane, n_src,
+            [&](int src, int col, typename C::Vec &v) {
+                if (src < n_smem) v = ld_cluster_vec<typename C::Vec>(warp_part(o_off, src) + (i * L::kLdO + col) * 4);
+                else if (col < p.part_ld)
+                    v = *reinterpret_cast<const typename C::Vec *>(p.part_o + ((src - n_smem) * p.rows + flat) * p.part_ld + col);
+            },
+            [&](int src, float &m, float &l, float &fix) {
+                if (src < n_smem) {
+                    const uint32_t at = warp_part(m_off, src) + i * 4;
+                    m = ld_cluster(at);
+                    l = ld_cluster(at + kRowsTile * 4);
+                    fix = ld_cluster(at + 2 * kRowsTile * 4);
+                } else {
+                    const long long at = (src - n_smem) * p.rows + flat;
+                    m = p.part_m[at];
+                    l = p.part_l[at];
+                    fix = p.part_c[at];
+                }
+            });
+        if (p.partial) {
+            const long long at = (p.share0 + share) * p.rows + flat;
+            if (c.col < p.part_ld)
+                *reinterpret_cast<typename C::Vec *>(p.part_o + at * p.part_ld + c.col) = c.vec();
             if (lane == 0) {
-                p.part_m[at] = M;
-                p.part_l[at] = Ls;
-                p.part_c[at] = Lo - Ls;
+                p.part_m[at] = c.M;
+                p.part_l[at] = c.Ls;
+                p.part_c[at] = c.Lo - c.Ls;
             }
         } else {
-            const int s = f / p.G, g = f - s * p.G;
-            const int h = hk * p.G + g;
-            const float inv = Ls == 0.0f ? 0.0f : 1.0f / Lo;  // a row without keys is 0
-            T *orow = static_cast<T *>(p.O) + b * p.o_sb + h * p.o_sh + s * p.o_ss + col;
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) acc[k] *= inv;
-            if (col + kCols <= p.D_v) {  // rows start on 16 bytes
-                if constexpr (kBf) {
-#pragma unroll
-                    for (int k = 0; k < kCols; k += 2)
-                        *reinterpret_cast<uint32_t *>(orow + k) = pack_bf16x2(acc[k], acc[k + 1]);
-                } else {
-                    *reinterpret_cast<VecC *>(orow) = *reinterpret_cast<const VecC *>(acc);
-                }
-            } else {
-                for (int k = 0; k < kCols && col + k < p.D_v; ++k) {
-                    if constexpr (kBf) {
-                        reinterpret_cast<uint16_t *>(orow)[k] = static_cast<uint16_t>(pack_bf16x2(acc[k], 0.0f) & 0xFFFFu);
-                    } else {
-                        reinterpret_cast<float *>(orow)[k] = acc[k];
-                    }
-                }
-            }
-            if (p.lse && lane == 0)
-                p.lse[(static_cast<long long>(b) * p.H + h) * p.S_q + s] =
-                    Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * 0.69314718055994531f;
+            c.store(p, lane, b, hk, f);
         }
     }
     if (p.cluster > 1) cluster_sync();  // the other CTAs have read this one's results
