@@ -370,6 +370,14 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _workspace_bytes(workspace, first) -> int:
+    if workspace is None:
+        return 0
+    if workspace.get_device() != first.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
+    return workspace.numel() * workspace.element_size()
+
+
 def _check(name, meta, dev, dtype, shape=None, dims=4):
     """Strides of a tensor of `dims` indices whose last one is contiguous, without the last."""
     t_shape, stride, t_dtype, t_dev = meta
@@ -558,7 +566,7 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
             dkw = torch.empty(D, dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = torch.empty(lib.vt_qk_rope_bwd_workspace_size(D), dtype=torch.uint8, device=dev)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_bytes = _workspace_bytes(workspace, dq_out)
     args = _QK_ROPE_PTRS.pack(_QK_ROPE_BYTES, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), freqs.data_ptr(),
                               positions.data_ptr(), dq.data_ptr(), _ptr(dk), 0, 0, 0) + rest
     rc = lib.vt_qk_rope_bwd(args, dq_out.data_ptr(), sgq, _ptr(dk_out), sgk, _ptr(dqw), _ptr(dkw), _ptr(workspace),
@@ -637,7 +645,7 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     args = _ATTN_PREFIX_PTRS.pack(_ATTN_PREFIX_BYTES, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache),
                                   _ptr(v_cache), _ptr(kv_len), out.data_ptr(), _ptr(lse), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size()) + rest
+                                  _workspace_bytes(workspace, q)) + rest
     rc = load().vt_attn_fwd_prefix(args, torch._C._cuda_getCurrentRawStream(q.get_device()))
     if rc != 0:
         raise VtError(rc, "vt_attn_fwd_prefix")

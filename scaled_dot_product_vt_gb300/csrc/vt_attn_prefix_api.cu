@@ -16,10 +16,11 @@ using Args = vt_attn_prefix_args;
 // workspace, from the two-tile tcgen05 kernel (`tiles`) or from the key-streaming kernel; the second launch streams
 // the caches and adds them.  Otherwise one launch streams the prefix and the cache of every sequence, or
 // (`seq_tiles`: many rows per sequence) takes them on the tcgen05 kernel.
-// (`merge`: the streaming launch leaves its results in the workspace too, and a third one adds them.)
+// (`merge`: the streaming launch leaves its results in the workspace too, and a last one adds them.)
 struct Plan {
     bool tiles, seq_tiles, with_prefix, merge;
     int prefix_shares, prefix_cluster, cluster;
+    int shares;  // of the streaming launch's keys, beyond a cluster's CTAs (more than 1: merge)
     size_t workspace;
 };
 
@@ -107,6 +108,7 @@ Plan plan_of(const Args &a, int sms) {
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
     const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
     const bool f32 = a.dtype == VT_F32;
+    p.shares = 1;
     p.seq_tiles = !f32 && z.per_b > kSeqTileRows;
     if (p.seq_tiles) return p;
     p.tiles = !f32 && a.B * z.per_b > kTileRows;
@@ -115,8 +117,18 @@ Plan plan_of(const Args &a, int sms) {
     // 2), beside the tcgen05 kernel overhead does (256 keys: 38 us with 1, 43 us with 2); fp32 is bound by its products
     const int64_t least = f32 ? 32 : (p.with_prefix || !p.tiles ? 96 : 192);
     p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, least, f32, sms);
+    const int64_t keys = (p.with_prefix ? a.S_p : 0) + a.S_c / 2;
+    if (kv_units * p.cluster < sms && keys >= 2 * 256LL * p.cluster) {
+        // few units of many keys (one sequence of 65536 tokens: 105 us without): shares of 256 keys a CTA or more
+        int64_t n = 2LL * sms / (kv_units * p.cluster);
+        if (n > keys / (256LL * p.cluster)) n = keys / (256LL * p.cluster);
+        if (n > st::kMaxCacheShares) n = st::kMaxCacheShares;
+        p.shares = static_cast<int>(n);
+    }
     if (p.with_prefix) {
         p.tiles = false;
+        p.merge = p.shares > 1;
+        p.workspace = p.merge ? partial_bytes(z.rows, a.D_v, p.shares) : 0;
         return p;
     }
     if (p.tiles) {
@@ -134,8 +146,8 @@ Plan plan_of(const Args &a, int sms) {
     const int64_t per_sm = f32 ? 1 : 3;
     const int64_t first = p.tiles ? per_sm * a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows) * p.prefix_shares
                                   : a.H_kv * z.tiles_all * p.prefix_shares * p.prefix_cluster;
-    p.merge = first + kv_units * p.cluster > per_sm * sms;
-    p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares + (p.merge ? 1 : 0));
+    p.merge = p.shares > 1 || first + kv_units * p.cluster > per_sm * sms;
+    p.workspace = partial_bytes(z.rows, a.D_v, p.prefix_shares + (p.merge ? p.shares : 0));
     return p;
 }
 
@@ -216,7 +228,7 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     p.kv_len = a.S_c > 0 ? a.kv_len : nullptr;
     p.rows = z.rows;
     if (plan.workspace) {
-        const int64_t n = z.rows * (plan.prefix_shares + (plan.merge ? 1 : 0));
+        const int64_t n = z.rows * (plan.prefix_shares + (plan.merge ? plan.shares : 0));
         p.part_o = static_cast<float *>(a.workspace);
         p.part_ld = static_cast<int>(partial_ld(a.D_v));
         p.part_m = p.part_o + n * p.part_ld;
@@ -410,14 +422,14 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.all_rows = 0;
     p.with_prefix = plan.with_prefix ? 1 : 0;
     p.row_tiles = static_cast<int>(z.tiles_b);
-    p.shares = 1;
+    p.shares = plan.shares;
     p.cluster = plan.cluster;
     p.partial = plan.merge ? 1 : 0;
     p.share0 = plan.merge ? plan.prefix_shares : 0;
     p.prior = plan.merge ? 0 : plan.prefix_shares;
-    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b, p.cluster, plan.prefix_shares > 0, dev, stream));
+    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b * p.shares, p.cluster, plan.prefix_shares > 0, dev, stream));
     if (plan.merge) {
-        p.prior = plan.prefix_shares + 1;
+        p.prior = plan.prefix_shares + plan.shares;
         const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
         // (an ordinary launch: it starts when both of the others have ended)
         const bool bf = a.dtype == VT_BF16;

@@ -32,8 +32,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;
 constexpr int kKeys = 16;        // keys per block of a warp
 constexpr int kMaxClusterCtas = 8;
-constexpr int kMaxShares = 31;   // partial results of the prefix, at most (and one of the caches)
-constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares + 1;
+constexpr int kMaxShares = 32;       // partial results of the prefix, at most
+constexpr int kMaxCacheShares = 32;  // and of the caches
+constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares;
+static_assert(kMaxSources >= kMaxShares + kMaxCacheShares, "attn_shares_kernel reads both");
 static_assert(kMaxSources == 64, "a lane holds the weights of two sources");
 constexpr float kTau = 8.0f;     // the reference max moves when the running max exceeds it by 2^8 (see kTau of vt_attn_bf16_2q.cuh)
 
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
     unsigned u = blockIdx.x / p.cluster;
     const int rank = static_cast<int>(blockIdx.x - u * p.cluster);
     int share = 0;
-    if (p.all_rows) {
+    if (p.shares > 1) {
         share = static_cast<int>(u % p.shares);
         u /= p.shares;
     }

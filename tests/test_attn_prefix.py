@@ -174,6 +174,9 @@ CASES = [
     ("bf16", 5, 8, 1, 33, 1000, 0, 128, 72),
     ("bf16", 40, 6, 2, 90, 70, 91, 40, 128),      # more of them than SMs
     ("bf16", 70, 4, 2, 1, 1000, 37, 64, 33),      # an odd value width in the shares
+    ("bf16", 1, 4, 1, 2, 0, 20000, 128, 128),     # one sequence: its keys in shares
+    ("bf16", 2, 4, 2, 1, 9000, 9000, 96, 33),     # the same behind a prefix of its own launch
+    ("f32", 1, 2, 1, 1, 5000, 3000, 64, 64),
     ("f32", 1, 1, 1, 1, 1, 1, 4, 4),
     ("f32", 8, 8, 2, 1, 1000, 333, 72, 72),
     ("f32", 40, 8, 2, 1, 1500, 40, 128, 128),
