@@ -284,8 +284,9 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
  *       with (u, v) = (i, i + R/2)   interleaved = 0
  *            (u, v) = (2i, 2i + 1)   interleaved != 0
  *   y_j = n_j for j >= R.
- * Everything between x and y is fp32 (the angle is formed in fp64, so far positions keep their phase) and y is
- * rounded once.  Several position axes (time, height, width of a video patch) need one row of `positions` each;
+ * Everything between x and y is fp32 and y is rounded once; the angle keeps its phase at any position (it is formed in
+ * fractions of a turn, 64 bits wide).  A row whose sum of squares leaves fp32's range becomes 0, and with eps = 0 a row
+ * of zeros becomes NaN.  Several position axes (time, height, width of a video patch) need one row of `positions` each;
  * pair_axis names the axis of every frequency pair, in any order.
  *
  * Append (kv_len not NULL): token s of sequence b belongs at cache row kv_len[b] - S + s, kv_len[b] being the
@@ -298,7 +299,8 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
  * Arguments, as a struct whose first field is its size.
  *   q, k          [B,H,S,D] and [B,H_kv,S,D]; k may be NULL with H_kv = 0 (one tensor only)
  *   q_out, k_out  as q and k, or (append) k_out the cache.  An output may be the same tensor as its input (same
- *                 pointer and strides); it must not overlap any input or output in another way.
+ *                 pointer and strides); it must not overlap any input or output in another way.  Heads beside each other
+ *                 in one tensor (Q, K and V of one projection) do not overlap.
  *   weights       [D] in the tensors' dtype, or NULL
  *   freqs         fp32 [R/2]; R even, 2 <= R <= D
  *   positions     int32, element strides pos_stride over (axis, b, s), 0 allowed (one row for the whole batch)

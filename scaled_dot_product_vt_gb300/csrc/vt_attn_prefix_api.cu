@@ -77,7 +77,7 @@ int cluster_for(int64_t units, int64_t keys, int64_t least, bool f32, int sms) {
 }
 
 // Shares of the prefix for the tcgen05 kernel.  A unit takes 1.6 us per 128-key tile (1 us when its rows fill one query
-// tile only) and 8 us besides; a streaming CTA takes 4.8 us besides its keys' time at 6 bytes per ns for all, three on
+// tile only) and 8 us besides; a streaming CTA takes 4.8 us besides its keys' time at 6 bytes per ns for all, three or four on
 // an SM.  The two launches run beside each other: the first should be done when both are, without more overhead
 // than that needs.
 int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
@@ -85,7 +85,7 @@ int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
     const int64_t blocks = a.H_kv * ((rows + q2::kRows - 1) / q2::kRows);
     const double tile_us = rows > kBM ? 1.6 : 1.0;
     const double stream_us = static_cast<double>(a.B * a.H_kv) * (a.S_c / 2) * (a.D_qk + a.D_v) * 2.0 / 6e6 +
-                             static_cast<double>(a.B * a.H_kv * z.tiles_b * cluster) * 4.8 / (3.0 * sms);
+                             static_cast<double>(a.B * a.H_kv * z.tiles_b * cluster) * 4.8 / ((a.D_v <= 64 ? 4.0 : 3.0) * sms);
     int best = 1;
     double best_us = 0.0;
     for (int n = 1; n <= st::kMaxShares && n <= tiles; ++n) {
@@ -143,7 +143,7 @@ Plan plan_of(const Args &a, int sms) {
         p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
     }
     // Streaming CTAs wait for the prefix's shares only where every CTA of both launches has room at once.
-    const int64_t per_sm = f32 ? 1 : 3;
+    const int64_t per_sm = f32 ? 1 : (a.D_v <= 64 ? 4 : 3);
     const int64_t first = p.tiles ? per_sm * a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows) * p.prefix_shares
                                   : a.H_kv * z.tiles_all * p.prefix_shares * p.prefix_cluster;
     p.merge = p.shares > 1 || first + kv_units * p.cluster > per_sm * sms;
@@ -427,15 +427,24 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.partial = plan.merge ? 1 : 0;
     p.share0 = plan.merge ? plan.prefix_shares : 0;
     p.prior = plan.merge ? 0 : plan.prefix_shares;
-    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b * p.shares, p.cluster, plan.prefix_shares > 0, dev, stream));
+    p.follows = plan.prefix_shares > 0 ? 1 : 0;
+    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b * p.shares, p.cluster, p.follows != 0, dev, stream));
     if (plan.merge) {
         p.prior = plan.prefix_shares + plan.shares;
         const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
-        // (an ordinary launch: it starts when both of the others have ended)
         const bool bf = a.dtype == VT_BF16;
         void (*kern)(const st::Params) = a.D_v <= 64 ? (bf ? st::attn_shares_kernel<uint16_t, 64> : st::attn_shares_kernel<float, 64>)
                                                      : (bf ? st::attn_shares_kernel<uint16_t, 128> : st::attn_shares_kernel<float, 128>);
-        kern<<<blocks, 32 * st::kMergeWarps, 0, stream>>>(p);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(blocks);
+        cfg.blockDim = dim3(32 * st::kMergeWarps);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
     }
     return env_check() ? read_status(stream) : VT_OK;

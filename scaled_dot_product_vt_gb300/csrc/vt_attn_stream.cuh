@@ -54,6 +54,7 @@ struct Params {
     int part_ld;  // floats between partial O rows
     int partial, share0;  // 1: write a partial result, to share0 and on; 0: write O
     int prior;            // shares in the workspace to add (partial = 0)
+    int follows;          // started ahead of the prefix's launch's end
     void *O;
     long long o_sb, o_sh, o_ss;
     float *lse;
@@ -149,9 +150,11 @@ struct Tile {
     static constexpr uint32_t kPiece = kKeys * 128;
     static constexpr uint32_t kBytesK = DQ / kCols * kPiece, kBytesV = DV / kCols * kPiece, kBytesQ = kBytesK;
     static constexpr uint32_t kStage = kBytesK + kBytesV;
-    // 16 KB a warp, so that three CTAs share an SM and one's start and end hide behind the others' loads
-    // (fp32 at full width: 32 KB, one CTA)
-    static constexpr int kStages = kStage <= 4096 ? 4 : (kStage <= 6144 ? 3 : 2);
+    // Two or three blocks a warp (16 KB at full width), so that three CTAs share an SM, four with narrow values, and
+    // one's start and end hide behind the others' loads: 37 sequences of 32 heads over up to 333 keys, D 96 and 64,
+    // take 22 us with four and 28 us with three.  (fp32 at full width: 32 KB, one CTA.)
+    static constexpr int kStages = kStage <= 4096 ? 3 : 2;
+    static constexpr int kPerSm = kElt == 2 ? (DV == 64 ? 4 : 3) : 1;
     static constexpr uint32_t kWarpBytes = kStages * kStage;
     static constexpr uint32_t kQ = kWarps * kWarpBytes;
     static constexpr uint32_t kSmem = 1024 + kQ + kBytesQ;  // pieces start on 1024 bytes
@@ -261,6 +264,7 @@ constexpr int kMergeWarps = 4;
 template <typename T, int DV>
 __global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __grid_constant__ Params p) {
     using C = Combine<T, DV>;
+    wait_prerequisites();
     const int lane = threadIdx.x & 31;
     const long long flat = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
     if (flat >= p.rows) return;
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __g
 }
 
 template <typename T, int DQ, int DV>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Tile<T, DQ, DV>;
     constexpr bool kBf = sizeof(T) == 2;
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
     }
     if (p.cluster > 1) cluster_sync();
     else __syncthreads();
-    if (p.prior) wait_prerequisites();  // (the whole grid waits, so that it ends after the prefix's launch)
+    if (p.prior) wait_prerequisites();
 
     // ---- combine: this CTA takes rows rank, rank + cluster, ... of the unit, one warp per row, over the cluster's warps
     // and the workspace's shares
@@ -610,6 +614,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 1)
         }
     }
     if (p.cluster > 1) cluster_sync();  // the other CTAs have read this one's results
+    if (!p.all_rows && p.partial) {
+        // The launch that adds the shares may start, and waits for this one to end.  That has to be after the prefix's
+        // launch ends too, which nothing else sees to: one cluster stays until then.
+        launch_dependents();
+        if (p.follows && blockIdx.x < static_cast<unsigned>(p.cluster)) wait_prerequisites();
+    }
 }
 
 }  // namespace st

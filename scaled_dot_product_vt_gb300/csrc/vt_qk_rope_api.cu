@@ -18,6 +18,7 @@ struct Piece {
     const int64_t *st;  // nullptr: contiguous
     bool out;
     int side;           // 1: Q's, 2: K's, 3: V's, 0: none of them
+    int64_t n[3], D;    // (with st) extents
 };
 struct Pieces {
     Piece at[20];
@@ -30,8 +31,23 @@ bool same_tensor(const Piece &a, const Piece &b) {
     return a.p == b.p && a.st && b.st && std::memcmp(a.st, b.st, 3 * sizeof(int64_t)) == 0;
 }
 
+// Two tensors that are different heads of one: their rows lie beside each other (a projection that holds Q, K and V
+// side by side), so their spans overlap and their elements do not.
+bool beside(const Piece &x, const Piece &y, int elt) {
+    if (!x.st || !y.st) return false;
+    const Piece &a = x.span.lo <= y.span.lo ? x : y, &b = x.span.lo <= y.span.lo ? y : x;
+    if (a.n[0] != b.n[0] || a.n[2] != b.n[2]) return false;
+    if ((a.n[0] > 1 && a.st[0] != b.st[0]) || (a.n[2] > 1 && a.st[2] != b.st[2])) return false;
+    const int64_t delta = static_cast<int64_t>((b.span.lo - a.span.lo) / elt);
+    if (delta <= 0 || (a.n[1] > 1 && b.n[1] > 1 && a.st[1] != b.st[1])) return false;
+    const int64_t sh = a.n[1] > 1 ? a.st[1] : (b.n[1] > 1 ? b.st[1] : delta);
+    if (sh <= 0 || delta % sh || delta / sh < a.n[1]) return false;
+    const int64_t st[3] = {a.st[0], sh, a.st[2]};
+    return rows_disjoint(st, a.n[0], delta / sh + b.n[1], a.n[2], a.D > b.D ? a.D : b.D);
+}
+
 // No output overlaps another piece, but for an output that is the same tensor as one of these inputs.
-bool outputs_clear(const Pieces &ps, const void *in0, const void *in1, const void *in2 = nullptr,
+bool outputs_clear(const Pieces &ps, int elt, const void *in0, const void *in1, const void *in2 = nullptr,
                    const void *in3 = nullptr) {
     for (int i = 0; i < ps.n; ++i)
         for (int j = 0; j < ps.n; ++j) {
@@ -39,6 +55,7 @@ bool outputs_clear(const Pieces &ps, const void *in0, const void *in1, const voi
             if (i == j || !x.out || !overlap(x.span, y.span)) continue;
             const bool named = y.p == in0 || y.p == in1 || y.p == in2 || y.p == in3;
             if (named && !y.out && x.side == y.side && same_tensor(x, y)) continue;
+            if (beside(x, y, elt)) continue;
             return false;
         }
     return true;
@@ -79,7 +96,7 @@ vt_status add_tensor(Pieces *ps, const void *p, const int64_t st[3], int64_t B, 
     Span s;
     if (!span_of(p, st, B, H, S, D, elt, &s)) return VT_ERR_INVALID_ARG;
     if (out && !rows_disjoint(st, B, H, S, D)) return VT_ERR_INVALID_ARG;
-    ps->add({s, p, st, out, side});
+    ps->add({s, p, st, out, side, {B, H, S}, D});
     return VT_OK;
 }
 
@@ -88,7 +105,7 @@ vt_status add_vector(Pieces *ps, const void *p, int64_t n, int elt, int align, b
     if (reinterpret_cast<uintptr_t>(p) % align) return VT_ERR_MISALIGNED;
     Span s;
     if (!span_bytes(p, n * elt, &s)) return VT_ERR_INVALID_ARG;
-    ps->add({s, p, nullptr, out, 0});
+    ps->add({s, p, nullptr, out, 0, {}, 0});
     return VT_OK;
 }
 
@@ -111,7 +128,7 @@ vt_status add_common(const Args &a, int elt, Pieces *ps) {
     }
     Span s;
     if (!span_of(a.positions, a.pos_stride, a.axes, a.B, a.S, 1, 4, &s)) return VT_ERR_INVALID_ARG;
-    ps->add({s, a.positions, nullptr, false, 0});
+    ps->add({s, a.positions, nullptr, false, 0, {}, 0});
     return VT_OK;
 }
 
@@ -241,7 +258,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     }
     if (append) VT_TRY(add_vector(&ps, a.kv_len, a.B, 4, 4, false));
     // Q and (without an append) K may be rotated in place
-    if (!outputs_clear(ps, a.q, append ? nullptr : a.k)) return VT_ERR_INVALID_ARG;
+    if (!outputs_clear(ps, elt, a.q, append ? nullptr : a.k)) return VT_ERR_INVALID_ARG;
 
     int dev = 0;
     DeviceInfo info;
@@ -299,10 +316,10 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
         if (reinterpret_cast<uintptr_t>(ws) % 256) return VT_ERR_MISALIGNED;
         Span s;
         if (!span_bytes(ws, static_cast<int64_t>(bwd_workspace(a.D)), &s)) return VT_ERR_INVALID_ARG;
-        ps.add({s, ws, nullptr, true, 0});
+        ps.add({s, ws, nullptr, true, 0, {}, 0});
     }
     // dq may take the place of q or of dq_out, dk that of k or of dk_out
-    if (!outputs_clear(ps, gq, gk, a.q, a.k)) return VT_ERR_INVALID_ARG;
+    if (!outputs_clear(ps, elt, gq, gk, a.q, a.k)) return VT_ERR_INVALID_ARG;
     if (empty) {  // no token: the weights' gradients are 0
         if (dwq && cudaMemsetAsync(dwq, 0, a.D * sizeof(float), stream) != cudaSuccess) return VT_ERR_CUDA;
         if (dwk && cudaMemsetAsync(dwk, 0, a.D * sizeof(float), stream) != cudaSuccess) return VT_ERR_CUDA;

@@ -296,6 +296,23 @@ def test_runs_give_the_same_bits_on_any_stream_and_from_a_graph():
 
 
 @gpu
+def test_calls_at_once_on_two_streams():
+    # each with a workspace of its own: the launches of both are in flight together, and in each of three the last
+    # reads what the first two left
+    ps = [Problem("bf16", 70, 8, 2, 1, 3000, 200, 128, 128, seed=s) for s in (20, 21)]
+    torch = ps[0].torch
+    want = [p.run() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[p.run(stream=s) for p, s in zip(ps, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for w, g in zip(want, pair):
+            assert all(torch.equal(a, b) for a, b in zip(w, g))
+    assert all(vt.vt_last_device_status(s) == 0 for s in streams)
+
+
+@gpu
 def test_long_caches_pass_32_bit_offsets():
     import torch
     if not torch.cuda.is_available():

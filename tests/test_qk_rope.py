@@ -97,6 +97,12 @@ def test_valid_calls_reach_the_launch():
     assert vt.vt_qk_rope_fwd(pack(), None) == 4
     assert vt.vt_qk_rope_fwd(pack(qo=A, ko=2 * A), None) == 4           # in place
     assert vt.vt_qk_rope_fwd(pack(**CACHE), None) == 4
+    # Q and K as heads of one projection, in place: their spans interleave, their rows do not
+    fused = dict(qs=(256, 16, 64), qos=(256, 16, 64), ks=(256, 16, 64), kos=(256, 16, 64))
+    assert vt.vt_qk_rope_fwd(pack(q=A, qo=A, k=A + 64, ko=A + 64, **fused), None) == 4
+    assert vt.vt_qk_rope_fwd(pack(q=A, qo=A, k=A + 32, ko=A + 32, **fused), None) == 1   # K's head is Q's second
+    assert vt.vt_qk_rope_fwd(pack(q=A, qo=A, k=A + 48, ko=A + 48, **fused), None) == 1   # between two heads
+    assert vt.vt_qk_rope_fwd(pack(q=A, qo=A, k=A + 128, ko=A + 128, **fused), None) == 1  # the next token's row
     assert vt.vt_qk_rope_fwd(pack(**dict(CACHE, qo=A)), None) == 4
     assert vt.vt_qk_rope_fwd(pack(H_kv=0, k=0, ko=0), None) == 4
     assert vt.vt_qk_rope_fwd(pack(ps=(0, 0, 0)), None) == 4
@@ -296,6 +302,33 @@ def test_append_writes_its_rows_and_no_others(dtype, S, D, D_v):
     x.close(kc, kc64, size, 64, "cache")
     assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
     assert np.array_equal(vc.to(torch.float64).cpu().numpy(), vc64)
+
+
+@gpu
+def test_given_outputs_shared_positions_and_keys_alone():
+    x = Inputs("bf16", 3, 6, 2, 37, 64, 64, seed=12)
+    torch = x.torch
+    x.pos[:] = x.pos[:, :1]
+    x.cos, x.sin = x.cos[:1].repeat(3, 0), x.sin[:1].repeat(3, 0)
+    one = x.pos[0, 0].expand(3, -1)  # one row of positions for the batch: stride 0
+    room = torch.full((3, 37, 8, 80), 7.0, dtype=x.t, device="cuda")
+    q_out, k_out = room[:, :, :6, 8:72].transpose(1, 2), room[:, :, 6:, 8:72].transpose(1, 2)
+    got = vt.qk_rope(x.q, x.k, x.freqs, one, q_out=q_out, k_out=k_out, **x.form())
+    assert got[0] is q_out and got[1] is k_out
+    x.check_forward(*got)
+    assert (room[..., :8] == 7).all() and (room[..., 72:] == 7).all()
+    # Q and K of one projection, rotated where they are
+    room = torch.full((3, 37, 10, 64), 7.0, dtype=x.t, device="cuda")
+    q, k = room[:, :, :6].transpose(1, 2), room[:, :, 6:8].transpose(1, 2)
+    q.copy_(x.q)
+    k.copy_(x.k)
+    x.check_forward(*vt.qk_rope(q, k, x.freqs, one, q_out=q, k_out=k, **x.form()))
+    assert (room[:, :, 8:] == 7).all()
+    # an append of keys without values
+    cache = torch.zeros(3, 2, 50, 64, dtype=x.t, device="cuda")
+    lens = torch.full((3,), 40, dtype=torch.int32, device="cuda")
+    vt.qk_rope(x.q, x.k, x.freqs, one, k_out=cache, kv_len=lens, **x.form())
+    assert torch.equal(cache[:, :, 3:40], k_out) and not cache[:, :, 40:].any() and not cache[:, :, :3].any()
 
 
 @gpu
