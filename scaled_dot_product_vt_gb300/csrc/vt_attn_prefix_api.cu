@@ -85,7 +85,8 @@ int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
     const int64_t blocks = a.H_kv * ((rows + q2::kRows - 1) / q2::kRows);
     const double tile_us = rows > kBM ? 1.6 : 1.0;
     const double stream_us = static_cast<double>(a.B * a.H_kv) * (a.S_c / 2) * (a.D_qk + a.D_v) * 2.0 / 6e6 +
-                             static_cast<double>(a.B * a.H_kv * z.tiles_b * cluster) * 4.8 / ((a.D_v <= 64 ? 4.0 : 3.0) * sms);
+                             static_cast<double>(a.B * a.H_kv * z.tiles_b * cluster) * 4.8 /
+                                 static_cast<double>((a.D_v <= 64 ? 4 : 3) * sms);
     int best = 1;
     double best_us = 0.0;
     for (int n = 1; n <= st::kMaxShares && n <= tiles; ++n) {
@@ -100,6 +101,9 @@ int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
     }
     return best;
 }
+
+// Streaming CTAs that share an SM (Tile::kPerSm).
+int64_t ctas_per_sm(const Args &a) { return a.dtype == VT_F32 ? 1 : (a.D_v <= 64 ? 4 : 3); }
 
 Plan plan_of(const Args &a, int sms) {
     const Sizes z = sizes_of(a);
@@ -143,7 +147,7 @@ Plan plan_of(const Args &a, int sms) {
         p.prefix_shares = shares < 1 ? 1 : static_cast<int>(shares);
     }
     // Streaming CTAs wait for the prefix's shares only where every CTA of both launches has room at once.
-    const int64_t per_sm = f32 ? 1 : (a.D_v <= 64 ? 4 : 3);
+    const int64_t per_sm = ctas_per_sm(a);
     const int64_t first = p.tiles ? per_sm * a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows) * p.prefix_shares
                                   : a.H_kv * z.tiles_all * p.prefix_shares * p.prefix_cluster;
     p.merge = p.shares > 1 || first + kv_units * p.cluster > per_sm * sms;
@@ -428,7 +432,9 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     p.share0 = plan.merge ? plan.prefix_shares : 0;
     p.prior = plan.merge ? 0 : plan.prefix_shares;
     p.follows = plan.prefix_shares > 0 ? 1 : 0;
-    VT_TRY(launch_stream(a, maps, p, a.B * a.H_kv * z.tiles_b * p.shares, p.cluster, p.follows != 0, dev, stream));
+    const int64_t units = a.B * a.H_kv * z.tiles_b * p.shares;
+    p.longest_first = p.kv_len && a.B > 1 && a.B <= st::kMaxSorted && (plan.tiles || units * p.cluster > ctas_per_sm(a) * info.sms);
+    VT_TRY(launch_stream(a, maps, p, units, p.cluster, p.follows != 0, dev, stream));
     if (plan.merge) {
         p.prior = plan.prefix_shares + plan.shares;
         const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);

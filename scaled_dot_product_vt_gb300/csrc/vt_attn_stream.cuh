@@ -20,6 +20,7 @@
 //     them all.  No atomics: the order of every sum is fixed.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "vt_attn_common.cuh"
@@ -37,6 +38,7 @@ constexpr int kMaxCacheShares = 32;  // and of the caches
 constexpr int kMaxSources = kWarps * kMaxClusterCtas + kMaxShares;
 static_assert(kMaxSources >= kMaxShares + kMaxCacheShares, "attn_shares_kernel reads both");
 static_assert(kMaxSources == 64, "a lane holds the weights of two sources");
+constexpr int kMaxSorted = 32;   // sequences that every warp ranks by their lengths
 constexpr float kTau = 8.0f;     // the reference max moves when the running max exceeds it by 2^8 (see kTau of vt_attn_bf16_2q.cuh)
 
 struct Params {
@@ -55,6 +57,7 @@ struct Params {
     int partial, share0;  // 1: write a partial result, to share0 and on; 0: write O
     int prior;            // shares in the workspace to add (partial = 0)
     int follows;          // started ahead of the prefix's launch's end
+    int longest_first;    // units in the order of their sequences' lengths (B <= kMaxSorted)
     void *O;
     long long o_sb, o_sh, o_ss;
     float *lse;
@@ -285,6 +288,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __g
     c.store(p, lane, seq - hk * p.B, hk, static_cast<int>(flat) - seq * per_b);
 }
 
+// The sequence with the n-th longest cache (equal lengths in order), by a warp: when the CTAs of a launch do not all fit
+// at once, those of the longest sequences start first and the short ones fill the end (16 sequences of up to 8192
+// tokens: 51 us against 56 us; ranking more of them costs every CTA more than it gains).
+__device__ __forceinline__ int nth_longest(const Params &p, int n, int lane) {
+    const int mine = lane < p.B ? p.kv_len[lane] : INT_MIN;
+    int rank = 0;
+    for (int j = 0; j < p.B; ++j) {
+        const int other = __shfl_sync(0xffffffffu, mine, j);
+        rank += other > mine || (other == mine && j < lane);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, lane < p.B && rank == n)) - 1;
+}
+
 template <typename T, int DQ, int DV>
 __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
@@ -311,8 +327,9 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     }
     const int rt = static_cast<int>(u % p.row_tiles);
     u /= p.row_tiles;
-    const int b = static_cast<int>(u / p.H_kv);  // 0 with all_rows
+    int b = static_cast<int>(u / p.H_kv);  // 0 with all_rows
     const int hk = static_cast<int>(u) - b * p.H_kv;
+    if (p.longest_first) b = nth_longest(p, b, lane);
     const int per_b = p.S_q * p.G;
     const int group_rows = p.all_rows ? p.B * per_b : per_b;
     const int f0 = rt * kRowsTile;
