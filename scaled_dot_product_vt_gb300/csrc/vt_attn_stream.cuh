@@ -102,14 +102,15 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &l
     hi = tf32_of(__uint_as_float(x));
     lo = tf32_of(__uint_as_float(x) - __uint_as_float(hi));
 }
-__device__ __forceinline__ void mma_3xtf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d += a b by three products; the two small ones go to `low`, which may be d itself.
+__device__ __forceinline__ void mma_3xtf32(float (&d)[4], float (&low)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
     split_tf32(b0, bh[0], bl[0]);
     split_tf32(b1, bh[1], bl[1]);
-    mma_tf32(d, al, bh[0], bh[1]);
-    mma_tf32(d, ah, bl[0], bl[1]);
+    mma_tf32(low, al, bh[0], bh[1]);
+    mma_tf32(low, ah, bl[0], bl[1]);
     mma_tf32(d, ah, bh[0], bh[1]);
 }
 
@@ -415,6 +416,15 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
         for (int ks = 0; ks < kSteps; ++ks)
             ldsm4(q[ks], row + (ks >> 2) * L::kPiece + (((2 * (ks & 3) + odd) ^ (r & 7)) << 4));
     }
+    // The scale is folded into the exponent (one rounding, near 0 for the keys that count), so it has to be positive:
+    // its sign goes to the queries, and 0 becomes a factor that changes nothing.
+    const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
+    if (p.scale_log2 < 0.0f) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[ks][j] ^= kBf ? 0x80008000u : 0x80000000u;
+    }
     const int lim[2] = {g8 < n_rows ? own(f0 + g8) : 0, g8 + 8 < n_rows ? own(f0 + g8 + 8) : 0};
 
     float o[DV / 8][4];
@@ -452,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
 
         // ---- scores of 16 rows x 16 keys: s[n] holds keys 8 n + 2 t4, + 1 of rows g8 (0, 1) and g8 + 8 (2, 3)
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float low[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // fp32: the small products' own sums
         {
             // lane 8 j + i addresses row i of matrix j: keys 0-7 and 8-15, 16-byte columns 2 ks and 2 ks + 1
             const int key = (lane & 7) + ((lane >> 4) << 3);
@@ -465,15 +476,17 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
                     mma_bf16(s[0], q[ks], kb[0], kb[1]);
                     mma_bf16(s[1], q[ks], kb[2], kb[3]);
                 } else {
-                    mma_3xtf32(s[0], q[ks], kb[0], kb[1]);
-                    mma_3xtf32(s[1], q[ks], kb[2], kb[3]);
+                    mma_3xtf32(s[0], low[0], q[ks], kb[0], kb[1]);
+                    mma_3xtf32(s[1], low[1], q[ks], kb[2], kb[3]);
                 }
             }
         }
+        if (!kBf) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] *= p.scale_log2;
+                for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
+        }
         if (k0 < c0 ? n_keys < kKeys : k0 + kKeys > c0 + own_first) {  // some row does not see every key
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -492,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
             float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx *= scale;
             alpha[r] = 1.0f;
             if (mx > m[r] + kTau || (m[r] == -INFINITY && mx > -INFINITY)) {
                 alpha[r] = ex2(m[r] - mx);  // 0 for the first keys
@@ -504,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 2 * r; i < 2 * r + 2; ++i) {
-                    s[n][i] = ex2(s[n][i] - ref);
+                    s[n][i] = ex2(fmaf(s[n][i], scale, -ref));
                     sum += s[n][i];
                     // bf16: P V weighs P as rounded to bf16; c makes l + c the sum of those weights
                     if (kBf) fix += __uint_as_float(pack_bf16x2(0.0f, s[n][i]) & 0xFFFF0000u) - s[n][i];
@@ -547,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
                 for (int n = 0; n < DV / 8; ++n) {
                     const int col = (n & 3) * 8 + g8;
                     const uint32_t in = (n >> 2) * L::kPiece + (col & 3) * 4, unit = col >> 2;
-                    mma_3xtf32(o[n], a, *reinterpret_cast<const uint32_t *>(r0 + in + ((unit ^ (key & 7)) << 4)),
+                    mma_3xtf32(o[n], o[n], a, *reinterpret_cast<const uint32_t *>(r0 + in + ((unit ^ (key & 7)) << 4)),
                                *reinterpret_cast<const uint32_t *>(r1 + in + ((unit ^ ((key + 1) & 7)) << 4)));
                 }
             }
