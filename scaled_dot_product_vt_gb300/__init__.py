@@ -9,7 +9,6 @@ raises.  PyTorch is used for device memory and the current stream.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
 
@@ -338,7 +337,19 @@ def attn_fwd_general(q, k, v, scale: float | None = None, mask: str = "none", of
 # ---------------------------------------------------------------- token preparation
 
 # The wrappers below check a call and pack the fixed part of its arguments once per combination of shapes, strides,
-# types and options (the functions under lru_cache, which see no address), and add the addresses per call.
+# types, devices and options (a plan, which holds no address), and add the addresses per call.  What they read of each
+# tensor is written out: it is most of what a small call costs on the host, and a function for it half as much again.
+
+_MOST_PLANS = 4096
+_rope_plans, _rope_bwd_plans, _prefix_plans = {}, {}, {}
+
+
+def _keep(plans, key, plan):
+    if len(plans) >= _MOST_PLANS:
+        plans.clear()
+    plans[key] = plan
+    return plan
+
 
 def _elsewhere(fn, first, stream, args, kw):
     """Run a wrapper on another stream (a torch stream or a raw handle) or for tensors of another device than the
@@ -356,14 +367,9 @@ def _elsewhere(fn, first, stream, args, kw):
 
 
 def _here(t) -> bool:
-    """The tensor is on the current device."""
+    """The tensor is on the current CUDA device."""
     import torch
     return t.is_cuda and t.get_device() == torch.cuda.current_device()
-
-
-def _meta(t):
-    """What the checks need to know of a tensor (None: absent)."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
 def _ptr(t) -> int:
@@ -431,7 +437,6 @@ def _pair_axis_bytes(pair_axis, pairs: int, axes: int) -> bytes:
 _NO3 = (0, 0, 0)
 
 
-@functools.lru_cache(maxsize=1024)
 def _rope_plan(q, k, freqs, positions, q_weight, k_weight, q_out, k_out, kv_len, v, v_out, pair_axis, interleaved, eps):
     """Checks of a qk_rope call from its tensors' metadata; the packed fixed part of its arguments."""
     import torch
@@ -500,9 +505,21 @@ def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False
     import torch
     if pair_axis is not None and type(pair_axis) is not tuple:
         pair_axis = tuple(pair_axis)
-    rest = _rope_plan(_meta(q), _meta(k), _meta(freqs), _meta(positions), _meta(q_weight), _meta(k_weight),
-                      _meta(q_out), _meta(k_out), _meta(kv_len), _meta(v), _meta(v_out), pair_axis, bool(interleaved),
-                      eps)
+    key = ((q.shape, q.stride(), q.dtype, q.get_device()),
+           None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
+           (freqs.shape, freqs.stride(), freqs.dtype, freqs.get_device()),
+           (positions.shape, positions.stride(), positions.dtype, positions.get_device()),
+           None if q_weight is None else (q_weight.shape, q_weight.stride(), q_weight.dtype, q_weight.get_device()),
+           None if k_weight is None else (k_weight.shape, k_weight.stride(), k_weight.dtype, k_weight.get_device()),
+           None if q_out is None else (q_out.shape, q_out.stride(), q_out.dtype, q_out.get_device()),
+           None if k_out is None else (k_out.shape, k_out.stride(), k_out.dtype, k_out.get_device()),
+           None if kv_len is None else (kv_len.shape, kv_len.stride(), kv_len.dtype, kv_len.get_device()),
+           None if v is None else (v.shape, v.stride(), v.dtype, v.get_device()),
+           None if v_out is None else (v_out.shape, v_out.stride(), v_out.dtype, v_out.get_device()),
+           pair_axis, bool(interleaved), eps)
+    rest = _rope_plans.get(key)
+    if rest is None:
+        rest = _keep(_rope_plans, key, _rope_plan(*key))
     if q_out is None:
         q_out = _new_rows(q.shape, q.dtype, q.device)
     if k_out is None and k is not None:
@@ -516,7 +533,6 @@ def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False
     return q_out, k_out
 
 
-@functools.lru_cache(maxsize=1024)
 def _rope_bwd_plan(gq, gk, freqs, positions, q, k, q_weight, k_weight, dq, dk, pair_axis, interleaved, eps):
     """Checks of a qk_rope_bwd call from its tensors' metadata: (packed fixed part of its arguments, strides of dq_out,
     strides of dk_out)."""
@@ -548,9 +564,21 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
     import torch
     if pair_axis is not None and type(pair_axis) is not tuple:
         pair_axis = tuple(pair_axis)
-    rest, sgq, sgk = _rope_bwd_plan(_meta(dq_out), _meta(dk_out), _meta(freqs), _meta(positions), _meta(q), _meta(k),
-                                    _meta(q_weight), _meta(k_weight), _meta(dq), _meta(dk), pair_axis,
-                                    bool(interleaved), eps)
+    key = ((dq_out.shape, dq_out.stride(), dq_out.dtype, dq_out.get_device()),
+           None if dk_out is None else (dk_out.shape, dk_out.stride(), dk_out.dtype, dk_out.get_device()),
+           (freqs.shape, freqs.stride(), freqs.dtype, freqs.get_device()),
+           (positions.shape, positions.stride(), positions.dtype, positions.get_device()),
+           None if q is None else (q.shape, q.stride(), q.dtype, q.get_device()),
+           None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
+           None if q_weight is None else (q_weight.shape, q_weight.stride(), q_weight.dtype, q_weight.get_device()),
+           None if k_weight is None else (k_weight.shape, k_weight.stride(), k_weight.dtype, k_weight.get_device()),
+           None if dq is None else (dq.shape, dq.stride(), dq.dtype, dq.get_device()),
+           None if dk is None else (dk.shape, dk.stride(), dk.dtype, dk.get_device()),
+           pair_axis, bool(interleaved), eps)
+    plan = _rope_bwd_plans.get(key)
+    if plan is None:
+        plan = _keep(_rope_bwd_plans, key, _rope_bwd_plan(*key))
+    rest, sgq, sgk = plan
     dt, dev = dq_out.dtype, dq_out.device
     if dq is None:
         dq = _new_rows(dq_out.shape, dt, dev)
@@ -578,7 +606,6 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
 
 # ---------------------------------------------------------------- attention behind a shared prefix
 
-@functools.lru_cache(maxsize=1024)
 def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, scale):
     """Checks of an attn_fwd_prefix call from its tensors' metadata: (packed fixed part of its arguments, shape of O,
     bytes of workspace)."""
@@ -634,8 +661,19 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
         return _elsewhere(attn_fwd_prefix, q, stream, (q, k_prefix, v_prefix, k_cache, v_cache, kv_len), dict(
             scale=scale, return_lse=return_lse, out=out, lse=lse, workspace=workspace))
     import torch
-    rest, o_shape, need = _prefix_plan(_meta(q), _meta(k_prefix), _meta(v_prefix), _meta(k_cache), _meta(v_cache),
-                                       _meta(kv_len), _meta(out), _meta(lse), scale)
+    key = ((q.shape, q.stride(), q.dtype, q.get_device()),
+           None if k_prefix is None else (k_prefix.shape, k_prefix.stride(), k_prefix.dtype, k_prefix.get_device()),
+           None if v_prefix is None else (v_prefix.shape, v_prefix.stride(), v_prefix.dtype, v_prefix.get_device()),
+           None if k_cache is None else (k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.get_device()),
+           None if v_cache is None else (v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.get_device()),
+           None if kv_len is None else (kv_len.shape, kv_len.stride(), kv_len.dtype, kv_len.get_device()),
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()),
+           None if lse is None else (lse.shape, lse.stride(), lse.dtype, lse.get_device()),
+           scale)
+    plan = _prefix_plans.get(key)
+    if plan is None:
+        plan = _keep(_prefix_plans, key, _prefix_plan(*key))
+    rest, o_shape, need = plan
     dev = q.device
     if out is None:
         out = _new_rows(o_shape, q.dtype, dev)
