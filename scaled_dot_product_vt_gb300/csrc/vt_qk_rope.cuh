@@ -27,7 +27,7 @@ namespace rope {
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
 constexpr int kMaxD = 256;
-constexpr int kAhead = 6, kAheadBwd = 4;  // rows a thread has under way (32 bytes each, the backward's 64)
+constexpr int kAhead = 4, kAheadBwd = 3;  // rows a thread has under way (32 bytes each, the backward's 64); more gain nothing
 constexpr int kBwdMaxBlocks = 608;  // blocks of a backward launch, each leaves one partial weight gradient
 
 struct Params {
@@ -310,10 +310,25 @@ __device__ __forceinline__ void chunk_angles(int chunk, bool in, const float2 *c
     }
 }
 
-// Sum over the tpr lanes of a row (a power of two, aligned in the warp).
-__device__ __forceinline__ float row_sum(float v, int tpr) {
-    for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// Sums of N values over the tpr lanes of a row (a power of two, aligned in the warp); the two usual widths unrolled.
+template <int N, int LANES>
+__device__ __forceinline__ void row_sums_of(float (&v)[N]) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int tpr) {
+    if (tpr == 8) {
+        row_sums_of<N, 8>(v);
+    } else if (tpr == 16) {
+        row_sums_of<N, 16>(v);
+    } else {
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
 }
 
 // NC: chunks per thread (4 covers D = 256 in single elements).
@@ -463,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
                 }
                 ring.popped();
                 if (NORM) {
-                    const float2 rs = both(rsqrtf(row_sum(ss.x + ss.y, tpr) * inv_d + eps));
+                    float sum[1] = {ss.x + ss.y};
+                    row_sums(sum, tpr);
+                    const float2 rs = both(rsqrtf(sum[0] * inv_d + eps));
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -663,13 +680,10 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
                         dot = fma2(mul2(w[c].a[j], u[c].a[j]), z[c].a[j],
                                    fma2(mul2(w[c].b[j], u[c].b[j]), z[c].b[j], dot));
                     }
-                float s1 = ss.x + ss.y, d1 = dot.x + dot.y;
-                for (int o = tpr >> 1; o > 0; o >>= 1) {
-                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-                    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
-                }
-                const float rs = rsqrtf(s1 * inv_d + eps);
-                const float2 rs2 = both(rs), m2 = both(-rs * rs * rs * d1 * inv_d);
+                float sums[2] = {ss.x + ss.y, dot.x + dot.y};
+                row_sums(sums, tpr);
+                const float rs = rsqrtf(sums[0] * inv_d + eps);
+                const float2 rs2 = both(rs), m2 = both(-rs * rs * rs * sums[1] * inv_d);
                 if (i < mine) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
