@@ -110,13 +110,14 @@ Plan plan_of(const Args &a, int sms) {
     Plan p{};
     const int64_t kv_units = a.B * a.H_kv * z.tiles_b;
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
-    const int64_t again = kv_units * a.S_p * (a.D_qk + a.D_v) * elt;
+    // (a double: up to 2^70)
+    const double again = static_cast<double>(kv_units) * static_cast<double>(a.S_p * (a.D_qk + a.D_v) * elt);
     const bool f32 = a.dtype == VT_F32;
     p.shares = 1;
     p.seq_tiles = !f32 && z.per_b > kSeqTileRows;
     if (p.seq_tiles) return p;
     p.tiles = !f32 && a.B * z.per_b > kTileRows;
-    p.with_prefix = again <= (f32 ? kReadAgainF32 : kReadAgainBf16) || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
+    p.with_prefix = again <= static_cast<double>(f32 ? kReadAgainF32 : kReadAgainBf16) || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
     // keys a CTA should keep: with one launch latency counts (16 rows over 460 keys: 6.6 us with 4 CTAs, 7.1 us with
     // 2), beside the tcgen05 kernel overhead does (256 keys: 38 us with 1, 43 us with 2); fp32 is bound by its products
     const int64_t least = f32 ? 32 : (p.with_prefix || !p.tiles ? 96 : 192);

@@ -395,3 +395,11 @@ def test_steps_of_a_batch_behind_a_prefix(dtype, S):
         p.q64 = q_rot.double().cpu().numpy()
         p.kc64, p.vc64 = p.kc.double().cpu().numpy(), p.vc.double().cpu().numpy()
         p.check(*out)
+
+
+# ---------------------------------------------------------------- sizes at the contract's limits (no GPU)
+
+def test_plan_of_the_largest_sizes():
+    """2^26 sequences of one row over 2^28 shared keys: the prefix read once per sequence would be 2^64 bytes, so it is
+    read once for all of them, with partial results in the workspace."""
+    assert vt.vt_attn_prefix_workspace_size(1 << 26, 1, 1, 1, 1 << 28, 16, 128, 128, vt.VT_F32) > 0
