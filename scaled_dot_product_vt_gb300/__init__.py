@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import numbers
 import struct
 
 from ._build import LIB, LIB_DEBUG, build  # noqa: F401
@@ -429,6 +430,8 @@ def _pair_axis_bytes(pair_axis, pairs: int, axes: int) -> bytes:
         if axes != 1:
             raise ValueError("pair_axis is required with more than one position axis")
         pair_axis = (0,) * pairs
+    if not all(isinstance(a, numbers.Integral) for a in pair_axis):
+        raise TypeError("pair_axis must hold whole numbers")
     if len(pair_axis) != pairs or any(not 0 <= a < axes for a in pair_axis):
         raise ValueError(f"pair_axis must name one of the {axes} axes for each of the {pairs} pairs")
     return bytes(pair_axis).ljust(128, b"\0")
@@ -505,6 +508,8 @@ def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False
     import torch
     if pair_axis is not None and type(pair_axis) is not tuple:
         pair_axis = tuple(pair_axis)
+    if eps is not None and type(eps) is not float:
+        eps = float(eps)  # (a plan is kept by values: a tensor's may change)
     key = ((q.shape, q.stride(), q.dtype, q.get_device()),
            None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()),
            (freqs.shape, freqs.stride(), freqs.dtype, freqs.get_device()),
@@ -564,6 +569,8 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
     import torch
     if pair_axis is not None and type(pair_axis) is not tuple:
         pair_axis = tuple(pair_axis)
+    if eps is not None and type(eps) is not float:
+        eps = float(eps)  # (a plan is kept by values: a tensor's may change)
     key = ((dq_out.shape, dq_out.stride(), dq_out.dtype, dq_out.get_device()),
            None if dk_out is None else (dk_out.shape, dk_out.stride(), dk_out.dtype, dk_out.get_device()),
            (freqs.shape, freqs.stride(), freqs.dtype, freqs.get_device()),
@@ -661,6 +668,8 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
         return _elsewhere(attn_fwd_prefix, q, stream, (q, k_prefix, v_prefix, k_cache, v_cache, kv_len), dict(
             scale=scale, return_lse=return_lse, out=out, lse=lse, workspace=workspace))
     import torch
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)  # (a plan is kept by values: a tensor's may change)
     key = ((q.shape, q.stride(), q.dtype, q.get_device()),
            None if k_prefix is None else (k_prefix.shape, k_prefix.stride(), k_prefix.dtype, k_prefix.get_device()),
            None if v_prefix is None else (v_prefix.shape, v_prefix.stride(), v_prefix.dtype, v_prefix.get_device()),

@@ -403,3 +403,50 @@ def test_plan_of_the_largest_sizes():
     """2^26 sequences of one row over 2^28 shared keys: the prefix read once per sequence would be 2^64 bytes, so it is
     read once for all of them, with partial results in the workspace."""
     assert vt.vt_attn_prefix_workspace_size(1 << 26, 1, 1, 1, 1 << 28, 16, 128, 128, vt.VT_F32) > 0
+
+
+# ---------------------------------------------------------------- scalar arguments that change in place (no GPU)
+
+def test_scalar_arguments_are_read_in_every_call(monkeypatch):
+    """A scale or eps held in a tensor is taken at its value of the call, not at that of an earlier call with it."""
+    import torch
+    lib, seen = vt.load(), []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return getattr(lib, name)
+
+        def vt_attn_fwd_prefix(self, args, stream):
+            seen.append(vt._ATTN_PREFIX_REST.unpack(args[vt._ATTN_PREFIX_PTRS.size:])[9])
+            return 0
+
+        def vt_qk_rope_fwd(self, args, stream):
+            seen.append(vt._QK_ROPE_REST.unpack(args[vt._QK_ROPE_PTRS.size:])[12])
+            return 0
+
+        def vt_qk_rope_bwd(self, args, *rest):
+            seen.append(vt._QK_ROPE_REST.unpack(args[vt._QK_ROPE_PTRS.size:])[12])
+            return 0
+
+    monkeypatch.setattr(vt, "load", Recorder)
+    monkeypatch.setattr(vt, "_here", lambda t: True)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    q, kc = torch.zeros(1, 2, 1, 16), torch.zeros(1, 2, 8, 16)
+    freqs, pos = torch.ones(8), torch.zeros(1, 1, dtype=torch.int32)
+    ws = torch.zeros(2 * 608 * 16 * 4, dtype=torch.uint8)
+    number = torch.tensor(0.25)
+    calls = (lambda: vt.attn_fwd_prefix(q, None, None, kc, kc, scale=number),
+             lambda: vt.qk_rope(q, None, freqs, pos, eps=number),
+             lambda: vt.qk_rope_bwd(q, None, freqs, pos, q=q, eps=number, workspace=ws))
+    for call in calls:
+        for value in (0.25, 0.5):
+            number.fill_(value)
+            call()
+    assert seen == [0.25, 0.5] * 3
+
+
+def test_pair_axis_takes_whole_numbers_only():
+    import torch
+    with pytest.raises(TypeError):
+        vt._pair_axis_bytes((torch.tensor(0), torch.tensor(1)), 2, 2)
+    assert vt._pair_axis_bytes((0, np.int64(1)), 2, 2)[:2] == b"\0\1"
