@@ -376,7 +376,8 @@ size_t vt_qk_rope_bwd_workspace_size(int64_t D);
  *                        or past kv_len[b] hold has no influence.
  *   kv_len               int32 [B], 0 <= kv_len[b] <= S_c, read on the device (a captured call replays with new
  *                        lengths); NULL: S_c for every sequence.  A length outside that range counts as the nearest
- *                        one inside and records VT_ERR_DEVICE_BOUNDS in the stream's status word.
+ *                        one inside and records VT_ERR_DEVICE_BOUNDS in the stream's status word; not read when
+ *                        S_c = 0.
  *   lse                  fp32 [B,H,S_q] or NULL
  *   workspace            DEVICE scratch, 256-byte aligned, at least vt_attn_prefix_workspace_size bytes (may be
  *                        NULL when that is 0).  Every call writes what it reads there; two calls that share it must

@@ -363,6 +363,8 @@ def _elsewhere(fn, first, stream, args, kw):
             return fn(*args, **kw)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+    if stream.device != first.device:
+        raise ValueError("the stream must be of the tensors' device")
     with torch.cuda.stream(stream):
         return fn(*args, **kw)
 

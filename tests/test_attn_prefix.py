@@ -450,3 +450,18 @@ def test_pair_axis_takes_whole_numbers_only():
     with pytest.raises(TypeError):
         vt._pair_axis_bytes((torch.tensor(0), torch.tensor(1)), 2, 2)
     assert vt._pair_axis_bytes((0, np.int64(1)), 2, 2)[:2] == b"\0\1"
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """A stream belongs to a device: work on tensors of another one would silently run elsewhere."""
+    import types
+
+    import torch
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    on_0 = types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="device"):
+        vt._elsewhere(lambda: None, on_0, Stream(), (), {})
