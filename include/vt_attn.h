@@ -342,12 +342,13 @@ vt_status vt_qk_rope_fwd(const vt_qk_rope_args *args, vt_stream_t stream);
  * Gradients of vt_qk_rope_fwd (without the append).  With g the gradient of an output row, u its rotation by
  * the opposite angles, r = 1 / sqrt(mean(x^2) + eps) and z = r x:
  *   dw_j = sum over tokens and heads of u_j z_j,   dx = r (w u - z mean_j(w_j u_j z_j)),
- * and dx = u when normalize is 0.  In `args`: q, k are the forward's inputs (not read, and may be NULL, when
- * normalize is 0); q_out, k_out are dq and dk, written; kv_len must be NULL.  dq_out, dk_out are the gradients
- * of the forward's outputs, with their strides; dq may be dq_out, or q (same pointer and strides), and dk the
- * same way.  dq_weight, dk_weight: fp32 [D], written (each may be NULL), summed in an order that does not change from
- * call to call.  The workspace (256-byte aligned, at least vt_qk_rope_bwd_workspace_size bytes) holds partial
- * sums of the weight gradients; it is not used, and may be NULL, when normalize is 0 or both are NULL.
+ * and dx = u when normalize is 0.  The products w u x of a row are summed in fp32, like its squares.  In `args`: q, k
+ * are the forward's inputs (not read, and may be NULL, when normalize is 0); q_out, k_out are dq and dk, written;
+ * kv_len must be NULL.  dq_out, dk_out are the gradients of the forward's outputs, with their strides; dq may be dq_out,
+ * or q (same pointer and strides), and dk the same way.  dq_weight, dk_weight: fp32 [D], written (each may be NULL),
+ * summed in fp32, in an order that does not change from call to call.  The workspace (256-byte aligned, at least
+ * vt_qk_rope_bwd_workspace_size bytes) holds partial sums of the weight gradients; it is not used, and may be NULL, when
+ * normalize is 0 or both are NULL.
  */
 vt_status vt_qk_rope_bwd(const vt_qk_rope_args *args, const void *dq_out, const int64_t dq_out_stride[3],
                          const void *dk_out, const int64_t dk_out_stride[3], float *dq_weight, float *dk_weight,

@@ -674,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
             }
             ring.popped();
             if (NORM) {
-                // dx = rs w u - x rs^3 mean(w u x),  dw += u x rs
+                // z = rs x:  dx = rs (w u - z mean(w u z)),  dw += u z.  (rs^3 would leave fp32's range long before a row's
+                // sum of squares does.)
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -686,16 +687,17 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
                 float sums[2] = {ss.x + ss.y, dot.x + dot.y};
                 row_sums(sums, tpr);
                 const float rs = rsqrtf(sums[0] * inv_d + eps);
-                const float2 rs2 = both(rs), m2 = both(-rs * rs * rs * sums[1] * inv_d);
+                const float2 rs2 = both(rs), m2 = both(-(rs * sums[1]) * inv_d);
                 if (i < mine) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
                         for (int j = 0; j < P::kN; ++j) {
-                            dw[c].a[j] = fma2(mul2(u[c].a[j], rs2), z[c].a[j], dw[c].a[j]);
-                            dw[c].b[j] = fma2(mul2(u[c].b[j], rs2), z[c].b[j], dw[c].b[j]);
-                            u[c].a[j] = fma2(mul2(rs2, w[c].a[j]), u[c].a[j], mul2(m2, z[c].a[j]));
-                            u[c].b[j] = fma2(mul2(rs2, w[c].b[j]), u[c].b[j], mul2(m2, z[c].b[j]));
+                            const float2 za = mul2(z[c].a[j], rs2), zb = mul2(z[c].b[j], rs2);
+                            dw[c].a[j] = fma2(u[c].a[j], za, dw[c].a[j]);
+                            dw[c].b[j] = fma2(u[c].b[j], zb, dw[c].b[j]);
+                            u[c].a[j] = mul2(rs2, fma2(w[c].a[j], u[c].a[j], mul2(m2, za)));
+                            u[c].b[j] = mul2(rs2, fma2(w[c].b[j], u[c].b[j], mul2(m2, zb)));
                         }
                 }
             }
