@@ -362,7 +362,9 @@ def _elsewhere(fn, first, stream, args, kw):
         with torch.cuda.device(first.device):
             return fn(*args, **kw)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        # (torch takes an external stream of handle 0 for no handle, and makes a new stream)
+        stream = (torch.cuda.ExternalStream(int(stream), device=first.device) if int(stream)
+                  else torch.cuda.default_stream(first.device))
     if stream.device != first.device:
         raise ValueError("the stream must be of the tensors' device")
     with torch.cuda.stream(stream):
