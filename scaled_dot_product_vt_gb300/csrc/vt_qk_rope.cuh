@@ -496,10 +496,18 @@ __global__ void __launch_bounds__(kThreads, NC > 1 ? 1 : 3) fwd_kernel(const __g
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         P y;
+                        if (turn[c]) {
 #pragma unroll
-                        for (int j = 0; j < P::kN; ++j) {
-                            y.a[j] = fma2(x[c].a[j], ac_bs[c].a[j], mul2(x[c].b[j], ac_bs[c].b[j]));
-                            y.b[j] = fma2(x[c].a[j], as_bc[c].a[j], mul2(x[c].b[j], as_bc[c].b[j]));
+                            for (int j = 0; j < P::kN; ++j) {
+                                y.a[j] = fma2(x[c].a[j], ac_bs[c].a[j], mul2(x[c].b[j], ac_bs[c].b[j]));
+                                y.b[j] = fma2(x[c].a[j], as_bc[c].a[j], mul2(x[c].b[j], as_bc[c].b[j]));
+                            }
+                        } else {  // columns of their own: 0 times another's infinity would be NaN
+#pragma unroll
+                            for (int j = 0; j < P::kN; ++j) {
+                                y.a[j] = mul2(x[c].a[j], ac_bs[c].a[j]);
+                                y.b[j] = mul2(x[c].b[j], as_bc[c].b[j]);
+                            }
                         }
                         if (NC == 1 || has[c]) store_raw<T, VEC, INTER>(dst, at_a[c], at_b[c], D, y);
                     }
@@ -666,10 +674,14 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) bwd_kernel(const __
                     if (VEC == 1 && at_b[c] >= D) raw.hi.zero();
                     unpack<T, VEC, INTER>(raw, z[c]);
                 }
+                if (turn[c]) {
 #pragma unroll
-                for (int j = 0; j < P::kN; ++j) {
-                    u[c].a[j] = fma2(gv.a[j], ang[c].a[j], mul2(gv.b[j], ang[c].b[j]));
-                    u[c].b[j] = fma2(gv.b[j], ang[c].a[j], mul2(gv.a[j], neg2(ang[c].b[j])));
+                    for (int j = 0; j < P::kN; ++j) {
+                        u[c].a[j] = fma2(gv.a[j], ang[c].a[j], mul2(gv.b[j], ang[c].b[j]));
+                        u[c].b[j] = fma2(gv.b[j], ang[c].a[j], mul2(gv.a[j], neg2(ang[c].b[j])));
+                    }
+                } else {
+                    u[c] = gv;
                 }
             }
             ring.popped();

@@ -31,3 +31,24 @@ def test_rows_of_any_size_whose_squares_stay_in_range(dtype, exponent):
     x.eps = 0.0
     x.check_forward(*vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form()))
     x.check_backward(*vt.qk_rope_bwd(x.gq, x.gk, x.freqs, x.pos, q=x.q, k=x.k, **x.form()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 96, 64), ("bf16", 72, 48), ("bf16", 33, 14), ("bf16", 201, 150),
+                                       ("f32", 128, 64), ("f32", 36, 10)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_columns_that_are_not_rotated_are_copied(dtype, D, R, interleaved, value):
+    """Without the norm, y_j = x_j for j >= R: an infinity or NaN in one of them stays there, in both directions."""
+    x = Inputs(dtype, 1, 3, 1, 9, D, R, 1, False, interleaved, seed=14)
+    clean = vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form())[0].clone()
+    clean_b = vt.qk_rope_bwd(x.gq, x.gk, x.freqs, x.pos, **x.form())[0].clone()
+    for at in (R, D - 1, (R + D) // 2):
+        for t in (x.q, x.gq):
+            t[:, 1, 4, at] = value
+        clean[:, 1, 4, at] = clean_b[:, 1, 4, at] = value
+    got = vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form())[0]
+    got_b = vt.qk_rope_bwd(x.gq, x.gk, x.freqs, x.pos, **x.form())[0]
+    for a, b in ((got, clean), (got_b, clean_b)):
+        assert x.torch.equal(a.isnan(), b.isnan()) and x.torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+    assert x.torch.equal(got[..., R:].nan_to_num(7.0), x.q[..., R:].nan_to_num(7.0))
