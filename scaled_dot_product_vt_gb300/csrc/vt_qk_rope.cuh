@@ -267,7 +267,8 @@ struct Walk {
 
 // One angle per thread (tok * half <= kThreads): thread i forms that of token i / half and pair i % half.
 struct Angle {
-    int tl, j, slot;
+    static constexpr int kLost = 1 << 16;
+    int tl, j, slot;  // slot: plus kLost when the frequency is infinite or NaN, which fixed point cannot hold
     bool on;
     long long pos_off;
     unsigned long long turn;
@@ -280,6 +281,7 @@ struct Angle {
         on = tl < p.tok;
         pos_off = on ? p.axis[j] * p.pos_st[0] : 0;
         turn = on ? turns_of(p, j) : 0;
+        if (on && !isfinite(p.freqs[j])) slot += kLost;
     }
     __device__ __forceinline__ int position(const Params &p, const Walk &w) const {
         if (!on || w.t0 + tl >= p.tokens) return 0;
@@ -291,10 +293,12 @@ struct Angle {
     __device__ __forceinline__ void form(int pos, float2 *cs) const {
         // the product modulo 2^64 is the angle modulo a turn; its high word, read as signed, is in half turns
         const unsigned long long phase = turn * static_cast<unsigned long long>(static_cast<long long>(pos));
+        // (the high 32 bits, rounded to 24: an angle is off by at most pi 2^-25, about a cosine's own rounding)
         const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
         float sn, cn;
         sincospif(half_turns, &sn, &cn);
-        if (on) cs[slot] = make_float2(cn, sn);
+        if (slot >= kLost) cn = sn = NAN;
+        if (on) cs[slot & (kLost - 1)] = make_float2(cn, sn);
     }
 };
 

@@ -52,3 +52,16 @@ def test_columns_that_are_not_rotated_are_copied(dtype, D, R, interleaved, value
     for a, b in ((got, clean), (got_b, clean_b)):
         assert x.torch.equal(a.isnan(), b.isnan()) and x.torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
     assert x.torch.equal(got[..., R:].nan_to_num(7.0), x.q[..., R:].nan_to_num(7.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_frequency_that_is_no_number_reaches_its_pair(value):
+    x = Inputs("f32", 1, 2, 1, 7, 32, 32, 1, False, False, seed=15)
+    want = vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form())[0].clone()
+    x.freqs[3] = value
+    got = vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form())[0]
+    pair = [3, 19]
+    assert got[..., pair].isnan().all()
+    got[..., pair] = want[..., pair]
+    assert x.torch.equal(got, want)
