@@ -105,13 +105,27 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &l
     hi = tf32_of(__uint_as_float(x));
     lo = tf32_of(__uint_as_float(x) - __uint_as_float(hi));
 }
+// The same for a value that may be infinite beside a factor p >= 0: hi is then the largest number and lo the infinity, so
+// that p lo is that infinity and no product is NaN (as hi it would meet p's lo, which may be 0 or of either sign).  Rounding
+// in integers is the conversion's, without its slow unit (all NaN bits overflow to 0; lo is NaN then).
+__device__ __forceinline__ void split_tf32_inf(uint32_t x, uint32_t &hi, uint32_t &lo) {
+    hi = (x + 0x1000u) & 0xFFFFE000u;
+    if (fabsf(__uint_as_float(hi)) == INFINITY) hi -= 0x2000u;
+    lo = tf32_of(__uint_as_float(x) - __uint_as_float(hi));
+}
 // d += a b by three products; the two small ones go to `low`, which may be d itself.
+template <bool kInfB>
 __device__ __forceinline__ void mma_3xtf32(float (&d)[4], float (&low)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
-    split_tf32(b0, bh[0], bl[0]);
-    split_tf32(b1, bh[1], bl[1]);
+    if constexpr (kInfB) {
+        split_tf32_inf(b0, bh[0], bl[0]);
+        split_tf32_inf(b1, bh[1], bl[1]);
+    } else {
+        split_tf32(b0, bh[0], bl[0]);
+        split_tf32(b1, bh[1], bl[1]);
+    }
     mma_tf32(low, al, bh[0], bh[1]);
     mma_tf32(low, ah, bl[0], bl[1]);
     mma_tf32(d, ah, bh[0], bh[1]);
@@ -479,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
                     mma_bf16(s[0], q[ks], kb[0], kb[1]);
                     mma_bf16(s[1], q[ks], kb[2], kb[3]);
                 } else {
-                    mma_3xtf32(s[0], low[0], q[ks], kb[0], kb[1]);
-                    mma_3xtf32(s[1], low[1], q[ks], kb[2], kb[3]);
+                    mma_3xtf32<false>(s[0], low[0], q[ks], kb[0], kb[1]);
+                    mma_3xtf32<false>(s[1], low[1], q[ks], kb[2], kb[3]);
                 }
             }
         }
@@ -488,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] += low[n][i];
+                for (int i = 0; i < 4; ++i)  // (beside an infinity the small products may be NaN)
+                    if (fabsf(s[n][i]) != INFINITY) s[n][i] += low[n][i];
         }
         if (k0 < c0 ? n_keys < kKeys : k0 + kKeys > c0 + own_first) {  // some row does not see every key
 #pragma unroll
@@ -564,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
                 for (int n = 0; n < DV / 8; ++n) {
                     const int col = (n & 3) * 8 + g8;
                     const uint32_t in = (n >> 2) * L::kPiece + (col & 3) * 4, unit = col >> 2;
-                    mma_3xtf32(o[n], o[n], a, *reinterpret_cast<const uint32_t *>(r0 + in + ((unit ^ (key & 7)) << 4)),
+                    mma_3xtf32<true>(o[n], o[n], a, *reinterpret_cast<const uint32_t *>(r0 + in + ((unit ^ (key & 7)) << 4)),
                                *reinterpret_cast<const uint32_t *>(r1 + in + ((unit ^ ((key + 1) & 7)) << 4)));
                 }
             }

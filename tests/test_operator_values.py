@@ -3,8 +3,10 @@
 Tolerances are those of the tests whose inputs and checks are used here.
 """
 
+import numpy as np
 import pytest
 
+from test_attn_prefix import Problem
 from test_qk_rope import Inputs
 
 import scaled_dot_product_vt_gb300 as vt
@@ -65,3 +67,43 @@ def test_a_frequency_that_is_no_number_reaches_its_pair(value):
     assert got[..., pair].isnan().all()
     got[..., pair] = want[..., pair]
     assert x.torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- attention behind a prefix
+
+# streamed once; the prefix in a launch of its own, streamed and on tiles; rows of one sequence on tiles
+FORMS = [("f32", 3, 1, 50), ("f32", 40, 1, 1500), ("f32", 2, 40, 100), ("bf16", 3, 1, 50), ("bf16", 90, 1, 1100),
+         ("bf16", 2, 70, 300)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,S_q,S_p", FORMS)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinite_value_fills_its_column_alone(dtype, B, S_q, S_p, value):
+    p = Problem(dtype, B, 4, 2, S_q, S_p, 80, 64, 64, lens=[80] * B, seed=16)
+    before = p.run()[0].clone()
+    p.vp[:, 7, 11] = value            # every query sees the prefix
+    p.vc[0, :, 80 - S_q, 30] = value  # and this row of its own cache
+    o, lse = p.run()
+    assert (o[..., 11] == value).all() and (o[0, ..., 30] == value).all()
+    o[..., 11] = before[..., 11]
+    o[0, ..., 30] = before[0, ..., 30]
+    p.check(o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,S_q,S_p", FORMS)
+def test_a_key_whose_score_is_minus_infinity_has_no_weight(dtype, B, S_q, S_p):
+    p = Problem(dtype, B, 4, 2, S_q, S_p, 80, 64, 64, lens=[80] * B, seed=17)
+    p.q[..., 5] = 0.75  # (exact in both types)
+    p.q64[..., 5] = 0.75
+    p.kp[:, 9, 5] = -float("inf")
+    p.kc[:, :, 0, 5] = -float("inf")
+    got = p.run()
+    # the same rows as if those two keys were not there
+    p.kp64, p.vp64 = np.delete(p.kp64, 9, axis=2), np.delete(p.vp64, 9, axis=2)
+    p.kc64, p.vc64 = p.kc64[:, :, 1:], p.vc64[:, :, 1:]
+    B, H, H_kv, S_q, S_p, S_c, D_qk, D_v = p.dims
+    p.dims = (B, H, H_kv, S_q, S_p - 1, S_c - 1, D_qk, D_v)
+    p.lens = p.lens - 1
+    p.check(*got)
