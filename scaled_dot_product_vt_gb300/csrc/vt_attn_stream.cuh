@@ -434,13 +434,14 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
             ldsm4(q[ks], row + (ks >> 2) * L::kPiece + (((2 * (ks & 3) + odd) ^ (r & 7)) << 4));
     }
     // The scale is folded into the exponent (one rounding, near 0 for the keys that count), so it has to be positive:
-    // its sign goes to the queries, and 0 becomes a factor that changes nothing.
-    const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
-    if (p.scale_log2 < 0.0f) {
+    // its sign goes to the queries, and with a scale of 0 they become 0.
+    const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+    if (p.scale_log2 <= 0.0f) {
+        const uint32_t keep = p.scale_log2 == 0.0f ? 0u : ~0u, sign = keep & (kBf ? 0x80008000u : 0x80000000u);
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[ks][j] ^= kBf ? 0x80008000u : 0x80000000u;
+            for (int j = 0; j < 4; ++j) q[ks][j] = (q[ks][j] & keep) ^ sign;
     }
     const int lim[2] = {g8 < n_rows ? own(f0 + g8) : 0, g8 + 8 < n_rows ? own(f0 + g8 + 8) : 0};
 

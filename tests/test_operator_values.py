@@ -107,3 +107,16 @@ def test_a_key_whose_score_is_minus_infinity_has_no_weight(dtype, B, S_q, S_p):
     p.dims = (B, H, H_kv, S_q, S_p - 1, S_c - 1, D_qk, D_v)
     p.lens = p.lens - 1
     p.check(*got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,S_q,S_p", FORMS)
+@pytest.mark.parametrize("scale", [0.0, 1e-39])
+def test_a_scale_of_nothing_weighs_every_key_alike(dtype, B, S_q, S_p, scale):
+    """Scores of about 1e36 (64 products of less than 2^125, in fp32's range) times 0, or times 1e-39."""
+    p = Problem(dtype, B, 4, 2, S_q, S_p, 80, 64, 64, lens=[80] * B, seed=18, scale=scale)
+    big = 2.0 ** 59  # (exact)
+    for t, a in ((p.q, p.q64), (p.kp, p.kp64), (p.kc, p.kc64)):
+        t.mul_(big)
+        a *= big
+    p.check(*p.run())
