@@ -173,8 +173,10 @@ vt_status vt_attn_fwd_splitkv(const void *Q, const int64_t q_stride[3],
                               int n_split, void *workspace, size_t workspace_bytes,
                               vt_stream_t stream);
 
-/* Bytes of workspace vt_attn_fwd_splitkv needs (0 when n_split <= 1, an extent is not positive, or
- * the size overflows: no such workspace can exist, and such a call is rejected).
+/* Bytes of workspace that serve vt_attn_fwd_splitkv (0 when n_split <= 1, an extent is not positive, or the size
+ * overflows: no such workspace can exist, and such a call is rejected).  For D_v that is no multiple of 4 it counts
+ * partial rows rounded up to 8 floats; a call with D_v below 16 (bf16) or below 4 (fp32) takes packed rows of D_v
+ * floats, and with them a smaller workspace.
  * Host-only arithmetic: no GPU call. */
 size_t vt_attn_splitkv_workspace_size(int64_t B, int64_t H, int64_t S_q, int64_t D_v, int n_split);
 
@@ -193,9 +195,8 @@ int vt_attn_splitkv_choose(int64_t B, int64_t H, int64_t S_q, int64_t S_k, int c
  * The shares' partial results live in a fixed 32 MiB array inside this library (a static
  * __device__ array: every GPU that loads the library holds it until the process exits).  The call
  * itself allocates nothing.  Arguments and errors are those of vt_attn_fwd_splitkv without the
- * workspace; in addition, a problem whose partial results need more than 32 MiB
- * (vt_attn_splitkv_workspace_size(B, H, S_q, D_v, n_split) > 33554432) is rejected with
- * VT_ERR_UNSUPPORTED before anything runs.  n_split = 1 uses no scratch at all.
+ * workspace; in addition, a problem whose partial results need more than 32 MiB (33554432 bytes; see
+ * vt_attn_splitkv_workspace_size) is rejected with VT_ERR_UNSUPPORTED before anything runs.  n_split = 1 uses no scratch at all.
  *
  * The first call with n_split > 1 on a device looks up the array's device address
  * (cudaGetSymbolAddress) and remembers it; make that first call before any stream capture.  All

@@ -189,15 +189,15 @@ bool lse_span(const float *lse, int64_t B, int64_t H, int64_t S_q, Span *out) {
 struct SplitLayout {
     size_t o_off, m_off, l_off, c_off, bytes;
 };
-// bytes = 0 when the sizes overflow (no such workspace can exist).
-SplitLayout split_layout(int64_t B, int64_t H, int64_t S_q, int64_t D_v, int n_split) {
+// `ld` floats per partial output row; bytes = 0 when the sizes overflow (no such workspace can exist).
+SplitLayout split_layout(int64_t B, int64_t H, int64_t S_q, int64_t ld, int n_split) {
     auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
     SplitLayout L{};
     uint64_t rows = 0, per = 0, o_bytes = 0;
-    if (B <= 0 || H <= 0 || S_q <= 0 || D_v <= 0 || D_v > (int64_t(1) << 40) || n_split <= 0 ||
+    if (B <= 0 || H <= 0 || S_q <= 0 || ld <= 0 || n_split <= 0 ||
         __builtin_mul_overflow(uint64_t(B), uint64_t(H), &rows) || __builtin_mul_overflow(rows, uint64_t(S_q), &rows) ||
         __builtin_mul_overflow(rows, uint64_t(n_split) * sizeof(float), &per) ||
-        __builtin_mul_overflow(per, uint64_t(partial_ld(D_v)), &o_bytes) || o_bytes > (uint64_t(1) << 60) ||
+        __builtin_mul_overflow(per, uint64_t(ld), &o_bytes) || o_bytes > (uint64_t(1) << 60) ||
         per > (uint64_t(1) << 60))
         return L;
     L.o_off = 0;
@@ -327,10 +327,11 @@ vt_status launch(const Problem &P, const vt_attn_opts *opts, int n_split, void *
     p.cluster = 1;
     p.n_split = n_split;
     if (n_split > 1) {
-        const SplitLayout L = split_layout(B, H, S_q, D_v, n_split);
+        const int64_t ld = split_ld(D_v, DT == kBF16);
+        const SplitLayout L = split_layout(B, H, S_q, ld, n_split);
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         p.part_o = reinterpret_cast<float *>(ws + L.o_off);
-        p.part_ld = static_cast<int>(partial_ld(D_v));
+        p.part_ld = static_cast<int>(ld);
         p.part_m = reinterpret_cast<float *>(ws + L.m_off);
         p.part_l = reinterpret_cast<float *>(ws + L.l_off);
         p.part_c = reinterpret_cast<float *>(ws + L.c_off);
@@ -607,7 +608,7 @@ vt_status check_args(const Problem &P, bool *empty) {
 // Checks of a split-KV workspace (n_split > 1): present, large enough, 256-byte aligned and clear of
 // every tensor of the call.
 vt_status check_workspace(const Problem &P, int n_split, const void *workspace, size_t workspace_bytes) {
-    const size_t need = vt::split_layout(P.B, P.H, P.S_q, P.D_v, n_split).bytes;
+    const size_t need = vt::split_layout(P.B, P.H, P.S_q, vt::split_ld(P.D_v, P.dtype == VT_BF16), n_split).bytes;
     if (!workspace || need == 0 || workspace_bytes < need) return VT_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) % 256) return VT_ERR_MISALIGNED;
     const vt::Span w{reinterpret_cast<uintptr_t>(workspace), reinterpret_cast<uintptr_t>(workspace) + workspace_bytes};
@@ -699,8 +700,9 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3], const vo
 }
 
 size_t vt_attn_splitkv_workspace_size(int64_t B, int64_t H, int64_t S_q, int64_t D_v, int n_split) {
-    if (B <= 0 || H <= 0 || S_q <= 0 || D_v <= 0 || n_split <= 1) return 0;
-    return vt::split_layout(B, H, S_q, D_v, n_split).bytes;
+    if (B <= 0 || H <= 0 || S_q <= 0 || D_v <= 0 || D_v > (int64_t(1) << 40) || n_split <= 1) return 0;
+    // enough for either element type
+    return vt::split_layout(B, H, S_q, D_v % 4 == 0 ? D_v : vt::partial_ld(D_v), n_split).bytes;
 }
 
 int vt_attn_splitkv_choose(int64_t B, int64_t H, int64_t S_q, int64_t S_k, int causal, vt_dtype dtype) {
@@ -762,7 +764,7 @@ vt_status vt_attn_fwd_splitkv_noalloc(const void *Q, const int64_t q_stride[3], 
     void *scratch = nullptr;
     if (n_split > 1) {
         // The shares' partial results must fit the fixed array; nothing is allocated instead.
-        const size_t need = vt::split_layout(B, H, S_q, D_v, n_split).bytes;
+        const size_t need = vt::split_layout(B, H, S_q, vt::split_ld(D_v, dtype == VT_BF16), n_split).bytes;
         if (need == 0 || need > vt::kNoAllocScratchBytes) return VT_ERR_UNSUPPORTED;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return VT_ERR_CUDA;

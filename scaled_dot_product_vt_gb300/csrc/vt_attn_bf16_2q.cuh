@@ -956,8 +956,9 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 float *orow = p.part_o + part * p.part_ld;
                 if (n_my > 0) tc_fence_after();
                 // Two lanes store their two rows together, 64 bytes of one and then of the other: a warp's store then
-                // touches 16 lines, where a row per lane would touch 32 (the store unit takes a line a cycle).
-                const bool odd = lane & 1;
+                // touches 16 lines, where a row per lane would touch 32 (the store unit takes a line a cycle).  Rows that
+                // start on 16 bytes only (packed widths of 8 n + 4) go a row per lane.
+                const bool odd = lane & 1, wide = (p.part_ld & 7) == 0;
                 const bool row_ok_e = q_row - (odd ? 1 : 0) < p.S_q, row_ok_o = q_row + (odd ? 0 : 1) < p.S_q;
                 float *pair = orow - (odd ? p.part_ld : 0) + (odd ? 8 : 0);  // the even row, this lane's 8 columns
                 for (int cc = 0; cc < p.n_pv; cc += 16) {
@@ -969,7 +970,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = 0u;
                     }
-                    if (cc + 16 <= p.part_ld) {
+                    if (wide && cc + 16 <= p.part_ld) {
                         uint32_t mine[8], other[8];
                         #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -978,6 +979,10 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         }
                         if (row_ok_e) st_global_v8(pair + cc, odd ? other : mine);
                         if (row_ok_o) st_global_v8(pair + p.part_ld + cc, odd ? mine : other);
+                    } else if (row_ok && cc + 16 <= p.D_v) {  // (a width below 16 takes no such store)
+                        #pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<uint4 *>(orow + cc + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                     } else if (row_ok) {
                         #pragma unroll
                         for (int k = 0; k < 16; ++k)

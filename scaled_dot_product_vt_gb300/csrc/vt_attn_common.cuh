@@ -20,7 +20,14 @@ constexpr unsigned kStatusBounds = 2u;
 
 enum : int { kF32 = 0, kBF16 = 1 };
 
+// Floats from one partial O row to the next where rows start on 32 bytes.
 __host__ __device__ constexpr long long partial_ld(long long D_v) { return (D_v + 7) / 8 * 8; }
+// The same for split-KV shares: packed rows wherever the kernels' stores allow them (16-byte stores of whole groups of 4
+// columns, of 16 in the bf16 kernel, and narrower rows element by element), so that a call needs no more scratch than
+// its results.
+constexpr long long split_ld(long long D_v, bool bf) {
+    return D_v % 4 == 0 || D_v < (bf ? 16 : 4) ? D_v : partial_ld(D_v);
+}
 
 struct AttnParams {
     int B, H, S_q, S_k, D_qk, D_v;
@@ -62,7 +69,7 @@ struct AttnParams {
     // as the bf16 values P V used, indexed [split][(b*H + h)*S_q + i].
     int n_split;
     float *part_o;
-    int part_ld;      // floats from one partial O row to the next: D_v rounded up to 8, so rows take 32-byte stores
+    int part_ld;      // floats from one partial O row to the next: partial_ld, or split_ld of a split-KV call
     float *part_m;
     float *part_l;
     float *part_c;
