@@ -2,9 +2,10 @@
 got wrong: raw stream handles, tensors that lie beside each other in one projection or cache, checked calls, and every
 combination of launches with guard bytes around what it writes."""
 
+import numpy as np
 import pytest
 
-from test_qk_rope import Inputs
+from test_qk_rope import A, Inputs, pack
 
 import scaled_dot_product_vt_gb300 as vt
 
@@ -38,3 +39,111 @@ def test_the_raw_handle_of_the_default_stream():
     torch.cuda.synchronize()
     want = vt.qk_rope(x.q, x.k, x.freqs, x.pos, **x.form())
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and not torch.equal(got[0], old[0])
+
+
+# ---------------------------------------------------------------- tensors beside each other (no GPU)
+
+def no_gpu():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: a valid call would launch on these fake addresses")
+
+
+LAUNCH, REFUSED = 4, 1  # a call that passes every check ends at the missing device
+APPEND = dict(lens=9 * A, cap=8, ko=7 << 28, kos=(256, 128, 16), vo=9 << 28, vos=(512, 256, 32))
+
+
+@pytest.mark.parametrize("kw,code", [
+    # one projection [B, S, H D + H_kv D + H_kv D_v] with D_v = 24: Q in place while K and V go to their caches
+    (dict(APPEND, H_kv=2, D_v=24, q=A, qo=A, k=A + 64, v=A + 128, qs=(448, 16, 112), qos=(448, 16, 112),
+          ks=(448, 16, 112), vs=(448, 24, 112)), LAUNCH),
+    # ... V's first 8 columns are Q's last ones
+    (dict(APPEND, H_kv=2, D_v=24, q=A, qo=A, k=A + 96, v=A + 48, qs=(448, 16, 112), qos=(448, 16, 112),
+          ks=(448, 16, 112), vs=(448, 24, 112)), REFUSED),
+    # ... V's last head reaches into the next token's Q
+    (dict(APPEND, H_kv=2, D_v=24, q=A, qo=A, k=A + 64, v=A + 144, qs=(448, 16, 112), qos=(448, 16, 112),
+          ks=(448, 16, 112), vs=(448, 24, 112)), REFUSED),
+    # a gate of 8 columns between Q and K, both in place
+    (dict(q=A, qo=A, k=A + 80, ko=A + 80, qs=(256, 16, 64), qos=(256, 16, 64), ks=(256, 16, 64), kos=(256, 16, 64)),
+     LAUNCH),
+    # every head's Q, K and V beside each other: [B, S, H, 3, D]
+    (dict(H_kv=2, q=A, qo=A, k=A + 32, ko=A + 32, qs=(384, 48, 96), qos=(384, 48, 96), ks=(384, 48, 96),
+          kos=(384, 48, 96)), LAUNCH),
+    # ... K 8 columns too early
+    (dict(H_kv=2, q=A, qo=A, k=A + 16, ko=A + 16, qs=(384, 48, 96), qos=(384, 48, 96), ks=(384, 48, 96),
+          kos=(384, 48, 96)), REFUSED),
+    # K and V rows beside each other in one cache [B, H_kv, cap, D + D_v]
+    (dict(APPEND, H_kv=2, D_v=24, v=10 * A, vs=(192, 96, 24), ks=(128, 64, 16), ko=1 << 32, vo=(1 << 32) + 32,
+          kos=(640, 320, 40), vos=(640, 320, 40)), LAUNCH),
+    # K's rows and V's of a head one after the other: [B, H_kv, cap D + cap D_v]
+    (dict(APPEND, H_kv=2, D_v=24, v=10 * A, vs=(192, 96, 24), ks=(128, 64, 16), ko=1 << 32, vo=(1 << 32) + 256,
+          kos=(640, 320, 16), vos=(640, 320, 24)), LAUNCH),
+    # ... with room for 7 rows of K
+    (dict(APPEND, H_kv=2, D_v=24, v=10 * A, vs=(192, 96, 24), ks=(128, 64, 16), ko=1 << 32, vo=(1 << 32) + 224,
+          kos=(640, 320, 16), vos=(640, 320, 24)), REFUSED),
+])
+def test_tensors_beside_each_other(kw, code):
+    no_gpu()
+    assert vt.vt_qk_rope_fwd(pack(**kw), None) == code
+
+
+def test_overlap_is_found_exactly():
+    """Random layouts of Q and K outputs in one buffer: a call is refused when two elements meet, and only then."""
+    no_gpu()
+    rng = np.random.default_rng(22)
+    counts = [0, 0]
+    for _ in range(3000):
+        B, S, H, H_kv = (int(n) for n in rng.integers(1, 4, 4))
+        tensors = []
+        for heads in (H, H_kv):
+            order = rng.permutation(3)
+            n, st, reach = (B, heads, S), [0, 0, 0], 16
+            for i in order:  # strides that nest, with gaps
+                st[i] = reach + 8 * int(rng.integers(0, 6)) if n[i] > 1 else 8 * int(rng.integers(0, 9))
+                reach = st[i] * (n[i] - 1) + reach if n[i] > 1 else reach
+            tensors.append((n, st))
+        if rng.random() < 0.5:  # heads and sequences of one projection
+            tensors[1] = (tensors[1][0], [tensors[0][1][0], tensors[1][1][1], tensors[0][1][2]])
+        at = 8 * int(rng.integers(-12, 40))
+        cells = []
+        for (n, st), first in zip(tensors, (0, at)):
+            b, h, s = np.ogrid[:n[0], :n[1], :n[2]]
+            cells.append((first + b * st[0] + h * st[1] + s * st[2]).reshape(-1, 1) + np.arange(16))
+        nested, reach = True, 16  # the rule for an output's own strides
+        for st, n in sorted((st, n) for n, st in zip(*tensors[1]) if n > 1):
+            nested, reach = nested and st >= reach, reach + st * (n - 1)
+        code = vt.vt_qk_rope_fwd(pack(B=B, S=S, H=H, H_kv=H_kv, q=1 << 32, k=2 << 32, qo=3 << 32, ko=(3 << 32) + 2 * at,
+                                      qs=(512, 128, 16), ks=(512, 128, 16), qos=tensors[0][1], kos=tensors[1][1]), None)
+        meet = len(np.intersect1d(*cells)) > 0
+        if nested:  # (else it is refused whatever lies beside it)
+            assert code == (REFUSED if meet else LAUNCH), (B, S, H, H_kv, tensors, at)
+            counts[meet] += 1
+        else:
+            assert code == REFUSED
+    assert min(counts) > 300
+
+
+@pytest.mark.gpu
+def test_a_projection_with_values_of_another_width():
+    """Q rotated where it is, K and V appended, all from one [B, S, H D + H_kv D + H_kv D_v] projection."""
+    B, S, H, H_kv, D, D_v, cap = 3, 5, 4, 2, 64, 40, 9
+    x = Inputs("bf16", B, H, H_kv, S, D, D, seed=25)
+    torch = x.torch
+    room = torch.full((B, S, H * D + H_kv * (D + D_v)), 7.0, dtype=x.t, device="cuda")
+    q, k, v = (t.unflatten(-1, (-1, d)).transpose(1, 2) for t, d in
+               zip(room.split([H * D, H_kv * D, H_kv * D_v], -1), (D, D, D_v)))
+    v64 = x.rng.standard_normal(v.shape)
+    for t, a in ((q, x.q), (k, x.k), (v, torch.from_numpy(v64))):
+        t.copy_(a)
+    kept = [k.clone(), v.clone()]
+    caches = [torch.full((B, H_kv, cap, d), 3.0, dtype=x.t, device="cuda") for d in (D, D_v)]
+    lens = torch.tensor([S, cap, S + 1], dtype=torch.int32, device="cuda")
+    got, _ = vt.qk_rope(q, k, x.freqs, x.pos, q_out=q, k_out=caches[0], v=v, v_out=caches[1], kv_len=lens, **x.form())
+    assert got is q and torch.equal(k, kept[0]) and torch.equal(v, kept[1])
+    rows = torch.stack([caches[0][b, :, n - S:n] for b, n in enumerate(lens.tolist())])
+    x.check_forward(q, rows)
+    for b, n in enumerate(lens.tolist()):
+        assert torch.equal(caches[1][b, :, n - S:n], v[b])
+        caches[0][b, :, n - S:n] = caches[1][b, :, n - S:n] = 3.0
+    assert (caches[0] == 3).all() and (caches[1] == 3).all()
+    assert vt.vt_last_device_status() == 0
