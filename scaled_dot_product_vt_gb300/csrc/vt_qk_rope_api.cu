@@ -359,7 +359,7 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
     if (empty) {  // no token: the weights' gradients are 0
         if (dwq && cudaMemsetAsync(dwq, 0, a.D * sizeof(float), stream) != cudaSuccess) return VT_ERR_CUDA;
         if (dwk && cudaMemsetAsync(dwk, 0, a.D * sizeof(float), stream) != cudaSuccess) return VT_ERR_CUDA;
-        return VT_OK;
+        return env_check() ? read_status(stream) : VT_OK;
     }
 
     int dev = 0;
@@ -392,7 +392,7 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
     const Variant v = pick<true>(a, sh);
     const int sums = norm ? kThreads / p.tpr * p.D * static_cast<int>(sizeof(float)) : 0;
     VT_TRY(launch(v, v.smem > sums ? v.smem : sums, static_cast<unsigned>(n_q + n_k), p, dev, stream));
-    if (!weights) return VT_OK;
+    if (!weights) return env_check() ? read_status(stream) : VT_OK;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.D + 7) / 8, 2);
     cfg.blockDim = dim3(8 * kSumRows);
@@ -406,7 +406,8 @@ vt_status backward(const Args &a, const void *gq, const int64_t gq_st[3], const 
     const int D = p.D;
     if (cudaLaunchKernelEx(&cfg, bwd_weights_kernel, part_q, part_k, dwq, dwk, n_q, n_k, D) != cudaSuccess)
         return VT_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    return env_check() ? read_status(stream) : VT_OK;
 }
 
 }  // namespace

@@ -2,6 +2,10 @@
 got wrong: raw stream handles, tensors that lie beside each other in one projection or cache, checked calls, and every
 combination of launches with guard bytes around what it writes."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -147,3 +151,32 @@ def test_a_projection_with_values_of_another_width():
         caches[0][b, :, n - S:n] = caches[1][b, :, n - S:n] = 3.0
     assert (caches[0] == 3).all() and (caches[1] == 3).all()
     assert vt.vt_last_device_status() == 0
+
+
+# ---------------------------------------------------------------- checked calls
+
+CHECKED = """
+import torch, scaled_dot_product_vt_gb300 as vt
+x = torch.randn(4, 32, 4096, 128, device="cuda", dtype=torch.bfloat16)
+f, p = torch.ones(64, device="cuda"), torch.zeros(4, 4096, dtype=torch.int32, device="cuda")
+vt.qk_rope_bwd(x, None, f, p, q=x, eps=1e-6)
+torch.cuda.synchronize()
+stream = torch.cuda.current_stream()
+for call in (lambda: vt.qk_rope(x, None, f, p, eps=1e-6), lambda: vt.qk_rope_bwd(x, None, f, p, q=x, eps=1e-6),
+             lambda: vt.attn_fwd_prefix(x, x[0], x[0], None, None)):
+    call()
+    assert stream.query()
+    print("done")
+"""
+
+
+@pytest.mark.gpu
+def test_checked_calls_wait_for_their_kernels():
+    """VT_CHECK: every call reads its stream's status itself, so it returns after its kernels ended."""
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHECKED], cwd=root, env=dict(os.environ, VT_CHECK="1"), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["done"] * 3, r.stdout + r.stderr
