@@ -9,6 +9,7 @@ import sys
 import numpy as np
 import pytest
 
+from test_attn_prefix import Problem
 from test_qk_rope import A, Inputs, pack
 
 import scaled_dot_product_vt_gb300 as vt
@@ -180,3 +181,63 @@ def test_checked_calls_wait_for_their_kernels():
     r = subprocess.run([sys.executable, "-c", CHECKED], cwd=root, env=dict(os.environ, VT_CHECK="1"), capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["done"] * 3, r.stdout + r.stderr
+
+
+# ---------------------------------------------------------------- every combination of launches
+
+# dtype, B, H, H_kv, S_q, S_p, S_c, D_qk, D_v; shares of the prefix, and of the caches (1: a cluster writes O, or its one
+# share, itself) on a device of 152 SMs
+PLANS = [
+    (("bf16", 2, 4, 2, 1, 20000, 9000, 96, 33), 9, 2),     # both launches stream, and a third adds their shares
+    (("f32", 4, 4, 1, 1, 20000, 9000, 33, 7), 32, 4),
+    (("bf16", 16, 2, 2, 1, 4096, 50, 128, 128), 2, 1),     # the prefix streamed for all rows
+    (("bf16", 5, 6, 2, 1, 20000, 60, 72, 40), 9, 1),
+    (("f32", 40, 8, 2, 1, 1500, 40, 128, 128), 4, 1),
+    (("bf16", 33, 8, 1, 2, 1500, 9, 80, 128), 11, 1),      # on tiles: three query tiles of rows, the last one short
+    (("bf16", 70, 4, 2, 1, 1000, 37, 64, 33), 7, 1),
+    (("bf16", 40, 8, 2, 1, 8192, 200, 128, 72), 31, 1),
+    (("bf16", 1, 4, 1, 2, 0, 20000, 128, 128), 0, 4),      # no prefix: the caches in shares
+    (("bf16", 5, 8, 4, 2, 333, 70, 64, 40), 0, 1),         # one launch
+    (("bf16", 3, 8, 2, 100, 129, 300, 128, 72), 0, 0),     # rows of a sequence on tiles
+]
+
+
+def shares_of(case):
+    dtype, B, H, H_kv, S_q, S_p, S_c, D_qk, D_v = case
+    need = vt.vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, vt.VT_BF16 if dtype == "bf16" else vt.VT_F32)
+    return need, need // (B * H * S_q * ((D_v + 7) // 8 * 8 + 3) * 4)
+
+
+@pytest.mark.parametrize("case,prefix,cache", PLANS, ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else None)
+def test_plans_are_the_ones_named(case, prefix, cache):
+    import torch
+    if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("a device of another size")
+    _, shares = shares_of(case)
+    assert shares in ((prefix, prefix + cache) if prefix and cache == 1 else (prefix + cache if prefix or cache > 1 else 0,))
+    again = case[1] * case[3] * -(-case[4] * (case[2] // case[3]) // 16) * case[5] * (case[7] + case[8]) * (
+        2 if case[0] == "bf16" else 4)
+    assert prefix == 0 or again > ((16 if case[0] == "bf16" else 2) << 20)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens_first", [False, True])
+@pytest.mark.parametrize("case,prefix,cache", PLANS, ids=lambda c: "-".join(map(str, c)) if isinstance(c, tuple) else None)
+def test_every_combination_of_launches(case, prefix, cache, tokens_first):
+    p = Problem(*case, seed=23, tokens_first=tokens_first)
+    torch = p.torch
+    _, B, H, _, S_q, _, _, _, D_v = case
+    need, _ = shares_of(case)
+    row = (D_v + 7) // 8 * 8 + 16  # 8 columns before and behind
+    room = torch.full((B, S_q + 1, H, row), 7.0, dtype=p.t, device="cuda")
+    out = room[:, :S_q, :, 8:8 + D_v].transpose(1, 2)
+    lse_room = torch.full((B * H * S_q + 2,), 7.0, device="cuda")
+    ws = torch.full((need + 1024,), 7, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        o, lse = p.run(out=out, lse=lse_room[1:-1].view(B, H, S_q), workspace=ws[512:512 + need] if need else None)
+        assert o is out
+        p.check(o, lse)
+        out.fill_(7.0)
+        assert (room == 7).all() and lse_room[0] == 7 and lse_room[-1] == 7
+        assert (ws[:512] == 7).all() and (ws[512 + need:] == 7).all()
+    assert vt.vt_last_device_status() == 0
