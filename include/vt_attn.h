@@ -285,9 +285,12 @@ vt_status vt_attn_fwd_general(const void *Q, const int64_t q_stride[3],
  *       with (u, v) = (i, i + R/2)   interleaved = 0
  *            (u, v) = (2i, 2i + 1)   interleaved != 0
  *   y_j = n_j for j >= R.
- * Everything between x and y is fp32 and y is rounded once; the angle keeps its phase at any position (it is formed in
- * fractions of a turn, 64 bits wide).  A row whose sum of squares leaves fp32's range becomes 0, and with eps = 0 a row
- * of zeros becomes NaN.  Several position axes (time, height, width of a video patch) need one row of `positions` each;
+ * Everything between x and y is fp32 and y is rounded once.  The angle keeps its phase at any position: it is reduced to
+ * a fraction of a turn in 64 bits, and that fraction is rounded to 24 (an error of the angle of at most pi 2^-25).  A
+ * frequency that is infinite or NaN makes its pairs NaN.  A row of numbers whose squares add up to more than fp32 holds
+ * becomes 0; with eps = 0 a row of zeros becomes NaN, and one whose squares are too small for fp32 infinite.  Without the
+ * norm, what a column holds reaches its pair alone, and itself alone where it is not rotated.  The weights are not looked
+ * at when normalize is 0.  Several position axes (time, height, width of a video patch) need one row of `positions` each;
  * pair_axis names the axis of every frequency pair, in any order.
  *
  * Append (kv_len not NULL): token s of sequence b belongs at cache row kv_len[b] - S + s, kv_len[b] being the
@@ -384,9 +387,11 @@ size_t vt_qk_rope_bwd_workspace_size(int64_t D);
  *   workspace            DEVICE scratch, 256-byte aligned, at least vt_attn_prefix_workspace_size bytes (may be
  *                        NULL when that is 0).  Every call writes what it reads there; two calls that share it must
  *                        not overlap on the GPU, replays of captured ones included.
- * Element types: VT_BF16, and VT_F32 with products of two TF32 parts per operand (about 2^-21 of every factor is
- * lost, against 2^-11 in the other fp32 calls of this header).  Sums and statistics are fp32.  A key that a query may
- * not see but that another query of the same sequence does must be finite, as in the other calls.
+ * Element types: VT_BF16, with probabilities rounded to bf16 as in the other calls, and VT_F32 with products of two TF32
+ * parts per operand (about 2^-21 of every factor is lost, against 2^-11 in the other fp32 calls).  Sums and statistics are
+ * fp32.  An infinite value fills its column of O with that infinity for every query that gives it a weight fp32 holds, and
+ * a key whose score is -inf has no weight.  A key that a query may not see but that another query of the same sequence does must be finite, as in the other
+ * calls.
  * Strides, alignment and errors as for vt_attn_fwd_strided (the stride of an index with one value is not looked at);
  * VT_ERR_INVALID_ARG also for H not a multiple of H_kv or a workspace that is too small, VT_ERR_UNSUPPORTED also for
  * S_p + S_c or B * H * S_q above 2^30.  B, H or S_q equal to 0 is a valid empty problem.

@@ -504,7 +504,8 @@ def qk_rope(q, k, freqs, positions, *, pair_axis=None, interleaved: bool = False
     [B,S] or [axes,B,S], and ``pair_axis`` (a tuple) names the axis of every pair.  ``eps=None`` leaves the norm out.
     ``q_out=q`` and ``k_out=k`` work in place.  With ``kv_len`` (int32 [B]: the lengths after these tokens), k_out
     is a cache [B,H_kv,cap,D] that K's rows are appended to, and v [B,H_kv,S,D_v] is appended to v_out.
-    ``stream`` may name another stream than the current one."""
+    ``stream`` may name another stream than the current one (a torch stream or a raw handle).  Nothing is recorded for
+    autograd: the results are detached, and ``qk_rope_bwd`` gives the gradients."""
     if stream is not None or not _here(q):
         return _elsewhere(qk_rope, q, stream, (q, k, freqs, positions), dict(
             pair_axis=pair_axis, interleaved=interleaved, eps=eps, q_weight=q_weight, k_weight=k_weight, q_out=q_out,

@@ -56,7 +56,11 @@ Sizes sizes_of(const Args &a) {
 // More rows that share the prefix's keys than this take the tcgen05 kernel (bf16): 37 rows of 32 heads over 8191 keys,
 // 52 us against 74 us streamed; with 64 rows of 8 heads over 2048 keys the two are level (59 us).
 constexpr int64_t kTileRows = 32;
-// More rows per sequence and key/value head than this take it for all their keys.
+// More rows per sequence and key/value head than this take it for all their keys, one CTA for 256 rows.  Measured on both
+// sides, 8 key/value heads of D = 128 and caches of up to 512: with many sequences it pays (64 sequences over 2048 shared
+// keys: 96 rows 128 us here and 139 us with the prefix in a launch of its own, 256 rows 133 and 349 us; 8 sequences of 256
+// rows 36 and 54 us), and with few rows or few sequences it loses, most behind a long prefix (8 sequences of 65 rows 37 and
+// 28 us; one sequence of 256 rows over 32768 keys 356 and 44 us), where its CTAs are fewer than SMs and share no keys.
 constexpr int64_t kSeqTileRows = 64;
 // Bytes of the prefix that the streaming launch may read again, once per sequence and row tile, to spare a launch
 // (4 sequences of 16 rows over 333 keys: 6.6 us against 9 us).  fp32 multiplies three times as much, and gains
@@ -101,6 +105,10 @@ int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
     }
     return best;
 }
+
+// Lengths live on the device, so the plan takes every cache as half full.  Where caches are mostly empty it gives the
+// prefix too few shares (64 sequences of up to 100 tokens behind 8192 shared keys: 23 us in caches of 128 rows, 35 us in
+// 1024, 99 us in 8192 and 32768).
 
 // Streaming CTAs that share an SM (Tile::kPerSm).
 int64_t ctas_per_sm(const Args &a) { return a.dtype == VT_F32 ? 1 : (a.D_v <= 64 ? 4 : 3); }
