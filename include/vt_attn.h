@@ -421,6 +421,52 @@ vt_status vt_attn_fwd_prefix(const vt_attn_prefix_args *args, vt_stream_t stream
 size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,
                                      int64_t D_qk, int64_t D_v, vt_dtype dtype);
 
+/*
+ * Attention over packed sequences: N sequences of different lengths whose rows lie behind each other in one tensor, as a
+ * batch of prompts or of training texts is laid out without padding.
+ *
+ * Sequence n has the queries cu_q[n] <= t < cu_q[n + 1] and the keys cu_k[n] <= t < cu_k[n + 1]; queries see keys of their
+ * own sequence only.  Its queries are the last of its keys' positions: query i of len_q sits at position
+ * i + len_k - len_q, and with o = len_k - len_q the mask kinds keep the keys that vt_attn_fwd_general's keep at offset o
+ * (here o may be negative: the first queries then see no key of a causal mask).
+ *   O = softmax(scale q . k) v over the keys a query sees,  LSE = log(sum exp(scale q . k)) (natural log);
+ * a query that sees no key has O = 0 and LSE = -inf.  Query head h reads key/value head h / (H / H_kv).
+ *
+ * Arguments, as a struct whose first field is its size.
+ *   q, o        [H,T_q,D_qk] and [H,T_q,D_v], strides (h, t); T_q >= cu_q[N].  Rows of O and of LSE that belong to no
+ *               sequence are not written.
+ *   k, v        [H_kv,T_k,D_qk] and [H_kv,T_k,D_v], strides (h, t); T_k >= cu_k[N].  What rows of other sequences, or of
+ *               none, hold has no influence.
+ *   cu_q, cu_k  int32 [N + 1], not decreasing, read on the device (a captured call replays with new lengths); they may
+ *               be one array.  First rows outside [0, T] count as the nearest ones inside, and a sequence that ends
+ *               before it starts as empty; both record VT_ERR_DEVICE_BOUNDS in the stream's status word.
+ *   lse         fp32 [H,T_q] packed, or NULL
+ *   mask        a vt_mask_kind, with its `window`
+ * Element types: VT_BF16, with probabilities rounded to bf16 as in the other calls, and VT_F32 with products of two TF32
+ * parts per operand (about 2^-21 of every factor is lost).  Sums and statistics are fp32.  A key that a query may not see
+ * but that another query of the same sequence does must be finite, as in the other calls.
+ * Strides, alignment and errors as for vt_attn_fwd_strided (the stride of an index with one value is not looked at);
+ * VT_ERR_INVALID_ARG also for H not a multiple of H_kv, an unknown mask or a window below 1 with a window kind,
+ * VT_ERR_UNSUPPORTED also for a window above 2^40, N, T_q or T_k above 2^30, or (T / 64 + N) H above 2^31 - 1.  N, H or T_q
+ * equal to 0 is a valid empty problem.
+ */
+typedef struct {
+    uint64_t struct_bytes; /* sizeof(vt_attn_packed_args) */
+    const void *q, *k, *v;
+    const int32_t *cu_q, *cu_k;
+    void *o;
+    float *lse;
+    int64_t N, H, H_kv, T_q, T_k, D_qk, D_v;
+    int64_t window;
+    int32_t dtype; /* vt_dtype */
+    float scale;
+    int32_t mask;     /* vt_mask_kind */
+    int32_t reserved; /* 0 */
+    int64_t q_stride[2], k_stride[2], v_stride[2], o_stride[2];
+} vt_attn_packed_args;
+
+vt_status vt_attn_fwd_packed(const vt_attn_packed_args *args, vt_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *vt_status_str(vt_status status);
 

@@ -32,6 +32,7 @@ EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
            "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
            "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size",
+           "vt_attn_fwd_packed",
            "vt_status_str", "vt_last_device_status")
 
 
@@ -95,6 +96,8 @@ def load(path: str | None = None):
     lib.vt_attn_fwd_prefix.restype = i
     lib.vt_attn_prefix_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i]
     lib.vt_attn_prefix_workspace_size.restype = sz
+    lib.vt_attn_fwd_packed.argtypes = [ctypes.c_char_p, vp]
+    lib.vt_attn_fwd_packed.restype = i
     lib.vt_status_str.argtypes = [i]
     lib.vt_status_str.restype = ctypes.c_char_p
     lib.vt_last_device_status.argtypes = [vp]
@@ -205,6 +208,17 @@ def vt_attn_fwd_prefix(args: bytes, stream) -> int:
 
 def vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype) -> int:
     return int(load().vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype))
+
+
+# vt_attn_packed_args in field order (every field is aligned without padding): its size and the addresses, then the rest
+_ATTN_PACKED_PTRS = struct.Struct("=8Q")
+_ATTN_PACKED_REST = struct.Struct("=8qifii8q")
+_ATTN_PACKED_BYTES = _ATTN_PACKED_PTRS.size + _ATTN_PACKED_REST.size
+
+
+def vt_attn_fwd_packed(args: bytes, stream) -> int:
+    """The C entry point: ``args`` is a packed vt_attn_packed_args; returns the vt_status code."""
+    return load().vt_attn_fwd_packed(args, stream)
 
 
 def vt_status_str(code: int) -> str:
@@ -342,7 +356,7 @@ def attn_fwd_general(q, k, v, scale: float | None = None, mask: str = "none", of
 # tensor is written out: it is most of what a small call costs on the host, and a function for it half as much again.
 
 _MOST_PLANS = 4096
-_rope_plans, _rope_bwd_plans, _prefix_plans = {}, {}, {}
+_rope_plans, _rope_bwd_plans, _prefix_plans, _packed_plans = {}, {}, {}, {}
 
 
 def _keep(plans, key, plan):
@@ -717,3 +731,104 @@ def attn_prefix_step(q, k, v, freqs, positions, k_prefix, v_prefix, k_cache, v_c
                        stream=stream)
     return attn_fwd_prefix(q_rot, k_prefix, v_prefix, k_cache, v_cache, kv_len, scale=scale, return_lse=return_lse,
                            out=out, lse=lse, workspace=workspace, stream=stream)
+
+
+# ---------------------------------------------------------------- attention over packed sequences
+
+def _new_tokens(shape, dtype, device):
+    """A new [H, T, D] tensor, token by token in memory ([T, H, D], as projections leave and take rows); rows that are no
+    multiple of 16 bytes are padded to one (a view is returned)."""
+    import torch
+    H, T, D = shape
+    step = 16 // dtype.itemsize
+    return torch.empty((T, H, (D + step - 1) // step * step), dtype=dtype, device=device)[..., :D].transpose(0, 1)
+
+
+def _new_token_strides(shape, dtype):
+    """Strides of _new_tokens(shape, dtype)."""
+    step = 16 // dtype.itemsize
+    row = (shape[2] + step - 1) // step * step
+    return (row, shape[0] * row)
+
+
+def _check_lse(name, meta, dev, shape):
+    if meta[3] != dev or meta[2] != _float32() or tuple(meta[0]) != shape or any(
+            n > 1 and st != want for n, st, want in zip(shape, meta[1], (shape[1], 1))):
+        raise ValueError(f"{name} must be a contiguous float32 [H, T_q] tensor on the device of the other tensors")
+
+
+def _float32():
+    import torch
+    return torch.float32
+
+
+def _packed_plan(q, k, v, cu_q, cu_k, out, lse, scale, mask, window):
+    """Checks of an attn_fwd_packed call from its tensors' metadata: (packed fixed part of its arguments, shape of O)."""
+    import torch
+    q_shape, _, dt, dev = q
+    code = VT_BF16 if dt == torch.bfloat16 else VT_F32 if dt == torch.float32 else None
+    if code is None:
+        raise TypeError(f"attention over packed sequences supports bfloat16 and float32 tensors, got {dt}")
+    sq = _check("q", q, dev, dt, dims=3)
+    H, T_q, D_qk = q_shape
+    if len(k[0]) != 3 or len(v[0]) != 3:
+        raise ValueError("k and v must have 3 dimensions")
+    H_kv, T_k, D_v = k[0][0], k[0][1], v[0][2]
+    sk = _check("k", k, dev, dt, (H_kv, T_k, D_qk), 3)
+    sv = _check("v", v, dev, dt, (H_kv, T_k, D_v), 3)
+    _check_vector("cu_q", cu_q, dev, torch.int32, None)
+    N = cu_q[0][0] - 1
+    if N < 0:
+        raise ValueError("cu_q must hold the first row of every sequence and the end of the last")
+    _check_vector("cu_k", cu_k, dev, torch.int32, N + 1)
+    o_shape = (H, T_q, D_v)
+    so = _check("out", out, dev, dt, o_shape, 3) if out is not None else _new_token_strides(o_shape, dt)
+    if lse is not None:
+        _check_lse("lse", lse, dev, (H, T_q))
+    if mask not in MASKS:
+        raise ValueError(f"mask must be one of {tuple(MASKS)}")
+    if scale is None:
+        scale = float(D_qk) ** -0.5
+    rest = _ATTN_PACKED_REST.pack(N, H, H_kv, T_q, T_k, D_qk, D_v, window, code, scale, MASKS[mask], 0, *sq, *sk, *sv, *so)
+    return rest, o_shape
+
+
+def attn_fwd_packed(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, mask: str = "causal", window: int = 0,
+                    return_lse: bool = False, out=None, lse=None, stream=None):
+    """Attention of sequences of different lengths that lie behind each other: q [H,T_q,D_qk], k [H_kv,T_k,D_qk] and
+    v [H_kv,T_k,D_v], with sequence n's queries in rows cu_q[n] to cu_q[n + 1] and its keys in rows cu_k[n] to cu_k[n + 1]
+    (int32 [N + 1] on the device; cu_k may be left out where it is cu_q): see vt_attn_fwd_packed in include/vt_attn.h.
+    The queries are the last of their sequence's positions; ``mask`` is one of ``MASKS`` with ``window``.
+
+    Returns O [H,T_q,D_v], or (O, LSE) with ``return_lse`` (float32 [H,T_q], natural log).  Rows of no sequence are not
+    written.  A new O lies token by token ([T_q,H,D_v] in memory).  ``stream`` may name another stream than the current
+    one.  Nothing is recorded for autograd."""
+    if stream is not None or not _here(q):
+        return _elsewhere(attn_fwd_packed, q, stream, (q, k, v, cu_q, cu_k), dict(
+            scale=scale, mask=mask, window=window, return_lse=return_lse, out=out, lse=lse))
+    import torch
+    if cu_k is None:
+        cu_k = cu_q
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)  # (a plan is kept by values: a tensor's may change)
+    if type(window) is not int:
+        window = int(window)
+    key = ((q.shape, q.stride(), q.dtype, q.get_device()), (k.shape, k.stride(), k.dtype, k.get_device()),
+           (v.shape, v.stride(), v.dtype, v.get_device()), (cu_q.shape, cu_q.stride(), cu_q.dtype, cu_q.get_device()),
+           (cu_k.shape, cu_k.stride(), cu_k.dtype, cu_k.get_device()),
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()),
+           None if lse is None else (lse.shape, lse.stride(), lse.dtype, lse.get_device()), scale, mask, window)
+    plan = _packed_plans.get(key)
+    if plan is None:
+        plan = _keep(_packed_plans, key, _packed_plan(*key))
+    rest, o_shape = plan
+    if out is None:
+        out = _new_tokens(o_shape, q.dtype, q.device)
+    if return_lse and lse is None:
+        lse = torch.empty(o_shape[:2], dtype=torch.float32, device=q.device)
+    args = _ATTN_PACKED_PTRS.pack(_ATTN_PACKED_BYTES, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+                                  cu_k.data_ptr(), out.data_ptr(), _ptr(lse)) + rest
+    rc = load().vt_attn_fwd_packed(args, torch._C._cuda_getCurrentRawStream(q.get_device()))
+    if rc != 0:
+        raise VtError(rc, "vt_attn_fwd_packed")
+    return (out, lse) if return_lse else out

@@ -50,6 +50,7 @@
 #pragma once
 
 #include "vt_attn_common.cuh"
+#include "vt_attn_packed.cuh"
 
 namespace vt {
 namespace q2 {
@@ -61,7 +62,7 @@ constexpr int kRegsControl = 72;    // warpgroup 0 after setmaxnreg
 constexpr int kRegsSoftmax = 216;   // softmax warpgroups after setmaxnreg
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split exceeds the launch");
 constexpr int kMaxSlots = 6;
-constexpr int kRowsPlain = 0, kRowsAll = 1, kRowsSeq = 2;  // what a tile's rows are (the kernel's ROWS)
+constexpr int kRowsPlain = 0, kRowsAll = 1, kRowsSeq = 2, kRowsPacked = 3;  // what a tile's rows are (the kernel's ROWS)
 constexpr int kEpiPlain = 0, kEpiSplit = 1, kEpiPlainFast = 2;  // epilogue variants (the kernel's EPI)
 constexpr int kUnitRing = 4;        // unit indices in flight between the producer and the other roles
 constexpr int kUnitReaders = 1 + 8;  // the MMA warp and one lane of each softmax warp (one more MMA warp with the score ring)
@@ -83,7 +84,8 @@ struct Unit {
     int b, h, hk, r0;
     int j0, n_kv;             // the share's first key tile and its number of key tiles
     int as0, es0, as1, es1;   // key tiles [as_t, es_t) of the share that query tile t needs
-    int len;                  // kRowsSeq: cached tokens of the sequence
+    int len;                  // kRowsSeq: cached tokens of the sequence; kRowsPacked: its keys
+    int rows, q0, k0;         // kRowsPacked: the sequence's queries, its first row of Q and of K and V
 };
 
 struct Ctl {
@@ -129,12 +131,32 @@ __device__ __forceinline__ void gathered_unit(const AttnParams &p, unsigned u, i
     if (ROWS == kRowsSeq) *qb = p.n_qblocks - 1 - *qb;  // (later blocks see more of the cache)
 }
 
+// Key tiles [*a, *e) that rows first..last of a packed sequence need (an empty range as 0, 0).
+__device__ __forceinline__ void packed_tiles(const AttnParams &p, const Unit &U, int first, int last, int *a, int *e) {
+    const int lo = packed_key_lo(p, U.len - U.rows, U.len, first), hi = packed_key_hi(p, U.len - U.rows, U.len, last);
+    *a = lo < hi ? lo / kBN : 0;
+    *e = lo < hi ? (hi + kBN - 1) / kBN : 0;
+}
+
 template <int ROWS>
 __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     Unit U;
-    U.len = 0;
+    U.len = U.rows = U.q0 = U.k0 = 0;
     U.u = u;
-    if constexpr (ROWS != kRowsPlain) {
+    if constexpr (ROWS == kRowsPacked) {
+        // the heads of a block are adjacent (they read the same keys), and later blocks, which see more keys, come first
+        const int slot = u / p.H;
+        const PackedSeq q = packed_find(p.cu_q, p.n_seq, p.S_q, kRows, p.n_qblocks - 1 - slot, p.status);
+        const PackedSeq k = packed_seq(p.cu_k, q.n, p.S_k, p.status);
+        U.split = U.b = 0;
+        U.h = u - slot * p.H;
+        U.hk = U.h / p.kv_group;
+        U.r0 = q.block * kRows;
+        U.rows = q.len;
+        U.q0 = q.start;
+        U.len = k.len;
+        U.k0 = k.start;
+    } else if constexpr (ROWS != kRowsPlain) {
         int qb;
         gathered_unit<ROWS>(p, u, &U.split, &U.b, &U.h, &qb);
         U.hk = U.h;
@@ -171,9 +193,11 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int first = U.r0 + t * kBM;
-        if (first >= p.S_q) {
+        if (first >= (ROWS == kRowsPacked ? U.rows : p.S_q)) {
             a[t] = 0;
             e[t] = 0;
+        } else if constexpr (ROWS == kRowsPacked) {
+            packed_tiles(p, U, first, min(first + kBM, U.rows) - 1, &a[t], &e[t]);
         } else if constexpr (ROWS == kRowsSeq) {
             a[t] = 0;
             e[t] = p.prefix_tiles + (own_keys(p, U.len, min(first + kBM, p.S_q) - 1) + kBN - 1) / kBN;
@@ -207,7 +231,15 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
 }
 
 // Invariants of a decoded unit, checked by the debug build before the unit's loads are issued.
+template <int ROWS>
 __device__ __forceinline__ bool unit_valid(const AttnParams &p, const Unit &U) {
+    if constexpr (ROWS == kRowsPacked) {
+        const int tiles = (U.len + kBN - 1) / kBN;
+        return U.h >= 0 && U.h < p.H && U.hk == U.h / p.kv_group && U.r0 >= 0 && U.r0 % kRows == 0 && U.rows >= 0 &&
+               U.q0 >= 0 && U.rows <= p.S_q - U.q0 && U.len >= 0 && U.k0 >= 0 && U.len <= p.S_k - U.k0 && U.j0 >= 0 &&
+               U.n_kv >= 0 && U.j0 + U.n_kv <= tiles && U.as0 >= 0 && U.as0 <= U.es0 && U.es0 <= U.n_kv && U.as1 >= 0 &&
+               U.as1 <= U.es1 && U.es1 <= U.n_kv;
+    }
     const int tiles = (p.S_k + kBN - 1) / kBN;
     return U.b >= 0 && U.b < p.B && U.h >= 0 && U.h < p.H && U.hk == U.h / p.kv_group && U.r0 >= 0 &&
            U.r0 < p.S_q && U.r0 % kRows == 0 && U.split >= 0 && U.split < p.n_split && U.j0 >= 0 && U.n_kv >= 0 &&
@@ -238,7 +270,12 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
     out->es0 = src->es0;
     out->as1 = src->as1;
     out->es1 = src->es1;
-    if (ROWS == kRowsSeq) out->len = src->len;
+    if (ROWS == kRowsSeq || ROWS == kRowsPacked) out->len = src->len;
+    if (ROWS == kRowsPacked) {
+        out->rows = src->rows;
+        out->q0 = src->q0;
+        out->k0 = src->k0;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_empty[k]));
     return true;
@@ -279,11 +316,13 @@ __device__ __forceinline__ void gather_done() {
     fence_async_shared();
 }
 
-// kRowsSeq: zero the V rows of key tile j that lie past the sequence's end (the whole warp): they may hold NaN, which
-// a probability of 0 does not hide.  The tensor core sees the zeros afterwards.
+// kRowsSeq, kRowsPacked: zero the V rows of key tile j that lie past the sequence's end (the whole warp): they may hold
+// NaN, which a probability of 0 does not hide.  The tensor core sees the zeros afterwards.
+template <int ROWS>
 __device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int j, int lane, const AttnParams &p) {
-    const int n = U.len - (U.j0 + j - p.prefix_tiles) * kBN;  // rows of the tile that exist
-    if (U.j0 + j < p.prefix_tiles || n >= kBN) return;
+    const int before = ROWS == kRowsSeq ? p.prefix_tiles : 0;  // tiles of the prefix
+    const int n = U.len - (U.j0 + j - before) * kBN;           // rows of the tile that exist
+    if (U.j0 + j < before || n >= kBN) return;
     for (int c = 0; c < p.v_chunks; ++c)
         for (int i = n * 8 + lane; i < kBN * 8; i += 32)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot + c * kChunkBytes + i * 16), "r"(0) : "memory");
@@ -316,7 +355,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             const AttnParams p) {
     using namespace q2;
     constexpr int BN = kBN;
-    constexpr bool GATHER = ROWS != kRowsPlain;
+    constexpr bool GATHER = ROWS == kRowsAll || ROWS == kRowsSeq;
     __shared__ Ctl ctl;
     extern __shared__ uint8_t smem_raw[];
 
@@ -425,10 +464,10 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 Unit U;
                 if (u >= 0) {
                     U = decode_unit<ROWS>(p, u);
-                    if (!VT_DEV_CHECK(!(p.flags & kFlagTestBounds) && unit_valid(p, U), ctl.abort_flag, p)) break;
+                    if (!VT_DEV_CHECK(!(p.flags & kFlagTestBounds) && unit_valid<ROWS>(p, U), ctl.abort_flag, p)) break;
                 } else {
                     U.u = -1;
-                    U.split = U.b = U.h = U.hk = U.r0 = U.j0 = U.n_kv = U.as0 = U.es0 = U.as1 = U.es1 = U.len = 0;
+                    U.split = U.b = U.h = U.hk = U.r0 = U.j0 = U.n_kv = U.as0 = U.es0 = U.as1 = U.es1 = U.len = U.rows = U.q0 = U.k0 = 0;
                 }
                 volatile Unit *dst_u = &ctl.unit[k];
                 dst_u->u = U.u;
@@ -443,16 +482,22 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 dst_u->es0 = U.es0;
                 dst_u->as1 = U.as1;
                 dst_u->es1 = U.es1;
-                if (ROWS == kRowsSeq) dst_u->len = U.len;
+                if (ROWS == kRowsSeq || ROWS == kRowsPacked) dst_u->len = U.len;
+                if (ROWS == kRowsPacked) {
+                    dst_u->rows = U.rows;
+                    dst_u->q0 = U.q0;
+                    dst_u->k0 = U.k0;
+                }
                 mbar_arrive(smem_u32(&ctl.unit_full[k]));
                 if (u < 0) break;
                 if (U.n_kv == 0) continue;
                 if constexpr (!GATHER) {
+                    const int q_row0 = U.r0 + (ROWS == kRowsPacked ? U.q0 : 0);
                     // The unit's Q may only be loaded once the previous unit's last Q K^T has read the Q buffers;
                     // fetch it into L2 now, so that the load after that point is an L2 hit.
                     for (int t = 0; t < 2; ++t)
                         if ((t ? U.es1 > U.as1 : U.es0 > U.as0))
-                            for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, U.r0 + t * kBM, U.h, U.b);
+                            for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, q_row0 + t * kBM, U.h, U.b);
                     if (q_loads > 0) {  // the previous unit's last Q K^T has read Q
                         ok = wait_bounded(smem_u32(&ctl.q_empty), (q_loads - 1) & 1, ctl.abort_flag, p);
                         if (!ok) break;
@@ -461,10 +506,10 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     mbar_arrive_expect_tx(smem_u32(&ctl.q_full), (int(load0) + int(load1)) * q_tile_bytes);
                     if (load0)
                         for (int c = 0; c < p.q_chunks; ++c)
-                            tma_load_4d(sQ0 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0, U.h, U.b);
+                            tma_load_4d(sQ0 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, q_row0, U.h, U.b);
                     if (load1)
                         for (int c = 0; c < p.q_chunks; ++c)
-                            tma_load_4d(sQ1 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, U.r0 + kBM, U.h,
+                            tma_load_4d(sQ1 + c * kChunkBytes, &tmQ, smem_u32(&ctl.q_full), c * kChunk, q_row0 + kBM, U.h,
                                         U.b);
                     ++q_loads;
                 }
@@ -477,14 +522,14 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     const uint32_t dst = sSlot0 + s * slot_bytes;
                     const uint32_t bar = smem_u32(&ctl.full[s]);
                     const int j = i >> 1;
-                    if (!VT_DEV_CHECK(s < n_slots && (U.j0 + j) * BN < p.S_k, ctl.abort_flag, p)) {
+                    if (!VT_DEV_CHECK(s < n_slots && (U.j0 + j) * BN < (ROWS == kRowsPacked ? U.len : p.S_k), ctl.abort_flag, p)) {
                         ok = false;
                         break;
                     }
                     // kRowsSeq: the prefix's tiles, then those of the sequence's cache
                     const int tile = U.j0 + j;
                     const bool own = ROWS == kRowsSeq && tile >= p.prefix_tiles;
-                    const int key = (own ? tile - p.prefix_tiles : tile) * BN;
+                    const int key = (own ? tile - p.prefix_tiles : tile) * BN + (ROWS == kRowsPacked ? U.k0 : 0);
                     const int seq = ROWS == kRowsSeq && !own ? 0 : U.b;
                     if ((i & 1) == 0) {
                         const CUtensorMap *m = own ? &tmQ : &tmK;
@@ -618,7 +663,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             mma_commit_lead(smem_u32(&ctl.empty[kn]), lead);
                         }
                         if (!(ok = wait_full(vs))) break;
-                        if constexpr (ROWS == kRowsSeq) clear_past_end(sSlot0 + vs * slot_bytes, U, j, lane, p);
+                        if constexpr (ROWS == kRowsSeq || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
                         if (act(j)) {
                             if (!(ok = wait1(smem_u32(&ctl.p_full[tm][h & 1u]), (h >> 1) & 1u))) break;
                             ++h;
@@ -664,7 +709,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     const int kn = vs + 1 == n_slots ? 0 : vs + 1;  // slot of K_{j+1} (or the next unit's K_0)
                     const bool more = j + 1 < n_kv;
                     if (!(ok = wait_full(vs))) break;
-                    if constexpr (ROWS == kRowsSeq) clear_past_end(sSlot0 + vs * slot_bytes, U, j, lane, p);
+                    if constexpr (ROWS == kRowsSeq || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
                     const uint32_t v_lo = v_lo0 + vs * slot_step;
                     const uint32_t kn_lo = k_lo0 + kn * slot_step;
                     if (act0(j)) {
@@ -746,6 +791,11 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 key_lo = mask_lo = 0;
                 key_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(q_row, p.S_q - 1));
                 mask_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(tile_row0, p.S_q - 1));
+            } else if constexpr (ROWS == kRowsPacked) {
+                const int off = U.len - U.rows;
+                key_lo = packed_key_lo(p, off, U.len, q_row), key_hi = packed_key_hi(p, off, U.len, q_row);
+                mask_lo = packed_key_lo(p, off, U.len, min(tile_row0 + kBM, U.rows) - 1);
+                mask_hi = packed_key_hi(p, off, U.len, tile_row0);
             } else {
                 key_lo = band_key_lo(p, q_row), key_hi = band_key_hi(p, q_row);
                 mask_lo = band_key_lo(p, min(tile_row0 + kBM, p.S_q) - 1);
@@ -897,14 +947,14 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                 }
             }
-            const bool row_ok = q_row < p.S_q;
+            const bool row_ok = q_row < (ROWS == kRowsPacked ? U.rows : p.S_q);
             if (ok && EPI != kEpiSplit) {
                 // ------------------------------------------------------------ epilogue: O = O_t / l
                 // A row with no allowed key (l = 0, or no key tile at all) is written as 0.
                 if (n_my > 0) tc_fence_after();
                 const float inv_l = (ROWS == kRowsSeq ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
                 // kRowsSeq: row q_row is query head U.h * row_heads + g at position s
-                const int s_row = ROWS == kRowsSeq ? q_row / p.row_heads : q_row;
+                const int s_row = ROWS == kRowsSeq ? q_row / p.row_heads : ROWS == kRowsPacked ? U.q0 + q_row : q_row;
                 const int h_row = ROWS == kRowsSeq ? U.h * p.row_heads + q_row - s_row * p.row_heads : U.h;
                 uint8_t *orow = reinterpret_cast<uint8_t *>(p.O) +
                                 (static_cast<long long>(U.b) * p.o_sb + static_cast<long long>(h_row) * p.o_sh +
@@ -945,7 +995,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         p.lse[(static_cast<long long>(U.b) * p.H * p.row_heads + h_row) * p.row_tokens + s_row] =
                             l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
                     else
-                        p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + q_row] = lse_from(m_used, l);
+                        p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + s_row] = lse_from(m_used, l);
                 }
             } else if (ok && EPI == kEpiSplit) {
                 // ------------------------------------------------------------ epilogue: partial O, m, l

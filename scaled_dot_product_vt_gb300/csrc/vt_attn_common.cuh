@@ -59,6 +59,9 @@ struct AttnParams {
     // kRowsSeq: the key axis is the prefix's tiles (prefix_keys keys), then the tiles of the sequence's cache
     int prefix_tiles, prefix_keys, cache_keys;
     const int *kv_len;  // cached tokens per sequence, or null: cache_keys
+    // bf16, packed sequences (kRowsPacked): S_q and S_k count the rows of all sequences, n_qblocks the slots of packed_find
+    const int *cu_q, *cu_k;  // [n_seq + 1] first rows
+    int n_seq;
     // fp32 kernel: query tiles per work unit (1 or 2), and the CTAs of a thread-block cluster that share
     // one unit's key tiles and merge their results in distributed shared memory (1: no cluster)
     int tiles_per_unit;

@@ -164,29 +164,6 @@ Plan plan_of(const Args &a, int sms) {
     return p;
 }
 
-// A tensor's checks (strides of an index with one value are not looked at).
-vt_status tensor(const void *p, const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D, int elt, bool out,
-                 Span *span) {
-    if (!p) return VT_ERR_INVALID_ARG;
-    const int64_t n[3] = {B, H, S};
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && st[i] <= 0) return VT_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(p) % 16) return VT_ERR_MISALIGNED;
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && st[i] >= kMaxStrideBytes / elt) return VT_ERR_UNSUPPORTED;
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && (st[i] * elt) % 16) return VT_ERR_MISALIGNED;
-    if (!span_of(p, st, B, H, S, D, elt, span)) return VT_ERR_INVALID_ARG;
-    if (out && !rows_disjoint(st, B, H, S, D)) return VT_ERR_INVALID_ARG;
-    return VT_OK;
-}
-
-#define VT_TRY(expr)                          \
-    do {                                      \
-        const vt_status vt_try_ = (expr);     \
-        if (vt_try_ != VT_OK) return vt_try_; \
-    } while (0)
-
 vt_status check_memory(const Args &a, const Plan &plan) {
     const int elt = a.dtype == VT_BF16 ? 2 : 4;
     Span in[6], out[3];

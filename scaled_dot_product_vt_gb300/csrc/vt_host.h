@@ -11,6 +11,12 @@
 
 #include "../../include/vt_attn.h"
 
+#define VT_TRY(expr)                          \
+    do {                                      \
+        const vt_status vt_try_ = (expr);     \
+        if (vt_try_ != VT_OK) return vt_try_; \
+    } while (0)
+
 #pragma GCC visibility push(hidden)
 namespace vt {
 
@@ -77,6 +83,23 @@ bool ensure_smem(const void *kern, int dev, int bytes);
 // 4-D map over [B][H][S][D] (D innermost), box = 128-byte chunk of D x `rows` rows of S.
 bool make_map(CUtensorMap *map, const void *ptr, const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D,
               int elt, int rows);
+
+// A tensor's checks (strides of an index with one value are not looked at).
+inline vt_status tensor(const void *p, const int64_t st[3], int64_t B, int64_t H, int64_t S, int64_t D, int elt, bool out,
+                        Span *span) {
+    if (!p) return VT_ERR_INVALID_ARG;
+    const int64_t n[3] = {B, H, S};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] <= 0) return VT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p) % 16) return VT_ERR_MISALIGNED;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] >= kMaxStrideBytes / elt) return VT_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] * elt) % 16) return VT_ERR_MISALIGNED;
+    if (!span_of(p, st, B, H, S, D, elt, span)) return VT_ERR_INVALID_ARG;
+    if (out && !rows_disjoint(st, B, H, S, D)) return VT_ERR_INVALID_ARG;
+    return VT_OK;
+}
 
 // Wait for `stream`, then read and clear its status word on the current device.
 vt_status read_status(cudaStream_t stream);
