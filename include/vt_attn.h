@@ -467,6 +467,39 @@ typedef struct {
 
 vt_status vt_attn_fwd_packed(const vt_attn_packed_args *args, vt_stream_t stream);
 
+/*
+ * Gradients of vt_attn_fwd_packed.  `args` are the forward's, with its results: o and lse are read (both are required).
+ * With P = exp(scale q . k - LSE) over the pairs the mask keeps, g = d_o and delta = sum_e g_e o_e - d_lse of every query,
+ *   dv = sum P g,   dS = P (g . v - delta),   dq = scale sum dS k,   dk = scale sum dS q;
+ * sums for a key run over the queries of all the heads that share it.  A query or key without a partner has a gradient
+ * of 0; rows that belong to no sequence are not written.
+ *   d_o          [H,T_q,D_v]: the gradient of O
+ *   d_lse        fp32 [H,T_q] packed: the gradient of LSE, or NULL (0)
+ *   dq, dk, dv   as q, k and v.  They may lie beside each other in one tensor (the gradient of one projection); they must
+ *                not overlap the inputs.
+ *   workspace    DEVICE scratch, 256-byte aligned, at least vt_attn_bwd_packed_workspace_size bytes.  Every call writes
+ *                what it reads there; two calls that share it must not overlap on the GPU, replays of captured ones
+ *                included.
+ * Every sum is fp32 in an order that does not change from call to call; VT_BF16 rounds P and dS to bf16 before they are
+ * multiplied.  N or H equal to 0, or no row at all, is a valid empty problem; with T_q equal to 0, dk and dv are written
+ * as 0.
+ */
+typedef struct {
+    uint64_t struct_bytes; /* sizeof(vt_attn_packed_grads) */
+    const void *d_o;
+    const float *d_lse;
+    void *dq, *dk, *dv;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t do_stride[2], dq_stride[2], dk_stride[2], dv_stride[2];
+} vt_attn_packed_grads;
+
+vt_status vt_attn_bwd_packed(const vt_attn_packed_args *args, const vt_attn_packed_grads *grads, vt_stream_t stream);
+
+/* Bytes of workspace vt_attn_bwd_packed needs on the current device (0: none, or the call would be refused). */
+size_t vt_attn_bwd_packed_workspace_size(int64_t N, int64_t H, int64_t H_kv, int64_t T_q, int64_t T_k, int64_t D_qk,
+                                         int64_t D_v, vt_dtype dtype);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *vt_status_str(vt_status status);
 

@@ -32,7 +32,7 @@ EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
            "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
            "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size",
-           "vt_attn_fwd_packed",
+           "vt_attn_fwd_packed", "vt_attn_bwd_packed", "vt_attn_bwd_packed_workspace_size",
            "vt_status_str", "vt_last_device_status")
 
 
@@ -98,6 +98,10 @@ def load(path: str | None = None):
     lib.vt_attn_prefix_workspace_size.restype = sz
     lib.vt_attn_fwd_packed.argtypes = [ctypes.c_char_p, vp]
     lib.vt_attn_fwd_packed.restype = i
+    lib.vt_attn_bwd_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]
+    lib.vt_attn_bwd_packed.restype = i
+    lib.vt_attn_bwd_packed_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i]
+    lib.vt_attn_bwd_packed_workspace_size.restype = sz
     lib.vt_status_str.argtypes = [i]
     lib.vt_status_str.restype = ctypes.c_char_p
     lib.vt_last_device_status.argtypes = [vp]
@@ -210,15 +214,29 @@ def vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype) -
     return int(load().vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype))
 
 
-# vt_attn_packed_args in field order (every field is aligned without padding): its size and the addresses, then the rest
+# vt_attn_packed_args and vt_attn_packed_grads in field order (every field is aligned without padding): the size and the
+# addresses (and the workspace's size), then the rest
 _ATTN_PACKED_PTRS = struct.Struct("=8Q")
 _ATTN_PACKED_REST = struct.Struct("=8qifii8q")
 _ATTN_PACKED_BYTES = _ATTN_PACKED_PTRS.size + _ATTN_PACKED_REST.size
+_PACKED_GRADS_PTRS = struct.Struct("=8Q")
+_PACKED_GRADS_REST = struct.Struct("=8q")
+_PACKED_GRADS_BYTES = _PACKED_GRADS_PTRS.size + _PACKED_GRADS_REST.size
 
 
 def vt_attn_fwd_packed(args: bytes, stream) -> int:
     """The C entry point: ``args`` is a packed vt_attn_packed_args; returns the vt_status code."""
     return load().vt_attn_fwd_packed(args, stream)
+
+
+def vt_attn_bwd_packed(args: bytes, grads: bytes, stream) -> int:
+    """The C entry point: ``args`` is a packed vt_attn_packed_args and ``grads`` a packed vt_attn_packed_grads; returns
+    the vt_status code."""
+    return load().vt_attn_bwd_packed(args, grads, stream)
+
+
+def vt_attn_bwd_packed_workspace_size(N, H, H_kv, T_q, T_k, D_qk, D_v, dtype) -> int:
+    return int(load().vt_attn_bwd_packed_workspace_size(N, H, H_kv, T_q, T_k, D_qk, D_v, dtype))
 
 
 def vt_status_str(code: int) -> str:
@@ -356,7 +374,7 @@ def attn_fwd_general(q, k, v, scale: float | None = None, mask: str = "none", of
 # tensor is written out: it is most of what a small call costs on the host, and a function for it half as much again.
 
 _MOST_PLANS = 4096
-_rope_plans, _rope_bwd_plans, _prefix_plans, _packed_plans = {}, {}, {}, {}
+_rope_plans, _rope_bwd_plans, _prefix_plans, _packed_plans, _packed_bwd_plans = {}, {}, {}, {}, {}
 
 
 def _keep(plans, key, plan):
@@ -802,7 +820,7 @@ def attn_fwd_packed(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, mas
 
     Returns O [H,T_q,D_v], or (O, LSE) with ``return_lse`` (float32 [H,T_q], natural log).  Rows of no sequence are not
     written.  A new O lies token by token ([T_q,H,D_v] in memory).  ``stream`` may name another stream than the current
-    one.  Nothing is recorded for autograd."""
+    one.  Nothing is recorded for autograd; ``attn_bwd_packed`` gives the gradients."""
     if stream is not None or not _here(q):
         return _elsewhere(attn_fwd_packed, q, stream, (q, k, v, cu_q, cu_k), dict(
             scale=scale, mask=mask, window=window, return_lse=return_lse, out=out, lse=lse))
@@ -832,3 +850,71 @@ def attn_fwd_packed(q, k, v, cu_q, cu_k=None, *, scale: float | None = None, mas
     if rc != 0:
         raise VtError(rc, "vt_attn_fwd_packed")
     return (out, lse) if return_lse else out
+
+
+def _packed_bwd_plan(do, q, k, v, cu_q, cu_k, o, lse, dlse, dq, dk, dv, scale, mask, window):
+    """Checks of an attn_bwd_packed call from its tensors' metadata: (packed fixed parts of its two structs, bytes of
+    workspace)."""
+    if lse is None:
+        raise ValueError("lse must be the forward's")
+    rest, o_shape = _packed_plan(q, k, v, cu_q, cu_k, o, lse, scale, mask, window)
+    dt, dev = q[2], q[3]
+    if dlse is not None:
+        _check_lse("dlse", dlse, dev, tuple(o_shape[:2]))
+    strides = [_check("do", do, dev, dt, o_shape, 3)]
+    for name, meta, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        strides.append(_check(name, meta, dev, dt, like[0], 3) if meta is not None else _new_token_strides(like[0], dt))
+    H, T_q, D_qk = q[0]
+    H_kv, T_k, D_v = v[0]
+    need = vt_attn_bwd_packed_workspace_size(cu_q[0][0] - 1, H, H_kv, T_q, T_k, D_qk, D_v,
+                                             VT_BF16 if dt.itemsize == 2 else VT_F32)
+    return rest, _PACKED_GRADS_REST.pack(*(x for st in strides for x in st)), need
+
+
+def attn_bwd_packed(do, q, k, v, o, lse, cu_q, cu_k=None, *, scale: float | None = None, mask: str = "causal",
+                    window: int = 0, dlse=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of ``attn_fwd_packed``: see vt_attn_bwd_packed in include/vt_attn.h.  ``do`` [H,T_q,D_v] is the gradient
+    of O (and ``dlse``, float32 [H,T_q], that of LSE), ``o`` and ``lse`` are the forward's results and the other arguments
+    its own.  Returns (dq, dk, dv); new ones lie token by token, and given ones may lie beside each other in one tensor.
+    ``workspace`` may be a preallocated uint8 CUDA tensor of at least ``vt_attn_bwd_packed_workspace_size`` bytes,
+    ``stream`` another stream than the current one."""
+    if stream is not None or not _here(q):
+        return _elsewhere(attn_bwd_packed, q, stream, (do, q, k, v, o, lse, cu_q, cu_k), dict(
+            scale=scale, mask=mask, window=window, dlse=dlse, dq=dq, dk=dk, dv=dv, workspace=workspace))
+    import torch
+    if cu_k is None:
+        cu_k = cu_q
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)  # (a plan is kept by values: a tensor's may change)
+    if type(window) is not int:
+        window = int(window)
+    key = ((do.shape, do.stride(), do.dtype, do.get_device()), (q.shape, q.stride(), q.dtype, q.get_device()),
+           (k.shape, k.stride(), k.dtype, k.get_device()), (v.shape, v.stride(), v.dtype, v.get_device()),
+           (cu_q.shape, cu_q.stride(), cu_q.dtype, cu_q.get_device()),
+           (cu_k.shape, cu_k.stride(), cu_k.dtype, cu_k.get_device()), (o.shape, o.stride(), o.dtype, o.get_device()),
+           None if lse is None else (lse.shape, lse.stride(), lse.dtype, lse.get_device()),
+           None if dlse is None else (dlse.shape, dlse.stride(), dlse.dtype, dlse.get_device()),
+           None if dq is None else (dq.shape, dq.stride(), dq.dtype, dq.get_device()),
+           None if dk is None else (dk.shape, dk.stride(), dk.dtype, dk.get_device()),
+           None if dv is None else (dv.shape, dv.stride(), dv.dtype, dv.get_device()), scale, mask, window)
+    plan = _packed_bwd_plans.get(key)
+    if plan is None:
+        plan = _keep(_packed_bwd_plans, key, _packed_bwd_plan(*key))
+    rest, grads_rest, need = plan
+    dev = q.device
+    if dq is None:
+        dq = _new_tokens(q.shape, q.dtype, dev)
+    if dk is None:
+        dk = _new_tokens(k.shape, q.dtype, dev)
+    if dv is None:
+        dv = _new_tokens(v.shape, q.dtype, dev)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    args = _ATTN_PACKED_PTRS.pack(_ATTN_PACKED_BYTES, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+                                  cu_k.data_ptr(), o.data_ptr(), lse.data_ptr()) + rest
+    grads = _PACKED_GRADS_PTRS.pack(_PACKED_GRADS_BYTES, do.data_ptr(), _ptr(dlse), dq.data_ptr(), dk.data_ptr(),
+                                    dv.data_ptr(), _ptr(workspace), _workspace_bytes(workspace, q)) + grads_rest
+    rc = load().vt_attn_bwd_packed(args, grads, torch._C._cuda_getCurrentRawStream(q.get_device()))
+    if rc != 0:
+        raise VtError(rc, "vt_attn_bwd_packed")
+    return dq, dk, dv

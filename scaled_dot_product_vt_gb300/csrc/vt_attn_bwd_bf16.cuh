@@ -1,0 +1,869 @@
+// Gradients of the attention over packed sequences, bf16, for sm_103a (contract in include/vt_attn.h, vt_attn_bwd_packed).
+//
+// With s = scale q . k, P = exp(s - LSE), g = dO, delta = sum_e g_e O_e - dLSE:
+//   dV = P^T g,   dS = P o (g V^T - delta),   dQ = scale dS K,   dK = scale dS^T Q.
+// Three launches.  attn_bwd_stats_kernel forms -LSE log2(e) and -delta of every query; attn_bwd_kv_bf16_kernel walks the
+// queries of a 128-key block (dK, dV); attn_bwd_q_bf16_kernel walks the keys of a 128-query block (dQ).  The two walks
+// form S and dO V^T twice, 7 products of 128 x 128 x D per pair of blocks where one walk would take 5; in return no sum
+// crosses CTAs: no atomics, no fp32 dQ in memory, the same result in every call.  Both are bound by the tensor pipe: a
+// 128 x 128 x 128 product takes 512 cycles, and the 16384 exponentials and the rest of a tile's element work, by two
+// warpgroups of 64 columns each, about as long as two of them.
+//
+// Every tensor core operand lies as TMA left it or as a warpgroup wrote it to TMEM: the keys' walk forms the transposed
+// S^T = K Q^T and dP^T = V dO^T, whose rows are keys, so that P^T and dS^T are A operands from TMEM; Q and dO are K-major B
+// operands of the first two products and N-major ones of the last two, from one copy in shared memory.
+//
+// Warps (both kernels, 12): 0 loads (TMA, one lane) and draws the units (cluster launch control, as in
+// vt_attn_bf16_2q.cuh); 1 allocates TMEM and issues every MMA (one lane); 4-7 and 8-11 compute, columns 0-63 and 64-127
+// of a tile, one row per thread.  A warpgroup writes its bf16 P or dS over the first half of the columns it read itself.
+#pragma once
+
+#include "vt_attn_packed.cuh"
+
+namespace vt {
+
+// What the gradients' kernels take beside the attention's parameters.
+struct BwdParams : AttnParams {
+    float scale;
+    float *stat;      // [H][slots_q][2][128]: -LSE log2(e), then -delta, of the slot's rows (-inf and 0 past the end)
+    int slots_q;      // slots of 128 query rows
+    int units;        // work units of a launch
+    int n_qk;         // MMA N of dQ and dK: D_qk rounded up to 16
+    const void *dO;
+    long long do_sh, do_ss;
+    const float *dlse;
+    void *dQ, *dK, *dV;
+    long long dq_sh, dq_ss, dk_sh, dk_ss, dv_sh, dv_ss;
+    int dq_vec32, dk_vec32, dv_vec32;  // rows start on 32 bytes
+};
+
+namespace bw {
+
+constexpr int kTile = 128;  // rows of a block, on both sides
+constexpr int kThreads = 384;
+constexpr int kRegsControl = 72, kRegsCompute = 216;
+static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * 168, "register split exceeds the launch");
+constexpr int kChunk = 64;                       // bf16 elements of a 128-byte chunk
+constexpr uint32_t kChunkBytes = kTile * 128;    // a 128-byte column chunk of a tile
+constexpr uint32_t kStatBytes = 2 * kTile * 4;
+constexpr int kMaxSlots = 8;
+constexpr int kUnitRing = 4, kUnitReaders = 1 + 8;
+constexpr uint32_t kTmemCols = 512;
+
+// A block of 128 rows of one head of a sequence, and the tiles of the other side that it walks.
+struct Unit {
+    int u;               // -1: no more units
+    int h;               // query head (dQ) or key/value head (dK, dV)
+    int r0;              // the block's first row in its sequence
+    int q0, len_q, k0, len_k;
+    int qslot;           // the sequence's first slot of 128 queries
+    int lo, n;           // first tile, and tiles
+};
+
+struct Ctl {
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t own_full, own_empty;   // the unit's own tiles (K and V, or Q and dO)
+    uint64_t s_full[2], dp_full, p_full, ds_full, done;
+    uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
+    Unit unit[kUnitRing];
+    uint4 clc_resp;
+    uint64_t clc_full;
+    uint64_t drain;
+    uint32_t tmem_base;
+    volatile uint32_t abort_flag;
+};
+
+__device__ __forceinline__ int clamp_to(long long x, int most) {
+    return static_cast<int>(x < 0 ? 0 : (x > most ? most : x));
+}
+
+// kKeys: a block of keys and the queries that see one of them; otherwise a block of queries and the keys they see.
+template <bool kKeys>
+__device__ __forceinline__ Unit decode(const BwdParams &p, int u) {
+    Unit U;
+    U.u = u;
+    const int heads = kKeys ? p.H / p.kv_group : p.H;
+    const int slot = u / heads;
+    U.h = u - slot * heads;
+    // the heads of a block are adjacent; blocks with more work come first (a causal mask gives early keys and late
+    // queries the most partners)
+    const PackedSeq own = kKeys ? packed_find(p.cu_k, p.n_seq, p.S_k, kTile, slot, p.status)
+                                : packed_find(p.cu_q, p.n_seq, p.S_q, kTile, p.slots_q - 1 - slot, p.status);
+    const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q, p.status) : packed_seq(p.cu_k, own.n, p.S_k, p.status);
+    U.r0 = own.block * kTile;
+    U.q0 = kKeys ? other.start : own.start;
+    U.len_q = kKeys ? other.len : own.len;
+    U.k0 = kKeys ? own.start : other.start;
+    U.len_k = kKeys ? own.len : other.len;
+    U.qslot = U.q0 / kTile + own.n;
+    U.lo = U.n = 0;
+    if (U.r0 < own.len) {
+        const long long off = static_cast<long long>(U.len_k) - U.len_q;
+        const int last = min(U.r0 + kTile, own.len) - 1;
+        // partners [a, e) of rows r0..last
+        const int a = clamp_to(kKeys ? U.r0 - off - p.band_hi : U.r0 + off + p.band_lo, other.len);
+        const int e = clamp_to(kKeys ? last - off - p.band_lo + 1 : last + off + p.band_hi + 1, other.len);
+        if (a < e) {
+            U.lo = a / kTile;
+            U.n = (e + kTile - 1) / kTile - U.lo;
+        }
+    }
+    return U;
+}
+
+// Invariants of a decoded unit, checked by the debug build.
+template <bool kKeys>
+__device__ __forceinline__ bool valid(const BwdParams &p, const Unit &U) {
+    const int other = kKeys ? U.len_q : U.len_k;
+    return U.h >= 0 && U.h < p.H && U.r0 >= 0 && U.q0 >= 0 && U.len_q >= 0 && U.len_q <= p.S_q - U.q0 && U.k0 >= 0 &&
+           U.len_k >= 0 && U.len_k <= p.S_k - U.k0 && U.lo >= 0 && U.n >= 0 && U.lo + U.n <= (other + kTile - 1) / kTile &&
+           U.qslot + (U.len_q + kTile - 1) / kTile <= p.slots_q;
+}
+
+__device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const BwdParams &p, int lane) {
+    const int k = n % kUnitRing;
+    bool ok = true;
+    if (lane == 0) ok = wait_bounded(smem_u32(&ctl.unit_full[k]), (n / kUnitRing) & 1, ctl.abort_flag, p);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    __syncwarp();
+    const volatile Unit *src = &ctl.unit[k];
+    out->u = src->u;
+    out->h = src->h;
+    out->r0 = src->r0;
+    out->q0 = src->q0;
+    out->len_q = src->len_q;
+    out->k0 = src->k0;
+    out->len_k = src->len_k;
+    out->qslot = src->qslot;
+    out->lo = src->lo;
+    out->n = src->n;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl.unit_empty[k]));
+    return true;
+}
+
+// The producer lane draws the n-th unit of this CTA and publishes it; false on abort.
+template <bool kKeys>
+__device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_done, uint32_t *clc_par, const BwdParams &p) {
+    const int k = n % kUnitRing;
+    if (n >= kUnitRing && !wait_bounded(smem_u32(&ctl.unit_empty[k]), ((n / kUnitRing) - 1) & 1, ctl.abort_flag, p))
+        return false;
+    int u = -1;
+    if (n == 0) {
+        u = static_cast<int>(blockIdx.x);
+    } else if (!*clc_done) {
+        mbar_arrive_expect_tx(smem_u32(&ctl.clc_full), 16);
+        clc_try_cancel(smem_u32(&ctl.clc_resp), smem_u32(&ctl.clc_full));
+        if (!wait_bounded(smem_u32(&ctl.clc_full), *clc_par, ctl.abort_flag, p)) return false;
+        *clc_par ^= 1u;
+        u = clc_cancelled_x(smem_u32(&ctl.clc_resp));
+        if (u < 0) *clc_done = true;
+    }
+    Unit U{};
+    U.u = -1;
+    if (u >= 0 && u < p.units) {
+        U = decode<kKeys>(p, u);
+        if (!VT_DEV_CHECK(valid<kKeys>(p, U), ctl.abort_flag, p)) return false;
+    }
+    volatile Unit *dst = &ctl.unit[k];
+    dst->u = U.u;
+    dst->h = U.h;
+    dst->r0 = U.r0;
+    dst->q0 = U.q0;
+    dst->len_q = U.len_q;
+    dst->k0 = U.k0;
+    dst->len_k = U.len_k;
+    dst->qslot = U.qslot;
+    dst->lo = U.lo;
+    dst->n = U.n;
+    mbar_arrive(smem_u32(&ctl.unit_full[k]));
+    *out = U;
+    return true;
+}
+
+__device__ __forceinline__ void init(Ctl &ctl, int n_slots) {
+    for (int s = 0; s < n_slots; ++s) {
+        mbar_init(smem_u32(&ctl.full[s]), 1);
+        mbar_init(smem_u32(&ctl.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl.own_full), 1);
+    mbar_init(smem_u32(&ctl.own_empty), 1);
+    mbar_init(smem_u32(&ctl.s_full[0]), 1);
+    mbar_init(smem_u32(&ctl.s_full[1]), 1);
+    mbar_init(smem_u32(&ctl.dp_full), 1);
+    mbar_init(smem_u32(&ctl.p_full), 256);
+    mbar_init(smem_u32(&ctl.ds_full), 256);
+    mbar_init(smem_u32(&ctl.done), 1);
+    for (int k = 0; k < kUnitRing; ++k) {
+        mbar_init(smem_u32(&ctl.unit_full[k]), 1);
+        mbar_init(smem_u32(&ctl.unit_empty[k]), kUnitReaders);
+    }
+    mbar_init(smem_u32(&ctl.clc_full), 1);
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort_flag = 0;
+    fence_mbar_init();
+}
+
+// Zero rows n and on of a tile in shared memory (the whole warp): rows behind a sequence's end may hold NaN, which a
+// factor of 0 does not hide.  The tensor core sees the zeros afterwards.
+__device__ __forceinline__ void clear_rows(uint32_t tile, int chunks, int n, int lane) {
+    for (int c = 0; c < chunks; ++c)
+        for (int i = n * 8 + lane; i < kTile * 8; i += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * kChunkBytes + i * 16), "r"(0) : "memory");
+}
+
+// A tile of 128 rows: `chunks` boxes from row `row` of head h.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *m, uint32_t bar, int chunks, int row, int h) {
+    for (int c = 0; c < chunks; ++c) tma_load_4d(dst + c * kChunkBytes, m, bar, c * kChunk, row, h, 0);
+}
+
+// D columns of this thread's TMEM row, times f, as a bf16 row of global memory.
+__device__ __forceinline__ void store_row(uint32_t tmem, bool any, uint16_t *row, bool ok, int D, float f, bool vec32) {
+    for (int cc = 0; cc < D; cc += 16) {
+        uint32_t o[16];
+        if (any) {
+            tmem_ld16(tmem + cc, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0u;
+        }
+        if (!ok) continue;
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+        if (cc + 16 <= D) {
+            if (vec32) {
+                st_global_v8(row + cc, w);
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(row + cc);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (cc + k < D) row[cc + k] = static_cast<uint16_t>((w[k >> 1] >> ((k & 1) * 16)) & 0xFFFFu);
+        }
+    }
+}
+
+// Products D (+)= A B^T of K-steps of 16 columns, A and B K-major tiles in shared memory.
+template <int KS>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t lead) {
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+        const uint32_t off = (kk >> 2) * (kChunkBytes >> 4) + (kk & 3) * 2;
+        mma_ss_lead(d, a_lo + off, hi, b_lo + off, hi, idesc, kk > 0, lead);
+    }
+}
+// D (+)= A B over 128 rows of B (N-major tile): A is the bf16 tile that the warpgroups wrote, 32 columns at `a` and 32 at
+// a + 64.
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc0,
+                                         uint32_t lead) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+        mma_ts_lead(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + kk * 128, hi, idesc, (acc0 | kk) ? 1u : 0u, lead);
+}
+
+}  // namespace bw
+
+// -LSE log2(e) and -delta of every query, by slots of 128 rows, so that a tile's lie together on 16 bytes.  Bound by the
+// bytes of O and dO.
+constexpr int kStatThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const BwdParams p) {
+    constexpr int kVec = 16 / sizeof(T), kLanes = 128 / kVec;  // lanes of a row: 16 (bf16) or 32
+    constexpr int kRows = kStatThreads / kLanes;               // rows at a time
+    const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
+    const PackedSeq s = packed_find(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, p.status);
+    const int lane = threadIdx.x % kLanes, col = lane * kVec;
+    float *out = p.stat + (static_cast<long long>(h) * p.slots_q + slot) * (2 * bw::kTile);
+    const int n = min(s.len - s.block * bw::kTile, bw::kTile);  // rows of the slot
+    const long long first = static_cast<long long>(s.start) + s.block * bw::kTile;
+    const T *o = static_cast<const T *>(p.O) + h * p.o_sh, *g = static_cast<const T *>(p.dO) + h * p.do_sh;
+#pragma unroll 4
+    for (int r = threadIdx.x / kLanes; r < bw::kTile; r += kRows) {
+        float sum = 0.0f;
+        if (r < n && col < p.D_v) {
+            const T *a = o + (first + r) * p.o_ss + col, *b = g + (first + r) * p.do_ss + col;
+            if (col + kVec <= p.D_v) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a)), y = __ldg(reinterpret_cast<const uint4 *>(b));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (sizeof(T) == 2) {
+                        sum = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum);
+                        sum = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum);
+                    } else {
+                        sum = fmaf(__uint_as_float(xs[k]), __uint_as_float(ys[k]), sum);
+                    }
+                }
+            } else {
+                for (int k = 0; col + k < p.D_v; ++k) {
+                    if constexpr (sizeof(T) == 2)
+                        sum = fmaf(__uint_as_float(static_cast<uint32_t>(a[k]) << 16),
+                                   __uint_as_float(static_cast<uint32_t>(b[k]) << 16), sum);
+                    else
+                        sum = fmaf(a[k], b[k], sum);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (lane == 0) {
+            float nl = -INFINITY, nd = 0.0f;
+            if (r < n) {
+                const long long at = static_cast<long long>(h) * p.S_q + first + r;
+                const float lse = p.lse[at];
+                if (lse != -INFINITY) nl = -lse * 1.4426950408889634f;  // (a row without keys has no weight at all)
+                nd = (p.dlse ? p.dlse[at] : 0.0f) - sum;
+            }
+            out[r] = nl;
+            out[bw::kTile + r] = nd;
+        }
+    }
+}
+
+// dK and dV of 128 keys of one key/value head.  Shared memory: K, V, then stages of Q, dO and the queries' statistics.
+// TMEM: S^T (P^T over it), dP^T (dS^T over it), dV, dK.  The tensor pipe's order per tile i is
+//   dV += P_i^T dO_i,  S_{i+1} = K Q_{i+1}^T,  dK += dS_i^T Q_i,  dP_{i+1} = V dO_{i+1}^T,
+// so that two products run while the warpgroups form dS_i, and two while they form P_{i+1}.
+// KQ, KV: K-steps of 16 columns of D_qk and D_v (rounded up; the TMA fills zeros).
+template <int KQ, int KV>
+__global__ void __launch_bounds__(bw::kThreads, 1)
+    attn_bwd_kv_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                            const __grid_constant__ BwdParams p) {
+    using namespace bw;
+    __shared__ Ctl ctl;
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t q_bytes = p.q_chunks * kChunkBytes, v_bytes = p.v_chunks * kChunkBytes;
+    const uint32_t sK = base, sV = sK + q_bytes, sStage = sV + v_bytes;
+    const uint32_t stage_bytes = q_bytes + v_bytes;  // Q then dO
+    const uint32_t sStat = sStage + p.stages * stage_bytes;
+    uint8_t *const smem = smem_raw + (base - raw);
+
+    if (threadIdx.x == 0) init(ctl, p.stages);
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmG);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+    const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+        if (warp == 0) {
+            if (lane == 0) {
+                bool ok = true, clc_done = false;
+                uint32_t clc_par = 0, empty_phase = 0;
+                int s = 0, loads = 0, owns = 0;
+                for (int n = 0; ok; ++n) {
+                    Unit U;
+                    if (!draw_unit<true>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
+                    if (U.n == 0) continue;
+                    if (owns > 0 && !wait_bounded(smem_u32(&ctl.own_empty), (owns - 1) & 1, ctl.abort_flag, p)) break;
+                    mbar_arrive_expect_tx(smem_u32(&ctl.own_full), q_bytes + v_bytes);
+                    load_tile(sK, &tmK, smem_u32(&ctl.own_full), p.q_chunks, U.k0 + U.r0, U.h);
+                    load_tile(sV, &tmV, smem_u32(&ctl.own_full), p.v_chunks, U.k0 + U.r0, U.h);
+                    ++owns;
+                    for (int g = 0; ok && g < p.kv_group; ++g) {
+                        const int h = U.h * p.kv_group + g;
+                        for (int t = U.lo; t < U.lo + U.n; ++t) {
+                            if (loads >= p.stages) {
+                                ok = wait_bounded(smem_u32(&ctl.empty[s]), (empty_phase >> s) & 1u, ctl.abort_flag, p);
+                                empty_phase ^= 1u << s;
+                                if (!ok) break;
+                            }
+                            const uint32_t dst = sStage + s * stage_bytes, bar = smem_u32(&ctl.full[s]);
+                            mbar_arrive_expect_tx(bar, stage_bytes + kStatBytes);
+                            load_tile(dst, &tmQ, bar, p.q_chunks, U.q0 + t * kTile, h);
+                            load_tile(dst + q_bytes, &tmG, bar, p.v_chunks, U.q0 + t * kTile, h);
+                            bulk_load(sStat + s * kStatBytes,
+                                      p.stat + (static_cast<long long>(h) * p.slots_q + U.qslot + t) * (2 * kTile), kStatBytes,
+                                      bar);
+                            ++loads;
+                            if (++s == p.stages) s = 0;
+                        }
+                    }
+                }
+                if (ctl.abort_flag) {  // every copy lands before the CTA's memory goes away
+                    if (owns > 0) wait_drain(smem_u32(&ctl.own_full), (owns - 1) & 1, p);
+                    for (int k = max(0, loads - p.stages); k < loads; ++k)
+                        wait_drain(smem_u32(&ctl.full[k % p.stages]), (k / p.stages) & 1, p);
+                }
+            }
+        } else if (warp == 1) {
+            const uint32_t idesc_s = instr_desc(1, kTile, kTile, 0);
+            const uint32_t idesc_v = instr_desc(1, kTile, p.n_pv, 1), idesc_k = instr_desc(1, kTile, p.n_qk, 1);
+            const uint64_t rows0 = smem_desc_sw128(sStage, 16, 1024), cols0 = smem_desc_sw128(sStage, kChunkBytes, 1024);
+            const uint32_t r_hi = static_cast<uint32_t>(rows0 >> 32), c_hi = static_cast<uint32_t>(cols0 >> 32);
+            const uint32_t k_lo = static_cast<uint32_t>(smem_desc_sw128(sK, 16, 1024));
+            const uint32_t v_lo = static_cast<uint32_t>(smem_desc_sw128(sV, 16, 1024));
+            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0);
+            const uint32_t step = stage_bytes >> 4, g_off = q_bytes >> 4;
+            const uint32_t lead = elect_leader();
+            bool ok = true, any = false;
+            uint32_t full_phase = 0, own_par = 0, p_par = 0, ds_par = 0;
+            auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
+            };
+            int s = 0;
+            for (int n = 0; ok; ++n) {
+                Unit U;
+                if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+                if (U.n == 0) continue;
+                if (!(ok = wait1(smem_u32(&ctl.own_full), own_par))) break;
+                own_par ^= 1u;
+                const int total = U.n * p.kv_group;
+                int tile = 0;  // of the head's tiles
+                // the next stage has landed, and rows behind the sequence's end are zeros
+                auto arrive_stage = [&](int st) -> bool {
+                    if (!wait1(smem_u32(&ctl.full[st]), (full_phase >> st) & 1u)) return false;
+                    full_phase ^= 1u << st;
+                    const int rows = U.len_q - (U.lo + tile) * kTile;
+                    if (rows < kTile) {
+                        clear_rows(sStage + st * stage_bytes, p.q_chunks, rows, lane);
+                        clear_rows(sStage + st * stage_bytes + q_bytes, p.v_chunks, rows, lane);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                    if (++tile == U.n) tile = 0;
+                    return true;
+                };
+                if (!(ok = arrive_stage(s))) break;
+                mma_rows<KQ>(tS, k_lo, r_lo + s * step, r_hi, idesc_s, lead);
+                mma_commit_lead(smem_u32(&ctl.s_full[0]), lead);
+                mma_rows<KV>(tP, v_lo, r_lo + s * step + g_off, r_hi, idesc_s, lead);
+                mma_commit_lead(smem_u32(&ctl.dp_full), lead);
+                if (total == 1) mma_commit_lead(smem_u32(&ctl.own_empty), lead);
+                any = true;
+                for (int i = 0; i < total; ++i) {
+                    const int nx = s + 1 == p.stages ? 0 : s + 1;
+                    const bool more = i + 1 < total;
+                    if (!(ok = wait1(smem_u32(&ctl.p_full), p_par))) break;
+                    p_par ^= 1u;
+                    tc_fence_after();
+                    mma_cols(tDV, tS, c_lo + s * step + g_off, c_hi, idesc_v, i > 0, lead);
+                    if (more) {
+                        if (!(ok = arrive_stage(nx))) break;
+                        mma_rows<KQ>(tS, k_lo, r_lo + nx * step, r_hi, idesc_s, lead);
+                        mma_commit_lead(smem_u32(&ctl.s_full[0]), lead);
+                    }
+                    if (!(ok = wait1(smem_u32(&ctl.ds_full), ds_par))) break;
+                    ds_par ^= 1u;
+                    tc_fence_after();
+                    mma_cols(tDK, tP, c_lo + s * step, c_hi, idesc_k, i > 0, lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[s]), lead);
+                    if (more) {
+                        mma_rows<KV>(tP, v_lo, r_lo + nx * step + g_off, r_hi, idesc_s, lead);
+                        mma_commit_lead(smem_u32(&ctl.dp_full), lead);
+                        if (i + 2 == total) mma_commit_lead(smem_u32(&ctl.own_empty), lead);  // K and V are read
+                    } else {
+                        mma_commit_lead(smem_u32(&ctl.done), lead);
+                    }
+                    s = nx;
+                }
+            }
+            if (!ok && any) {
+                mma_commit_lead(smem_u32(&ctl.drain), lead);
+                if (lane == 0) wait_drain(smem_u32(&ctl.drain), 0, p);
+                __syncwarp();
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+        const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t aS = tS + lanes + wg * 64, aP = tP + lanes + wg * 64;
+        const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+        uint32_t s_par = 0, dp_par = 0, done_par = 0, full_phase = 0;
+        int s = 0;
+        bool ok = true;
+        auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
+        };
+        for (int n = 0; ok; ++n) {
+            Unit U;
+            if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+            const int total = U.n * p.kv_group;
+            // queries [q_lo, q_hi) see this thread's key
+            const long long at = static_cast<long long>(U.r0) + row - (static_cast<long long>(U.len_k) - U.len_q);
+            const int q_lo = clamp_to(at - p.band_hi, U.len_q), q_hi = clamp_to(at - p.band_lo + 1, U.len_q);
+            // tiles that every key of the block sees in whole
+            const int all_lo = clamp_to(at - row + kTile - 1 - p.band_hi, U.len_q);
+            const int all_hi = clamp_to(at - row - p.band_lo + 1, U.len_q);
+            // A query that sees one key has P = 1 whatever its score: dS is 0 (or dLSE), and not the rounding of dP - delta.
+            // That is every query (window of 1, one key), or the one whose band ends at key 0.
+            const bool lone = !p.dlse && (U.len_k == 1 || p.band_lo == p.band_hi);
+            const int q_lone = !p.dlse && U.r0 + row == 0 && q_lo - at + p.band_hi == 0 ? q_lo : -1;
+            int tile = U.lo;
+            for (int i = 0; i < total; ++i) {
+                const int q_first = tile * kTile;
+                if (++tile == U.lo + U.n) tile = U.lo;
+                const bool cut = q_first < all_lo || min(q_first + kTile, U.len_q) > all_hi;
+                const float4 *stat = reinterpret_cast<const float4 *>(smem + (sStat - base) + s * kStatBytes) + wg * 16;
+                if (!(ok = wait1(smem_u32(&ctl.full[s]), (full_phase >> s) & 1u))) break;  // the statistics
+                full_phase ^= 1u << s;
+                if (++s == p.stages) s = 0;
+                if (!(ok = wait1(smem_u32(&ctl.s_full[0]), s_par))) break;
+                s_par ^= 1u;
+                tc_fence_after();
+                uint32_t x[64];
+                tmem_ld32(aS, x);
+                tmem_ld32(aS + 32, x + 32);
+                tmem_wait_ld();
+                float2 pr[32];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float4 nl = stat[k];
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), c2,
+                                                make_float2(nl.x, nl.y));
+                    const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), c2,
+                                                make_float2(nl.z, nl.w));
+                    pr[2 * k] = make_float2(ex2(a.x), ex2(a.y));
+                    pr[2 * k + 1] = make_float2(ex2(b.x), ex2(b.y));
+                }
+                if (cut) {
+                    const int q = q_first + wg * 64;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (q + 2 * k < q_lo || q + 2 * k >= q_hi) pr[k].x = 0.0f;
+                        if (q + 2 * k + 1 < q_lo || q + 2 * k + 1 >= q_hi) pr[k].y = 0.0f;
+                    }
+                }
+                // P goes into dV's product as bf16 (2^-9 of each weight), dS below into dK's the same way
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(pr[16 * half + k].x, pr[16 * half + k].y);
+                    tmem_st16(aS + 16 * half, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&ctl.p_full));
+                if (lone || (q_lone >= q_first && q_lone < q_first + kTile)) {
+                    const int q = q_first + wg * 64;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (lone || q + 2 * k == q_lone) pr[k].x = 0.0f;
+                        if (lone || q + 2 * k + 1 == q_lone) pr[k].y = 0.0f;
+                    }
+                }
+
+                if (!(ok = wait1(smem_u32(&ctl.dp_full), dp_par))) break;
+                dp_par ^= 1u;
+                tc_fence_after();
+                tmem_ld32(aP, x);
+                tmem_ld32(aP + 32, x + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 nd = stat[32 + 8 * half + k];
+                        const uint32_t *d = x + 32 * half + 4 * k;
+                        const float2 *pp = pr + 16 * half + 2 * k;
+                        const float2 a = __fmul2_rn(pp[0], __fadd2_rn(make_float2(__uint_as_float(d[0]), __uint_as_float(d[1])),
+                                                                      make_float2(nd.x, nd.y)));
+                        const float2 b = __fmul2_rn(pp[1], __fadd2_rn(make_float2(__uint_as_float(d[2]), __uint_as_float(d[3])),
+                                                                      make_float2(nd.z, nd.w)));
+                        w[2 * k] = pack_bf16x2(a.x, a.y);
+                        w[2 * k + 1] = pack_bf16x2(b.x, b.y);
+                    }
+                    tmem_st16(aP + 16 * half, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&ctl.ds_full));
+            }
+            if (!ok) break;
+            if (total > 0) {
+                if (!(ok = wait1(smem_u32(&ctl.done), done_par))) break;
+                done_par ^= 1u;
+                tc_fence_after();
+            }
+            // warpgroup 0 stores dV, warpgroup 1 dK
+            const bool mine = U.r0 + row < U.len_k;
+            const long long key = static_cast<long long>(U.k0) + U.r0 + row;
+            if (wg == 0)
+                store_row(tDV + lanes, total > 0, static_cast<uint16_t *>(p.dV) + U.h * p.dv_sh + key * p.dv_ss, mine, p.D_v,
+                          1.0f, p.dv_vec32);
+            else
+                store_row(tDK + lanes, total > 0, static_cast<uint16_t *>(p.dK) + U.h * p.dk_sh + key * p.dk_ss, mine, p.D_qk,
+                          p.scale, p.dk_vec32);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// dQ of 128 queries of one head.  Shared memory: Q, dO, then a ring of equal slots for K_0, V_0, K_1, V_1, ...
+// TMEM: S of even and of odd key tiles (dS over them), dP, dQ.  The tensor pipe's order per tile j is
+//   dP_{j+1} = dO V_{j+1}^T,  dQ += dS_j K_j,  S_{j+2} = Q K_{j+2}^T,
+// so that the warpgroups, once past dS_j, wait for one product at most.
+template <int KQ, int KV>
+__global__ void __launch_bounds__(bw::kThreads, 1)
+    attn_bwd_q_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                           const __grid_constant__ BwdParams p) {
+    using namespace bw;
+    __shared__ Ctl ctl;
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t q_bytes = p.q_chunks * kChunkBytes, v_bytes = p.v_chunks * kChunkBytes;
+    const uint32_t sQ = base, sG = sQ + q_bytes, sSlot = sG + v_bytes;
+    const uint32_t slot_bytes = max(q_bytes, v_bytes);
+    const int n_slots = p.stages;
+
+    if (threadIdx.x == 0) init(ctl, n_slots);
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmG);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+    const uint32_t tS = tmem, tP = tmem + 256, tDQ = tmem + 384;  // S of tile j at tS + 128 (j & 1)
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+        if (warp == 0) {
+            if (lane == 0) {
+                bool ok = true, clc_done = false;
+                uint32_t clc_par = 0, empty_phase = 0;
+                int s = 0, loads = 0, owns = 0;
+                for (int n = 0; ok; ++n) {
+                    Unit U;
+                    if (!draw_unit<false>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
+                    if (U.n == 0) continue;
+                    // the unit's Q and dO replace the previous one's, once those have been read: into L2 until then
+                    for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, U.q0 + U.r0, U.h, 0);
+                    for (int c = 0; c < p.v_chunks; ++c) tma_prefetch_l2_4d(&tmG, c * kChunk, U.q0 + U.r0, U.h, 0);
+                    if (owns > 0 && !wait_bounded(smem_u32(&ctl.own_empty), (owns - 1) & 1, ctl.abort_flag, p)) break;
+                    mbar_arrive_expect_tx(smem_u32(&ctl.own_full), q_bytes + v_bytes);
+                    load_tile(sQ, &tmQ, smem_u32(&ctl.own_full), p.q_chunks, U.q0 + U.r0, U.h);
+                    load_tile(sG, &tmG, smem_u32(&ctl.own_full), p.v_chunks, U.q0 + U.r0, U.h);
+                    ++owns;
+                    const int hk = U.h / p.kv_group;
+                    for (int i = 0; i < 2 * U.n; ++i) {
+                        if (loads >= n_slots) {
+                            ok = wait_bounded(smem_u32(&ctl.empty[s]), (empty_phase >> s) & 1u, ctl.abort_flag, p);
+                            empty_phase ^= 1u << s;
+                            if (!ok) break;
+                        }
+                        const uint32_t dst = sSlot + s * slot_bytes, bar = smem_u32(&ctl.full[s]);
+                        const int key = U.k0 + (U.lo + (i >> 1)) * kTile;
+                        mbar_arrive_expect_tx(bar, (i & 1) ? v_bytes : q_bytes);
+                        if (i & 1) load_tile(dst, &tmV, bar, p.v_chunks, key, hk);
+                        else load_tile(dst, &tmK, bar, p.q_chunks, key, hk);
+                        ++loads;
+                        if (++s == n_slots) s = 0;
+                    }
+                }
+                if (ctl.abort_flag) {
+                    if (owns > 0) wait_drain(smem_u32(&ctl.own_full), (owns - 1) & 1, p);
+                    for (int k = max(0, loads - n_slots); k < loads; ++k)
+                        wait_drain(smem_u32(&ctl.full[k % n_slots]), (k / n_slots) & 1, p);
+                }
+            }
+        } else if (warp == 1) {
+            const uint32_t idesc_s = instr_desc(1, kTile, kTile, 0), idesc_q = instr_desc(1, kTile, p.n_qk, 1);
+            const uint64_t rows0 = smem_desc_sw128(sSlot, 16, 1024), cols0 = smem_desc_sw128(sSlot, kChunkBytes, 1024);
+            const uint32_t r_hi = static_cast<uint32_t>(rows0 >> 32), c_hi = static_cast<uint32_t>(cols0 >> 32);
+            const uint32_t q_lo = static_cast<uint32_t>(smem_desc_sw128(sQ, 16, 1024));
+            const uint32_t g_lo = static_cast<uint32_t>(smem_desc_sw128(sG, 16, 1024));
+            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0);
+            const uint32_t step = slot_bytes >> 4;
+            const uint32_t lead = elect_leader();
+            bool ok = true, any = false;
+            uint32_t full_phase = 0, own_par = 0, ds_par = 0, g = 0;  // g: key tiles of this CTA so far
+            auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
+            };
+            auto wait_slot = [&](int st) -> bool {
+                const bool r = wait1(smem_u32(&ctl.full[st]), (full_phase >> st) & 1u);
+                full_phase ^= 1u << st;
+                return r;
+            };
+            auto after = [&](int st, int d) { return st + d >= n_slots ? st + d - n_slots : st + d; };
+            int s = 0;  // slot of K_j
+            for (int n = 0; ok; ++n) {
+                Unit U;
+                if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+                if (U.n == 0) continue;
+                if (!(ok = wait1(smem_u32(&ctl.own_full), own_par))) break;
+                own_par ^= 1u;
+                // S_j from slot `st` (rows behind the sequence's end are zeros: dQ multiplies K by weights of 0)
+                auto scores = [&](int j, int st) -> bool {
+                    if (!wait_slot(st)) return false;
+                    const int rows = U.len_k - (U.lo + j) * kTile;
+                    if (rows < kTile) {
+                        clear_rows(sSlot + st * slot_bytes, p.q_chunks, rows, lane);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                    mma_rows<KQ>(tS + ((g + j) & 1u) * 128, q_lo, r_lo + st * step, r_hi, idesc_s, lead);
+                    mma_commit_lead(smem_u32(&ctl.s_full[(g + j) & 1u]), lead);
+                    return true;
+                };
+                auto dscores = [&](int j, int st) -> bool {
+                    if (!wait_slot(st)) return false;
+                    const int rows = U.len_k - (U.lo + j) * kTile;
+                    if (rows < kTile) {
+                        clear_rows(sSlot + st * slot_bytes, p.v_chunks, rows, lane);
+                        fence_async_shared();
+                        __syncwarp();
+                    }
+                    mma_rows<KV>(tP, g_lo, r_lo + st * step, r_hi, idesc_s, lead);
+                    mma_commit_lead(smem_u32(&ctl.dp_full), lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[st]), lead);  // V_j is read
+                    return true;
+                };
+                any = true;
+                if (!(ok = scores(0, s) && dscores(0, after(s, 1)))) break;
+                if (U.n == 1) mma_commit_lead(smem_u32(&ctl.own_empty), lead);
+                else if (!(ok = scores(1, after(s, 2)))) break;
+                for (int j = 0; j < U.n; ++j) {
+                    if (!(ok = wait1(smem_u32(&ctl.ds_full), ds_par))) break;
+                    ds_par ^= 1u;
+                    tc_fence_after();
+                    if (j + 1 < U.n) {
+                        if (!(ok = dscores(j + 1, after(s, 3)))) break;
+                        if (j + 2 == U.n) mma_commit_lead(smem_u32(&ctl.own_empty), lead);  // Q and dO are read
+                    }
+                    mma_cols(tDQ, tS + ((g + j) & 1u) * 128, c_lo + s * step, c_hi, idesc_q, j > 0, lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[s]), lead);
+                    if (j + 1 == U.n) mma_commit_lead(smem_u32(&ctl.done), lead);
+                    if (j + 2 < U.n && !(ok = scores(j + 2, after(s, 4)))) break;
+                    s = after(s, 2);
+                }
+                g += U.n;
+            }
+            if (!ok && any) {
+                mma_commit_lead(smem_u32(&ctl.drain), lead);
+                if (lane == 0) wait_drain(smem_u32(&ctl.drain), 0, p);
+                __syncwarp();
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+        const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+        uint32_t dp_par = 0, done_par = 0, g = 0;
+        bool ok = true;
+        auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
+        };
+        for (int n = 0; ok; ++n) {
+            Unit U;
+            if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
+            const int off = U.len_k - U.len_q;
+            const int last = min(U.r0 + kTile, U.len_q) - 1;
+            const int key_lo = packed_key_lo(p, off, U.len_k, U.r0 + row), key_hi = packed_key_hi(p, off, U.len_k, U.r0 + row);
+            const int all_lo = packed_key_lo(p, off, U.len_k, last), all_hi = packed_key_hi(p, off, U.len_k, U.r0);
+            float2 nl = make_float2(-INFINITY, -INFINITY), nd = make_float2(0.0f, 0.0f);
+            if (U.n > 0 && (key_hi - key_lo > 1 || p.dlse)) {  // (a query that sees one key: dS is 0, and not the rounding of dP - delta)
+                const float *st = p.stat + (static_cast<long long>(U.h) * p.slots_q + U.qslot + U.r0 / kTile) * (2 * kTile) + row;
+                nl.x = nl.y = st[0];
+                nd.x = nd.y = st[kTile];
+            }
+            for (int j = 0; j < U.n; ++j, ++g) {
+                const uint32_t aS = tS + lanes + (g & 1u) * 128 + wg * 64, aP = tP + lanes + wg * 64;
+                const int k0 = (U.lo + j) * kTile;
+                if (!(ok = wait1(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u))) break;
+                tc_fence_after();
+                uint32_t x[64];
+                tmem_ld32(aS, x);
+                tmem_ld32(aS + 32, x + 32);
+                tmem_wait_ld();
+                float2 pr[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nl);
+                    pr[k] = make_float2(ex2(a.x), ex2(a.y));
+                }
+                if (k0 < all_lo || k0 + kTile > all_hi) {
+                    const int k1 = k0 + wg * 64;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (k1 + 2 * k < key_lo || k1 + 2 * k >= key_hi) pr[k].x = 0.0f;
+                        if (k1 + 2 * k + 1 < key_lo || k1 + 2 * k + 1 >= key_hi) pr[k].y = 0.0f;
+                    }
+                }
+                if (!(ok = wait1(smem_u32(&ctl.dp_full), dp_par))) break;
+                dp_par ^= 1u;
+                tc_fence_after();
+                tmem_ld32(aP, x);
+                tmem_ld32(aP + 32, x + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint32_t *d = x + 32 * half + 2 * k;
+                        const float2 a = __fmul2_rn(pr[16 * half + k], __fadd2_rn(make_float2(__uint_as_float(d[0]),
+                                                                                              __uint_as_float(d[1])), nd));
+                        w[k] = pack_bf16x2(a.x, a.y);
+                    }
+                    tmem_st16(aS + 16 * half, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&ctl.ds_full));
+            }
+            if (!ok) break;
+            if (U.n > 0) {
+                if (!(ok = wait1(smem_u32(&ctl.done), done_par))) break;
+                done_par ^= 1u;
+                tc_fence_after();
+            }
+            // each warpgroup stores half of the columns, whole groups of 16
+            const bool mine = U.r0 + row < U.len_q;
+            const int half = min((p.n_qk / 16 + 1) / 2 * 16, p.D_qk), c0 = wg ? half : 0, cols = wg ? p.D_qk - half : half;
+            uint16_t *dst = static_cast<uint16_t *>(p.dQ) + U.h * p.dq_sh +
+                            (static_cast<long long>(U.q0) + U.r0 + row) * p.dq_ss + c0;
+            store_row(tDQ + lanes + c0, U.n > 0, dst, mine, cols, p.scale, p.dq_vec32);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace vt

@@ -1,7 +1,8 @@
-// Host side of vt_attn_fwd_packed: argument checks and launches (contract in include/vt_attn.h).
+// Host side of vt_attn_fwd_packed and vt_attn_bwd_packed: argument checks and launches (contract in include/vt_attn.h).
 #include <cmath>
 
 #include "vt_attn_bf16_2q.cuh"
+#include "vt_attn_bwd_bf16.cuh"
 #include "vt_attn_packed.cuh"
 #include "vt_host.h"
 #include "vt_pieces.h"
@@ -11,6 +12,7 @@ namespace packed {
 namespace {
 
 using Args = vt_attn_packed_args;
+using Grads = vt_attn_packed_grads;
 
 constexpr int kLeastRows = 64;  // rows of the smallest block a launch is cut into
 
@@ -178,6 +180,129 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     return env_check() ? read_status(stream) : VT_OK;
 }
 
+// ---------------------------------------------------------------- gradients
+
+// The workspace: the queries' statistics.
+size_t workspace_bytes(const Args &a) {
+    const int64_t slots = packed_slots(a.T_q, a.N, bw::kTile);
+    return static_cast<size_t>(a.H * slots) * bw::kStatBytes;
+}
+
+// Rows start on 32 bytes.
+bool vec32(const void *p, const int64_t st[2], int64_t H, int64_t T, int elt) {
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && (H < 2 || st[0] * elt % 32 == 0) && (T < 2 || st[1] * elt % 32 == 0);
+}
+
+using GradKern = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const BwdParams);
+
+template <template <int, int> class K>
+GradKern pick_grad(const BwdParams &p) {
+    const int kq = (p.D_qk + 15) / 16;
+    if (p.D_v <= 64) return kq <= 4 ? K<4, 4>::kern() : kq <= 6 ? K<6, 4>::kern() : K<8, 4>::kern();
+    return kq <= 4 ? K<4, 8>::kern() : kq <= 6 ? K<6, 8>::kern() : K<8, 8>::kern();
+}
+template <int KQ, int KV>
+struct KeysKern {
+    static GradKern kern() { return attn_bwd_kv_bf16_kernel<KQ, KV>; }
+};
+template <int KQ, int KV>
+struct QueriesKern {
+    static GradKern kern() { return attn_bwd_q_bf16_kernel<KQ, KV>; }
+};
+
+vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cudaStream_t stream) {
+    CUtensorMap tq, tk, tv, tg;
+    const int64_t H_kv = a.H_kv;
+    if (a.T_q > 0 && (!rows_map(&tq, a.q, a.q_stride, a.H, a.T_q, a.D_qk, 2, bw::kTile) ||
+                      !rows_map(&tg, g.d_o, g.do_stride, a.H, a.T_q, a.D_v, 2, bw::kTile)))
+        return VT_ERR_CUDA;
+    if (a.T_k > 0 && (!rows_map(&tk, a.k, a.k_stride, H_kv, a.T_k, a.D_qk, 2, bw::kTile) ||
+                      !rows_map(&tv, a.v, a.v_stride, H_kv, a.T_k, a.D_v, 2, bw::kTile)))
+        return VT_ERR_CUDA;
+    if (a.T_q == 0) tq = tk, tg = tv;  // (a side without rows is not read)
+    if (a.T_k == 0) tk = tq, tv = tg;
+    p.q_chunks = (p.D_qk + bw::kChunk - 1) / bw::kChunk;
+    p.v_chunks = (p.D_v + bw::kChunk - 1) / bw::kChunk;
+    p.n_pv = (p.D_v + 15) / 16 * 16;
+    p.n_qk = (p.D_qk + 15) / 16 * 16;
+    const int q_bytes = p.q_chunks * static_cast<int>(bw::kChunkBytes), v_bytes = p.v_chunks * static_cast<int>(bw::kChunkBytes);
+    const int room = kSmemLimit - 1024 - static_cast<int>(sizeof(bw::Ctl)) - 256 - q_bytes - v_bytes;
+    if (a.T_k > 0) {
+        const int stage = q_bytes + v_bytes + static_cast<int>(bw::kStatBytes);
+        p.stages = room / stage < 4 ? room / stage : 4;  // two at full width
+        p.units = static_cast<int>(packed_slots(a.T_k, a.N, bw::kTile) * H_kv);
+        const GradKern kern = pick_grad<KeysKern>(p);
+        const int smem = 1024 + q_bytes + v_bytes + p.stages * stage;
+        if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
+        kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
+        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    }
+    if (a.T_q > 0) {
+        const int slot = q_bytes > v_bytes ? q_bytes : v_bytes;
+        p.stages = room / slot < bw::kMaxSlots ? room / slot : bw::kMaxSlots;  // five at full width
+        p.units = static_cast<int>(p.slots_q * a.H);
+        const GradKern kern = pick_grad<QueriesKern>(p);
+        const int smem = 1024 + q_bytes + v_bytes + p.stages * slot;
+        if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
+        kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
+        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    }
+    return VT_OK;
+}
+
+vt_status backward(const Args &a, const Grads &g, cudaStream_t stream) {
+    VT_TRY(check_shape(a));
+    if (g.struct_bytes != sizeof(Grads)) return VT_ERR_INVALID_ARG;
+    if (a.N == 0 || a.H == 0 || (a.T_q == 0 && a.T_k == 0)) return VT_OK;
+    Memory m(a);
+    VT_TRY(m.inputs());
+    if (a.T_q > 0) {
+        VT_TRY(m.rows(a.o, a.o_stride, a.H, a.T_q, a.D_v, false));
+        VT_TRY(m.vector(a.lse, a.H * a.T_q * 4, 4, false));
+        VT_TRY(m.rows(g.d_o, g.do_stride, a.H, a.T_q, a.D_v, false));
+        if (g.d_lse) VT_TRY(m.vector(g.d_lse, a.H * a.T_q * 4, 4, false));
+    }
+    VT_TRY(m.rows(g.dq, g.dq_stride, a.H, a.T_q, a.D_qk, true));
+    VT_TRY(m.rows(g.dk, g.dk_stride, a.H_kv, a.T_k, a.D_qk, true));
+    VT_TRY(m.rows(g.dv, g.dv_stride, a.H_kv, a.T_k, a.D_v, true));
+    const size_t need = workspace_bytes(a);
+    if (g.workspace_bytes < need) return VT_ERR_INVALID_ARG;
+    VT_TRY(m.vector(g.workspace, static_cast<int64_t>(need), 256, true));
+    VT_TRY(m.clear());
+    int dev = 0;
+    DeviceInfo info;
+    if (cudaGetDevice(&dev) != cudaSuccess || !device_info(dev, &info)) return VT_ERR_CUDA;
+    BwdParams p{};
+    static_cast<AttnParams &>(p) = params_of(a, info.status + status_slot(stream));
+    const int elt = a.dtype == VT_BF16 ? 2 : 4;
+    p.scale = a.scale;
+    p.stat = static_cast<float *>(g.workspace);
+    p.slots_q = static_cast<int>(packed_slots(a.T_q, a.N, bw::kTile));
+    p.dO = g.d_o;
+    p.do_sh = g.do_stride[0];
+    p.do_ss = g.do_stride[1];
+    p.dlse = g.d_lse;
+    p.dQ = g.dq;
+    p.dq_sh = g.dq_stride[0];
+    p.dq_ss = g.dq_stride[1];
+    p.dK = g.dk;
+    p.dk_sh = g.dk_stride[0];
+    p.dk_ss = g.dk_stride[1];
+    p.dV = g.dv;
+    p.dv_sh = g.dv_stride[0];
+    p.dv_ss = g.dv_stride[1];
+    p.dq_vec32 = vec32(g.dq, g.dq_stride, a.H, a.T_q, elt);
+    p.dk_vec32 = vec32(g.dk, g.dk_stride, a.H_kv, a.T_k, elt);
+    p.dv_vec32 = vec32(g.dv, g.dv_stride, a.H_kv, a.T_k, elt);
+    if (a.T_q > 0) {
+        attn_bwd_stats_kernel<uint16_t><<<static_cast<unsigned>(p.slots_q * a.H), kStatThreads, 0, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
+    }
+    if (a.dtype != VT_BF16) return VT_ERR_UNSUPPORTED;
+    VT_TRY(backward_bf16(a, g, p, dev, stream));
+    return env_check() ? read_status(stream) : VT_OK;
+}
+
 }  // namespace
 }  // namespace packed
 }  // namespace vt
@@ -188,6 +313,22 @@ vt_status vt_attn_fwd_packed(const vt_attn_packed_args *args, vt_stream_t stream
     const vt::NvtxRange range("vt_attn_fwd_packed");
     if (!args) return VT_ERR_INVALID_ARG;
     return vt::packed::forward(*args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vt_status vt_attn_bwd_packed(const vt_attn_packed_args *args, const vt_attn_packed_grads *grads, vt_stream_t stream) {
+    const vt::NvtxRange range("vt_attn_bwd_packed");
+    if (!args || !grads) return VT_ERR_INVALID_ARG;
+    return vt::packed::backward(*args, *grads, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t vt_attn_bwd_packed_workspace_size(int64_t N, int64_t H, int64_t H_kv, int64_t T_q, int64_t T_k, int64_t D_qk,
+                                         int64_t D_v, vt_dtype dtype) {
+    vt_attn_packed_args a{};
+    a.struct_bytes = sizeof a;
+    a.N = N; a.H = H; a.H_kv = H_kv; a.T_q = T_q; a.T_k = T_k; a.D_qk = D_qk; a.D_v = D_v;
+    a.dtype = dtype;
+    if (vt::packed::check_shape(a) != VT_OK || N == 0 || H == 0 || (T_q == 0 && T_k == 0)) return 0;
+    return vt::packed::workspace_bytes(a);
 }
 
 }  // extern "C"

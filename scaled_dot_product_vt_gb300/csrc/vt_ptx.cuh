@@ -72,6 +72,13 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const void *tmap, int c0, int
                  : "memory");
 }
 
+// `bytes` consecutive bytes (a multiple of 16) into shared memory, both on 16 bytes; counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- asynchronous copies by threads
 
 // 16 bytes from global to shared memory: `bytes` (0 to 16) are read, the rest are zeros.
