@@ -422,6 +422,21 @@ size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t
                                      int64_t D_qk, int64_t D_v, vt_dtype dtype);
 
 /*
+ * vt_attn_fwd_prefix for trees of drafted tokens: the S_q <= 64 new tokens of a sequence are the nodes of a tree, or of
+ * several, that are checked in one call.  Node s lies in cache row kv_len[b] - S_q + s, as vt_qk_rope_fwd appends it (its
+ * position is the caller's: that of its depth), and parents[b * S_q + s] is the node that it continues, an earlier one, or
+ * -1 where it continues the tokens before the tree.  Its queries attend to the prefix, to the cache's rows before the tree
+ * (those below kv_len[b] - S_q), to the node's ancestors and to the node itself, and to no other node.  With parents s - 1
+ * the call is vt_attn_fwd_prefix.
+ * `parents` is int32 [B,S_q], packed, on the device, read there (a captured call replays with new trees).  A parent that is
+ * neither -1 nor an earlier node counts as -1 and records VT_ERR_DEVICE_BOUNDS in the stream's status word.  A node whose
+ * row is negative (a sequence shorter than the tree) has no key: its queries see the prefix alone.
+ * Arguments, workspace and errors otherwise as for vt_attn_fwd_prefix; VT_ERR_INVALID_ARG also for parents NULL,
+ * VT_ERR_UNSUPPORTED also for S_q above 64.
+ */
+vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *parents, vt_stream_t stream);
+
+/*
  * Attention over packed sequences: N sequences of different lengths whose rows lie behind each other in one tensor, as a
  * batch of prompts or of training texts is laid out without padding.
  *

@@ -31,7 +31,7 @@ STATUS = {
 EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_splitkv",
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
            "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
-           "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size",
+           "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size", "vt_attn_fwd_tree",
            "vt_attn_fwd_packed", "vt_attn_bwd_packed", "vt_attn_bwd_packed_workspace_size",
            "vt_status_str", "vt_last_device_status")
 
@@ -94,6 +94,8 @@ def load(path: str | None = None):
     lib.vt_qk_rope_bwd_workspace_size.restype = sz
     lib.vt_attn_fwd_prefix.argtypes = [ctypes.c_char_p, vp]
     lib.vt_attn_fwd_prefix.restype = i
+    lib.vt_attn_fwd_tree.argtypes = [ctypes.c_char_p, vp, vp]
+    lib.vt_attn_fwd_tree.restype = i
     lib.vt_attn_prefix_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i]
     lib.vt_attn_prefix_workspace_size.restype = sz
     lib.vt_attn_fwd_packed.argtypes = [ctypes.c_char_p, vp]
@@ -208,6 +210,11 @@ _ATTN_PREFIX_BYTES = _ATTN_PREFIX_PTRS.size + _ATTN_PREFIX_REST.size
 def vt_attn_fwd_prefix(args: bytes, stream) -> int:
     """The C entry point: ``args`` is a packed vt_attn_prefix_args; returns the vt_status code."""
     return load().vt_attn_fwd_prefix(args, stream)
+
+
+def vt_attn_fwd_tree(args: bytes, parents, stream) -> int:
+    """The C entry point: ``args`` is a packed vt_attn_prefix_args; returns the vt_status code."""
+    return load().vt_attn_fwd_tree(args, parents, stream)
 
 
 def vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype) -> int:
@@ -650,8 +657,8 @@ def qk_rope_bwd(dq_out, dk_out, freqs, positions, *, q=None, k=None, pair_axis=N
 
 # ---------------------------------------------------------------- attention behind a shared prefix
 
-def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, scale):
-    """Checks of an attn_fwd_prefix call from its tensors' metadata: (packed fixed part of its arguments, shape of O,
+def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, out, lse, scale):
+    """Checks of an attn_fwd_prefix or attn_fwd_tree call from its tensors' metadata: (packed fixed part of its arguments, shape of O,
     bytes of workspace)."""
     import torch
     q_shape, _, dt, dev = q
@@ -681,6 +688,9 @@ def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, kv_len, out, lse, scal
         svc = _check("v_cache", v_cache, dev, dt, (B, H_kv, S_c, D_v))
     if kv_len is not None:
         _check_vector("kv_len", kv_len, dev, torch.int32, B)
+    if parents is not None and (parents[3] != dev or parents[2] != torch.int32 or tuple(parents[0]) != (B, S_q) or any(
+            n > 1 and st != want for n, st, want in zip((B, S_q), parents[1], (S_q, 1)))):
+        raise ValueError("parents must be a contiguous int32 [B, S_q] tensor on the device of the other tensors")
     o_shape = (B, H, S_q, D_v)
     so = _check("out", out, dev, dt, o_shape) if out is not None else _new_strides(o_shape, dt)
     if lse is not None and (lse[3] != dev or lse[2] != torch.float32 or tuple(lse[0]) != (B, H, S_q) or any(
@@ -701,9 +711,26 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
     Prefix or cache may be None.  Returns O, or (O, LSE) with ``return_lse``.  ``workspace`` may be a preallocated
     uint8 CUDA tensor of at least ``vt_attn_prefix_workspace_size`` bytes, ``stream`` another stream than the
     current one."""
+    return _prefix_call(q, k_prefix, v_prefix, k_cache, v_cache, None, kv_len, scale, return_lse, out, lse, workspace,
+                        stream)
+
+
+def attn_fwd_tree(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len=None, *, scale: float | None = None,
+                  return_lse: bool = False, out=None, lse=None, workspace=None, stream=None):
+    """``attn_fwd_prefix`` for trees of drafted tokens: the S_q <= 64 tokens of each sequence that its last cache rows hold
+    are nodes, and parents (int32 [B,S_q], contiguous, on the device) names the earlier node that each continues, or -1.
+    A node sees the prefix, the cache before the tree, its ancestors and itself: see vt_attn_fwd_tree in
+    include/vt_attn.h.  The other arguments are those of ``attn_fwd_prefix``."""
+    if parents is None:
+        raise ValueError("parents is required")
+    return _prefix_call(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, scale, return_lse, out, lse, workspace,
+                        stream)
+
+
+def _prefix_call(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, scale, return_lse, out, lse, workspace, stream):
     if stream is not None or not _here(q):
-        return _elsewhere(attn_fwd_prefix, q, stream, (q, k_prefix, v_prefix, k_cache, v_cache, kv_len), dict(
-            scale=scale, return_lse=return_lse, out=out, lse=lse, workspace=workspace))
+        return _elsewhere(_prefix_call, q, stream, (q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, scale,
+                                                    return_lse, out, lse, workspace, None), {})
     import torch
     if scale is not None and type(scale) is not float:
         scale = float(scale)  # (a plan is kept by values: a tensor's may change)
@@ -712,6 +739,7 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
            None if v_prefix is None else (v_prefix.shape, v_prefix.stride(), v_prefix.dtype, v_prefix.get_device()),
            None if k_cache is None else (k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.get_device()),
            None if v_cache is None else (v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.get_device()),
+           None if parents is None else (parents.shape, parents.stride(), parents.dtype, parents.get_device()),
            None if kv_len is None else (kv_len.shape, kv_len.stride(), kv_len.dtype, kv_len.get_device()),
            None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()),
            None if lse is None else (lse.shape, lse.stride(), lse.dtype, lse.get_device()),
@@ -730,9 +758,10 @@ def attn_fwd_prefix(q, k_prefix, v_prefix, k_cache, v_cache, kv_len=None, *, sca
     args = _ATTN_PREFIX_PTRS.pack(_ATTN_PREFIX_BYTES, q.data_ptr(), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache),
                                   _ptr(v_cache), _ptr(kv_len), out.data_ptr(), _ptr(lse), _ptr(workspace),
                                   _workspace_bytes(workspace, q)) + rest
-    rc = load().vt_attn_fwd_prefix(args, torch._C._cuda_getCurrentRawStream(q.get_device()))
+    raw = torch._C._cuda_getCurrentRawStream(q.get_device())
+    rc = load().vt_attn_fwd_prefix(args, raw) if parents is None else load().vt_attn_fwd_tree(args, parents.data_ptr(), raw)
     if rc != 0:
-        raise VtError(rc, "vt_attn_fwd_prefix")
+        raise VtError(rc, "vt_attn_fwd_prefix" if parents is None else "vt_attn_fwd_tree")
     return (out, lse) if return_lse else out
 
 

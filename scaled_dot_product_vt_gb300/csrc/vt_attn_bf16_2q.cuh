@@ -51,6 +51,7 @@
 
 #include "vt_attn_common.cuh"
 #include "vt_attn_packed.cuh"
+#include "vt_attn_tree.cuh"
 
 namespace vt {
 namespace q2 {
@@ -62,7 +63,8 @@ constexpr int kRegsControl = 72;    // warpgroup 0 after setmaxnreg
 constexpr int kRegsSoftmax = 216;   // softmax warpgroups after setmaxnreg
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split exceeds the launch");
 constexpr int kMaxSlots = 6;
-constexpr int kRowsPlain = 0, kRowsAll = 1, kRowsSeq = 2, kRowsPacked = 3;  // what a tile's rows are (the kernel's ROWS)
+constexpr int kRowsPlain = 0, kRowsAll = 1, kRowsSeq = 2, kRowsPacked = 3, kRowsTree = 4;  // what a tile's rows are (the kernel's ROWS)
+__host__ __device__ constexpr bool of_sequence(int rows) { return rows == kRowsSeq || rows == kRowsTree; }  // over a prefix and a cache
 constexpr int kEpiPlain = 0, kEpiSplit = 1, kEpiPlainFast = 2;  // epilogue variants (the kernel's EPI)
 constexpr int kUnitRing = 4;        // unit indices in flight between the producer and the other roles
 constexpr int kUnitReaders = 1 + 8;  // the MMA warp and one lane of each softmax warp (one more MMA warp with the score ring)
@@ -126,9 +128,9 @@ __device__ __forceinline__ void gathered_unit(const AttnParams &p, unsigned u, i
     *split = static_cast<int>(u - item * p.n_split);
     const unsigned slice = p.n_qblocks > 1 ? item / p.n_qblocks : item;
     *qb = static_cast<int>(item - slice * p.n_qblocks);
-    *h = static_cast<int>(ROWS == kRowsSeq ? slice / p.B : slice);
-    *b = static_cast<int>(ROWS == kRowsSeq ? slice - *h * p.B : 0);
-    if (ROWS == kRowsSeq) *qb = p.n_qblocks - 1 - *qb;  // (later blocks see more of the cache)
+    *h = static_cast<int>(of_sequence(ROWS) ? slice / p.B : slice);
+    *b = static_cast<int>(of_sequence(ROWS) ? slice - *h * p.B : 0);
+    if (of_sequence(ROWS)) *qb = p.n_qblocks - 1 - *qb;  // (later blocks see more of the cache)
 }
 
 // Key tiles [*a, *e) that rows first..last of a packed sequence need (an empty range as 0, 0).
@@ -179,7 +181,7 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
     U.r0 = qb * kRows;
     }
     const int split = U.split;
-    if constexpr (ROWS == kRowsSeq) {
+    if constexpr (of_sequence(ROWS)) {
         int len = p.kv_len ? p.kv_len[U.b] : p.cache_keys;
         if (len < 0 || len > p.cache_keys) {  // a length outside the cache counts as the nearest one inside
             atomicOr(p.status, kStatusBounds);
@@ -198,7 +200,7 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
             e[t] = 0;
         } else if constexpr (ROWS == kRowsPacked) {
             packed_tiles(p, U, first, min(first + kBM, U.rows) - 1, &a[t], &e[t]);
-        } else if constexpr (ROWS == kRowsSeq) {
+        } else if constexpr (of_sequence(ROWS)) {
             a[t] = 0;
             e[t] = p.prefix_tiles + (own_keys(p, U.len, min(first + kBM, p.S_q) - 1) + kBN - 1) / kBN;
         } else {
@@ -270,7 +272,7 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const Attn
     out->es0 = src->es0;
     out->as1 = src->as1;
     out->es1 = src->es1;
-    if (ROWS == kRowsSeq || ROWS == kRowsPacked) out->len = src->len;
+    if (of_sequence(ROWS) || ROWS == kRowsPacked) out->len = src->len;
     if (ROWS == kRowsPacked) {
         out->rows = src->rows;
         out->q0 = src->q0;
@@ -320,7 +322,7 @@ __device__ __forceinline__ void gather_done() {
 // NaN, which a probability of 0 does not hide.  The tensor core sees the zeros afterwards.
 template <int ROWS>
 __device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int j, int lane, const AttnParams &p) {
-    const int before = ROWS == kRowsSeq ? p.prefix_tiles : 0;  // tiles of the prefix
+    const int before = of_sequence(ROWS) ? p.prefix_tiles : 0;  // tiles of the prefix
     const int n = U.len - (U.j0 + j - before) * kBN;           // rows of the tile that exist
     if (U.j0 + j < before || n >= kBN) return;
     for (int c = 0; c < p.v_chunks; ++c)
@@ -344,7 +346,8 @@ __device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int
 // sequence still fill a tile; no TMA box covers them for every group size, so the softmax warpgroups copy them.
 // kRowsAll: rows of all sequences, over keys that all of them see; the launch that follows may start early
 // (griddepcontrol).  kRowsSeq: rows of one sequence, over a shared prefix and then the sequence's own cache (tmK, tmV
-// and tmQ, tmV2), causal in the cache.
+// and tmQ, tmV2), causal in the cache.  kRowsTree: the same, and the tokens are the nodes of a tree (AttnParams::parents).
+// kRowsPacked: consecutive queries of one head of a packed sequence, loaded by TMA (vt_attn_packed.cuh).
 // Measured: kRowsAll, 256 rows of each of 8 key/value heads over 8192 shared keys, D = 128: 22 us with the launches for
 // empty caches and for adding the shares.  kRowsSeq, 8 sequences of 256 tokens (256 units), 8192 shared keys and caches up to 1024: 207 us, 1.43 PFLOP/s;
 // 256 units are two waves of 152 CTAs, 84 % full, which is what keeps it below the plain rows' 1.65.
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             const AttnParams p) {
     using namespace q2;
     constexpr int BN = kBN;
-    constexpr bool GATHER = ROWS == kRowsAll || ROWS == kRowsSeq;
+    constexpr bool GATHER = ROWS == kRowsAll || of_sequence(ROWS);
     __shared__ Ctl ctl;
     extern __shared__ uint8_t smem_raw[];
 
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 dst_u->es0 = U.es0;
                 dst_u->as1 = U.as1;
                 dst_u->es1 = U.es1;
-                if (ROWS == kRowsSeq || ROWS == kRowsPacked) dst_u->len = U.len;
+                if (of_sequence(ROWS) || ROWS == kRowsPacked) dst_u->len = U.len;
                 if (ROWS == kRowsPacked) {
                     dst_u->rows = U.rows;
                     dst_u->q0 = U.q0;
@@ -528,9 +531,9 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     }
                     // kRowsSeq: the prefix's tiles, then those of the sequence's cache
                     const int tile = U.j0 + j;
-                    const bool own = ROWS == kRowsSeq && tile >= p.prefix_tiles;
+                    const bool own = of_sequence(ROWS) && tile >= p.prefix_tiles;
                     const int key = (own ? tile - p.prefix_tiles : tile) * BN + (ROWS == kRowsPacked ? U.k0 : 0);
-                    const int seq = ROWS == kRowsSeq && !own ? 0 : U.b;
+                    const int seq = of_sequence(ROWS) && !own ? 0 : U.b;
                     if ((i & 1) == 0) {
                         const CUtensorMap *m = own ? &tmQ : &tmK;
                         mbar_arrive_expect_tx(bar, k_bytes);
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             mma_commit_lead(smem_u32(&ctl.empty[kn]), lead);
                         }
                         if (!(ok = wait_full(vs))) break;
-                        if constexpr (ROWS == kRowsSeq || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
+                        if constexpr (of_sequence(ROWS) || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
                         if (act(j)) {
                             if (!(ok = wait1(smem_u32(&ctl.p_full[tm][h & 1u]), (h >> 1) & 1u))) break;
                             ++h;
@@ -709,7 +712,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     const int kn = vs + 1 == n_slots ? 0 : vs + 1;  // slot of K_{j+1} (or the next unit's K_0)
                     const bool more = j + 1 < n_kv;
                     if (!(ok = wait_full(vs))) break;
-                    if constexpr (ROWS == kRowsSeq || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
+                    if constexpr (of_sequence(ROWS) || ROWS == kRowsPacked) clear_past_end<ROWS>(sSlot0 + vs * slot_bytes, U, j, lane, p);
                     const uint32_t v_lo = v_lo0 + vs * slot_step;
                     const uint32_t kn_lo = k_lo0 + kn * slot_step;
                     if (act0(j)) {
@@ -787,10 +790,18 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
             // this row's allowed keys [key_lo, key_hi); a key tile starting below mask_lo or ending past
             // mask_hi cuts some row's range and is masked (the same decision for the whole warpgroup)
             int key_lo, key_hi, mask_lo, mask_hi;
-            if constexpr (ROWS == kRowsSeq) {  // in the cache's tiles; in the prefix's, prefix_keys (below)
+            unsigned long long seen = 0;  // kRowsTree: the nodes that this row sees
+            if constexpr (of_sequence(ROWS)) {  // in the cache's tiles; in the prefix's, prefix_keys (below)
                 key_lo = mask_lo = 0;
                 key_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(q_row, p.S_q - 1));
-                mask_hi = p.prefix_tiles * BN + own_keys(p, U.len, min(tile_row0, p.S_q - 1));
+                mask_hi = p.prefix_tiles * BN + (ROWS == kRowsTree ? max(0, U.len - p.row_tokens)
+                                                                   : own_keys(p, U.len, min(tile_row0, p.S_q - 1)));
+                if constexpr (ROWS == kRowsTree) {
+                    TreeNodes tree;
+                    tree.load(p.parents + static_cast<long long>(U.b) * p.row_tokens, p.row_tokens, lane);
+                    tree.follow(p.row_tokens, lane, p.status);
+                    seen = tree.of(min(q_row, p.S_q - 1) / p.row_heads);
+                }
             } else if constexpr (ROWS == kRowsPacked) {
                 const int off = U.len - U.rows;
                 key_lo = packed_key_lo(p, off, U.len, q_row), key_hi = packed_key_hi(p, off, U.len, q_row);
@@ -844,10 +855,20 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     for (int k = 0; k < BN; ++k) s[k] *= p.scale_log2;
                 }
                 const int k0 = (U.j0 + as_my + j) * BN;
-                if constexpr (ROWS == kRowsSeq) {
+                if constexpr (of_sequence(ROWS)) {
                     const bool pre = k0 < p.prefix_tiles * BN;
                     const int hi = pre ? p.prefix_keys : key_hi;
                     if (k0 + BN > (pre ? p.prefix_keys : mask_hi)) {
+                        if (ROWS == kRowsTree && !pre) {
+                            const int first = p.prefix_tiles * BN + U.len - p.row_tokens - k0;  // of the tree, in this tile
+                            #pragma unroll
+                            for (int w = 0; w < BN / 32; ++w) {
+                                const uint32_t bits = tree_window(seen, 32 * w - first);
+                                #pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((bits >> k) & 1u)) s[32 * w + k] = -INFINITY;
+                            }
+                        }
                         #pragma unroll
                         for (int k = 0; k < BN; ++k)
                             if (k0 + k >= hi) s[k] = -INFINITY;
@@ -952,10 +973,10 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 // ------------------------------------------------------------ epilogue: O = O_t / l
                 // A row with no allowed key (l = 0, or no key tile at all) is written as 0.
                 if (n_my > 0) tc_fence_after();
-                const float inv_l = (ROWS == kRowsSeq ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
+                const float inv_l = (of_sequence(ROWS) ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
                 // kRowsSeq: row q_row is query head U.h * row_heads + g at position s
-                const int s_row = ROWS == kRowsSeq ? q_row / p.row_heads : ROWS == kRowsPacked ? U.q0 + q_row : q_row;
-                const int h_row = ROWS == kRowsSeq ? U.h * p.row_heads + q_row - s_row * p.row_heads : U.h;
+                const int s_row = of_sequence(ROWS) ? q_row / p.row_heads : ROWS == kRowsPacked ? U.q0 + q_row : q_row;
+                const int h_row = of_sequence(ROWS) ? U.h * p.row_heads + q_row - s_row * p.row_heads : U.h;
                 uint8_t *orow = reinterpret_cast<uint8_t *>(p.O) +
                                 (static_cast<long long>(U.b) * p.o_sb + static_cast<long long>(h_row) * p.o_sh +
                                  static_cast<long long>(s_row) * p.o_ss) * 2;
@@ -991,7 +1012,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     }
                 }
                 if (EPI == kEpiPlain && p.lse && row_ok) {
-                    if constexpr (ROWS == kRowsSeq)
+                    if constexpr (of_sequence(ROWS))
                         p.lse[(static_cast<long long>(U.b) * p.H * p.row_heads + h_row) * p.row_tokens + s_row] =
                             l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
                     else

@@ -4,6 +4,7 @@
 #include "vt_attn_bf16_2q.cuh"
 #include "vt_attn_bwd_bf16.cuh"
 #include "vt_attn_packed.cuh"
+#include "vt_attn_packed_f32.cuh"
 #include "vt_host.h"
 #include "vt_pieces.h"
 
@@ -163,6 +164,45 @@ vt_status forward_bf16(const Args &a, AttnParams p, int dev, cudaStream_t stream
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
+// The fp32 kernels' parameters beside those of params_of.
+void set_inputs(const Args &a, PackedF32Params *p) {
+    p->Q = a.q;
+    p->q_sh = a.q_stride[0];
+    p->q_ss = a.q_stride[1];
+    p->K = a.k;
+    p->k_sh = a.k_stride[0];
+    p->k_ss = a.k_stride[1];
+    p->V = a.v;
+    p->v_sh = a.v_stride[0];
+    p->v_ss = a.v_stride[1];
+}
+
+using F32Kern = void (*)(const PackedF32Params);
+
+vt_status launch_f32(F32Kern kern, int smem, int64_t ctas, const PackedF32Params &p, int dev, cudaStream_t stream) {
+    if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
+    kern<<<static_cast<unsigned>(ctas), pf::kThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
+
+// Columns of shared memory rows: a multiple of 32 that holds both widths.
+int padded(const Args &a) {
+    const int64_t D = a.D_qk > a.D_v ? a.D_qk : a.D_v;
+    return D <= 64 ? 64 : D <= 96 ? 96 : 128;
+}
+
+vt_status forward_f32(const Args &a, const AttnParams &base, int dev, cudaStream_t stream) {
+    PackedF32Params p{};
+    static_cast<AttnParams &>(p) = base;
+    set_inputs(a, &p);
+    const int64_t ctas = packed_slots(a.T_q, a.N, pf::kRows) * a.H;
+    switch (padded(a)) {
+        case 64: return launch_f32(attn_packed_f32_kernel<64>, pf::fwd_smem<64>(), ctas, p, dev, stream);
+        case 96: return launch_f32(attn_packed_f32_kernel<96>, pf::fwd_smem<96>(), ctas, p, dev, stream);
+        default: return launch_f32(attn_packed_f32_kernel<128>, pf::fwd_smem<128>(), ctas, p, dev, stream);
+    }
+}
+
 vt_status forward(const Args &a, cudaStream_t stream) {
     VT_TRY(check_shape(a));
     if (a.N == 0 || a.H == 0 || a.T_q == 0) return VT_OK;
@@ -175,8 +215,7 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     DeviceInfo info;
     if (cudaGetDevice(&dev) != cudaSuccess || !device_info(dev, &info)) return VT_ERR_CUDA;
     const AttnParams p = params_of(a, info.status + status_slot(stream));
-    if (a.dtype != VT_BF16) return VT_ERR_UNSUPPORTED;
-    VT_TRY(forward_bf16(a, p, dev, stream));
+    VT_TRY(a.dtype == VT_BF16 ? forward_bf16(a, p, dev, stream) : forward_f32(a, p, dev, stream));
     return env_check() ? read_status(stream) : VT_OK;
 }
 
@@ -250,6 +289,25 @@ vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cud
     return VT_OK;
 }
 
+vt_status backward_f32(const Args &a, const BwdParams &base, int dev, cudaStream_t stream) {
+    PackedF32Params p{};
+    static_cast<BwdParams &>(p) = base;
+    set_inputs(a, &p);
+    const int D = padded(a);
+    const int smem = D == 64 ? pf::bwd_smem<64>() : D == 96 ? pf::bwd_smem<96>() : pf::bwd_smem<128>();
+    if (a.T_k > 0)
+        VT_TRY(launch_f32(D == 64   ? attn_bwd_kv_f32_kernel<64>
+                          : D == 96 ? attn_bwd_kv_f32_kernel<96>
+                                    : attn_bwd_kv_f32_kernel<128>,
+                          smem, packed_slots(a.T_k, a.N, pf::kRows) * a.H_kv, p, dev, stream));
+    if (a.T_q > 0)
+        VT_TRY(launch_f32(D == 64   ? attn_bwd_q_f32_kernel<64>
+                          : D == 96 ? attn_bwd_q_f32_kernel<96>
+                                    : attn_bwd_q_f32_kernel<128>,
+                          smem, packed_slots(a.T_q, a.N, pf::kRows) * a.H, p, dev, stream));
+    return VT_OK;
+}
+
 vt_status backward(const Args &a, const Grads &g, cudaStream_t stream) {
     VT_TRY(check_shape(a));
     if (g.struct_bytes != sizeof(Grads)) return VT_ERR_INVALID_ARG;
@@ -295,11 +353,12 @@ vt_status backward(const Args &a, const Grads &g, cudaStream_t stream) {
     p.dk_vec32 = vec32(g.dk, g.dk_stride, a.H_kv, a.T_k, elt);
     p.dv_vec32 = vec32(g.dv, g.dv_stride, a.H_kv, a.T_k, elt);
     if (a.T_q > 0) {
-        attn_bwd_stats_kernel<uint16_t><<<static_cast<unsigned>(p.slots_q * a.H), kStatThreads, 0, stream>>>(p);
+        const unsigned ctas = static_cast<unsigned>(p.slots_q * a.H);
+        if (a.dtype == VT_BF16) attn_bwd_stats_kernel<uint16_t><<<ctas, kStatThreads, 0, stream>>>(p);
+        else attn_bwd_stats_kernel<float><<<ctas, kStatThreads, 0, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
     }
-    if (a.dtype != VT_BF16) return VT_ERR_UNSUPPORTED;
-    VT_TRY(backward_bf16(a, g, p, dev, stream));
+    VT_TRY(a.dtype == VT_BF16 ? backward_bf16(a, g, p, dev, stream) : backward_f32(a, p, dev, stream));
     return env_check() ? read_status(stream) : VT_OK;
 }
 

@@ -1,4 +1,4 @@
-// Host side of vt_attn_fwd_prefix: argument checks, the plan of a call, launches (contract in include/vt_attn.h).
+// Host side of vt_attn_fwd_prefix and vt_attn_fwd_tree: argument checks, the plan of a call, launches (contract in include/vt_attn.h).
 #include <cmath>
 #include <cstring>
 
@@ -164,9 +164,9 @@ Plan plan_of(const Args &a, int sms) {
     return p;
 }
 
-vt_status check_memory(const Args &a, const Plan &plan) {
+vt_status check_memory(const Args &a, const int32_t *parents, const Plan &plan) {
     const int elt = a.dtype == VT_BF16 ? 2 : 4;
-    Span in[6], out[3];
+    Span in[7], out[3];
     int n_in = 0, n_out = 0;
     VT_TRY(tensor(a.q, a.q_stride, a.B, a.H, a.S_q, a.D_qk, elt, false, &in[n_in++]));
     if (a.S_p > 0) {
@@ -181,6 +181,10 @@ vt_status check_memory(const Args &a, const Plan &plan) {
     if (a.kv_len) {
         if (reinterpret_cast<uintptr_t>(a.kv_len) % 4) return VT_ERR_MISALIGNED;
         if (!span_bytes(a.kv_len, a.B * 4, &in[n_in++])) return VT_ERR_INVALID_ARG;
+    }
+    if (parents) {
+        if (reinterpret_cast<uintptr_t>(parents) % 4) return VT_ERR_MISALIGNED;
+        if (!span_bytes(parents, a.B * a.S_q * 4, &in[n_in++])) return VT_ERR_INVALID_ARG;
     }
     VT_TRY(tensor(a.o, a.o_stride, a.B, a.H, a.S_q, a.D_v, elt, true, &out[n_out++]));
     if (a.lse) {
@@ -258,20 +262,22 @@ bool kv_maps(const Args &a, int rows, st::Maps *m) {
 
 using Kern = void (*)(const st::Maps, const st::Params);
 
-template <typename T>
+template <typename T, bool TREE>
 Kern pick(const Args &a, int *smem) {
     const bool k64 = a.D_qk <= 64, v64 = a.D_v <= 64;
-    if (k64 && v64) { *smem = st::Tile<T, 64, 64>::kSmem; return st::attn_stream_kernel<T, 64, 64>; }
-    if (k64) { *smem = st::Tile<T, 64, 128>::kSmem; return st::attn_stream_kernel<T, 64, 128>; }
-    if (v64) { *smem = st::Tile<T, 128, 64>::kSmem; return st::attn_stream_kernel<T, 128, 64>; }
+    if (k64 && v64) { *smem = st::Tile<T, 64, 64>::kSmem; return st::attn_stream_kernel<T, 64, 64, TREE>; }
+    if (k64) { *smem = st::Tile<T, 64, 128>::kSmem; return st::attn_stream_kernel<T, 64, 128, TREE>; }
+    if (v64) { *smem = st::Tile<T, 128, 64>::kSmem; return st::attn_stream_kernel<T, 128, 64, TREE>; }
     *smem = st::Tile<T, 128, 128>::kSmem;
-    return st::attn_stream_kernel<T, 128, 128>;
+    return st::attn_stream_kernel<T, 128, 128, TREE>;
 }
 
 vt_status launch_stream(const Args &a, const st::Maps &maps, const st::Params &p, int64_t units, int cluster, bool follows, int dev,
                         cudaStream_t stream) {
     int smem = 0;
-    const Kern kern = a.dtype == VT_BF16 ? pick<uint16_t>(a, &smem) : pick<float>(a, &smem);
+    const bool tree = p.parents && !p.all_rows;  // (the prefix's own launch reads no cache)
+    const Kern kern = a.dtype == VT_BF16 ? (tree ? pick<uint16_t, true>(a, &smem) : pick<uint16_t, false>(a, &smem))
+                                         : (tree ? pick<float, true>(a, &smem) : pick<float, false>(a, &smem));
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
     const int64_t ctas = units * cluster;
     if (ctas > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
@@ -330,6 +336,7 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.prefix_keys = sp.S_p;
     p.cache_keys = sp.S_c;
     p.kv_len = sp.kv_len;
+    p.parents = sp.parents;
     p.S_k = seq ? (p.prefix_tiles + (sp.S_c + q2::kBN - 1) / q2::kBN) * q2::kBN : sp.S_p;
     p.D_qk = sp.D_qk;
     p.D_v = sp.D_v;
@@ -375,13 +382,16 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     const int64_t units = per_head * heads;
     if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
     p.n_units = static_cast<int>(units);
-    const TileKern kern = seq ? pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p) : pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p);
+    const TileKern kern = !seq        ? pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p)
+                          : p.parents ? pick_tiles<q2::kEpiPlain, q2::kRowsTree>(p)
+                                      : pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p);
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
     kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(m.kc, m.kp, m.vp, m.vc, p);
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
-vt_status forward(const Args &a, cudaStream_t stream) {
+// (`parents`: the sequences' new tokens are the nodes of trees)
+vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     bool empty = false;
     VT_TRY(check_shape(a, &empty));
     if (empty) return VT_OK;
@@ -389,10 +399,11 @@ vt_status forward(const Args &a, cudaStream_t stream) {
     DeviceInfo info;
     const bool have = cudaGetDevice(&dev) == cudaSuccess && device_info(dev, &info);
     const Plan plan = plan_of(a, have ? info.sms : 152);
-    VT_TRY(check_memory(a, plan));
+    VT_TRY(check_memory(a, parents, plan));
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
+    p.parents = a.S_c > 0 ? parents : nullptr;
     if (plan.seq_tiles) {
         VT_TRY(launch_tiles(a, plan, z, p, true, info, dev, stream));
         return env_check() ? read_status(stream) : VT_OK;
@@ -451,7 +462,18 @@ extern "C" {
 vt_status vt_attn_fwd_prefix(const vt_attn_prefix_args *args, vt_stream_t stream) {
     const vt::NvtxRange range("vt_attn_fwd_prefix");
     if (!args) return VT_ERR_INVALID_ARG;
-    return vt::prefix::forward(*args, reinterpret_cast<cudaStream_t>(stream));
+    return vt::prefix::forward(*args, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *parents, vt_stream_t stream) {
+    const vt::NvtxRange range("vt_attn_fwd_tree");
+    if (!args) return VT_ERR_INVALID_ARG;
+    bool empty = false;
+    VT_TRY(vt::prefix::check_shape(*args, &empty));
+    if (empty) return VT_OK;
+    if (args->S_q > vt::kMaxNodes) return VT_ERR_UNSUPPORTED;
+    if (!parents) return VT_ERR_INVALID_ARG;
+    return vt::prefix::forward(*args, parents, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "vt_attn_common.cuh"
+#include "vt_attn_tree.cuh"
 
 namespace vt {
 namespace st {
@@ -53,6 +54,7 @@ struct Params {
     const void *Q;
     long long q_sb, q_sh, q_ss;
     const int *kv_len;  // [B], or null: S_c
+    const int *parents;  // kTree: [B][S_q]
     // partial results: [share][rows], rows = H_kv * B * S_q * G indexed ((hk * B + b) * S_q + s) * G + g
     float *part_o, *part_m, *part_l, *part_c;
     long long rows;
@@ -319,7 +321,8 @@ __device__ __forceinline__ int nth_longest(const Params &p, int n, int lane) {
     return __ffs(__ballot_sync(0xffffffffu, lane < p.B && rank == n)) - 1;
 }
 
-template <typename T, int DQ, int DV>
+// kTree: the S_q tokens of a sequence are the nodes of a tree, and its keys its cache (or with the prefix).
+template <typename T, int DQ, int DV, bool kTree = false>
 __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
     using L = Tile<T, DQ, DV>;
@@ -354,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     const int n_rows = min(kRowsTile, group_rows - f0);
 
     int len = p.all_rows ? 0 : (p.kv_len ? p.kv_len[b] : p.S_c);  // (asked for first: the keys wait for it)
+    TreeNodes tree;
+    if constexpr (kTree) tree.load(p.parents + static_cast<long long>(b) * p.S_q, p.S_q, lane);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(p.all_rows ? &maps.kp : &maps.kc);
         tma_prefetch_desc(p.all_rows ? &maps.vp : &maps.vc);
@@ -389,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     const int nP = (p.all_rows || p.with_prefix) ? p.S_p : 0;
     const int c0 = (nP + kKeys - 1) / kKeys * kKeys;  // where the cache starts on it
     auto own = [&](int f) { return p.all_rows ? 0 : max(0, len - p.S_q + f / p.G + 1); };
-    const int own_last = own(f0 + n_rows - 1), own_first = own(f0);
+    const int context = kTree ? max(0, len - p.S_q) : 0;  // keys before the tree
+    const int own_last = own(f0 + n_rows - 1), own_first = kTree ? context : own(f0);
     const int blocks = (c0 + own_last + kKeys - 1) / kKeys;
     const int cuts = p.cluster * p.shares;
     const int per = (blocks + cuts - 1) / cuts;
@@ -444,6 +450,12 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
             for (int j = 0; j < 4; ++j) q[ks][j] = (q[ks][j] & keep) ^ sign;
     }
     const int lim[2] = {g8 < n_rows ? own(f0 + g8) : 0, g8 + 8 < n_rows ? own(f0 + g8 + 8) : 0};
+    unsigned long long seen[2] = {0, 0};  // kTree: the nodes that the two rows see
+    if constexpr (kTree) {
+        tree.follow(p.S_q, lane, p.status);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) seen[r] = tree.of(min(f0 + g8 + 8 * r, per_b - 1) / p.G);
+    }
 
     float o[DV / 8][4];
 #pragma unroll
@@ -511,8 +523,12 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int seen = k0 < c0 ? nP : c0 + lim[i >> 1];
-                    if (k0 + 8 * n + 2 * t4 + (i & 1) >= seen) s[n][i] = -INFINITY;
+                    const int key = k0 + 8 * n + 2 * t4 + (i & 1);
+                    if (key >= (k0 < c0 ? nP : c0 + lim[i >> 1])) s[n][i] = -INFINITY;
+                    if (kTree && k0 >= c0) {
+                        const int node = key - c0 - (len - p.S_q);
+                        if (node >= 0 && !((seen[i >> 1] >> (node & 63)) & 1ull)) s[n][i] = -INFINITY;
+                    }
                 }
         }
 
