@@ -787,8 +787,8 @@ def _new_tokens(shape, dtype, device):
     multiple of 16 bytes are padded to one (a view is returned)."""
     import torch
     H, T, D = shape
-    step = 16 // dtype.itemsize
-    return torch.empty((T, H, (D + step - 1) // step * step), dtype=dtype, device=device)[..., :D].transpose(0, 1)
+    row, token = _new_token_strides(shape, dtype)
+    return torch.empty_strided((H, T, D), (row, token, 1), dtype=dtype, device=device)
 
 
 def _new_token_strides(shape, dtype):

@@ -29,6 +29,7 @@ struct BwdParams : AttnParams {
     int slots_q;      // slots of 128 query rows
     int units;        // work units of a launch
     int n_qk;         // MMA N of dQ and dK: D_qk rounded up to 16
+    int q_slots, v_slots;  // ring slots: of Q and dO (keys' walk), or of K and V (queries' walk)
     const void *dO;
     long long do_sh, do_ss;
     const float *dlse;
@@ -46,7 +47,7 @@ static_assert(128 * kRegsControl + 256 * kRegsCompute <= kThreads * 168, "regist
 constexpr int kChunk = 64;                       // bf16 elements of a 128-byte chunk
 constexpr uint32_t kChunkBytes = kTile * 128;    // a 128-byte column chunk of a tile
 constexpr uint32_t kStatBytes = 2 * kTile * 4;
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 4;  // of one ring
 constexpr int kUnitRing = 4, kUnitReaders = 1 + 8;
 constexpr uint32_t kTmemCols = 512;
 
@@ -61,7 +62,8 @@ struct Unit {
 };
 
 struct Ctl {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    // the walked side's two rings: [0] Q or K, with the queries' statistics, [1] dO or V
+    uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];
     uint64_t own_full, own_empty;   // the unit's own tiles (K and V, or Q and dO)
     uint64_t s_full[2], dp_full, p_full, ds_full, done;
     uint64_t unit_full[kUnitRing], unit_empty[kUnitRing];
@@ -142,6 +144,36 @@ __device__ __forceinline__ bool next_unit(Ctl &ctl, int n, Unit *out, const BwdP
     return true;
 }
 
+// A ring of shared-memory slots, as one role follows it: slot s, and for each slot the parity of its next phase.
+struct Ring {
+    int s = 0, n;
+    uint32_t phase = 0;
+    __device__ __forceinline__ explicit Ring(int slots) : n(slots) {}
+    __device__ __forceinline__ uint32_t parity() const { return (phase >> s) & 1u; }
+    __device__ __forceinline__ void next() {
+        phase ^= 1u << s;
+        if (++s == n) s = 0;
+    }
+};
+// The producer's side: the slot to load next, free once its previous tile has been read.
+struct LoadRing : Ring {
+    int loads = 0;
+    __device__ __forceinline__ explicit LoadRing(int slots) : Ring(slots) {}
+    __device__ __forceinline__ bool wait(Ctl &ctl, int which, const BwdParams &p) {
+        // (the first round finds every slot free: its phases are not waited for)
+        return loads < n || wait_bounded(smem_u32(&ctl.empty[which][s]), parity(), ctl.abort_flag, p);
+    }
+    __device__ __forceinline__ void loaded() {
+        if (loads >= n) phase ^= 1u << s;
+        ++loads;
+        if (++s == n) s = 0;
+    }
+    // Every copy lands before the CTA's memory goes away.
+    __device__ __forceinline__ void drain(Ctl &ctl, int which, const BwdParams &p) const {
+        for (int k = max(0, loads - n); k < loads; ++k) wait_drain(smem_u32(&ctl.full[which][k % n]), (k / n) & 1, p);
+    }
+};
+
 // The producer lane draws the n-th unit of this CTA and publishes it; false on abort.
 template <bool kKeys>
 __device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_done, uint32_t *clc_par, const BwdParams &p) {
@@ -181,10 +213,10 @@ __device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_
     return true;
 }
 
-__device__ __forceinline__ void init(Ctl &ctl, int n_slots) {
-    for (int s = 0; s < n_slots; ++s) {
-        mbar_init(smem_u32(&ctl.full[s]), 1);
-        mbar_init(smem_u32(&ctl.empty[s]), 1);
+__device__ __forceinline__ void init(Ctl &ctl) {
+    for (int i = 0; i < 2 * kMaxSlots; ++i) {
+        mbar_init(smem_u32(&ctl.full[0][i]), 1);
+        mbar_init(smem_u32(&ctl.empty[0][i]), 1);
     }
     mbar_init(smem_u32(&ctl.own_full), 1);
     mbar_init(smem_u32(&ctl.own_empty), 1);
@@ -210,6 +242,8 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int chunks, int n, int
     for (int c = 0; c < chunks; ++c)
         for (int i = n * 8 + lane; i < kTile * 8; i += 32)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * kChunkBytes + i * 16), "r"(0) : "memory");
+    fence_async_shared();
+    __syncwarp();
 }
 
 // A tile of 128 rows: `chunks` boxes from row `row` of head h.
@@ -325,7 +359,8 @@ __global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const BwdP
     }
 }
 
-// dK and dV of 128 keys of one key/value head.  Shared memory: K, V, then stages of Q, dO and the queries' statistics.
+// dK and dV of 128 keys of one key/value head.  Shared memory: K, V, then rings of Q (with its
+// queries' statistics) and of dO.
 // TMEM: S^T (P^T over it), dP^T (dS^T over it), dV, dK.  The tensor pipe's order per tile i is
 //   dV += P_i^T dO_i,  S_{i+1} = K Q_{i+1}^T,  dK += dS_i^T Q_i,  dP_{i+1} = V dO_{i+1}^T,
 // so that two products run while the warpgroups form dS_i, and two while they form P_{i+1}.
@@ -341,12 +376,11 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     const uint32_t q_bytes = p.q_chunks * kChunkBytes, v_bytes = p.v_chunks * kChunkBytes;
-    const uint32_t sK = base, sV = sK + q_bytes, sStage = sV + v_bytes;
-    const uint32_t stage_bytes = q_bytes + v_bytes;  // Q then dO
-    const uint32_t sStat = sStage + p.stages * stage_bytes;
+    const uint32_t sK = base, sV = sK + q_bytes, sQ = sV + v_bytes, sG = sQ + p.q_slots * q_bytes;
+    const uint32_t sStat = sG + p.v_slots * v_bytes;
     uint8_t *const smem = smem_raw + (base - raw);
 
-    if (threadIdx.x == 0) init(ctl, p.stages);
+    if (threadIdx.x == 0) init(ctl);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -368,8 +402,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         if (warp == 0) {
             if (lane == 0) {
                 bool ok = true, clc_done = false;
-                uint32_t clc_par = 0, empty_phase = 0;
-                int s = 0, loads = 0, owns = 0;
+                uint32_t clc_par = 0;
+                int owns = 0;
+                LoadRing rq(p.q_slots), rg(p.v_slots);
                 for (int n = 0; ok; ++n) {
                     Unit U;
                     if (!draw_unit<true>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
@@ -382,45 +417,45 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                     for (int g = 0; ok && g < p.kv_group; ++g) {
                         const int h = U.h * p.kv_group + g;
                         for (int t = U.lo; t < U.lo + U.n; ++t) {
-                            if (loads >= p.stages) {
-                                ok = wait_bounded(smem_u32(&ctl.empty[s]), (empty_phase >> s) & 1u, ctl.abort_flag, p);
-                                empty_phase ^= 1u << s;
-                                if (!ok) break;
-                            }
-                            const uint32_t dst = sStage + s * stage_bytes, bar = smem_u32(&ctl.full[s]);
-                            mbar_arrive_expect_tx(bar, stage_bytes + kStatBytes);
-                            load_tile(dst, &tmQ, bar, p.q_chunks, U.q0 + t * kTile, h);
-                            load_tile(dst + q_bytes, &tmG, bar, p.v_chunks, U.q0 + t * kTile, h);
-                            bulk_load(sStat + s * kStatBytes,
+                            if (!(ok = rq.wait(ctl, 0, p))) break;
+                            uint32_t bar = smem_u32(&ctl.full[0][rq.s]);
+                            mbar_arrive_expect_tx(bar, q_bytes + kStatBytes);
+                            load_tile(sQ + rq.s * q_bytes, &tmQ, bar, p.q_chunks, U.q0 + t * kTile, h);
+                            bulk_load(sStat + rq.s * kStatBytes,
                                       p.stat + (static_cast<long long>(h) * p.slots_q + U.qslot + t) * (2 * kTile), kStatBytes,
                                       bar);
-                            ++loads;
-                            if (++s == p.stages) s = 0;
+                            rq.loaded();
+                            if (!(ok = rg.wait(ctl, 1, p))) break;
+                            bar = smem_u32(&ctl.full[1][rg.s]);
+                            mbar_arrive_expect_tx(bar, v_bytes);
+                            load_tile(sG + rg.s * v_bytes, &tmG, bar, p.v_chunks, U.q0 + t * kTile, h);
+                            rg.loaded();
                         }
                     }
                 }
-                if (ctl.abort_flag) {  // every copy lands before the CTA's memory goes away
+                if (ctl.abort_flag) {
                     if (owns > 0) wait_drain(smem_u32(&ctl.own_full), (owns - 1) & 1, p);
-                    for (int k = max(0, loads - p.stages); k < loads; ++k)
-                        wait_drain(smem_u32(&ctl.full[k % p.stages]), (k / p.stages) & 1, p);
+                    rq.drain(ctl, 0, p);
+                    rg.drain(ctl, 1, p);
                 }
             }
         } else if (warp == 1) {
             const uint32_t idesc_s = instr_desc(1, kTile, kTile, 0);
             const uint32_t idesc_v = instr_desc(1, kTile, p.n_pv, 1), idesc_k = instr_desc(1, kTile, p.n_qk, 1);
-            const uint64_t rows0 = smem_desc_sw128(sStage, 16, 1024), cols0 = smem_desc_sw128(sStage, kChunkBytes, 1024);
+            const uint64_t rows0 = smem_desc_sw128(sQ, 16, 1024), cols0 = smem_desc_sw128(sQ, kChunkBytes, 1024);
             const uint32_t r_hi = static_cast<uint32_t>(rows0 >> 32), c_hi = static_cast<uint32_t>(cols0 >> 32);
             const uint32_t k_lo = static_cast<uint32_t>(smem_desc_sw128(sK, 16, 1024));
             const uint32_t v_lo = static_cast<uint32_t>(smem_desc_sw128(sV, 16, 1024));
-            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0);
-            const uint32_t step = stage_bytes >> 4, g_off = q_bytes >> 4;
+            // low words of slot 0 as rows (K-major) and as columns (N-major): Q, and dO behind it
+            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0), g_off = (sG - sQ) >> 4;
+            const uint32_t q_step = q_bytes >> 4, g_step = v_bytes >> 4;
             const uint32_t lead = elect_leader();
             bool ok = true, any = false;
-            uint32_t full_phase = 0, own_par = 0, p_par = 0, ds_par = 0;
+            uint32_t own_par = 0, p_par = 0, ds_par = 0;
             auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
             };
-            int s = 0;
+            Ring rq(p.q_slots), rg(p.v_slots);   // the next tile's slots
             for (int n = 0; ok; ++n) {
                 Unit U;
                 if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
@@ -428,53 +463,52 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                 if (!(ok = wait1(smem_u32(&ctl.own_full), own_par))) break;
                 own_par ^= 1u;
                 const int total = U.n * p.kv_group;
-                int tile = 0;  // of the head's tiles
-                // the next stage has landed, and rows behind the sequence's end are zeros
-                auto arrive_stage = [&](int st) -> bool {
-                    if (!wait1(smem_u32(&ctl.full[st]), (full_phase >> st) & 1u)) return false;
-                    full_phase ^= 1u << st;
-                    const int rows = U.len_q - (U.lo + tile) * kTile;
-                    if (rows < kTile) {
-                        clear_rows(sStage + st * stage_bytes, p.q_chunks, rows, lane);
-                        clear_rows(sStage + st * stage_bytes + q_bytes, p.v_chunks, rows, lane);
-                        fence_async_shared();
-                        __syncwarp();
-                    }
+                int tile = 0, rows = 0;  // of the head's tiles, and the rows of the next one that exist
+                int q_at = 0, g_at = 0;  // slots of the current tile
+                // S^T and dP^T of the next tile, once it has landed; rows behind the sequence's end become zeros
+                auto scores = [&]() -> bool {
+                    if (!wait1(smem_u32(&ctl.full[0][rq.s]), rq.parity())) return false;
+                    rows = U.len_q - (U.lo + tile) * kTile;
                     if (++tile == U.n) tile = 0;
+                    q_at = rq.s;
+                    rq.next();
+                    if (rows < kTile) clear_rows(sQ + q_at * q_bytes, p.q_chunks, rows, lane);
+                    mma_rows<KQ>(tS, k_lo, r_lo + q_at * q_step, r_hi, idesc_s, lead);
+                    mma_commit_lead(smem_u32(&ctl.s_full[0]), lead);
                     return true;
                 };
-                if (!(ok = arrive_stage(s))) break;
-                mma_rows<KQ>(tS, k_lo, r_lo + s * step, r_hi, idesc_s, lead);
-                mma_commit_lead(smem_u32(&ctl.s_full[0]), lead);
-                mma_rows<KV>(tP, v_lo, r_lo + s * step + g_off, r_hi, idesc_s, lead);
-                mma_commit_lead(smem_u32(&ctl.dp_full), lead);
-                if (total == 1) mma_commit_lead(smem_u32(&ctl.own_empty), lead);
+                auto dscores = [&]() -> bool {
+                    if (!wait1(smem_u32(&ctl.full[1][rg.s]), rg.parity())) return false;
+                    g_at = rg.s;
+                    rg.next();
+                    if (rows < kTile) clear_rows(sG + g_at * v_bytes, p.v_chunks, rows, lane);
+                    mma_rows<KV>(tP, v_lo, r_lo + g_off + g_at * g_step, r_hi, idesc_s, lead);
+                    mma_commit_lead(smem_u32(&ctl.dp_full), lead);
+                    return true;
+                };
                 any = true;
+                if (!(ok = scores() && dscores())) break;
+                if (total == 1) mma_commit_lead(smem_u32(&ctl.own_empty), lead);
                 for (int i = 0; i < total; ++i) {
-                    const int nx = s + 1 == p.stages ? 0 : s + 1;
                     const bool more = i + 1 < total;
+                    const int q_now = q_at;
                     if (!(ok = wait1(smem_u32(&ctl.p_full), p_par))) break;
                     p_par ^= 1u;
                     tc_fence_after();
-                    mma_cols(tDV, tS, c_lo + s * step + g_off, c_hi, idesc_v, i > 0, lead);
-                    if (more) {
-                        if (!(ok = arrive_stage(nx))) break;
-                        mma_rows<KQ>(tS, k_lo, r_lo + nx * step, r_hi, idesc_s, lead);
-                        mma_commit_lead(smem_u32(&ctl.s_full[0]), lead);
-                    }
+                    mma_cols(tDV, tS, c_lo + g_off + g_at * g_step, c_hi, idesc_v, i > 0, lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[1][g_at]), lead);
+                    if (more && !(ok = scores())) break;
                     if (!(ok = wait1(smem_u32(&ctl.ds_full), ds_par))) break;
                     ds_par ^= 1u;
                     tc_fence_after();
-                    mma_cols(tDK, tP, c_lo + s * step, c_hi, idesc_k, i > 0, lead);
-                    mma_commit_lead(smem_u32(&ctl.empty[s]), lead);
+                    mma_cols(tDK, tP, c_lo + q_now * q_step, c_hi, idesc_k, i > 0, lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[0][q_now]), lead);
                     if (more) {
-                        mma_rows<KV>(tP, v_lo, r_lo + nx * step + g_off, r_hi, idesc_s, lead);
-                        mma_commit_lead(smem_u32(&ctl.dp_full), lead);
+                        if (!(ok = dscores())) break;
                         if (i + 2 == total) mma_commit_lead(smem_u32(&ctl.own_empty), lead);  // K and V are read
                     } else {
                         mma_commit_lead(smem_u32(&ctl.done), lead);
                     }
-                    s = nx;
                 }
             }
             if (!ok && any) {
@@ -489,8 +523,8 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t aS = tS + lanes + wg * 64, aP = tP + lanes + wg * 64;
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-        uint32_t s_par = 0, dp_par = 0, done_par = 0, full_phase = 0;
-        int s = 0;
+        uint32_t s_par = 0, dp_par = 0, done_par = 0;
+        Ring rq(p.q_slots);
         bool ok = true;
         auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
@@ -514,10 +548,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                 const int q_first = tile * kTile;
                 if (++tile == U.lo + U.n) tile = U.lo;
                 const bool cut = q_first < all_lo || min(q_first + kTile, U.len_q) > all_hi;
-                const float4 *stat = reinterpret_cast<const float4 *>(smem + (sStat - base) + s * kStatBytes) + wg * 16;
-                if (!(ok = wait1(smem_u32(&ctl.full[s]), (full_phase >> s) & 1u))) break;  // the statistics
-                full_phase ^= 1u << s;
-                if (++s == p.stages) s = 0;
+                const float4 *stat = reinterpret_cast<const float4 *>(smem + (sStat - base) + rq.s * kStatBytes) + wg * 16;
+                if (!(ok = wait1(smem_u32(&ctl.full[0][rq.s]), rq.parity()))) break;  // the statistics
+                rq.next();
                 if (!(ok = wait1(smem_u32(&ctl.s_full[0]), s_par))) break;
                 s_par ^= 1u;
                 tc_fence_after();
@@ -618,7 +651,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     }
 }
 
-// dQ of 128 queries of one head.  Shared memory: Q, dO, then a ring of equal slots for K_0, V_0, K_1, V_1, ...
+// dQ of 128 queries of one head.  Shared memory: Q, dO, then rings of K and of V.
 // TMEM: S of even and of odd key tiles (dS over them), dP, dQ.  The tensor pipe's order per tile j is
 //   dP_{j+1} = dO V_{j+1}^T,  dQ += dS_j K_j,  S_{j+2} = Q K_{j+2}^T,
 // so that the warpgroups, once past dS_j, wait for one product at most.
@@ -633,11 +666,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     const uint32_t q_bytes = p.q_chunks * kChunkBytes, v_bytes = p.v_chunks * kChunkBytes;
-    const uint32_t sQ = base, sG = sQ + q_bytes, sSlot = sG + v_bytes;
-    const uint32_t slot_bytes = max(q_bytes, v_bytes);
-    const int n_slots = p.stages;
+    const uint32_t sQ = base, sG = sQ + q_bytes, sK = sG + v_bytes, sV = sK + p.q_slots * q_bytes;
 
-    if (threadIdx.x == 0) init(ctl, n_slots);
+    if (threadIdx.x == 0) init(ctl);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
@@ -659,8 +690,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         if (warp == 0) {
             if (lane == 0) {
                 bool ok = true, clc_done = false;
-                uint32_t clc_par = 0, empty_phase = 0;
-                int s = 0, loads = 0, owns = 0;
+                uint32_t clc_par = 0;
+                int owns = 0;
+                LoadRing rk(p.q_slots), rv(p.v_slots);
                 for (int n = 0; ok; ++n) {
                     Unit U;
                     if (!draw_unit<false>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
@@ -674,97 +706,86 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                     load_tile(sG, &tmG, smem_u32(&ctl.own_full), p.v_chunks, U.q0 + U.r0, U.h);
                     ++owns;
                     const int hk = U.h / p.kv_group;
-                    for (int i = 0; i < 2 * U.n; ++i) {
-                        if (loads >= n_slots) {
-                            ok = wait_bounded(smem_u32(&ctl.empty[s]), (empty_phase >> s) & 1u, ctl.abort_flag, p);
-                            empty_phase ^= 1u << s;
-                            if (!ok) break;
-                        }
-                        const uint32_t dst = sSlot + s * slot_bytes, bar = smem_u32(&ctl.full[s]);
-                        const int key = U.k0 + (U.lo + (i >> 1)) * kTile;
-                        mbar_arrive_expect_tx(bar, (i & 1) ? v_bytes : q_bytes);
-                        if (i & 1) load_tile(dst, &tmV, bar, p.v_chunks, key, hk);
-                        else load_tile(dst, &tmK, bar, p.q_chunks, key, hk);
-                        ++loads;
-                        if (++s == n_slots) s = 0;
+                    for (int j = 0; j < U.n; ++j) {
+                        const int key = U.k0 + (U.lo + j) * kTile;
+                        if (!(ok = rk.wait(ctl, 0, p))) break;
+                        uint32_t bar = smem_u32(&ctl.full[0][rk.s]);
+                        mbar_arrive_expect_tx(bar, q_bytes);
+                        load_tile(sK + rk.s * q_bytes, &tmK, bar, p.q_chunks, key, hk);
+                        rk.loaded();
+                        if (!(ok = rv.wait(ctl, 1, p))) break;
+                        bar = smem_u32(&ctl.full[1][rv.s]);
+                        mbar_arrive_expect_tx(bar, v_bytes);
+                        load_tile(sV + rv.s * v_bytes, &tmV, bar, p.v_chunks, key, hk);
+                        rv.loaded();
                     }
                 }
                 if (ctl.abort_flag) {
                     if (owns > 0) wait_drain(smem_u32(&ctl.own_full), (owns - 1) & 1, p);
-                    for (int k = max(0, loads - n_slots); k < loads; ++k)
-                        wait_drain(smem_u32(&ctl.full[k % n_slots]), (k / n_slots) & 1, p);
+                    rk.drain(ctl, 0, p);
+                    rv.drain(ctl, 1, p);
                 }
             }
         } else if (warp == 1) {
             const uint32_t idesc_s = instr_desc(1, kTile, kTile, 0), idesc_q = instr_desc(1, kTile, p.n_qk, 1);
-            const uint64_t rows0 = smem_desc_sw128(sSlot, 16, 1024), cols0 = smem_desc_sw128(sSlot, kChunkBytes, 1024);
+            const uint64_t rows0 = smem_desc_sw128(sK, 16, 1024), cols0 = smem_desc_sw128(sK, kChunkBytes, 1024);
             const uint32_t r_hi = static_cast<uint32_t>(rows0 >> 32), c_hi = static_cast<uint32_t>(cols0 >> 32);
             const uint32_t q_lo = static_cast<uint32_t>(smem_desc_sw128(sQ, 16, 1024));
             const uint32_t g_lo = static_cast<uint32_t>(smem_desc_sw128(sG, 16, 1024));
-            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0);
-            const uint32_t step = slot_bytes >> 4;
+            const uint32_t r_lo = static_cast<uint32_t>(rows0), c_lo = static_cast<uint32_t>(cols0), v_off = (sV - sK) >> 4;
+            const uint32_t k_step = q_bytes >> 4, v_step = v_bytes >> 4;
             const uint32_t lead = elect_leader();
             bool ok = true, any = false;
-            uint32_t full_phase = 0, own_par = 0, ds_par = 0, g = 0;  // g: key tiles of this CTA so far
+            uint32_t own_par = 0, ds_par = 0, g = 0;  // g: key tiles of this CTA so far
             auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
             };
-            auto wait_slot = [&](int st) -> bool {
-                const bool r = wait1(smem_u32(&ctl.full[st]), (full_phase >> st) & 1u);
-                full_phase ^= 1u << st;
-                return r;
-            };
-            auto after = [&](int st, int d) { return st + d >= n_slots ? st + d - n_slots : st + d; };
-            int s = 0;  // slot of K_j
+            Ring rk(p.q_slots), rv(p.v_slots);  // the next tiles' slots
+            int k_at = 0;                       // slot of K_j
             for (int n = 0; ok; ++n) {
                 Unit U;
                 if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
                 if (U.n == 0) continue;
                 if (!(ok = wait1(smem_u32(&ctl.own_full), own_par))) break;
                 own_par ^= 1u;
-                // S_j from slot `st` (rows behind the sequence's end are zeros: dQ multiplies K by weights of 0)
-                auto scores = [&](int j, int st) -> bool {
-                    if (!wait_slot(st)) return false;
+                // S_j and dP_j, once K_j and V_j have landed; rows behind the sequence's end become zeros (dQ multiplies K by
+                // weights of 0)
+                auto scores = [&](int j) -> bool {
+                    if (!wait1(smem_u32(&ctl.full[0][rk.s]), rk.parity())) return false;
                     const int rows = U.len_k - (U.lo + j) * kTile;
-                    if (rows < kTile) {
-                        clear_rows(sSlot + st * slot_bytes, p.q_chunks, rows, lane);
-                        fence_async_shared();
-                        __syncwarp();
-                    }
-                    mma_rows<KQ>(tS + ((g + j) & 1u) * 128, q_lo, r_lo + st * step, r_hi, idesc_s, lead);
+                    if (rows < kTile) clear_rows(sK + rk.s * q_bytes, p.q_chunks, rows, lane);
+                    mma_rows<KQ>(tS + ((g + j) & 1u) * 128, q_lo, r_lo + rk.s * k_step, r_hi, idesc_s, lead);
                     mma_commit_lead(smem_u32(&ctl.s_full[(g + j) & 1u]), lead);
+                    rk.next();
                     return true;
                 };
-                auto dscores = [&](int j, int st) -> bool {
-                    if (!wait_slot(st)) return false;
+                auto dscores = [&](int j) -> bool {
+                    if (!wait1(smem_u32(&ctl.full[1][rv.s]), rv.parity())) return false;
                     const int rows = U.len_k - (U.lo + j) * kTile;
-                    if (rows < kTile) {
-                        clear_rows(sSlot + st * slot_bytes, p.v_chunks, rows, lane);
-                        fence_async_shared();
-                        __syncwarp();
-                    }
-                    mma_rows<KV>(tP, g_lo, r_lo + st * step, r_hi, idesc_s, lead);
+                    if (rows < kTile) clear_rows(sV + rv.s * v_bytes, p.v_chunks, rows, lane);
+                    mma_rows<KV>(tP, g_lo, r_lo + v_off + rv.s * v_step, r_hi, idesc_s, lead);
                     mma_commit_lead(smem_u32(&ctl.dp_full), lead);
-                    mma_commit_lead(smem_u32(&ctl.empty[st]), lead);  // V_j is read
+                    mma_commit_lead(smem_u32(&ctl.empty[1][rv.s]), lead);
+                    rv.next();
                     return true;
                 };
                 any = true;
-                if (!(ok = scores(0, s) && dscores(0, after(s, 1)))) break;
+                if (!(ok = scores(0) && dscores(0))) break;
                 if (U.n == 1) mma_commit_lead(smem_u32(&ctl.own_empty), lead);
-                else if (!(ok = scores(1, after(s, 2)))) break;
+                else if (!(ok = scores(1))) break;
                 for (int j = 0; j < U.n; ++j) {
                     if (!(ok = wait1(smem_u32(&ctl.ds_full), ds_par))) break;
                     ds_par ^= 1u;
                     tc_fence_after();
                     if (j + 1 < U.n) {
-                        if (!(ok = dscores(j + 1, after(s, 3)))) break;
+                        if (!(ok = dscores(j + 1))) break;
                         if (j + 2 == U.n) mma_commit_lead(smem_u32(&ctl.own_empty), lead);  // Q and dO are read
                     }
-                    mma_cols(tDQ, tS + ((g + j) & 1u) * 128, c_lo + s * step, c_hi, idesc_q, j > 0, lead);
-                    mma_commit_lead(smem_u32(&ctl.empty[s]), lead);
+                    mma_cols(tDQ, tS + ((g + j) & 1u) * 128, c_lo + k_at * k_step, c_hi, idesc_q, j > 0, lead);
+                    mma_commit_lead(smem_u32(&ctl.empty[0][k_at]), lead);
+                    if (++k_at == p.q_slots) k_at = 0;
                     if (j + 1 == U.n) mma_commit_lead(smem_u32(&ctl.done), lead);
-                    if (j + 2 < U.n && !(ok = scores(j + 2, after(s, 4)))) break;
-                    s = after(s, 2);
+                    if (j + 2 < U.n && !(ok = scores(j + 2))) break;
                 }
                 g += U.n;
             }

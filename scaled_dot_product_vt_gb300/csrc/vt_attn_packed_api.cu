@@ -266,22 +266,33 @@ vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cud
     p.n_qk = (p.D_qk + 15) / 16 * 16;
     const int q_bytes = p.q_chunks * static_cast<int>(bw::kChunkBytes), v_bytes = p.v_chunks * static_cast<int>(bw::kChunkBytes);
     const int room = kSmemLimit - 1024 - static_cast<int>(sizeof(bw::Ctl)) - 256 - q_bytes - v_bytes;
+    // slots of the two rings: as many as fit, the second ring's first where both are as long
+    auto rings = [&](int first_bytes, int second_bytes, int q_least, int v_least) {
+        p.q_slots = q_least;
+        p.v_slots = v_least;
+        int left = room - q_least * first_bytes - v_least * second_bytes;
+        for (;;) {
+            const bool second = p.v_slots - v_least < p.q_slots - q_least + 1 && p.v_slots < p.q_slots;
+            int &slots = second ? p.v_slots : p.q_slots;
+            const int bytes = second ? second_bytes : first_bytes;
+            if (slots == bw::kMaxSlots || left < bytes) break;
+            ++slots;
+            left -= bytes;
+        }
+        return 1024 + q_bytes + v_bytes + p.q_slots * first_bytes + p.v_slots * second_bytes;
+    };
     if (a.T_k > 0) {
-        const int stage = q_bytes + v_bytes + static_cast<int>(bw::kStatBytes);
-        p.stages = room / stage < 4 ? room / stage : 4;  // two at full width
+        const int smem = rings(q_bytes + static_cast<int>(bw::kStatBytes), v_bytes, 2, 2);
         p.units = static_cast<int>(packed_slots(a.T_k, a.N, bw::kTile) * H_kv);
         const GradKern kern = pick_grad<KeysKern>(p);
-        const int smem = 1024 + q_bytes + v_bytes + p.stages * stage;
         if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
         kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
     }
     if (a.T_q > 0) {
-        const int slot = q_bytes > v_bytes ? q_bytes : v_bytes;
-        p.stages = room / slot < bw::kMaxSlots ? room / slot : bw::kMaxSlots;  // five at full width
+        const int smem = rings(q_bytes, v_bytes, 3, 2);
         p.units = static_cast<int>(p.slots_q * a.H);
         const GradKern kern = pick_grad<QueriesKern>(p);
-        const int smem = 1024 + q_bytes + v_bytes + p.stages * slot;
         if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
         kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
