@@ -214,10 +214,11 @@ __device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_
 }
 
 __device__ __forceinline__ void init(Ctl &ctl) {
-    for (int i = 0; i < 2 * kMaxSlots; ++i) {
-        mbar_init(smem_u32(&ctl.full[0][i]), 1);
-        mbar_init(smem_u32(&ctl.empty[0][i]), 1);
-    }
+    for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(smem_u32(&ctl.full[r][i]), 1);
+            mbar_init(smem_u32(&ctl.empty[r][i]), 1);
+        }
     mbar_init(smem_u32(&ctl.own_full), 1);
     mbar_init(smem_u32(&ctl.own_empty), 1);
     mbar_init(smem_u32(&ctl.s_full[0]), 1);
