@@ -454,7 +454,8 @@ vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *paren
  *               none, hold has no influence.
  *   cu_q, cu_k  int32 [N + 1], not decreasing, read on the device (a captured call replays with new lengths); they may
  *               be one array.  First rows outside [0, T] count as the nearest ones inside, and a sequence that ends
- *               before it starts as empty; both record VT_ERR_DEVICE_BOUNDS in the stream's status word.
+ *               before it starts as empty; both record VT_ERR_DEVICE_BOUNDS in the stream's status word.  (Where such
+ *               arrays put rows into two sequences, either one's result may be left there.)
  *   lse         fp32 [H,T_q] packed, or NULL
  *   mask        a vt_mask_kind, with its `window`
  * Element types: VT_BF16, with probabilities rounded to bf16 as in the other calls, and VT_F32 with products of two TF32

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                             const AttnParams p) {
     using namespace q2;
     constexpr int BN = kBN;
+    constexpr bool kNanRows = ROWS != kRowsPlain;  // a row whose scores are NaN has a sum that is NaN, and not 0
     constexpr bool GATHER = ROWS == kRowsAll || of_sequence(ROWS);
     __shared__ Ctl ctl;
     extern __shared__ uint8_t smem_raw[];
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 // ------------------------------------------------------------ epilogue: O = O_t / l
                 // A row with no allowed key (l = 0, or no key tile at all) is written as 0.
                 if (n_my > 0) tc_fence_after();
-                const float inv_l = (of_sequence(ROWS) ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
+                const float inv_l = (kNanRows ? l != 0.0f : l > 0.0f) ? 1.0f / (l + l_fix) : 0.0f;
                 // kRowsSeq: row q_row is query head U.h * row_heads + g at position s
                 const int s_row = of_sequence(ROWS) ? q_row / p.row_heads : ROWS == kRowsPacked ? U.q0 + q_row : q_row;
                 const int h_row = of_sequence(ROWS) ? U.h * p.row_heads + q_row - s_row * p.row_heads : U.h;
@@ -1016,7 +1017,8 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                         p.lse[(static_cast<long long>(U.b) * p.H * p.row_heads + h_row) * p.row_tokens + s_row] =
                             l == 0.0f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
                     else
-                        p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + s_row] = lse_from(m_used, l);
+                        p.lse[(static_cast<long long>(U.b) * p.H + U.h) * p.S_q + s_row] =
+                            kNanRows && l != l ? l : lse_from(m_used, l);
                 }
             } else if (ok && EPI == kEpiSplit) {
                 // ------------------------------------------------------------ epilogue: partial O, m, l
