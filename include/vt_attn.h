@@ -431,10 +431,15 @@ size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t
  * `parents` is int32 [B,S_q], packed, on the device, read there (a captured call replays with new trees).  A parent that is
  * neither -1 nor an earlier node counts as -1 and records VT_ERR_DEVICE_BOUNDS in the stream's status word.  A node whose
  * row is negative (a sequence shorter than the tree) has no key: its queries see the prefix alone.
- * Arguments, workspace and errors otherwise as for vt_attn_fwd_prefix; VT_ERR_INVALID_ARG also for parents NULL,
+ * The workspace has vt_attn_tree_workspace_size bytes; other arguments and errors as for vt_attn_fwd_prefix,
+ * VT_ERR_INVALID_ARG also for parents NULL,
  * VT_ERR_UNSUPPORTED also for S_q above 64.
  */
 vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *parents, vt_stream_t stream);
+
+/* Bytes of workspace vt_attn_fwd_tree needs on the current device (0: none, or the call would be refused). */
+size_t vt_attn_tree_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,
+                                   int64_t D_qk, int64_t D_v, vt_dtype dtype);
 
 /*
  * Attention over packed sequences: N sequences of different lengths whose rows lie behind each other in one tensor, as a
@@ -463,7 +468,7 @@ vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *paren
  * but that another query of the same sequence does must be finite, as in the other calls.
  * Strides, alignment and errors as for vt_attn_fwd_strided (the stride of an index with one value is not looked at);
  * VT_ERR_INVALID_ARG also for H not a multiple of H_kv, an unknown mask or a window below 1 with a window kind,
- * VT_ERR_UNSUPPORTED also for a window above 2^40, N, T_q or T_k above 2^30, or (T / 64 + N) H above 2^31 - 1.  N, H or T_q
+ * VT_ERR_UNSUPPORTED also for a window above 2^40, N, T_q or T_k above 2^30, or 4 (T / 32 + N) H above 2^31 - 1.  N, H or T_q
  * equal to 0 is a valid empty problem.
  */
 typedef struct {

@@ -32,6 +32,7 @@ EXPORTS = ("vt_attn_fwd", "vt_attn_fwd_strided", "vt_attn_fwd_ex", "vt_attn_fwd_
            "vt_attn_splitkv_workspace_size", "vt_attn_splitkv_choose", "vt_attn_fwd_splitkv_noalloc",
            "vt_attn_fwd_general", "vt_qk_rope_fwd", "vt_qk_rope_bwd", "vt_qk_rope_bwd_workspace_size",
            "vt_attn_fwd_prefix", "vt_attn_prefix_workspace_size", "vt_attn_fwd_tree",
+           "vt_attn_tree_workspace_size",
            "vt_attn_fwd_packed", "vt_attn_bwd_packed", "vt_attn_bwd_packed_workspace_size",
            "vt_status_str", "vt_last_device_status")
 
@@ -98,6 +99,8 @@ def load(path: str | None = None):
     lib.vt_attn_fwd_tree.restype = i
     lib.vt_attn_prefix_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64, i]
     lib.vt_attn_prefix_workspace_size.restype = sz
+    lib.vt_attn_tree_workspace_size.argtypes = lib.vt_attn_prefix_workspace_size.argtypes
+    lib.vt_attn_tree_workspace_size.restype = sz
     lib.vt_attn_fwd_packed.argtypes = [ctypes.c_char_p, vp]
     lib.vt_attn_fwd_packed.restype = i
     lib.vt_attn_bwd_packed.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp]
@@ -210,6 +213,10 @@ _ATTN_PREFIX_BYTES = _ATTN_PREFIX_PTRS.size + _ATTN_PREFIX_REST.size
 def vt_attn_fwd_prefix(args: bytes, stream) -> int:
     """The C entry point: ``args`` is a packed vt_attn_prefix_args; returns the vt_status code."""
     return load().vt_attn_fwd_prefix(args, stream)
+
+
+def vt_attn_tree_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype) -> int:
+    return int(load().vt_attn_tree_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype))
 
 
 def vt_attn_fwd_tree(args: bytes, parents, stream) -> int:
@@ -698,7 +705,8 @@ def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, out, 
         raise ValueError("lse must be a contiguous float32 [B, H, S_q] tensor on the device of the other tensors")
     if scale is None:
         scale = float(D_qk) ** -0.5
-    need = vt_attn_prefix_workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code)
+    size = vt_attn_prefix_workspace_size if parents is None else vt_attn_tree_workspace_size
+    need = size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code)
     rest = _ATTN_PREFIX_REST.pack(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, code, scale, *sq, *skp, *svp, *skc, *svc, *so)
     return rest, o_shape, need
 
@@ -720,7 +728,8 @@ def attn_fwd_tree(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len=None,
     """``attn_fwd_prefix`` for trees of drafted tokens: the S_q <= 64 tokens of each sequence that its last cache rows hold
     are nodes, and parents (int32 [B,S_q], contiguous, on the device) names the earlier node that each continues, or -1.
     A node sees the prefix, the cache before the tree, its ancestors and itself: see vt_attn_fwd_tree in
-    include/vt_attn.h.  The other arguments are those of ``attn_fwd_prefix``."""
+    include/vt_attn.h.  The other arguments are those of ``attn_fwd_prefix``; a given ``workspace`` has
+    ``vt_attn_tree_workspace_size`` bytes."""
     if parents is None:
         raise ValueError("parents is required")
     return _prefix_call(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, scale, return_lse, out, lse, workspace,

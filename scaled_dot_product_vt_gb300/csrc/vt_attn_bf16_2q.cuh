@@ -140,18 +140,25 @@ __device__ __forceinline__ void packed_tiles(const AttnParams &p, const Unit &U,
     *e = lo < hi ? (hi + kBN - 1) / kBN : 0;
 }
 
+// kRowsPacked: the block of unit u, by one lane or (the first unit) by a whole warp.
+template <bool kWarp>
+__device__ __forceinline__ PackedSeq packed_block(const AttnParams &p, int u) {
+    const int slot = p.n_qblocks - 1 - u / p.H;  // later blocks, which see more keys, come first
+    if constexpr (kWarp) return packed_find_warp(p.cu_q, p.n_seq, p.S_q, kRows, slot, threadIdx.x & 31, p.status);
+    return packed_find(p.cu_q, p.n_seq, p.S_q, kRows, slot, p.status);
+}
+
 template <int ROWS>
-__device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u) {
+__device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const PackedSeq *found = nullptr) {
     Unit U;
     U.len = U.rows = U.q0 = U.k0 = 0;
     U.u = u;
     if constexpr (ROWS == kRowsPacked) {
-        // the heads of a block are adjacent (they read the same keys), and later blocks, which see more keys, come first
-        const int slot = u / p.H;
-        const PackedSeq q = packed_find(p.cu_q, p.n_seq, p.S_q, kRows, p.n_qblocks - 1 - slot, p.status);
+        // the heads of a block are adjacent (they read the same keys)
+        const PackedSeq q = found ? *found : packed_block<false>(p, u);
         const PackedSeq k = packed_seq(p.cu_k, q.n, p.S_k, p.status);
         U.split = U.b = 0;
-        U.h = u - slot * p.H;
+        U.h = u % p.H;
         U.hk = U.h / p.kv_group;
         U.r0 = q.block * kRows;
         U.rows = q.len;
@@ -436,6 +443,8 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
+        PackedSeq first_block{};
+        if constexpr (ROWS == kRowsPacked) first_block = packed_block<true>(p, blockIdx.x);
         if (lane == 0) {
             // loads i = 2j (K_j) and 2j + 1 (V_j) of a unit go to the ring's next slots
             int s = 0;
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 if (u >= p.n_units) u = -1;
                 Unit U;
                 if (u >= 0) {
-                    U = decode_unit<ROWS>(p, u);
+                    U = decode_unit<ROWS>(p, u, ROWS == kRowsPacked && n == 0 ? &first_block : nullptr);
                     if (!VT_DEV_CHECK(!(p.flags & kFlagTestBounds) && unit_valid<ROWS>(p, U), ctl.abort_flag, p)) break;
                 } else {
                     U.u = -1;
@@ -1024,8 +1033,11 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 // ------------------------------------------------------------ epilogue: partial O, m, l
                 // Unnormalised O_t with its reference max m (log2 units) and sum l; a share with no
                 // key tile for this query tile writes the empty partial (m = -inf, l = 0, O = 0).
-                const long long row_lin = (static_cast<long long>(U.b) * p.H + U.h) * p.S_q + q_row;
-                const long long part = static_cast<long long>(U.split) * p.B * p.H * p.S_q + row_lin;
+                const long long slice = of_sequence(ROWS) ? static_cast<long long>(U.h) * p.B + U.b
+                                                          : static_cast<long long>(U.b) * p.H + U.h;
+                const long long row_lin = slice * p.S_q + q_row;
+                const int share = U.split + (of_sequence(ROWS) ? p.part_share0 : 0);
+                const long long part = static_cast<long long>(share) * p.B * p.H * p.S_q + row_lin;
                 float *orow = p.part_o + part * p.part_ld;
                 if (n_my > 0) tc_fence_after();
                 // Two lanes store their two rows together, 64 bytes of one and then of the other: a warp's store then
@@ -1071,6 +1083,8 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         }
     }
 
+    if constexpr (ROWS == kRowsTree)  // this launch ends after the prefix's: the next one reads the results of both
+        if (p.follows && blockIdx.x == 0 && threadIdx.x == 0) wait_prerequisites();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

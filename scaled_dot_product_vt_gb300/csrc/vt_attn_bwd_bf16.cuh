@@ -18,6 +18,8 @@
 // of a tile, one row per thread.  A warpgroup writes its bf16 P or dS over the first half of the columns it read itself.
 #pragma once
 
+#include <cstring>
+
 #include "vt_attn_packed.cuh"
 
 namespace vt {
@@ -28,6 +30,11 @@ struct BwdParams : AttnParams {
     float *stat;      // [H][slots_q][2][128]: -LSE log2(e), then -delta, of the slot's rows (-inf and 0 past the end)
     int slots_q;      // slots of 128 query rows
     int units;        // work units of a launch
+    // The keys' walk: query heads of a unit and units of a key/value head.  All heads of the group in one unit, or (few
+    // blocks of keys) one head a unit, whose results go to part_k and part_v for attn_bwd_heads_kernel to add.
+    int groups, head_units;
+    float *part_k, *part_v;  // [H][T_k][part_ldk], [H][T_k][part_ldv]; null with one unit
+    int part_ldk, part_ldv;
     int n_qk;         // MMA N of dQ and dK: D_qk rounded up to 16
     int q_slots, v_slots;  // ring slots: of Q and dO (keys' walk), or of K and V (queries' walk)
     const void *dO;
@@ -79,18 +86,25 @@ __device__ __forceinline__ int clamp_to(long long x, int most) {
     return static_cast<int>(x < 0 ? 0 : (x > most ? most : x));
 }
 
-// kKeys: a block of keys and the queries that see one of them; otherwise a block of queries and the keys they see.
+// kKeys: a block of keys and the queries that see one of them; otherwise a block of queries and the keys they see.  The heads
+// of a block are adjacent, and blocks with more work come first (a causal mask gives early keys and late queries the most
+// partners).
 template <bool kKeys>
-__device__ __forceinline__ Unit decode(const BwdParams &p, int u) {
+__device__ __forceinline__ int unit_heads(const BwdParams &p) { return kKeys ? p.H / p.groups : p.H; }
+// The block of unit u, by one lane or (first units) by a whole warp.
+template <bool kKeys, bool kWarp>
+__device__ __forceinline__ PackedSeq unit_block(const BwdParams &p, int u) {
+    const int slot = u / unit_heads<kKeys>(p);
+    const int *cu = kKeys ? p.cu_k : p.cu_q;
+    const int T = kKeys ? p.S_k : p.S_q, at = kKeys ? slot : p.slots_q - 1 - slot;
+    if constexpr (kWarp) return packed_find_warp(cu, p.n_seq, T, kTile, at, threadIdx.x & 31, p.status);
+    return packed_find(cu, p.n_seq, T, kTile, at, p.status);
+}
+template <bool kKeys>
+__device__ __forceinline__ Unit decode(const BwdParams &p, int u, const PackedSeq &own) {
     Unit U;
     U.u = u;
-    const int heads = kKeys ? p.H / p.kv_group : p.H;
-    const int slot = u / heads;
-    U.h = u - slot * heads;
-    // the heads of a block are adjacent; blocks with more work come first (a causal mask gives early keys and late
-    // queries the most partners)
-    const PackedSeq own = kKeys ? packed_find(p.cu_k, p.n_seq, p.S_k, kTile, slot, p.status)
-                                : packed_find(p.cu_q, p.n_seq, p.S_q, kTile, p.slots_q - 1 - slot, p.status);
+    U.h = u % unit_heads<kKeys>(p);
     const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q, p.status) : packed_seq(p.cu_k, own.n, p.S_k, p.status);
     U.r0 = own.block * kTile;
     U.q0 = kKeys ? other.start : own.start;
@@ -174,9 +188,10 @@ struct LoadRing : Ring {
     }
 };
 
-// The producer lane draws the n-th unit of this CTA and publishes it; false on abort.
+// The producer lane draws the n-th unit of this CTA and publishes it; false on abort.  `first`: the block of the first.
 template <bool kKeys>
-__device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_done, uint32_t *clc_par, const BwdParams &p) {
+__device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, const PackedSeq &first, Unit *out, bool *clc_done, uint32_t *clc_par,
+                                          const BwdParams &p) {
     const int k = n % kUnitRing;
     if (n >= kUnitRing && !wait_bounded(smem_u32(&ctl.unit_empty[k]), ((n / kUnitRing) - 1) & 1, ctl.abort_flag, p))
         return false;
@@ -194,7 +209,7 @@ __device__ __forceinline__ bool draw_unit(Ctl &ctl, int n, Unit *out, bool *clc_
     Unit U{};
     U.u = -1;
     if (u >= 0 && u < p.units) {
-        U = decode<kKeys>(p, u);
+        U = decode<kKeys>(p, u, n == 0 ? first : unit_block<kKeys, false>(p, u));
         if (!VT_DEV_CHECK(valid<kKeys>(p, U), ctl.abort_flag, p)) return false;
     }
     volatile Unit *dst = &ctl.unit[k];
@@ -283,6 +298,25 @@ __device__ __forceinline__ void store_row(uint32_t tmem, bool any, uint16_t *row
     }
 }
 
+// The same row of fp32, `ld` columns (a multiple of 8).
+__device__ __forceinline__ void store_part(uint32_t tmem, bool any, float *row, bool ok, int ld) {
+    for (int cc = 0; cc < ld; cc += 16) {
+        uint32_t o[16];
+        if (any) {
+            tmem_ld16(tmem + cc, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0u;
+        }
+        if (!ok) continue;
+        const uint32_t a[8] = {o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]};
+        const uint32_t b[8] = {o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]};
+        st_global_v8(row + cc, a);
+        if (cc + 16 <= ld) st_global_v8(row + cc + 8, b);
+    }
+}
+
 // Products D (+)= A B^T of K-steps of 16 columns, A and B K-major tiles in shared memory.
 template <int KS>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t lead) {
@@ -304,60 +338,103 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t b_lo, 
 }  // namespace bw
 
 // -LSE log2(e) and -delta of every query, by slots of 128 rows, so that a tile's lie together on 16 bytes.  Bound by the
-// bytes of O and dO.
+// bytes of O and dO; 32 rows a CTA, two or four a thread at once, keep enough of them on their way.
 constexpr int kStatThreads = 256;
+constexpr int kStatRows = 32;
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const __grid_constant__ BwdParams p) {
     constexpr int kVec = 16 / sizeof(T), kLanes = 128 / kVec;  // lanes of a row: 16 (bf16) or 32
-    constexpr int kRows = kStatThreads / kLanes;               // rows at a time
-    const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
-    const PackedSeq s = packed_find(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, p.status);
+    constexpr int kStep = kStatThreads / kLanes, kEach = kStatRows / kStep;  // rows at a time, and of a thread
+    constexpr int kParts = bw::kTile / kStatRows;
+    const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts, slot = unit / p.H, h = unit - slot * p.H;
+    const PackedSeq s = packed_find_warp(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, threadIdx.x & 31, p.status);
     const int lane = threadIdx.x % kLanes, col = lane * kVec;
     float *out = p.stat + (static_cast<long long>(h) * p.slots_q + slot) * (2 * bw::kTile);
     const int n = min(s.len - s.block * bw::kTile, bw::kTile);  // rows of the slot
     const long long first = static_cast<long long>(s.start) + s.block * bw::kTile;
     const T *o = static_cast<const T *>(p.O) + h * p.o_sh, *g = static_cast<const T *>(p.dO) + h * p.do_sh;
-#pragma unroll 4
-    for (int r = threadIdx.x / kLanes; r < bw::kTile; r += kRows) {
-        float sum = 0.0f;
-        if (r < n && col < p.D_v) {
-            const T *a = o + (first + r) * p.o_ss + col, *b = g + (first + r) * p.do_ss + col;
-            if (col + kVec <= p.D_v) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a)), y = __ldg(reinterpret_cast<const uint4 *>(b));
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    const int r0 = part * kStatRows + threadIdx.x / kLanes;
+    uint4 x[kEach], y[kEach];
+    float lse[kEach], dl[kEach];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (sizeof(T) == 2) {
-                        sum = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum);
-                        sum = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum);
-                    } else {
-                        sum = fmaf(__uint_as_float(xs[k]), __uint_as_float(ys[k]), sum);
-                    }
-                }
-            } else {
-                for (int k = 0; col + k < p.D_v; ++k) {
-                    if constexpr (sizeof(T) == 2)
-                        sum = fmaf(__uint_as_float(static_cast<uint32_t>(a[k]) << 16),
-                                   __uint_as_float(static_cast<uint32_t>(b[k]) << 16), sum);
-                    else
-                        sum = fmaf(a[k], b[k], sum);
-                }
+    for (int i = 0; i < kEach; ++i) {
+        const int r = r0 + i * kStep;
+        const long long at = first + r;
+        x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+        lse[i] = -INFINITY;
+        dl[i] = 0.0f;
+        if (r < n && col < p.D_v) {
+            const T *a = o + at * p.o_ss + col, *b = g + at * p.do_ss + col;
+            if (col + kVec <= p.D_v) {
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(a));
+                y[i] = __ldg(reinterpret_cast<const uint4 *>(b));
+            } else {  // (columns behind the last one are not read)
+                T ta[kVec] = {}, tb[kVec] = {};
+#pragma unroll
+                for (int k = 0; k < kVec; ++k)
+                    if (col + k < p.D_v) ta[k] = a[k], tb[k] = b[k];
+                memcpy(&x[i], ta, 16);
+                memcpy(&y[i], tb, 16);
             }
         }
-#pragma unroll
-        for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (lane == 0) {
-            float nl = -INFINITY, nd = 0.0f;
-            if (r < n) {
-                const long long at = static_cast<long long>(h) * p.S_q + first + r;
-                const float lse = p.lse[at];
-                if (lse != -INFINITY) nl = -lse * 1.4426950408889634f;  // (a row without keys has no weight at all)
-                nd = (p.dlse ? p.dlse[at] : 0.0f) - sum;
-            }
-            out[r] = nl;
-            out[bw::kTile + r] = nd;
+        if (r < n && lane == 0) {
+            lse[i] = p.lse[static_cast<long long>(h) * p.S_q + at];
+            if (p.dlse) dl[i] = p.dlse[static_cast<long long>(h) * p.S_q + at];
         }
     }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 2) {
+                sum = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), sum);
+                sum = fmaf(__uint_as_float(xs[k] & 0xFFFF0000u), __uint_as_float(ys[k] & 0xFFFF0000u), sum);
+            } else {
+                sum = fmaf(__uint_as_float(xs[k]), __uint_as_float(ys[k]), sum);
+            }
+        }
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const int r = r0 + i * kStep;
+        if (lane == 0) {  // (a row without keys has no weight at all)
+            out[r] = lse[i] == -INFINITY ? -INFINITY : -lse[i] * 1.4426950408889634f;
+            out[bw::kTile + r] = r < n ? dl[i] - sum : 0.0f;
+        }
+    }
+}
+
+// dK and dV of ROWS keys of one key/value head, from those of its query heads, added in their order.
+constexpr int kHeadsThreads = 256, kHeadsRows = 8;  // rows of a CTA: a thread adds four columns of one, for dK and for dV
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kHeadsThreads) attn_bwd_heads_kernel(const __grid_constant__ BwdParams p) {
+    constexpr int kParts = ROWS / kHeadsRows;
+    const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts;
+    const int heads = p.H / p.kv_group, slot = unit / heads, hk = unit - slot * heads;
+    const PackedSeq s = packed_find_warp(p.cu_k, p.n_seq, p.S_k, ROWS, slot, threadIdx.x & 31, p.status);
+    const int r = part * kHeadsRows + threadIdx.x / 32, c = threadIdx.x % 32 * 4;
+    if (r >= min(s.len - s.block * ROWS, ROWS)) return;
+    const long long row = static_cast<long long>(s.start) + s.block * ROWS + r;
+    auto add = [&](const float *from, int ld, int D, float f, T *out) {
+        if (c >= D) return;
+        const float *src = from + (static_cast<long long>(hk) * p.kv_group * p.S_k + row) * ld + c;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int g = 0; g < p.kv_group; ++g) {
+            const float4 x = *reinterpret_cast<const float4 *>(src + static_cast<long long>(g) * p.S_k * ld);
+            sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+        }
+        const float v[4] = {sum.x * f, sum.y * f, sum.z * f, sum.w * f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < D) {
+                if constexpr (sizeof(T) == 2) out[c + k] = static_cast<T>(pack_bf16x2(v[k], 0.0f) & 0xFFFFu);
+                else out[c + k] = v[k];
+            }
+    };
+    add(p.part_k, p.part_ldk, p.D_qk, p.scale, static_cast<T *>(p.dK) + hk * p.dk_sh + row * p.dk_ss);
+    add(p.part_v, p.part_ldv, p.D_v, 1.0f, static_cast<T *>(p.dV) + hk * p.dv_sh + row * p.dv_ss);
 }
 
 // dK and dV of 128 keys of one key/value head.  Shared memory: K, V, then rings of Q (with its
@@ -374,6 +451,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     using namespace bw;
     __shared__ Ctl ctl;
     extern __shared__ uint8_t smem_raw[];
+    launch_dependents();  // the queries' walk takes the SMs that this one no longer fills
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     const uint32_t q_bytes = p.q_chunks * kChunkBytes, v_bytes = p.v_chunks * kChunkBytes;
@@ -401,6 +479,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
         if (warp == 0) {
+            const PackedSeq first = unit_block<true, true>(p, blockIdx.x);
             if (lane == 0) {
                 bool ok = true, clc_done = false;
                 uint32_t clc_par = 0;
@@ -408,15 +487,15 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                 LoadRing rq(p.q_slots), rg(p.v_slots);
                 for (int n = 0; ok; ++n) {
                     Unit U;
-                    if (!draw_unit<true>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
+                    if (!draw_unit<true>(ctl, n, first, &U, &clc_done, &clc_par, p) || U.u < 0) break;
                     if (U.n == 0) continue;
                     if (owns > 0 && !wait_bounded(smem_u32(&ctl.own_empty), (owns - 1) & 1, ctl.abort_flag, p)) break;
                     mbar_arrive_expect_tx(smem_u32(&ctl.own_full), q_bytes + v_bytes);
-                    load_tile(sK, &tmK, smem_u32(&ctl.own_full), p.q_chunks, U.k0 + U.r0, U.h);
-                    load_tile(sV, &tmV, smem_u32(&ctl.own_full), p.v_chunks, U.k0 + U.r0, U.h);
+                    load_tile(sK, &tmK, smem_u32(&ctl.own_full), p.q_chunks, U.k0 + U.r0, U.h / p.head_units);
+                    load_tile(sV, &tmV, smem_u32(&ctl.own_full), p.v_chunks, U.k0 + U.r0, U.h / p.head_units);
                     ++owns;
-                    for (int g = 0; ok && g < p.kv_group; ++g) {
-                        const int h = U.h * p.kv_group + g;
+                    for (int g = 0; ok && g < p.groups; ++g) {
+                        const int h = U.h * p.groups + g;
                         for (int t = U.lo; t < U.lo + U.n; ++t) {
                             if (!(ok = rq.wait(ctl, 0, p))) break;
                             uint32_t bar = smem_u32(&ctl.full[0][rq.s]);
@@ -463,7 +542,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                 if (U.n == 0) continue;
                 if (!(ok = wait1(smem_u32(&ctl.own_full), own_par))) break;
                 own_par ^= 1u;
-                const int total = U.n * p.kv_group;
+                const int total = U.n * p.groups;
                 int tile = 0, rows = 0;  // of the head's tiles, and the rows of the next one that exist
                 int q_at = 0, g_at = 0;  // slots of the current tile
                 // S^T and dP^T of the next tile, once it has landed; rows behind the sequence's end become zeros
@@ -533,7 +612,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         for (int n = 0; ok; ++n) {
             Unit U;
             if (!(ok = next_unit(ctl, n, &U, p, lane)) || U.u < 0) break;
-            const int total = U.n * p.kv_group;
+            const int total = U.n * p.groups;
             // queries [q_lo, q_hi) see this thread's key
             const long long at = static_cast<long long>(U.r0) + row - (static_cast<long long>(U.len_k) - U.len_q);
             const int q_lo = clamp_to(at - p.band_hi, U.len_q), q_hi = clamp_to(at - p.band_lo + 1, U.len_q);
@@ -634,12 +713,17 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
             // warpgroup 0 stores dV, warpgroup 1 dK
             const bool mine = U.r0 + row < U.len_k;
             const long long key = static_cast<long long>(U.k0) + U.r0 + row;
-            if (wg == 0)
+            if (p.part_k) {
+                const long long at = static_cast<long long>(U.h) * p.S_k + key;
+                if (wg == 0) store_part(tDV + lanes, total > 0, p.part_v + at * p.part_ldv, mine, p.part_ldv);
+                else store_part(tDK + lanes, total > 0, p.part_k + at * p.part_ldk, mine, p.part_ldk);
+            } else if (wg == 0) {
                 store_row(tDV + lanes, total > 0, static_cast<uint16_t *>(p.dV) + U.h * p.dv_sh + key * p.dv_ss, mine, p.D_v,
                           1.0f, p.dv_vec32);
-            else
+            } else {
                 store_row(tDK + lanes, total > 0, static_cast<uint16_t *>(p.dK) + U.h * p.dk_sh + key * p.dk_ss, mine, p.D_qk,
                           p.scale, p.dk_vec32);
+            }
         }
     }
 
@@ -689,6 +773,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
         if (warp == 0) {
+            const PackedSeq first = unit_block<false, true>(p, blockIdx.x);
             if (lane == 0) {
                 bool ok = true, clc_done = false;
                 uint32_t clc_par = 0;
@@ -696,7 +781,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
                 LoadRing rk(p.q_slots), rv(p.v_slots);
                 for (int n = 0; ok; ++n) {
                     Unit U;
-                    if (!draw_unit<false>(ctl, n, &U, &clc_done, &clc_par, p) || U.u < 0) break;
+                    if (!draw_unit<false>(ctl, n, first, &U, &clc_done, &clc_par, p) || U.u < 0) break;
                     if (U.n == 0) continue;
                     // the unit's Q and dO replace the previous one's, once those have been read: into L2 until then
                     for (int c = 0; c < p.q_chunks; ++c) tma_prefetch_l2_4d(&tmQ, c * kChunk, U.q0 + U.r0, U.h, 0);
@@ -879,6 +964,8 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         }
     }
 
+    // this launch ends after the one it was started ahead of: the next one may read the results of both
+    if (p.follows && blockIdx.x == 0 && threadIdx.x == 0) wait_prerequisites();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

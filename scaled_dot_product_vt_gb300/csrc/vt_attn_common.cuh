@@ -77,6 +77,8 @@ struct AttnParams {
     float *part_m;
     float *part_l;
     float *part_c;
+    int part_share0;  // kRowsSeq, kRowsTree: the partial results' first share
+    int follows;      // (kRowsTree, gradients) started ahead of the end of the launch before it
     unsigned long long timeout_ns;
     unsigned flags;
     unsigned *status;  // device status word of the launching stream

@@ -52,6 +52,23 @@ __device__ __forceinline__ PackedSeq packed_find(const int *cu, int N, int T, in
     return s;
 }
 
+// The same by a whole warp, 32 candidates at a time: one or two reads after each other where a lane alone makes
+// log2(N) (3 us of a launch's start with 17 sequences).
+__device__ __forceinline__ PackedSeq packed_find_warp(const int *cu, int N, int T, int R, int slot, int lane, unsigned *status) {
+    int lo = 0, hi = N;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool before = lane == 0 || (at < hi && packed_cu(cu, min(at, hi - 1), T) / R + at <= slot);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
+        lo += last * step;
+        hi = min(hi, lo + step);
+    }
+    PackedSeq s = packed_seq(cu, lo, T, status);
+    s.block = slot - (s.start / R + lo);
+    if (s.block < 0) s.block = s.len = 0;  // ahead of the first sequence
+    return s;
+}
+
 // First key that query i of a packed sequence of `len` keys sees, and one past its last: the band around its own
 // position i + off (empty when lo >= hi).
 __device__ __forceinline__ int packed_key_lo(const AttnParams &p, int off, int len, int i) {

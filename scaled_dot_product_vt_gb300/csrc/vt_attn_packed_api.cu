@@ -15,7 +15,7 @@ namespace {
 using Args = vt_attn_packed_args;
 using Grads = vt_attn_packed_grads;
 
-constexpr int kLeastRows = 64;  // rows of the smallest block a launch is cut into
+constexpr int kLeastRows = 32;  // rows of the smallest block a launch is cut into
 
 vt_status check_shape(const Args &a) {
     if (a.struct_bytes != sizeof(Args) || a.reserved != 0) return VT_ERR_INVALID_ARG;
@@ -30,7 +30,7 @@ vt_status check_shape(const Args &a) {
         return VT_ERR_UNSUPPORTED;
     int64_t units = 0;
     const int64_t T = a.T_q > a.T_k ? a.T_q : a.T_k;
-    if (__builtin_mul_overflow(packed_slots(T, a.N, kLeastRows), a.H, &units) || units > kMaxExtent) return VT_ERR_UNSUPPORTED;
+    if (__builtin_mul_overflow(4 * packed_slots(T, a.N, kLeastRows), a.H, &units) || units > kMaxExtent) return VT_ERR_UNSUPPORTED;
     return VT_OK;
 }
 
@@ -221,10 +221,27 @@ vt_status forward(const Args &a, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- gradients
 
-// The workspace: the queries' statistics.
-size_t workspace_bytes(const Args &a) {
-    const int64_t slots = packed_slots(a.T_q, a.N, bw::kTile);
-    return static_cast<size_t>(a.H * slots) * bw::kStatBytes;
+// The workspace: the queries' statistics, and (split) dK and dV of every query head.
+struct Layout {
+    bool split;
+    size_t part_k, part_v, bytes;
+};
+
+// Few blocks of keys are walked by one CTA per query head, whose results another launch adds, so that more SMs take part:
+// where the key/value heads' blocks would not give every SM one (bf16, one CTA on an SM), or two (fp32).
+Layout layout_of(const Args &a, int sms) {
+    const bool bf = a.dtype == VT_BF16;
+    const int64_t G = a.H / a.H_kv, blocks = packed_slots(a.T_k, a.N, bf ? bw::kTile : pf::kRows) * a.H_kv;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    Layout l{};
+    l.split = G > 1 && a.T_k > 0 && blocks < (bf ? 1 : 2) * sms;
+    l.bytes = l.part_k = up(static_cast<size_t>(a.H * packed_slots(a.T_q, a.N, bw::kTile)) * bw::kStatBytes);
+    if (l.split) {
+        const size_t rows = static_cast<size_t>(a.H * a.T_k) * sizeof(float);
+        l.part_v = up(l.part_k + rows * partial_ld(a.D_qk));
+        l.bytes = up(l.part_v + rows * partial_ld(a.D_v));
+    }
+    return l;
 }
 
 // Rows start on 32 bytes.
@@ -248,6 +265,14 @@ template <int KQ, int KV>
 struct QueriesKern {
     static GradKern kern() { return attn_bwd_q_bf16_kernel<KQ, KV>; }
 };
+
+template <typename T, int ROWS>
+vt_status launch_heads(const Args &a, const BwdParams &p, cudaStream_t stream) {
+    const int64_t blocks = packed_slots(a.T_k, a.N, ROWS) * a.H_kv * (ROWS / kHeadsRows);
+    if (blocks > kMaxExtent) return VT_ERR_UNSUPPORTED;
+    attn_bwd_heads_kernel<T, ROWS><<<static_cast<unsigned>(blocks), kHeadsThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
 
 vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cudaStream_t stream) {
     CUtensorMap tq, tk, tv, tg;
@@ -283,7 +308,7 @@ vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cud
     };
     if (a.T_k > 0) {
         const int smem = rings(q_bytes + static_cast<int>(bw::kStatBytes), v_bytes, 2, 2);
-        p.units = static_cast<int>(packed_slots(a.T_k, a.N, bw::kTile) * H_kv);
+        p.units = static_cast<int>(packed_slots(a.T_k, a.N, bw::kTile) * (a.H / p.groups));
         const GradKern kern = pick_grad<KeysKern>(p);
         if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
         kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
@@ -294,10 +319,21 @@ vt_status backward_bf16(const Args &a, const Grads &g, BwdParams p, int dev, cud
         p.units = static_cast<int>(p.slots_q * a.H);
         const GradKern kern = pick_grad<QueriesKern>(p);
         if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
-        kern<<<static_cast<unsigned>(p.units), bw::kThreads, smem, stream>>>(tq, tk, tv, tg, p);
+        p.follows = a.T_k > 0 ? 1 : 0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(p.units));
+        cfg.blockDim = dim3(bw::kThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = p.follows ? 1 : 0;
+        if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, tg, p) != cudaSuccess) return VT_ERR_CUDA;
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
     }
-    return VT_OK;
+    return p.part_k ? launch_heads<uint16_t, bw::kTile>(a, p, stream) : VT_OK;
 }
 
 vt_status backward_f32(const Args &a, const BwdParams &base, int dev, cudaStream_t stream) {
@@ -306,11 +342,14 @@ vt_status backward_f32(const Args &a, const BwdParams &base, int dev, cudaStream
     set_inputs(a, &p);
     const int D = padded(a);
     const int smem = D == 64 ? pf::bwd_smem<64>() : D == 96 ? pf::bwd_smem<96>() : pf::bwd_smem<128>();
-    if (a.T_k > 0)
+    if (a.T_k > 0) {
+        const int64_t slots = packed_slots(a.T_k, a.N, pf::kRows);
         VT_TRY(launch_f32(D == 64   ? attn_bwd_kv_f32_kernel<64>
                           : D == 96 ? attn_bwd_kv_f32_kernel<96>
                                     : attn_bwd_kv_f32_kernel<128>,
-                          smem, packed_slots(a.T_k, a.N, pf::kRows) * a.H_kv, p, dev, stream));
+                          smem, slots * (a.H / p.groups), p, dev, stream));
+        if (p.part_k) VT_TRY((launch_heads<float, pf::kRows>(a, p, stream)));
+    }
     if (a.T_q > 0)
         VT_TRY(launch_f32(D == 64   ? attn_bwd_q_f32_kernel<64>
                           : D == 96 ? attn_bwd_q_f32_kernel<96>
@@ -334,18 +373,27 @@ vt_status backward(const Args &a, const Grads &g, cudaStream_t stream) {
     VT_TRY(m.rows(g.dq, g.dq_stride, a.H, a.T_q, a.D_qk, true));
     VT_TRY(m.rows(g.dk, g.dk_stride, a.H_kv, a.T_k, a.D_qk, true));
     VT_TRY(m.rows(g.dv, g.dv_stride, a.H_kv, a.T_k, a.D_v, true));
-    const size_t need = workspace_bytes(a);
-    if (g.workspace_bytes < need) return VT_ERR_INVALID_ARG;
-    VT_TRY(m.vector(g.workspace, static_cast<int64_t>(need), 256, true));
-    VT_TRY(m.clear());
     int dev = 0;
     DeviceInfo info;
-    if (cudaGetDevice(&dev) != cudaSuccess || !device_info(dev, &info)) return VT_ERR_CUDA;
+    const bool have = cudaGetDevice(&dev) == cudaSuccess && device_info(dev, &info);
+    const Layout lay = layout_of(a, have ? info.sms : 152);
+    if (g.workspace_bytes < lay.bytes) return VT_ERR_INVALID_ARG;
+    VT_TRY(m.vector(g.workspace, static_cast<int64_t>(lay.bytes), 256, true));
+    VT_TRY(m.clear());
+    if (!have) return VT_ERR_CUDA;
     BwdParams p{};
     static_cast<AttnParams &>(p) = params_of(a, info.status + status_slot(stream));
     const int elt = a.dtype == VT_BF16 ? 2 : 4;
     p.scale = a.scale;
     p.stat = static_cast<float *>(g.workspace);
+    p.groups = lay.split ? 1 : p.kv_group;
+    p.head_units = lay.split ? p.kv_group : 1;
+    if (lay.split) {
+        p.part_k = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + lay.part_k);
+        p.part_v = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + lay.part_v);
+        p.part_ldk = static_cast<int>(partial_ld(a.D_qk));
+        p.part_ldv = static_cast<int>(partial_ld(a.D_v));
+    }
     p.slots_q = static_cast<int>(packed_slots(a.T_q, a.N, bw::kTile));
     p.dO = g.d_o;
     p.do_sh = g.do_stride[0];
@@ -364,7 +412,7 @@ vt_status backward(const Args &a, const Grads &g, cudaStream_t stream) {
     p.dk_vec32 = vec32(g.dk, g.dk_stride, a.H_kv, a.T_k, elt);
     p.dv_vec32 = vec32(g.dv, g.dv_stride, a.H_kv, a.T_k, elt);
     if (a.T_q > 0) {
-        const unsigned ctas = static_cast<unsigned>(p.slots_q * a.H);
+        const unsigned ctas = static_cast<unsigned>(p.slots_q * a.H * (bw::kTile / kStatRows));
         if (a.dtype == VT_BF16) attn_bwd_stats_kernel<uint16_t><<<ctas, kStatThreads, 0, stream>>>(p);
         else attn_bwd_stats_kernel<float><<<ctas, kStatThreads, 0, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
@@ -398,7 +446,10 @@ size_t vt_attn_bwd_packed_workspace_size(int64_t N, int64_t H, int64_t H_kv, int
     a.N = N; a.H = H; a.H_kv = H_kv; a.T_q = T_q; a.T_k = T_k; a.D_qk = D_qk; a.D_v = D_v;
     a.dtype = dtype;
     if (vt::packed::check_shape(a) != VT_OK || N == 0 || H == 0 || (T_q == 0 && T_k == 0)) return 0;
-    return vt::packed::workspace_bytes(a);
+    int dev = 0;
+    vt::DeviceInfo info;
+    const bool have = cudaGetDevice(&dev) == cudaSuccess && vt::device_info(dev, &info);
+    return vt::packed::layout_of(a, have ? info.sms : 152).bytes;
 }
 
 }  // extern "C"

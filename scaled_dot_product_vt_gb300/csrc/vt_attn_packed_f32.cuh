@@ -168,11 +168,11 @@ struct Block {
 template <bool kKeys>
 __device__ __forceinline__ Block block_of(const BwdParams &p, int tile) {
     Block B;
-    const int heads = kKeys ? p.H / p.kv_group : p.H;
+    const int heads = kKeys ? p.H / p.groups : p.H;
     const int slot = blockIdx.x / heads, slots = gridDim.x / heads;
     B.h = blockIdx.x - slot * heads;
-    const PackedSeq own = kKeys ? packed_find(p.cu_k, p.n_seq, p.S_k, kRows, slot, p.status)
-                                : packed_find(p.cu_q, p.n_seq, p.S_q, kRows, slots - 1 - slot, p.status);
+    const PackedSeq own = packed_find_warp(kKeys ? p.cu_k : p.cu_q, p.n_seq, kKeys ? p.S_k : p.S_q, kRows,
+                                           kKeys ? slot : slots - 1 - slot, threadIdx.x & 31, p.status);
     const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q, p.status) : packed_seq(p.cu_k, own.n, p.S_k, p.status);
     B.r0 = own.block * kRows;
     B.q0 = kKeys ? other.start : own.start;
@@ -380,12 +380,13 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_kv_f32_kernel(const 
     float *const stat = reinterpret_cast<float *>(smem_raw + (2 * kRows + 4 * kTile) * DP * 4);  // [stage][2][kTile]
     const Block B = block_of<true>(p, kTile);
     if (B.r0 >= B.len_k) return;
-    copy_rows<DP>(sK, static_cast<const float *>(p.K) + B.h * p.k_sh + B.k0 * p.k_ss, p.k_ss, B.r0, kRows, B.len_k, p.D_qk);
-    copy_rows<DP>(sV, static_cast<const float *>(p.V) + B.h * p.v_sh + B.k0 * p.v_ss, p.v_ss, B.r0, kRows, B.len_k, p.D_v);
-    const int tiles = (B.hi - B.lo + kTile - 1) / kTile, total = tiles * p.kv_group;
+    const int hk = B.h / p.head_units;
+    copy_rows<DP>(sK, static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss, p.k_ss, B.r0, kRows, B.len_k, p.D_qk);
+    copy_rows<DP>(sV, static_cast<const float *>(p.V) + hk * p.v_sh + B.k0 * p.v_ss, p.v_ss, B.r0, kRows, B.len_k, p.D_v);
+    const int tiles = (B.hi - B.lo + kTile - 1) / kTile, total = tiles * p.groups;
     int g = 0, q_next = B.lo;  // of the next tile to load
     auto load = [&](int stage) {
-        const int h = B.h * p.kv_group + g;
+        const int h = B.h * p.groups + g;
         copy_rows<DP>(sQG + 2 * stage * kTileBytes, static_cast<const float *>(p.Q) + h * p.q_sh + B.q0 * p.q_ss, p.q_ss, q_next,
                       kTile, B.len_q, p.D_qk);
         copy_rows<DP>(sQG + (2 * stage + 1) * kTileBytes, static_cast<const float *>(p.dO) + h * p.do_sh + B.q0 * p.do_ss,
@@ -454,9 +455,14 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_kv_f32_kernel(const 
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         if (row[x] >= B.len_k) continue;
-        const long long at = static_cast<long long>(B.k0) + row[x];
-        store<DP>(static_cast<float *>(p.dK) + B.h * p.dk_sh + at * p.dk_ss, dk, x, p.scale, p.D_qk, lane);
-        store<DP>(static_cast<float *>(p.dV) + B.h * p.dv_sh + at * p.dv_ss, dv, x, 1.0f, p.D_v, lane);
+        const long long at = static_cast<long long>(B.k0) + row[x], part = static_cast<long long>(B.h) * p.S_k + at;
+        if (p.part_k) {
+            store<DP>(p.part_k + part * p.part_ldk, dk, x, 1.0f, p.part_ldk, lane);
+            store<DP>(p.part_v + part * p.part_ldv, dv, x, 1.0f, p.part_ldv, lane);
+        } else {
+            store<DP>(static_cast<float *>(p.dK) + B.h * p.dk_sh + at * p.dk_ss, dk, x, p.scale, p.D_qk, lane);
+            store<DP>(static_cast<float *>(p.dV) + B.h * p.dv_sh + at * p.dv_ss, dv, x, 1.0f, p.D_v, lane);
+        }
     }
 }
 

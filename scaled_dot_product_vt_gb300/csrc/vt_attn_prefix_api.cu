@@ -21,6 +21,8 @@ struct Plan {
     bool tiles, seq_tiles, with_prefix, merge;
     int prefix_shares, prefix_cluster, cluster;
     int shares;  // of the streaming launch's keys, beyond a cluster's CTAs (more than 1: merge)
+    int tree_shares;  // (seq_tiles) partial results of each sequence's own launch: its cache where the prefix has shares of
+                      // its own, else all its keys; a last launch adds them.  0: one launch writes the answer
     size_t workspace;
 };
 
@@ -113,7 +115,46 @@ int tile_shares(const Args &a, const Sizes &z, int cluster, int sms) {
 // Streaming CTAs that share an SM (Tile::kPerSm).
 int64_t ctas_per_sm(const Args &a) { return a.dtype == VT_F32 ? 1 : (a.D_v <= 64 ? 4 : 3); }
 
-Plan plan_of(const Args &a, int sms) {
+// Trees of many rows (Plan::seq_tiles): whether the prefix is taken once for the rows of all sequences, and into how many
+// shares the keys are cut.  A 128-key step of the two-tile kernel takes 1.6 us and a unit 5 us besides, caches count as half
+// full, and a partial result is written and read at 5 bytes per ns.  32 trees of 25 nodes in 4 heads, behind 8192 shared keys
+// and caches of 1024: 225 us in one launch (256 units of 68 steps on 152 SMs, twice the prefix's work: 100 rows fill one tile
+// of two); 16 trees of 64 over up to 8192 keys: 102 us in one launch of 128 units.  (vt_attn_fwd_prefix keeps its plan, and
+// so the rounding of its results.)
+void tree_plan(const Args &a, const Sizes &z, int sms, Plan *p) {
+    const double step = 1.6, unit = 5.0;
+    const int64_t tp = (a.S_p + q2::kBN - 1) / q2::kBN, tc = (a.S_c / 2 + q2::kBN - 1) / q2::kBN;
+    const int64_t own = a.B * a.H_kv * ((z.per_b + q2::kRows - 1) / q2::kRows);
+    const int64_t all = a.H_kv * ((a.B * z.per_b + q2::kRows - 1) / q2::kRows);
+    const double share_us = static_cast<double>(z.rows) * static_cast<double>(partial_ld(a.D_v) + 3) * 8.0 / 5e6;
+    // units of `tiles` steps, the longest of `most`
+    auto launch_us = [&](int64_t units, int64_t tiles, int64_t most, int n) {
+        const double waves = static_cast<double>((units * n + sms - 1) / sms);
+        const double longest = unit + step * static_cast<double>((most + n - 1) / n);
+        const double all_of_them = waves * (unit + step * static_cast<double>((tiles + n - 1) / n));
+        return longest > all_of_them ? longest : all_of_them;
+    };
+    // the best number of shares of a launch, and its time with theirs
+    auto best = [&](int64_t units, int64_t tiles, int64_t most, int *n) {
+        double us = 0.0;
+        for (int k = 1; k <= st::kMaxShares && (k == 1 || k <= most); ++k) {
+            const double t = launch_us(units, tiles, most, k) + share_us * k;
+            if (k == 1 || t < us) us = t, *n = k;
+        }
+        return us;
+    };
+    const int64_t full = (a.S_c + q2::kBN - 1) / q2::kBN;
+    double least = launch_us(own, tp + tc, tp + full, 1);
+    int n = 0, n_prefix = 0;
+    if (const double us = 4.0 + best(own, tp + tc, tp + full, &n); us < least) least = us, p->tree_shares = n;
+    if (tp > 0 && a.S_c > 0) {
+        const double us = 8.0 + best(all, tp, tp, &n_prefix) + best(own, tc, full, &n);
+        if (us < least) p->tree_shares = n, p->prefix_shares = n_prefix;
+    }
+    if (p->tree_shares) p->workspace = partial_bytes(z.rows, a.D_v, p->prefix_shares + p->tree_shares);
+}
+
+Plan plan_of(const Args &a, bool tree, int sms) {
     const Sizes z = sizes_of(a);
     Plan p{};
     const int64_t kv_units = a.B * a.H_kv * z.tiles_b;
@@ -123,7 +164,10 @@ Plan plan_of(const Args &a, int sms) {
     const bool f32 = a.dtype == VT_F32;
     p.shares = 1;
     p.seq_tiles = !f32 && z.per_b > kSeqTileRows;
-    if (p.seq_tiles) return p;
+    if (p.seq_tiles) {
+        if (tree) tree_plan(a, z, sms, &p);
+        return p;
+    }
     p.tiles = !f32 && a.B * z.per_b > kTileRows;
     p.with_prefix = again <= static_cast<double>(f32 ? kReadAgainF32 : kReadAgainBf16) || (!p.tiles && z.tiles_all >= a.B * z.tiles_b);
     // keys a CTA should keep: with one launch latency counts (16 rows over 460 keys: 6.6 us with 4 CTAs, 7.1 us with
@@ -222,7 +266,7 @@ st::Params params_of(const Args &a, const Plan &plan, const Sizes &z, unsigned *
     p.kv_len = a.S_c > 0 ? a.kv_len : nullptr;
     p.rows = z.rows;
     if (plan.workspace) {
-        const int64_t n = z.rows * (plan.prefix_shares + (plan.merge ? plan.shares : 0));
+        const int64_t n = z.rows * (plan.prefix_shares + (plan.merge ? plan.shares : 0) + plan.tree_shares);
         p.part_o = static_cast<float *>(a.workspace);
         p.part_ld = static_cast<int>(partial_ld(a.D_v));
         p.part_m = p.part_o + n * p.part_ld;
@@ -332,8 +376,9 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.B = seq ? sp.B : 1;
     p.H = sp.H_kv;
     p.S_q = static_cast<int>(seq ? z.per_b : a.B * z.per_b);
-    p.prefix_tiles = (sp.S_p + q2::kBN - 1) / q2::kBN;
-    p.prefix_keys = sp.S_p;
+    const bool own_only = seq && plan.prefix_shares > 0;  // (the prefix has its own launch)
+    p.prefix_tiles = own_only ? 0 : (sp.S_p + q2::kBN - 1) / q2::kBN;
+    p.prefix_keys = own_only ? 0 : sp.S_p;
     p.cache_keys = sp.S_c;
     p.kv_len = sp.kv_len;
     p.parents = sp.parents;
@@ -363,7 +408,8 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     p.lse = sp.lse;
     p.tiles_per_unit = 2;
     p.cluster = 1;
-    p.n_split = seq ? 1 : plan.prefix_shares;
+    p.n_split = !seq ? plan.prefix_shares : plan.tree_shares ? plan.tree_shares : 1;
+    p.part_share0 = plan.prefix_shares;
     p.part_o = sp.part_o;
     p.part_ld = sp.part_ld;
     p.part_m = sp.part_m;
@@ -382,11 +428,43 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     const int64_t units = per_head * heads;
     if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
     p.n_units = static_cast<int>(units);
-    const TileKern kern = !seq        ? pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p)
-                          : p.parents ? pick_tiles<q2::kEpiPlain, q2::kRowsTree>(p)
-                                      : pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p);
+    const TileKern kern = !seq               ? pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p)
+                          : plan.tree_shares ? pick_tiles<q2::kEpiSplit, q2::kRowsTree>(p)
+                          : p.parents        ? pick_tiles<q2::kEpiPlain, q2::kRowsTree>(p)
+                                             : pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p);
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
-    kern<<<static_cast<unsigned>(units), q2::kThreads, smem, stream>>>(m.kc, m.kp, m.vp, m.vc, p);
+    p.follows = own_only ? 1 : 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(units));
+    cfg.blockDim = dim3(q2::kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];  // takes the SMs that the prefix's launch no longer fills
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.follows ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, m.kc, m.kp, m.vp, m.vc, p) != cudaSuccess) return VT_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
+}
+
+// The workspace's `n` shares of every row combined into O.  (`early`: started ahead of the end of the launch before it.)
+vt_status launch_shares(const Args &a, const Sizes &z, st::Params p, int n, bool early, cudaStream_t stream) {
+    p.prior = n;
+    const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
+    const bool bf = a.dtype == VT_BF16;
+    void (*kern)(const st::Params) = a.D_v <= 64 ? (bf ? st::attn_shares_kernel<uint16_t, 64> : st::attn_shares_kernel<float, 64>)
+                                                 : (bf ? st::attn_shares_kernel<uint16_t, 128> : st::attn_shares_kernel<float, 128>);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * st::kMergeWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
@@ -398,14 +476,16 @@ vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     int dev = 0;
     DeviceInfo info;
     const bool have = cudaGetDevice(&dev) == cudaSuccess && device_info(dev, &info);
-    const Plan plan = plan_of(a, have ? info.sms : 152);
+    const Plan plan = plan_of(a, parents != nullptr, have ? info.sms : 152);
     VT_TRY(check_memory(a, parents, plan));
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
     p.parents = a.S_c > 0 ? parents : nullptr;
     if (plan.seq_tiles) {
+        if (plan.prefix_shares) VT_TRY(launch_tiles(a, plan, z, p, false, info, dev, stream));
         VT_TRY(launch_tiles(a, plan, z, p, true, info, dev, stream));
+        if (plan.tree_shares) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.tree_shares, false, stream));
         return env_check() ? read_status(stream) : VT_OK;
     }
     st::Maps maps{};
@@ -432,25 +512,22 @@ vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     const int64_t units = a.B * a.H_kv * z.tiles_b * p.shares;
     p.longest_first = p.kv_len && a.B > 1 && a.B <= st::kMaxSorted && (plan.tiles || units * p.cluster > ctas_per_sm(a) * info.sms);
     VT_TRY(launch_stream(a, maps, p, units, p.cluster, p.follows != 0, dev, stream));
-    if (plan.merge) {
-        p.prior = plan.prefix_shares + plan.shares;
-        const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
-        const bool bf = a.dtype == VT_BF16;
-        void (*kern)(const st::Params) = a.D_v <= 64 ? (bf ? st::attn_shares_kernel<uint16_t, 64> : st::attn_shares_kernel<float, 64>)
-                                                     : (bf ? st::attn_shares_kernel<uint16_t, 128> : st::attn_shares_kernel<float, 128>);
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(blocks);
-        cfg.blockDim = dim3(32 * st::kMergeWarps);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
-        if (cudaGetLastError() != cudaSuccess) return VT_ERR_CUDA;
-    }
+    if (plan.merge) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.shares, true, stream));
     return env_check() ? read_status(stream) : VT_OK;
+}
+
+size_t workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c, int64_t D_qk, int64_t D_v,
+                      vt_dtype dtype, bool tree) {
+    Args a{};
+    a.struct_bytes = sizeof a;
+    a.B = B; a.H = H; a.H_kv = H_kv; a.S_q = S_q; a.S_p = S_p; a.S_c = S_c; a.D_qk = D_qk; a.D_v = D_v;
+    a.dtype = dtype;
+    bool empty = false;
+    if (check_shape(a, &empty) != VT_OK || empty) return 0;
+    int dev = 0;
+    DeviceInfo info;
+    const bool have = cudaGetDevice(&dev) == cudaSuccess && device_info(dev, &info);
+    return plan_of(a, tree, have ? info.sms : 152).workspace;
 }
 
 }  // namespace
@@ -478,16 +555,12 @@ vt_status vt_attn_fwd_tree(const vt_attn_prefix_args *args, const int32_t *paren
 
 size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c,
                                      int64_t D_qk, int64_t D_v, vt_dtype dtype) {
-    vt_attn_prefix_args a{};
-    a.struct_bytes = sizeof a;
-    a.B = B; a.H = H; a.H_kv = H_kv; a.S_q = S_q; a.S_p = S_p; a.S_c = S_c; a.D_qk = D_qk; a.D_v = D_v;
-    a.dtype = dtype;
-    bool empty = false;
-    if (vt::prefix::check_shape(a, &empty) != VT_OK || empty) return 0;
-    int dev = 0;
-    vt::DeviceInfo info;
-    const bool have = cudaGetDevice(&dev) == cudaSuccess && vt::device_info(dev, &info);
-    return vt::prefix::plan_of(a, have ? info.sms : 152).workspace;
+    return vt::prefix::workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype, false);
+}
+
+size_t vt_attn_tree_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S_q, int64_t S_p, int64_t S_c, int64_t D_qk,
+                                   int64_t D_v, vt_dtype dtype) {
+    return S_q > vt::kMaxNodes ? 0 : vt::prefix::workspace_size(B, H, H_kv, S_q, S_p, S_c, D_qk, D_v, dtype, true);
 }
 
 }  // extern "C"

@@ -175,7 +175,7 @@ def test_writes_nothing_else_and_gives_the_same_bits(B, nodes):
     first = t.run()
     room = torch.full((B, nodes + 1, 8, 96), 7.0, dtype=t.t, device="cuda")
     out = room[:, :nodes].transpose(1, 2)[..., 8:80]
-    need = vt.vt_attn_prefix_workspace_size(B, 8, 2, nodes, 1500, 200, 128, 72, vt.VT_BF16)
+    need = vt.vt_attn_tree_workspace_size(B, 8, 2, nodes, 1500, 200, 128, 72, vt.VT_BF16)
     ws = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
