@@ -110,6 +110,7 @@ struct Ctl {
     uint64_t stall;
     uint32_t tmem_base;
     volatile uint32_t abort_flag;
+    uint8_t order[32];  // kRowsTree: the sequences, longest first (the producer's own)
 };
 
 
@@ -131,6 +132,10 @@ __device__ __forceinline__ void gathered_unit(const AttnParams &p, unsigned u, i
     *h = static_cast<int>(of_sequence(ROWS) ? slice / p.B : slice);
     *b = static_cast<int>(of_sequence(ROWS) ? slice - *h * p.B : 0);
     if (of_sequence(ROWS)) *qb = p.n_qblocks - 1 - *qb;  // (later blocks see more of the cache)
+    if (ROWS == kRowsTree && p.longest_first) {  // sequence by sequence: *b is the place in the order of their lengths
+        *b = static_cast<int>(slice / p.H);
+        *h = static_cast<int>(slice - *b * p.H);
+    }
 }
 
 // Key tiles [*a, *e) that rows first..last of a packed sequence need (an empty range as 0, 0).
@@ -149,7 +154,7 @@ __device__ __forceinline__ PackedSeq packed_block(const AttnParams &p, int u) {
 }
 
 template <int ROWS>
-__device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const PackedSeq *found = nullptr) {
+__device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const PackedSeq *found = nullptr, const uint8_t *order = nullptr) {
     Unit U;
     U.len = U.rows = U.q0 = U.k0 = 0;
     U.u = u;
@@ -168,6 +173,7 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const Pa
     } else if constexpr (ROWS != kRowsPlain) {
         int qb;
         gathered_unit<ROWS>(p, u, &U.split, &U.b, &U.h, &qb);
+        if (ROWS == kRowsTree && p.longest_first) U.b = order[U.b];
         U.hk = U.h;
         U.r0 = qb * kRows;
     } else {
@@ -392,6 +398,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         if (warp >= 4) {
             int split, b, h, qb;
             gathered_unit<ROWS>(p, blockIdx.x, &split, &b, &h, &qb);
+            if (ROWS == kRowsTree && p.longest_first) b = nth_longest(p.kv_len, p.B, b, lane);
             const int t = (warp - 4) >> 2;
             gather_rows<ROWS>(t ? sQ1 : sQ0, qb * kRows + t * kBM, b, h, p);
         }
@@ -445,6 +452,13 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
         // ------------------------------------------------------------ TMA producer
         PackedSeq first_block{};
         if constexpr (ROWS == kRowsPacked) first_block = packed_block<true>(p, blockIdx.x);
+        if constexpr (ROWS == kRowsTree) {
+            if (p.longest_first) {
+                const int rank = length_rank(p.kv_len, p.B, lane);
+                if (lane < p.B) ctl.order[rank] = static_cast<uint8_t>(lane);
+                __syncwarp();
+            }
+        }
         if (lane == 0) {
             // loads i = 2j (K_j) and 2j + 1 (V_j) of a unit go to the ring's next slots
             int s = 0;
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 if (u >= p.n_units) u = -1;
                 Unit U;
                 if (u >= 0) {
-                    U = decode_unit<ROWS>(p, u, ROWS == kRowsPacked && n == 0 ? &first_block : nullptr);
+                    U = decode_unit<ROWS>(p, u, ROWS == kRowsPacked && n == 0 ? &first_block : nullptr, ctl.order);
                     if (!VT_DEV_CHECK(!(p.flags & kFlagTestBounds) && unit_valid<ROWS>(p, U), ctl.abort_flag, p)) break;
                 } else {
                     U.u = -1;

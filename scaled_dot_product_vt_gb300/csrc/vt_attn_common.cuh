@@ -78,6 +78,7 @@ struct AttnParams {
     float *part_l;
     float *part_c;
     int part_share0;  // kRowsSeq, kRowsTree: the partial results' first share
+    int longest_first;  // kRowsTree: units in the order of their sequences' lengths (B <= 32)
     int follows;      // (kRowsTree, gradients) started ahead of the end of the launch before it
     unsigned long long timeout_ns;
     unsigned flags;

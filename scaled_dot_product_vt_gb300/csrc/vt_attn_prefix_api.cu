@@ -434,6 +434,7 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
                                              : pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p);
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
     p.follows = own_only ? 1 : 0;
+    p.longest_first = seq && p.parents && p.kv_len && sp.B > 1 && sp.B <= st::kMaxSorted && units > info.sms;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units));
     cfg.blockDim = dim3(q2::kThreads);
@@ -448,8 +449,8 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
 
-// The workspace's `n` shares of every row combined into O.  (`early`: started ahead of the end of the launch before it.)
-vt_status launch_shares(const Args &a, const Sizes &z, st::Params p, int n, bool early, cudaStream_t stream) {
+// The workspace's `n` shares of every row combined into O (by a kernel that waits for the launch before it itself).
+vt_status launch_shares(const Args &a, const Sizes &z, st::Params p, int n, cudaStream_t stream) {
     p.prior = n;
     const unsigned blocks = static_cast<unsigned>((z.rows + st::kMergeWarps - 1) / st::kMergeWarps);
     const bool bf = a.dtype == VT_BF16;
@@ -463,7 +464,7 @@ vt_status launch_shares(const Args &a, const Sizes &z, st::Params p, int n, bool
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return VT_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? VT_OK : VT_ERR_CUDA;
 }
@@ -485,7 +486,7 @@ vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     if (plan.seq_tiles) {
         if (plan.prefix_shares) VT_TRY(launch_tiles(a, plan, z, p, false, info, dev, stream));
         VT_TRY(launch_tiles(a, plan, z, p, true, info, dev, stream));
-        if (plan.tree_shares) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.tree_shares, false, stream));
+        if (plan.tree_shares) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.tree_shares, stream));
         return env_check() ? read_status(stream) : VT_OK;
     }
     st::Maps maps{};
@@ -512,7 +513,7 @@ vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     const int64_t units = a.B * a.H_kv * z.tiles_b * p.shares;
     p.longest_first = p.kv_len && a.B > 1 && a.B <= st::kMaxSorted && (plan.tiles || units * p.cluster > ctas_per_sm(a) * info.sms);
     VT_TRY(launch_stream(a, maps, p, units, p.cluster, p.follows != 0, dev, stream));
-    if (plan.merge) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.shares, true, stream));
+    if (plan.merge) VT_TRY(launch_shares(a, z, p, plan.prefix_shares + plan.shares, stream));
     return env_check() ? read_status(stream) : VT_OK;
 }
 

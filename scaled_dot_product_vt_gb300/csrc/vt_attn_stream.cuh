@@ -308,19 +308,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __g
     c.store(p, lane, seq - hk * p.B, hk, static_cast<int>(flat) - seq * per_b);
 }
 
-// The sequence with the n-th longest cache (equal lengths in order), by a warp: when the CTAs of a launch do not all fit
-// at once, those of the longest sequences start first and the short ones fill the end (16 sequences of up to 8192
-// tokens: 51 us against 56 us; ranking more of them costs every CTA more than it gains).
-__device__ __forceinline__ int nth_longest(const Params &p, int n, int lane) {
-    const int mine = lane < p.B ? p.kv_len[lane] : INT_MIN;
-    int rank = 0;
-    for (int j = 0; j < p.B; ++j) {
-        const int other = __shfl_sync(0xffffffffu, mine, j);
-        rank += other > mine || (other == mine && j < lane);
-    }
-    return __ffs(__ballot_sync(0xffffffffu, lane < p.B && rank == n)) - 1;
-}
-
 // kTree: the S_q tokens of a sequence are the nodes of a tree, and its keys its cache (or with the prefix).
 template <typename T, int DQ, int DV, bool kTree = false>
 __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
@@ -350,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     u /= p.row_tiles;
     int b = static_cast<int>(u / p.H_kv);  // 0 with all_rows
     const int hk = static_cast<int>(u) - b * p.H_kv;
-    if (p.longest_first) b = nth_longest(p, b, lane);
+    // When the CTAs of a launch do not all fit at once, those of the longest sequences start first and the short ones fill the
+    // end (16 sequences of up to 8192 tokens: 51 us against 56 us; ranking more of them costs every CTA more than it gains).
+    if (p.longest_first) b = nth_longest(p.kv_len, p.B, b, lane);
     const int per_b = p.S_q * p.G;
     const int group_rows = p.all_rows ? p.B * per_b : per_b;
     const int f0 = rt * kRowsTile;

@@ -3,6 +3,7 @@
 // 64-bit word, formed from the parents by each warp that masks with it.
 #pragma once
 
+#include <climits>
 #include <cstdint>
 
 #include "vt_attn_common.cuh"
@@ -57,6 +58,22 @@ struct TreeNodes {
         return s < 32 ? a : b;
     }
 };
+
+// The place of this lane's sequence in the order of B <= 32 lengths, longest first (equal ones in order), by a whole warp.
+__device__ __forceinline__ int length_rank(const int *kv_len, int B, int lane) {
+    const int mine = lane < B ? kv_len[lane] : INT_MIN;
+    int rank = 0;
+    for (int j = 0; j < B; ++j) {
+        const int other = __shfl_sync(0xffffffffu, mine, j);
+        rank += other > mine || (other == mine && j < lane);
+    }
+    return rank;
+}
+// The sequence with the n-th longest cache.
+__device__ __forceinline__ int nth_longest(const int *kv_len, int B, int n, int lane) {
+    const int rank = length_rank(kv_len, B, lane);
+    return __ffs(__ballot_sync(0xffffffffu, lane < B && rank == n)) - 1;
+}
 
 // 32 keys from the `from`-th node on, as bits: the keys before the tree (from < 0) are seen, those behind it are not.
 __device__ __forceinline__ uint32_t tree_window(unsigned long long seen, int from) {

@@ -200,6 +200,9 @@ class Problem:
     def untouched(self, x, side, fill=7.0):
         a, e = self.cu[side][0], self.cu[side][-1]
         assert (x[:, :a] == fill).all() and (x[:, e:] == fill).all()
+        if x.dim() == 3:  # and the columns behind the rows' last
+            room = x._base
+            assert (room[..., x.shape[2]:] == fill).all()
 
     def check_forward(self, o, lse):
         h2, bf, f, acc = self.constants()
@@ -498,6 +501,33 @@ def test_gradients_against_differences():
     got = sum(float((a.double() * w.double()).sum()) for a, w in zip(grads_, way))
     want = (loss(2.0 ** -10) - loss(-2.0 ** -10)) * 2.0 ** 9
     assert abs(got - want) <= 1e-4 * sum(float((a.double() * w.double()).abs().sum()) for a, w in zip(grads_, way))
+
+
+@gpu
+def test_the_debug_library_finds_nothing():
+    """Its index checks pass, and its results are the release library's."""
+    import torch
+    dbg = vt.load_debug()
+    for dtype, mask, window in (("bf16", "causal", 0), ("bf16", "window", 50), ("f32", "causal", 0)):
+        p = Problem(dtype, 4, 2, 64, 64, [(200, 300), (1, 1), (0, 4), (140, 90), (300, 300)], mask, window, seed=14, behind=0)
+        o, lse = p.forward()
+        got = p.backward(o, lse)
+        o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+        new = [torch.empty_like(x) for x in got]
+        code = vt.VT_BF16 if dtype == "bf16" else vt.VT_F32
+        st = lambda x: (x.stride(0), x.stride(1))
+        dims = (len(p.lengths), 4, 2, p.q.shape[1], p.k.shape[1], 64, 64)
+        args = pack(q=p.q.data_ptr(), k=p.k.data_ptr(), v=p.v.data_ptr(), cu_q=p.cu_q.data_ptr(), cu_k=p.cu_k.data_ptr(),
+                    o=o2.data_ptr(), lse=lse2.data_ptr(), N=dims[0], H=4, H_kv=2, T_q=dims[3], T_k=dims[4], D_qk=64, D_v=64,
+                    window=window, dtype=code, scale=p.form["scale"], mask=vt.MASKS[mask], qs=st(p.q), ks=st(p.k), vs=st(p.v),
+                    os=st(o2))
+        ws = torch.empty(vt.vt_attn_bwd_packed_workspace_size(*dims, code), dtype=torch.uint8, device="cuda")
+        g = grads(do=p.do.data_ptr(), dlse=0, dq=new[0].data_ptr(), dk=new[1].data_ptr(), dv=new[2].data_ptr(), ws=ws.data_ptr(),
+                  wsb=ws.numel(), dos=st(p.do), dqs=st(new[0]), dks=st(new[1]), dvs=st(new[2]))
+        stream = torch.cuda.current_stream().cuda_stream
+        assert dbg.vt_attn_fwd_packed(args, stream) == 0 and dbg.vt_attn_bwd_packed(args, g, stream) == 0
+        assert dbg.vt_last_device_status(stream) == 0
+        assert all(torch.equal(a, b) for a, b in zip((o, lse, *got), (o2, lse2, *new)))
 
 
 @gpu
