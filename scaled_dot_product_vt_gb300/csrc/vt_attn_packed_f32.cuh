@@ -12,7 +12,6 @@
 //   P B (acc): these rows are k = t, t + 4; n = g of four column tiles is column 4 g + m of 32, so a thread's results are
 //   8 consecutive columns 8 t .. 8 t + 7.
 // Both loads fall into different banks (swizzle gives 8 lanes' units different low bits).
-// The three products bound it: 16 x 8 x 8 of each take the tensor pipe as long as the splits take the ALU.
 #pragma once
 
 #include "vt_attn_bwd_bf16.cuh"
@@ -54,21 +53,33 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const float *src, long l
     }
 }
 
+// x as hi + lo: hi rounded to TF32 (10 explicit mantissa bits) in integers, lo the rest, of which the tensor core takes the
+// upper bits: what is left out is below 2^-21 of x.  (The conversion instruction runs at an eighth of this rate, and the
+// splits, about as many as MMAs, bounded the kernels by it: 146 us for five sequences of up to 1000 tokens, 8 heads of 72.)
+// kInf: for a value that may be infinite beside a weight p >= 0: hi is then the largest number and lo the infinity, so that
+// p lo is that infinity and no product is NaN.
 struct Split {
     uint32_t hi, lo;
 };
 template <bool kInf = false>
 __device__ __forceinline__ Split split(float x) {
     Split s;
-    if constexpr (kInf) st::split_tf32_inf(__float_as_uint(x), s.hi, s.lo);
-    else st::split_tf32(__float_as_uint(x), s.hi, s.lo);
+    s.hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    if (kInf && fabsf(__uint_as_float(s.hi)) == INFINITY) s.hi -= 0x2000u;
+    s.lo = __float_as_uint(x - __uint_as_float(s.hi));
     return s;
 }
-__device__ __forceinline__ void mma3(float (&d)[4], float (&low)[4], const Split (&a)[4], Split b0, Split b1) {
+// d[i] += a b[i] for N accumulators, the small products to low[i] (which may be d[i] itself).  One product of every
+// accumulator after the other: an MMA waits for the last one on its accumulator, and for no other.
+template <int N>
+__device__ __forceinline__ void mma3(float (*d)[4], float (*low)[4], const Split (&a)[4], const Split (&b)[N][2]) {
     const uint32_t ah[4] = {a[0].hi, a[1].hi, a[2].hi, a[3].hi}, al[4] = {a[0].lo, a[1].lo, a[2].lo, a[3].lo};
-    st::mma_tf32(low, al, b0.hi, b1.hi);
-    st::mma_tf32(low, ah, b0.lo, b1.lo);
-    st::mma_tf32(d, ah, b0.hi, b1.hi);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st::mma_tf32(low[i], al, b[i][0].hi, b[i][1].hi);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st::mma_tf32(low[i], ah, b[i][0].lo, b[i][1].lo);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st::mma_tf32(d[i], ah, b[i][0].hi, b[i][1].hi);
 }
 
 // s[n] = A B^T over D columns: 16 rows of this warp at `a`, 8 NT rows at `b`.  Accumulators 0, 1 of tile n are rows 8 n + t and
@@ -86,12 +97,15 @@ __device__ __forceinline__ void dot(float (&s)[NT][4], uint32_t a, uint32_t b, i
         const float4 x = lds4(a + unit_at<DP>(r, 4 * c + t)), y = lds4(a + unit_at<DP>(r + 8, 4 * c + t));
         const Split a0[4] = {split(x.x), split(y.x), split(x.y), split(y.y)};
         const Split a1[4] = {split(x.z), split(y.z), split(x.w), split(y.w)};
+        Split b0[NT][2], b1[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float4 z = lds4(b + unit_at<DP>(8 * n + r, 4 * c + t));
-            mma3(s[n], low[n], a0, split(z.x), split(z.y));
-            mma3(s[n], low[n], a1, split(z.z), split(z.w));
+            b0[n][0] = split(z.x), b0[n][1] = split(z.y);
+            b1[n][0] = split(z.z), b1[n][1] = split(z.w);
         }
+        mma3<NT>(s, low, a0, b0);
+        mma3<NT>(s, low, a1, b1);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -122,10 +136,9 @@ __device__ __forceinline__ void acc(float (&o)[DP / 8][4], const float (&w)[NT][
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float4 x = lds4(b + unit_at<DP>(8 * n + t, 8 * q + g)), y = lds4(b + unit_at<DP>(8 * n + t + 4, 8 * q + g));
-            mma3(sum[0], sum[0], a[n], split<kInf>(x.x), split<kInf>(y.x));
-            mma3(sum[1], sum[1], a[n], split<kInf>(x.y), split<kInf>(y.y));
-            mma3(sum[2], sum[2], a[n], split<kInf>(x.z), split<kInf>(y.z));
-            mma3(sum[3], sum[3], a[n], split<kInf>(x.w), split<kInf>(y.w));
+            const Split z[4][2] = {{split<kInf>(x.x), split<kInf>(y.x)}, {split<kInf>(x.y), split<kInf>(y.y)},
+                                   {split<kInf>(x.z), split<kInf>(y.z)}, {split<kInf>(x.w), split<kInf>(y.w)}};
+            mma3<4>(sum, sum, a[n], z);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -160,7 +173,7 @@ __device__ __forceinline__ void store(float *row, const float (&o)[DP / 8][4], i
         }
 }
 
-// The block of 64 rows that a CTA takes, as bw::decode.
+// The block of rows that a CTA takes, as bw::decode.
 struct Block {
     int h, r0, q0, len_q, k0, len_k, qslot;
     int lo, hi;  // partners [lo, hi), lo on a tile's start
