@@ -75,10 +75,12 @@ size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
 
 // CTAs of a cluster that share a unit's keys: two CTAs per SM in all, as long as every CTA keeps `least` keys.  The
 // fp32 kernel fills an SM per CTA, and clusters of 8 then wait for room (26 us against 20 us with 4).
-int cluster_for(int64_t units, int64_t keys, int64_t least, bool f32, int sms) {
+// (`one_wave`: no more CTAs than SMs, where the fp32 kernel has several row tiles per sequence and its second wave of CTAs,
+// each of a few keys, takes as long as the first: trees, which have no results of earlier plans to keep.)
+int cluster_for(int64_t units, int64_t keys, int64_t least, bool f32, bool one_wave, int sms) {
     int c = 1;
     const int most = f32 ? 4 : st::kMaxClusterCtas;
-    while (c < most && units * c < 2LL * sms && keys >= 2 * least * c) c *= 2;
+    while (c < most && (one_wave ? 2 * units * c <= sms : units * c < 2LL * sms) && keys >= 2 * least * c) c *= 2;
     return c;
 }
 
@@ -161,7 +163,7 @@ Plan plan_of(const Args &a, bool tree, int sms) {
     const int64_t elt = a.dtype == VT_BF16 ? 2 : 4;
     // (a double: up to 2^70)
     const double again = static_cast<double>(kv_units) * static_cast<double>(a.S_p * (a.D_qk + a.D_v) * elt);
-    const bool f32 = a.dtype == VT_F32;
+    const bool f32 = a.dtype == VT_F32, one_wave = f32 && tree;
     p.shares = 1;
     p.seq_tiles = !f32 && z.per_b > kSeqTileRows;
     if (p.seq_tiles) {
@@ -173,7 +175,7 @@ Plan plan_of(const Args &a, bool tree, int sms) {
     // keys a CTA should keep: with one launch latency counts (16 rows over 460 keys: 6.6 us with 4 CTAs, 7.1 us with
     // 2), beside the tcgen05 kernel overhead does (256 keys: 38 us with 1, 43 us with 2); fp32 is bound by its products
     const int64_t least = f32 ? 32 : (p.with_prefix || !p.tiles ? 96 : 192);
-    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, least, f32, sms);
+    p.cluster = cluster_for(kv_units, (p.with_prefix ? a.S_p : 0) + a.S_c / 2, least, f32, one_wave, sms);
     const int64_t keys = (p.with_prefix ? a.S_p : 0) + a.S_c / 2;
     if (kv_units * p.cluster < sms && keys >= 2 * 256LL * p.cluster) {
         // few units of many keys (one sequence of 65536 tokens: 105 us without): shares of 256 keys a CTA or more
@@ -192,8 +194,8 @@ Plan plan_of(const Args &a, bool tree, int sms) {
         p.prefix_shares = tile_shares(a, z, p.cluster, sms);
     } else {
         const int64_t units = a.H_kv * z.tiles_all;
-        p.prefix_cluster = cluster_for(units, a.S_p, f32 ? 32 : 96, f32, sms);
-        int64_t shares = (2LL * sms) / (units * p.prefix_cluster);
+        p.prefix_cluster = cluster_for(units, a.S_p, f32 ? 32 : 96, f32, one_wave, sms);
+        int64_t shares = (one_wave ? sms : 2LL * sms) / (units * p.prefix_cluster);
         const int64_t most = a.S_p / ((f32 ? 64LL : 256LL) * p.prefix_cluster);
         if (shares > most) shares = most;
         if (shares > st::kMaxShares) shares = st::kMaxShares;

@@ -103,8 +103,9 @@ __device__ __forceinline__ uint32_t tf32_of(float x) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
+// (hi in integers, which is the conversion's value at eight times its rate; of a NaN lo alone is left.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-    hi = tf32_of(__uint_as_float(x));
+    hi = (x + 0x1000u) & 0xFFFFE000u;
     lo = tf32_of(__uint_as_float(x) - __uint_as_float(hi));
 }
 // The same for a value that may be infinite beside a factor p >= 0: hi is then the largest number and lo the infinity, so
