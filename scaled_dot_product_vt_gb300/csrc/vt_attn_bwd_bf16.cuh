@@ -5,13 +5,18 @@
 // Three launches.  attn_bwd_stats_kernel forms -LSE log2(e) and -delta of every query; attn_bwd_kv_bf16_kernel walks the
 // queries of a 128-key block (dK, dV); attn_bwd_q_bf16_kernel walks the keys of a 128-query block (dQ).  The two walks
 // form S and dO V^T twice, 7 products of 128 x 128 x D per pair of blocks where one walk would take 5; in return no sum
-// crosses CTAs: no atomics, no fp32 dQ in memory, the same result in every call.  Both are bound by the tensor pipe: a
-// 128 x 128 x 128 product takes 512 cycles, and the 16384 exponentials and the rest of a tile's element work, by two
-// warpgroups of 64 columns each, about as long as two of them.
+// crosses CTAs: no atomics, no fp32 dQ in memory, the same result in every call.
 //
 // Every tensor core operand lies as TMA left it or as a warpgroup wrote it to TMEM: the keys' walk forms the transposed
 // S^T = K Q^T and dP^T = V dO^T, whose rows are keys, so that P^T and dS^T are A operands from TMEM; Q and dO are K-major B
 // operands of the first two products and N-major ones of the last two, from one copy in shared memory.
+//
+// Measured (16 texts of 128 to 4096 tokens, 32 heads on 8, D = 128, causal): statistics 59 us, keys' walk 498 us (1.49
+// PFLOP/s of its four products), queries' walk 437 us (1.27 of its three).  Sequences of 4096 keep the tensor pipe 75 and 64 %
+// busy (ncu).  A tile's products take the pipe 2048 and 1536 cycles; a tile takes 2830 and 2160 (clock64): the pipe waits
+// for the warpgroups' exponentials (about 1000 cycles for 64 columns a thread) in the keys' walk, whose next scores need
+// P's place in TMEM, and a unit's end and start cost 4200 cycles beside its 9 tiles in the queries' walk.
+// Widths up to 64 halve the products and not the exponentials: 9 images of 256 to 2048 patches, 16 heads, 182 us in all.
 //
 // Warps (both kernels, 12): 0 loads (TMA, one lane) and draws the units (cluster launch control, as in
 // vt_attn_bf16_2q.cuh); 1 allocates TMEM and issues every MMA (one lane); 4-7 and 8-11 compute, columns 0-63 and 64-127

@@ -59,7 +59,7 @@ struct AttnParams {
     // kRowsSeq: the key axis is the prefix's tiles (prefix_keys keys), then the tiles of the sequence's cache
     int prefix_tiles, prefix_keys, cache_keys;
     const int *kv_len;  // cached tokens per sequence, or null: cache_keys
-    const int *parents;  // kRowsTree: [B, row_tokens] (vt_attn_tree.cuh)
+    const int *parents;  // kRowsTree: [B, row_tokens] (vt_attn_tree.cuh); the rest as kRowsSeq
     // bf16, packed sequences (kRowsPacked): S_q and S_k count the rows of all sequences, n_qblocks the slots of packed_find
     const int *cu_q, *cu_k;  // [n_seq + 1] first rows
     int n_seq;

@@ -52,8 +52,7 @@ __device__ __forceinline__ PackedSeq packed_find(const int *cu, int N, int T, in
     return s;
 }
 
-// The same by a whole warp, 32 candidates at a time: one or two reads after each other where a lane alone makes
-// log2(N) (3 us of a launch's start with 17 sequences).
+// The same by a whole warp, 32 candidates at a time: one or two reads after each other where a lane alone makes log2(N).
 __device__ __forceinline__ PackedSeq packed_find_warp(const int *cu, int N, int T, int R, int slot, int lane, unsigned *status) {
     int lo = 0, hi = N;
     while (hi - lo > 1) {

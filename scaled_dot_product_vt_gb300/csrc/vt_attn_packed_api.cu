@@ -228,7 +228,9 @@ struct Layout {
 };
 
 // Few blocks of keys are walked by one CTA per query head, whose results another launch adds, so that more SMs take part:
-// where the key/value heads' blocks would not give every SM one (bf16, one CTA on an SM), or two (fp32).
+// where the key/value heads' blocks would not give every SM one (bf16, one CTA on an SM), or two (fp32).  Six texts of up to
+// 333 tokens, 16 heads on 4: keys' walk 30 us with 44 units, 17 us and 6 us for the sums with 176; fp32, three of up to 500,
+// 8 heads on 2: 198 us with 30 CTAs, 56 and 5 us with 120.  With more blocks the sums' bytes only add.
 Layout layout_of(const Args &a, int sms) {
     const bool bf = a.dtype == VT_BF16;
     const int64_t G = a.H / a.H_kv, blocks = packed_slots(a.T_k, a.N, bf ? bw::kTile : pf::kRows) * a.H_kv;

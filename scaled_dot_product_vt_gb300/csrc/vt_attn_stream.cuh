@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_shares_kernel(const __g
     c.store(p, lane, seq - hk * p.B, hk, static_cast<int>(flat) - seq * per_b);
 }
 
-// kTree: the S_q tokens of a sequence are the nodes of a tree, and its keys its cache (or with the prefix).
+// kTree: the S_q tokens of a sequence are the nodes of a tree, and its keys its cache (or with the prefix).  Four trees of 8
+// behind 333 keys: 8.3 us, as for tokens in a row.
 template <typename T, int DQ, int DV, bool kTree = false>
 __global__ void __launch_bounds__(kThreads, Tile<T, DQ, DV>::kPerSm)
     attn_stream_kernel(const __grid_constant__ Maps maps, const Params p) {
