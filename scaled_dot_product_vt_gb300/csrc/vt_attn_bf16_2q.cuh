@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
     }
 
     if constexpr (ROWS == kRowsTree)  // this launch ends after the prefix's: the next one reads the results of both
-        if (p.follows && blockIdx.x == 0 && threadIdx.x == 0) wait_prerequisites();
+        if (p.follows && threadIdx.x == 0) wait_prerequisites();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -276,6 +276,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *m, ui
 __device__ __forceinline__ void store_row(uint32_t tmem, bool any, uint16_t *row, bool ok, int D, float f, bool vec32) {
     for (int cc = 0; cc < D; cc += 16) {
         uint32_t o[16];
+        __syncwarp();  // (lanes part below)
         if (any) {
             tmem_ld16(tmem + cc, o);
             tmem_wait_ld();
@@ -307,6 +308,7 @@ __device__ __forceinline__ void store_row(uint32_t tmem, bool any, uint16_t *row
 __device__ __forceinline__ void store_part(uint32_t tmem, bool any, float *row, bool ok, int ld) {
     for (int cc = 0; cc < ld; cc += 16) {
         uint32_t o[16];
+        __syncwarp();  // (lanes part below)
         if (any) {
             tmem_ld16(tmem + cc, o);
             tmem_wait_ld();
@@ -969,8 +971,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
         }
     }
 
-    // this launch ends after the one it was started ahead of: the next one may read the results of both
-    if (p.follows && blockIdx.x == 0 && threadIdx.x == 0) wait_prerequisites();
+    // This launch ends after the one it was started ahead of: the next one may read the results of both.  (Every CTA waits:
+    // which of them run, and which are drawn by others as units, is the hardware's choice.)
+    if (p.follows && threadIdx.x == 0) wait_prerequisites();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
