@@ -77,7 +77,7 @@ size_t partial_bytes(int64_t rows, int64_t D_v, int shares) {
 // fp32 kernel fills an SM per CTA, and clusters of 8 then wait for room (26 us against 20 us with 4).
 // (`one_wave`: no more CTAs than SMs, where the fp32 kernel has several row tiles per sequence and its second wave of CTAs,
 // each of a few keys, takes as long as the first: trees, which have no results of earlier plans to keep.  Eight trees of 13
-// in 4 heads behind 1000 keys, fp32: 49 us with two waves, 39 us with one.)
+// in 4 heads behind 1000 keys, fp32: 51 us with two waves, 41 us with one.)
 int cluster_for(int64_t units, int64_t keys, int64_t least, bool f32, bool one_wave, int sms) {
     int c = 1;
     const int most = f32 ? 4 : st::kMaxClusterCtas;
@@ -323,7 +323,8 @@ Kern pick(const Args &a, int *smem) {
 vt_status launch_stream(const Args &a, const st::Maps &maps, const st::Params &p, int64_t units, int cluster, bool follows, int dev,
                         cudaStream_t stream) {
     int smem = 0;
-    const bool tree = p.parents && !p.all_rows;  // (the prefix's own launch reads no cache)
+    // (the prefix's own launch reads no cache; in fp32 it takes the trees' sums)
+    const bool tree = p.parents && (a.dtype == VT_F32 || !p.all_rows);
     const Kern kern = a.dtype == VT_BF16 ? (tree ? pick<uint16_t, true>(a, &smem) : pick<uint16_t, false>(a, &smem))
                                          : (tree ? pick<float, true>(a, &smem) : pick<float, false>(a, &smem));
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
