@@ -431,6 +431,7 @@ size_t vt_attn_prefix_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t
  * `parents` is int32 [B,S_q], packed, on the device, read there (a captured call replays with new trees).  A parent that is
  * neither -1 nor an earlier node counts as -1 and records VT_ERR_DEVICE_BOUNDS in the stream's status word.  A node whose
  * row is negative (a sequence shorter than the tree) has no key: its queries see the prefix alone.
+ * Without a cache (S_c equal to 0) every node's queries see the prefix alone; kv_len is not read, parents are.
  * The workspace has vt_attn_tree_workspace_size bytes; other arguments and errors as for vt_attn_fwd_prefix,
  * VT_ERR_INVALID_ARG also for parents NULL,
  * VT_ERR_UNSUPPORTED also for S_q above 64.

@@ -433,10 +433,11 @@ vt_status launch_tiles(const Args &a, const Plan &plan, const Sizes &z, const st
     const int64_t units = per_head * heads;
     if (units > 0x7FFFFFFFll) return VT_ERR_UNSUPPORTED;
     p.n_units = static_cast<int>(units);
+    // (kRowsTree reads the parents of every sequence, without a cache too; plan_of cuts a sequence's keys for trees alone)
     const TileKern kern = !seq               ? pick_tiles<q2::kEpiSplit, q2::kRowsAll>(p)
+                          : !p.parents       ? pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p)
                           : plan.tree_shares ? pick_tiles<q2::kEpiSplit, q2::kRowsTree>(p)
-                          : p.parents        ? pick_tiles<q2::kEpiPlain, q2::kRowsTree>(p)
-                                             : pick_tiles<q2::kEpiPlain, q2::kRowsSeq>(p);
+                                             : pick_tiles<q2::kEpiPlain, q2::kRowsTree>(p);
     if (!ensure_smem(reinterpret_cast<const void *>(kern), dev, smem)) return VT_ERR_CUDA;
     p.follows = own_only ? 1 : 0;
     p.longest_first = seq && p.parents && p.kv_len && sp.B > 1 && sp.B <= st::kMaxSorted && units > info.sms;
@@ -487,7 +488,7 @@ vt_status forward(const Args &a, const int32_t *parents, cudaStream_t stream) {
     if (!have) return VT_ERR_CUDA;
     const Sizes z = sizes_of(a);
     st::Params p = params_of(a, plan, z, info.status + status_slot(stream));
-    p.parents = a.S_c > 0 ? parents : nullptr;
+    p.parents = parents;
     if (plan.seq_tiles) {
         if (plan.prefix_shares) VT_TRY(launch_tiles(a, plan, z, p, false, info, dev, stream));
         VT_TRY(launch_tiles(a, plan, z, p, true, info, dev, stream));

@@ -167,6 +167,42 @@ def test_parents_that_are_no_earlier_node_are_reported(nodes):
     assert vt.vt_last_device_status() == 0
 
 
+NO_CACHE = [
+    # dtype, B, H, H_kv, nodes, S_p, S_c, D_qk, D_v
+    ("bf16", 1, 32, 8, 64, 1024, 0, 128, 128),     # 256 rows a key/value head, the prefix in shares
+    ("bf16", 1, 8, 2, 40, 640, 0, 128, 128),
+    ("bf16", 3, 6, 2, 40, 2000, 0, 72, 40),
+    ("bf16", 40, 8, 2, 33, 300, 0, 64, 64),        # many sequences, one launch
+    ("bf16", 2, 8, 1, 9, 1, 0, 64, 128),
+    ("bf16", 20, 8, 2, 4, 3000, 0, 128, 64),       # streamed rows, the prefix on its own
+    ("bf16", 1, 4, 1, 3, 4000, 0, 64, 64),         # streamed with the prefix, in shares
+    ("f32", 2, 8, 2, 33, 700, 0, 64, 64),
+    ("f32", 1, 2, 1, 5, 60, 0, 33, 20),
+]
+
+
+def test_a_tree_without_a_cache_has_its_own_plan():
+    """Shares of the prefix (and so partial results) where a sequence's rows fill tiles: the kernel that reads the parents."""
+    size = vt.vt_attn_tree_workspace_size
+    assert size(1, 32, 8, 64, 1024, 0, 128, 128, vt.VT_BF16) > 0 == vt.vt_attn_prefix_workspace_size(
+        1, 32, 8, 64, 1024, 0, 128, 128, vt.VT_BF16)
+
+
+@gpu
+@pytest.mark.parametrize("case", NO_CACHE, ids=lambda c: "-".join(map(str, c)))
+def test_without_a_cache_the_nodes_see_the_prefix_alone(case):
+    """And parents that are no earlier node are reported all the same."""
+    t = Tree(*case, seed=9)
+    B, nodes = t.dims[0], t.dims[3]
+    for kv_len in (t.kv_len, None):  # (not read)
+        t.kv_len = kv_len
+        t.check(*t.run())
+        assert vt.vt_last_device_status() == 0
+    t.par[B - 1, nodes - 1] = nodes
+    t.check(*t.run())
+    assert vt.vt_last_device_status() == 6 and vt.vt_last_device_status() == 0
+
+
 @gpu
 @pytest.mark.parametrize("B,nodes", [(70, 4), (20, 30)])
 def test_writes_nothing_else_and_gives_the_same_bits(B, nodes):
