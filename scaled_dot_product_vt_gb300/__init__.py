@@ -459,6 +459,16 @@ def _check_vector(name, meta, dev, dtype, n):
         raise ValueError(f"{name} must be a contiguous vector" + (f" of {n} elements" if n is not None else ""))
 
 
+def _contiguous(shape, strides) -> bool:
+    """Whether elements of this shape lie behind each other (any strides do where there is none)."""
+    want = 1
+    for n, st in zip(reversed(shape), reversed(strides)):
+        if n > 1 and st != want:
+            return 0 in shape
+        want *= n
+    return True
+
+
 def _new_rows(shape, dtype, device):
     """A new [B, H, S, D] tensor; rows that are no multiple of 16 bytes are padded to one (a view is returned)."""
     import torch
@@ -695,13 +705,13 @@ def _prefix_plan(q, k_prefix, v_prefix, k_cache, v_cache, parents, kv_len, out, 
         svc = _check("v_cache", v_cache, dev, dt, (B, H_kv, S_c, D_v))
     if kv_len is not None:
         _check_vector("kv_len", kv_len, dev, torch.int32, B)
-    if parents is not None and (parents[3] != dev or parents[2] != torch.int32 or tuple(parents[0]) != (B, S_q) or any(
-            n > 1 and st != want for n, st, want in zip((B, S_q), parents[1], (S_q, 1)))):
+    if parents is not None and (parents[3] != dev or parents[2] != torch.int32 or tuple(parents[0]) != (B, S_q)
+                                or not _contiguous(*parents[:2])):
         raise ValueError("parents must be a contiguous int32 [B, S_q] tensor on the device of the other tensors")
     o_shape = (B, H, S_q, D_v)
     so = _check("out", out, dev, dt, o_shape) if out is not None else _new_strides(o_shape, dt)
-    if lse is not None and (lse[3] != dev or lse[2] != torch.float32 or tuple(lse[0]) != (B, H, S_q) or any(
-            n > 1 and st != want for n, st, want in zip(lse[0], lse[1], (H * S_q, S_q, 1)))):
+    if lse is not None and (lse[3] != dev or lse[2] != torch.float32 or tuple(lse[0]) != (B, H, S_q)
+                            or not _contiguous(*lse[:2])):
         raise ValueError("lse must be a contiguous float32 [B, H, S_q] tensor on the device of the other tensors")
     if scale is None:
         scale = float(D_qk) ** -0.5
@@ -808,8 +818,7 @@ def _new_token_strides(shape, dtype):
 
 
 def _check_lse(name, meta, dev, shape):
-    if meta[3] != dev or meta[2] != _float32() or tuple(meta[0]) != shape or any(
-            n > 1 and st != want for n, st, want in zip(shape, meta[1], (shape[1], 1))):
+    if meta[3] != dev or meta[2] != _float32() or tuple(meta[0]) != shape or not _contiguous(*meta[:2]):
         raise ValueError(f"{name} must be a contiguous float32 [H, T_q] tensor on the device of the other tensors")
 
 

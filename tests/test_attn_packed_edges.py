@@ -1,0 +1,52 @@
+"""Attention over packed sequences at the ends of what its contract takes: a side without rows, many short sequences, first
+rows that are out of order, gradients that nothing may reach.  Tolerances are those of test_attn_packed.py."""
+
+import numpy as np
+import pytest
+
+from test_attn_packed import Problem
+
+import scaled_dot_product_vt_gb300 as vt
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    vt.build()
+    vt.load()
+
+
+def test_contiguity_of_an_empty_tensor():
+    """torch gives [2, 0] the strides (1, 1): nothing lies apart there."""
+    torch = pytest.importorskip("torch")
+    for shape in ((2, 0), (0, 5), (1, 0), (3, 1), (3, 5), (2, 0, 4), (2, 3, 4)):
+        x = torch.empty(shape)
+        assert vt._contiguous(x.shape, x.stride())
+        vt._check_lse("lse", (x.shape, x.stride(), x.dtype, 0), 0, shape)
+    for x in (torch.empty(3, 5)[:, :4], torch.empty(5, 3).T, torch.empty(2, 3, 4).transpose(0, 1), torch.empty(3, 1).expand(3, 2)):
+        assert not vt._contiguous(x.shape, x.stride())
+        with pytest.raises(ValueError):
+            vt._check_lse("lse", (x.shape, x.stride(), x.dtype, 0), 0, tuple(x.shape))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_side_has_no_rows(dtype):
+    """Keys without a query have gradients of 0, queries without a key O = 0, a log-sum-exp of -inf and a gradient of 0."""
+    p = Problem(dtype, 4, 2, 64, 40, [(30, 30), (200, 200)], seed=1, behind=0)
+    torch = p.torch
+    res, none = p.results(), torch.zeros_like(p.cu_q)
+    q, do, o, lse = (x[:, :0] for x in (p.q, p.do, *res))
+    dq, dk, dv = vt.attn_bwd_packed(do, q, p.k, p.v, o, lse, none, p.cu_k, dlse=lse, **p.form)
+    assert dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+    for out in (None, o.clone()):
+        o2, lse2 = vt.attn_fwd_packed(q, p.k, p.v, none, p.cu_k, out=out, lse=lse if out is not None else None, return_lse=True,
+                                      **p.form)
+        assert o2.shape == (4, 0, 40) and lse2.shape == (4, 0)
+    k, v = p.k[:, :0], p.v[:, :0]
+    o, lse = vt.attn_fwd_packed(p.q, k, v, p.cu_q, none, return_lse=True, **p.form)
+    assert (o == 0).all() and (lse == -torch.inf).all()
+    dq, dk, dv = vt.attn_bwd_packed(p.do, p.q, k, v, o, lse, p.cu_q, none, dlse=p.dlse, **p.form)
+    assert (dq == 0).all() and dk.shape == k.shape and dv.shape == v.shape
+    assert vt.vt_last_device_status() == 0
