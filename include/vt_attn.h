@@ -459,9 +459,9 @@ size_t vt_attn_tree_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t S
  *   k, v        [H_kv,T_k,D_qk] and [H_kv,T_k,D_v], strides (h, t); T_k >= cu_k[N].  What rows of other sequences, or of
  *               none, hold has no influence.
  *   cu_q, cu_k  int32 [N + 1], not decreasing, read on the device (a captured call replays with new lengths); they may
- *               be one array.  First rows outside [0, T] count as the nearest ones inside, and a sequence that ends
- *               before it starts as empty; both record VT_ERR_DEVICE_BOUNDS in the stream's status word.  (Where such
- *               arrays put rows into two sequences, either one's result may be left there.)
+ *               be one array.  First rows outside [0, T] count as the nearest ones inside and record VT_ERR_DEVICE_BOUNDS in
+ *               the stream's status word.  So does an array that decreases anywhere: every access stays inside the tensors
+ *               then and rows of no sequence are left as they were, but the sequences' results are not specified.
  *   lse         fp32 [H,T_q] packed, or NULL
  *   mask        a vt_mask_kind, with its `window`
  * Element types: VT_BF16, with probabilities rounded to bf16 as in the other calls, and VT_F32 with products of two TF32

@@ -149,8 +149,8 @@ __device__ __forceinline__ void packed_tiles(const AttnParams &p, const Unit &U,
 template <bool kWarp>
 __device__ __forceinline__ PackedSeq packed_block(const AttnParams &p, int u) {
     const int slot = p.n_qblocks - 1 - u / p.H;  // later blocks, which see more keys, come first
-    if constexpr (kWarp) return packed_find_warp(p.cu_q, p.n_seq, p.S_q, kRows, slot, threadIdx.x & 31, p.status);
-    return packed_find(p.cu_q, p.n_seq, p.S_q, kRows, slot, p.status);
+    if constexpr (kWarp) return packed_find_warp(p.cu_q, p.n_seq, p.S_q, kRows, slot, threadIdx.x & 31);
+    return packed_find(p.cu_q, p.n_seq, p.S_q, kRows, slot);
 }
 
 template <int ROWS>
@@ -161,9 +161,10 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const Pa
     if constexpr (ROWS == kRowsPacked) {
         // the heads of a block are adjacent (they read the same keys)
         const PackedSeq q = found ? *found : packed_block<false>(p, u);
-        const PackedSeq k = packed_seq(p.cu_k, q.n, p.S_k, p.status);
+        const PackedSeq k = packed_seq(p.cu_k, q.n, p.S_k);
         U.split = U.b = 0;
         U.h = u % p.H;
+        if (U.h == 0) packed_check(p, p.n_qblocks - 1 - u / p.H);
         U.hk = U.h / p.kv_group;
         U.r0 = q.block * kRows;
         U.rows = q.len;

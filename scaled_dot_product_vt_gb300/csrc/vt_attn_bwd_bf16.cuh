@@ -107,15 +107,16 @@ __device__ __forceinline__ PackedSeq unit_block(const BwdParams &p, int u) {
     const int slot = u / unit_heads<kKeys>(p);
     const int *cu = kKeys ? p.cu_k : p.cu_q;
     const int T = kKeys ? p.S_k : p.S_q, at = kKeys ? slot : p.slots_q - 1 - slot;
-    if constexpr (kWarp) return packed_find_warp(cu, p.n_seq, T, kTile, at, threadIdx.x & 31, p.status);
-    return packed_find(cu, p.n_seq, T, kTile, at, p.status);
+    if constexpr (kWarp) return packed_find_warp(cu, p.n_seq, T, kTile, at, threadIdx.x & 31);
+    return packed_find(cu, p.n_seq, T, kTile, at);
 }
 template <bool kKeys>
 __device__ __forceinline__ Unit decode(const BwdParams &p, int u, const PackedSeq &own) {
     Unit U;
     U.u = u;
     U.h = u % unit_heads<kKeys>(p);
-    const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q, p.status) : packed_seq(p.cu_k, own.n, p.S_k, p.status);
+    if (kKeys && p.S_q == 0 && U.h == 0) packed_check(p, u / unit_heads<kKeys>(p));  // (else the statistics' launch does)
+    const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q) : packed_seq(p.cu_k, own.n, p.S_k);
     U.r0 = own.block * kTile;
     U.q0 = kKeys ? other.start : own.start;
     U.len_q = kKeys ? other.len : own.len;
@@ -359,7 +360,8 @@ __global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const __gr
     constexpr int kStep = kStatThreads / kLanes, kEach = kStatRows / kStep;  // rows at a time, and of a thread
     constexpr int kParts = bw::kTile / kStatRows;
     const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts, slot = unit / p.H, h = unit - slot * p.H;
-    const PackedSeq s = packed_find_warp(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, threadIdx.x & 31, p.status);
+    if (part == 0 && h == 0 && threadIdx.x == 0) packed_check(p, slot);
+    const PackedSeq s = packed_find_warp(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, threadIdx.x & 31);
     const int lane = threadIdx.x % kLanes, col = lane * kVec;
     float *out = p.stat + (static_cast<long long>(h) * p.slots_q + slot) * (2 * bw::kTile);
     const int n = min(s.len - s.block * bw::kTile, bw::kTile);  // rows of the slot
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kHeadsThreads) attn_bwd_heads_kernel(const __g
     constexpr int kParts = ROWS / kHeadsRows;
     const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts;
     const int heads = p.H / p.kv_group, slot = unit / heads, hk = unit - slot * heads;
-    const PackedSeq s = packed_find_warp(p.cu_k, p.n_seq, p.S_k, ROWS, slot, threadIdx.x & 31, p.status);
+    const PackedSeq s = packed_find_warp(p.cu_k, p.n_seq, p.S_k, ROWS, slot, threadIdx.x & 31);
     const int r = part * kHeadsRows + threadIdx.x / 32, c = threadIdx.x % 32 * 4;
     if (r >= min(s.len - s.block * ROWS, ROWS)) return;
     const long long row = static_cast<long long>(s.start) + s.block * ROWS + r;

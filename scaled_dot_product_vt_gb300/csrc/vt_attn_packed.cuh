@@ -25,47 +25,66 @@ __host__ __device__ constexpr long long packed_slots(long long T, long long N, i
 // First row n, brought into [0, T].
 __device__ __forceinline__ int packed_cu(const int *cu, int n, int T) { return min(max(__ldg(cu + n), 0), T); }
 
-// Rows of sequence n.  Ends outside [0, T] count as the nearest inside, an end before its start as the start, and the
-// status word records both.
-__device__ __forceinline__ PackedSeq packed_seq(const int *cu, int n, int T, unsigned *status) {
-    const int a = __ldg(cu + n), e = __ldg(cu + n + 1);
+// Rows of sequence n.  Ends outside [0, T] count as the nearest inside, an end before its start as the start.
+__device__ __forceinline__ PackedSeq packed_seq(const int *cu, int n, int T) {
     PackedSeq s;
     s.n = n;
     s.block = 0;
-    s.start = min(max(a, 0), T);
-    s.len = max(min(max(e, 0), T) - s.start, 0);
-    if (a < 0 || e > T || e < a) atomicOr(status, kStatusBounds);
+    s.start = packed_cu(cu, n, T);
+    s.len = max(packed_cu(cu, n + 1, T) - s.start, 0);
     return s;
 }
 
-// The sequence and block of a slot (its rows may end before the block).
-__device__ __forceinline__ PackedSeq packed_find(const int *cu, int N, int T, int R, int slot, unsigned *status) {
+// What is wrong with sequence n's first rows goes to the status word.  Every sequence is looked at by the unit of the slot of
+// its number (there are as many slots as sequences, and more), whether or not an array that decreases leaves it one of its own.
+__device__ __forceinline__ void packed_check(const AttnParams &p, int n) {
+    if (n >= p.n_seq) return;
+    const int a = __ldg(p.cu_q + n), b = __ldg(p.cu_q + n + 1), c = __ldg(p.cu_k + n), d = __ldg(p.cu_k + n + 1);
+    if (a < 0 || b > p.S_q || b < a || c < 0 || d > p.S_k || d < c) atomicOr(p.status, kStatusBounds);
+}
+
+// The search for a slot takes 32 candidates lo, lo + step, ... at a time and halves them: `before(i)` says whether candidate
+// i's sequence starts at the slot or before it.  By a lane alone or (a call's first units) by a whole warp, it looks at the
+// same candidates and finds the same sequence, in arrays that decrease too.
+template <typename Before>
+__device__ __forceinline__ int packed_halve(Before before) {
+    int i = 0, end = 32;
+    while (end - i > 1) {
+        const int mid = (i + end) >> 1;
+        if (before(mid)) i = mid;
+        else end = mid;
+    }
+    return i;
+}
+template <typename Round>
+__device__ __forceinline__ PackedSeq packed_search(const int *cu, int N, int T, int R, int slot, Round round) {
     int lo = 0, hi = N;  // sequence lo starts at the slot or before it, sequence hi behind it
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (packed_cu(cu, mid, T) / R + mid <= slot) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) / 32;
+        lo += step * round([&](int i) {
+            const int at = lo + i * step;
+            return at < hi && packed_cu(cu, min(at, hi - 1), T) / R + at <= slot;
+        });
+        hi = min(hi, lo + step);
     }
-    PackedSeq s = packed_seq(cu, lo, T, status);
+    PackedSeq s = packed_seq(cu, lo, T);
     s.block = slot - (s.start / R + lo);
     if (s.block < 0) s.block = s.len = 0;  // ahead of the first sequence
     return s;
 }
 
-// The same by a whole warp, 32 candidates at a time: one or two reads after each other where a lane alone makes log2(N).
-__device__ __forceinline__ PackedSeq packed_find_warp(const int *cu, int N, int T, int R, int slot, int lane, unsigned *status) {
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool before = lane == 0 || (at < hi && packed_cu(cu, min(at, hi - 1), T) / R + at <= slot);
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
-        lo += last * step;
-        hi = min(hi, lo + step);
-    }
-    PackedSeq s = packed_seq(cu, lo, T, status);
-    s.block = slot - (s.start / R + lo);
-    if (s.block < 0) s.block = s.len = 0;  // ahead of the first sequence
-    return s;
+// The sequence and block of a slot (its rows may end before the block), by one lane.
+__device__ __forceinline__ PackedSeq packed_find(const int *cu, int N, int T, int R, int slot) {
+    return packed_search(cu, N, T, R, slot, [](auto before) { return packed_halve(before); });
+}
+
+// The same by a whole warp, which reads 32 candidates at once: one or two reads after each other where a lane alone makes
+// log2(N).
+__device__ __forceinline__ PackedSeq packed_find_warp(const int *cu, int N, int T, int R, int slot, int lane) {
+    return packed_search(cu, N, T, R, slot, [lane](auto before) {
+        const unsigned set = __ballot_sync(0xffffffffu, before(lane));
+        return packed_halve([set](int i) { return (set >> i & 1u) != 0; });
+    });
 }
 
 // First key that query i of a packed sequence of `len` keys sees, and one past its last: the band around its own

@@ -188,20 +188,21 @@ __device__ __forceinline__ void store(float *row, const float (&o)[DP / 8][4], i
         }
 }
 
-// The block of rows that a CTA takes, as bw::decode.
+// The block of rows that a CTA takes, as bw::decode.  `check`: this launch looks at the first rows (packed_check).
 struct Block {
     int h, r0, q0, len_q, k0, len_k, qslot;
     int lo, hi;  // partners [lo, hi), lo on a tile's start
 };
 template <bool kKeys>
-__device__ __forceinline__ Block block_of(const BwdParams &p, int tile) {
+__device__ __forceinline__ Block block_of(const BwdParams &p, int tile, bool check) {
     Block B;
     const int heads = kKeys ? p.H / p.groups : p.H;
     const int slot = blockIdx.x / heads, slots = gridDim.x / heads;
     B.h = blockIdx.x - slot * heads;
+    if (check && B.h == 0 && threadIdx.x == 0) packed_check(p, slot);
     const PackedSeq own = packed_find_warp(kKeys ? p.cu_k : p.cu_q, p.n_seq, kKeys ? p.S_k : p.S_q, kRows,
-                                           kKeys ? slot : slots - 1 - slot, threadIdx.x & 31, p.status);
-    const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q, p.status) : packed_seq(p.cu_k, own.n, p.S_k, p.status);
+                                           kKeys ? slot : slots - 1 - slot, threadIdx.x & 31);
+    const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q) : packed_seq(p.cu_k, own.n, p.S_k);
     B.r0 = own.block * kRows;
     B.q0 = kKeys ? other.start : own.start;
     B.len_q = kKeys ? other.len : own.len;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_packed_f32_kernel(const 
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = smem_u32(smem_raw), sKV = sQ + kRows * DP * 4;  // stages of K, V
-    const Block B = block_of<false>(p, kTile);
+    const Block B = block_of<false>(p, kTile, true);
     if (B.r0 >= B.len_q) return;
     const int hk = B.h / p.kv_group;
     const float *Q = static_cast<const float *>(p.Q) + B.h * p.q_sh + B.q0 * p.q_ss;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_q_f32_kernel(const _
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = smem_u32(smem_raw), sG = sQ + kRows * DP * 4, sKV = sG + kRows * DP * 4;
-    const Block B = block_of<false>(p, kTile);
+    const Block B = block_of<false>(p, kTile, false);
     if (B.r0 >= B.len_q) return;
     const int hk = B.h / p.kv_group;
     const float *K = static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_kv_f32_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sK = smem_u32(smem_raw), sV = sK + kRows * DP * 4, sQG = sV + kRows * DP * 4;
     float *const stat = reinterpret_cast<float *>(smem_raw + (2 * kRows + 4 * kTile) * DP * 4);  // [stage][2][kTile]
-    const Block B = block_of<true>(p, kTile);
+    const Block B = block_of<true>(p, kTile, p.S_q == 0);
     if (B.r0 >= B.len_k) return;
     const int hk = B.h / p.head_units;
     copy_rows<DP>(sK, static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss, p.k_ss, B.r0, kRows, B.len_k, p.D_qk);

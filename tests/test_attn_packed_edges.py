@@ -50,3 +50,38 @@ def test_one_side_has_no_rows(dtype):
     dq, dk, dv = vt.attn_bwd_packed(p.do, p.q, k, v, o, lse, p.cu_q, none, dlse=p.dlse, **p.form)
     assert (dq == 0).all() and dk.shape == k.shape and dv.shape == v.shape
     assert vt.vt_last_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("which", ["both", "queries", "keys"])
+def test_arrays_that_decrease_are_reported_wherever_they_do(dtype, which):
+    """Also by a sequence that no block belongs to, and in the array of the other side; rows of no sequence stay."""
+    p = Problem(dtype, 2, 1, 64, 64, [(1000, 1000)] + [(0, 0)] * 60, seed=15, before=2)
+    torch = p.torch
+    res = p.results()
+    for at, row in ((2, 10), (2, 990), (30, 400), (33, 3), (59, 999)):
+        cu = p.cu[0].copy()
+        cu[at] = 2 + row  # behind a sequence that ends before it starts, the next one shares rows with the first
+        for x, side in ((p.cu_q, "queries"), (p.cu_k, "keys")):
+            x.copy_(torch.tensor(cu if which in ("both", side) else p.cu[0]))
+        (out, lse), gr = p.outputs()
+        p.forward(out=out, lse=lse)
+        assert vt.vt_last_device_status() == 6 and vt.vt_last_device_status() == 0, (at, row)
+        p.backward(*res, dq=gr[0], dk=gr[1], dv=gr[2])
+        assert vt.vt_last_device_status() == 6 and vt.vt_last_device_status() == 0, (at, row)
+        for x, side in zip((out, lse, *gr), (0, 0, 0, 1, 1)):
+            p.untouched(x, side)
+        if which != "queries":  # no query at all: dK and dV are 0, and the keys' array is looked at
+            empty = [x[:, :0] for x in (p.do, p.q, *res)]
+            cu_q = torch.zeros_like(p.cu_q)
+            _, dk, dv = vt.attn_bwd_packed(empty[0], empty[1], p.k, p.v, empty[2], empty[3], cu_q, p.cu_k, **p.form)
+            assert vt.vt_last_device_status() == 6 and (dk[:, 2:12] == 0).all() and (dv[:, 2:12] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_sequences(dtype):
+    """More than 32 * 32 of them, so that a slot is found in three rounds."""
+    rng = np.random.default_rng(16)
+    Problem(dtype, 1, 1, 16, 16, [(int(n), int(n)) for n in rng.integers(0, 3, 1100)], seed=16).check()
