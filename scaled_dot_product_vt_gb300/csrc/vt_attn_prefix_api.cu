@@ -293,9 +293,15 @@ bool kv_map(CUtensorMap *map, const void *ptr, const int64_t st[3], int64_t B, i
     return make_map(map, ptr, strides, B, H_kv, S, D, elt, rows);
 }
 
-// The four maps with boxes of `rows` keys (an absent prefix or cache gets the other's: it is not read).
+// The four maps with boxes of `rows` keys (an absent prefix or cache gets the other's, and where both are absent the queries'
+// stand in: they are not read, but the kernels ask for the descriptors).
 bool kv_maps(const Args &a, int rows, st::Maps *m) {
     const int elt = a.dtype == VT_BF16 ? 2 : 4;
+    if (a.S_p == 0 && a.S_c == 0) {
+        if (!kv_map(&m->kp, a.q, a.q_stride, a.B, a.H, a.S_q, a.D_qk, elt, rows)) return false;
+        m->vp = m->kc = m->vc = m->kp;
+        return true;
+    }
     const int64_t kp[3] = {0, a.kp_stride[0], a.kp_stride[1]}, vp[3] = {0, a.vp_stride[0], a.vp_stride[1]};
     if (a.S_p > 0 && (!kv_map(&m->kp, a.k_prefix, kp, 1, a.H_kv, a.S_p, a.D_qk, elt, rows) ||
                       !kv_map(&m->vp, a.v_prefix, vp, 1, a.H_kv, a.S_p, a.D_v, elt, rows)))

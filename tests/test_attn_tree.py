@@ -204,6 +204,18 @@ def test_without_a_cache_the_nodes_see_the_prefix_alone(case):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,S_q", [("bf16", 1), ("bf16", 3), ("bf16", 20), ("f32", 3)])
+def test_no_key_at_all(dtype, S_q):
+    """O = 0 and a log-sum-exp of -inf, for tokens in a row and for trees."""
+    t = Tree(dtype, 3, 8, 2, S_q, 0, 0, 64, 40, seed=10)
+    for run in (t.run, lambda **kw: prefix.Problem.run(t, **kw)):
+        out = t.torch.full((3, 8, S_q, 40), 7.0, dtype=t.t, device="cuda")
+        o, lse = run(out=out)
+        assert (o == 0).all() and (lse == -math.inf).all()
+    assert vt.vt_last_device_status() == 0
+
+
+@gpu
 @pytest.mark.parametrize("B,nodes", [(70, 4), (20, 30)])
 def test_writes_nothing_else_and_gives_the_same_bits(B, nodes):
     t = Tree("bf16", B, 8, 2, nodes, 1500, 200, 128, 72, seed=5)
