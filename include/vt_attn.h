@@ -494,7 +494,8 @@ vt_status vt_attn_fwd_packed(const vt_attn_packed_args *args, vt_stream_t stream
  * With P = exp(scale q . k - LSE) over the pairs the mask keeps, g = d_o and delta = sum_e g_e o_e - d_lse of every query,
  *   dv = sum P g,   dS = P (g . v - delta),   dq = scale sum dS k,   dk = scale sum dS q;
  * sums for a key run over the queries of all the heads that share it.  A query or key without a partner has a gradient
- * of 0; rows that belong to no sequence are not written.
+ * of 0; rows that belong to no sequence are not written.  A query without a key adds nothing to any gradient, whatever its
+ * d_lse; d_o is finite in every row of a sequence, as q, k and v are.
  *   d_o          [H,T_q,D_v]: the gradient of O
  *   d_lse        fp32 [H,T_q] packed: the gradient of LSE, or NULL (0)
  *   dq, dk, dv   as q, k and v.  They may lie beside each other in one tensor (the gradient of one projection); they must

@@ -412,9 +412,9 @@ __global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const __gr
 #pragma unroll
         for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         const int r = r0 + i * kStep;
-        if (lane == 0) {  // (a row without keys has no weight at all)
+        if (lane == 0) {  // (a row without keys has no weight at all, and 0 times its delta would not hide a NaN)
             out[r] = lse[i] == -INFINITY ? -INFINITY : -lse[i] * 1.4426950408889634f;
-            out[bw::kTile + r] = r < n ? dl[i] - sum : 0.0f;
+            out[bw::kTile + r] = lse[i] == -INFINITY ? 0.0f : dl[i] - sum;
         }
     }
 }

@@ -85,3 +85,22 @@ def test_many_short_sequences(dtype):
     """More than 32 * 32 of them, so that a slot is found in three rounds."""
     rng = np.random.default_rng(16)
     Problem(dtype, 1, 1, 16, 16, [(int(n), int(n)) for n in rng.integers(0, 3, 1100)], seed=16).check()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,mask,window", [([(300, 100), (70, 70), (5, 1)], "causal", 0),
+                                                 ([(200, 200), (40, 40)], "window_complement", 60)])
+def test_queries_without_a_key_add_nothing_whatever_their_dlse(dtype, lengths, mask, window):
+    """A log-sum-exp of -inf often has a gradient that is NaN (exp of inf - inf)."""
+    p = Problem(dtype, 4, 2, 64, 64, lengths, mask, window, seed=17, behind=0)
+    torch = p.torch
+    o, lse = p.results()
+    none = lse == -torch.inf
+    assert none.any()
+    want = [x.clone() for x in p.backward(o, lse, dlse=torch.where(none, 0.0, p.dlse))]
+    p.check_backward(*want, dlse=torch.where(none, 0.0, p.dlse))
+    for bad in (float("nan"), float("inf")):
+        got = p.backward(o, lse, dlse=torch.where(none, bad, p.dlse))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (want[0][none] == 0).all()
