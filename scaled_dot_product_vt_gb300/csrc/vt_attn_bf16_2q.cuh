@@ -164,7 +164,6 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams &p, int u, const Pa
         const PackedSeq k = packed_seq(p.cu_k, q.n, p.S_k);
         U.split = U.b = 0;
         U.h = u % p.H;
-        if (U.h == 0) packed_check(p, p.n_qblocks - 1 - u / p.H);
         U.hk = U.h / p.kv_group;
         U.r0 = q.block * kRows;
         U.rows = q.len;
@@ -519,7 +518,13 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                 }
                 mbar_arrive(smem_u32(&ctl.unit_full[k]));
                 if (u < 0) break;
-                if (U.n_kv == 0) continue;
+                auto check = [&]() {  // (behind the unit's loads, which do not wait for it)
+                    if (ROWS == kRowsPacked && U.h == 0) packed_check(p, p.n_qblocks - 1 - u / p.H);
+                };
+                if (U.n_kv == 0) {
+                    check();
+                    continue;
+                }
                 if constexpr (!GATHER) {
                     const int q_row0 = U.r0 + (ROWS == kRowsPacked ? U.q0 : 0);
                     // The unit's Q may only be loaded once the previous unit's last Q K^T has read the Q buffers;
@@ -574,6 +579,7 @@ __global__ void __launch_bounds__(q2::kThreads, 1)
                     ++loads;
                     if (++s == n_slots) s = 0;
                 }
+                check();
             }
             if (ctl.abort_flag) {
                 // Let every copy this thread started land before the CTA's memory goes away: the

@@ -360,7 +360,6 @@ __global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const __gr
     constexpr int kStep = kStatThreads / kLanes, kEach = kStatRows / kStep;  // rows at a time, and of a thread
     constexpr int kParts = bw::kTile / kStatRows;
     const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts, slot = unit / p.H, h = unit - slot * p.H;
-    if (part == 0 && h == 0 && threadIdx.x == 0) packed_check(p, slot);
     const PackedSeq s = packed_find_warp(p.cu_q, p.n_seq, p.S_q, bw::kTile, slot, threadIdx.x & 31);
     const int lane = threadIdx.x % kLanes, col = lane * kVec;
     float *out = p.stat + (static_cast<long long>(h) * p.slots_q + slot) * (2 * bw::kTile);
@@ -417,6 +416,7 @@ __global__ void __launch_bounds__(kStatThreads) attn_bwd_stats_kernel(const __gr
             out[bw::kTile + r] = lse[i] == -INFINITY ? 0.0f : dl[i] - sum;
         }
     }
+    if (part == 0 && h == 0 && threadIdx.x == 0) packed_check(p, slot);
 }
 
 // dK and dV of ROWS keys of one key/value head, from those of its query heads, added in their order.

@@ -45,16 +45,16 @@ __device__ __forceinline__ void packed_check(const AttnParams &p, int n) {
 
 // The search for a slot takes 32 candidates lo, lo + step, ... at a time and halves them: `before(i)` says whether candidate
 // i's sequence starts at the slot or before it.  By a lane alone or (a call's first units) by a whole warp, it looks at the
-// same candidates and finds the same sequence, in arrays that decrease too.
+// same candidates and finds the same sequence, in arrays that decrease too.  A lane reads for two halvings at once.
 template <typename Before>
 __device__ __forceinline__ int packed_halve(Before before) {
-    int i = 0, end = 32;
-    while (end - i > 1) {
-        const int mid = (i + end) >> 1;
-        if (before(mid)) i = mid;
-        else end = mid;
+    int i = 0;
+#pragma unroll
+    for (int b = 8; b > 1; b /= 4) {
+        const bool quarter = before(i + b), half = before(i + 2 * b), three = before(i + 3 * b);
+        i += half ? (three ? 3 * b : 2 * b) : (quarter ? b : 0);
     }
-    return i;
+    return before(i + 1) ? i + 1 : i;
 }
 template <typename Round>
 __device__ __forceinline__ PackedSeq packed_search(const int *cu, int N, int T, int R, int slot, Round round) {
@@ -63,7 +63,7 @@ __device__ __forceinline__ PackedSeq packed_search(const int *cu, int N, int T, 
         const int step = (hi - lo + 31) / 32;
         lo += step * round([&](int i) {
             const int at = lo + i * step;
-            return at < hi && packed_cu(cu, min(at, hi - 1), T) / R + at <= slot;
+            return (at < hi) & (packed_cu(cu, min(at, hi - 1), T) / R + at <= slot);
         });
         hi = min(hi, lo + step);
     }

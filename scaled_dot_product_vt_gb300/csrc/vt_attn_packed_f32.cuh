@@ -188,18 +188,18 @@ __device__ __forceinline__ void store(float *row, const float (&o)[DP / 8][4], i
         }
 }
 
-// The block of rows that a CTA takes, as bw::decode.  `check`: this launch looks at the first rows (packed_check).
+// The block of rows that a CTA takes, as bw::decode.
 struct Block {
-    int h, r0, q0, len_q, k0, len_k, qslot;
+    int slot, h, r0, q0, len_q, k0, len_k, qslot;
     int lo, hi;  // partners [lo, hi), lo on a tile's start
 };
 template <bool kKeys>
-__device__ __forceinline__ Block block_of(const BwdParams &p, int tile, bool check) {
+__device__ __forceinline__ Block block_of(const BwdParams &p, int tile) {
     Block B;
     const int heads = kKeys ? p.H / p.groups : p.H;
     const int slot = blockIdx.x / heads, slots = gridDim.x / heads;
     B.h = blockIdx.x - slot * heads;
-    if (check && B.h == 0 && threadIdx.x == 0) packed_check(p, slot);
+    B.slot = slot;
     const PackedSeq own = packed_find_warp(kKeys ? p.cu_k : p.cu_q, p.n_seq, kKeys ? p.S_k : p.S_q, kRows,
                                            kKeys ? slot : slots - 1 - slot, threadIdx.x & 31);
     const PackedSeq other = kKeys ? packed_seq(p.cu_q, own.n, p.S_q) : packed_seq(p.cu_k, own.n, p.S_k);
@@ -238,8 +238,12 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_packed_f32_kernel(const 
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = smem_u32(smem_raw), sKV = sQ + kRows * DP * 4;  // stages of K, V
-    const Block B = block_of<false>(p, kTile, true);
-    if (B.r0 >= B.len_q) return;
+    const Block B = block_of<false>(p, kTile);
+    const bool check = B.h == 0 && threadIdx.x == 0;  // (behind the block's results, which do not wait for it)
+    if (B.r0 >= B.len_q) {
+        if (check) packed_check(p, B.slot);
+        return;
+    }
     const int hk = B.h / p.kv_group;
     const float *Q = static_cast<const float *>(p.Q) + B.h * p.q_sh + B.q0 * p.q_ss;
     const float *K = static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss;
@@ -326,6 +330,7 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_packed_f32_kernel(const 
             p.lse[static_cast<long long>(B.h) * p.S_q + at] =
                 l[x] == 0.0f ? -INFINITY : (m[x] + log2f(l[x])) * 0.69314718055994531f;
     }
+    if (check) packed_check(p, B.slot);
 }
 
 template <int DP>
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_q_f32_kernel(const _
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = smem_u32(smem_raw), sG = sQ + kRows * DP * 4, sKV = sG + kRows * DP * 4;
-    const Block B = block_of<false>(p, kTile, false);
+    const Block B = block_of<false>(p, kTile);
     if (B.r0 >= B.len_q) return;
     const int hk = B.h / p.kv_group;
     const float *K = static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss;
@@ -407,7 +412,8 @@ __global__ void __launch_bounds__(pf::kThreads, 2) attn_bwd_kv_f32_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sK = smem_u32(smem_raw), sV = sK + kRows * DP * 4, sQG = sV + kRows * DP * 4;
     float *const stat = reinterpret_cast<float *>(smem_raw + (2 * kRows + 4 * kTile) * DP * 4);  // [stage][2][kTile]
-    const Block B = block_of<true>(p, kTile, p.S_q == 0);
+    const Block B = block_of<true>(p, kTile);
+    if (p.S_q == 0 && B.h == 0 && threadIdx.x == 0) packed_check(p, B.slot);  // (else the statistics' launch does)
     if (B.r0 >= B.len_k) return;
     const int hk = B.h / p.head_units;
     copy_rows<DP>(sK, static_cast<const float *>(p.K) + hk * p.k_sh + B.k0 * p.k_ss, p.k_ss, B.r0, kRows, B.len_k, p.D_qk);
