@@ -361,7 +361,8 @@ __device__ __forceinline__ void clear_past_end(uint32_t slot, const Unit &U, int
 // (griddepcontrol).  kRowsSeq: rows of one sequence, over a shared prefix and then the sequence's own cache (tmK, tmV
 // and tmQ, tmV2), causal in the cache.  kRowsTree: the same, and the tokens are the nodes of a tree (AttnParams::parents).
 // kRowsPacked: consecutive queries of one head of a packed sequence, loaded by TMA (vt_attn_packed.cuh); 16 prompts of 128 to
-// 8192 tokens, 32 heads on 8, D = 128, causal: 905 to 926 us, 1.39 to 1.43 PFLOP/s.
+// 8192 tokens, 32 heads on 8, D = 128, causal: 908 to 925 us in a captured graph (1.39 to 1.42 PFLOP/s), 954 to 967 us called
+// from Python.
 // Measured: kRowsAll, 256 rows of each of 8 key/value heads over 8192 shared keys, D = 128: 22 us with the launches for
 // empty caches and for adding the shares.  kRowsSeq, 8 sequences of 256 tokens (256 units), 8192 shared keys and caches up to 1024: 207 us, 1.43 PFLOP/s;
 // 256 units are two waves of 152 CTAs, 84 % full, which is what keeps it below the plain rows' 1.65.

@@ -2,10 +2,12 @@
 //
 // With s = scale q . k, P = exp(s - LSE), g = dO, delta = sum_e g_e O_e - dLSE:
 //   dV = P^T g,   dS = P o (g V^T - delta),   dQ = scale dS K,   dK = scale dS^T Q.
-// Three launches.  attn_bwd_stats_kernel forms -LSE log2(e) and -delta of every query; attn_bwd_kv_bf16_kernel walks the
-// queries of a 128-key block (dK, dV); attn_bwd_q_bf16_kernel walks the keys of a 128-query block (dQ).  The two walks
-// form S and dO V^T twice, 7 products of 128 x 128 x D per pair of blocks where one walk would take 5; in return no sum
-// crosses CTAs: no atomics, no fp32 dQ in memory, the same result in every call.
+// Three launches, or four.  attn_bwd_stats_kernel forms -LSE log2(e) and -delta of every query; attn_bwd_kv_bf16_kernel walks
+// the queries of a 128-key block (dK, dV); attn_bwd_q_bf16_kernel walks the keys of a 128-query block (dQ).  The two walks
+// form S and dO V^T twice, 7 products of 128 x 128 x D per pair of blocks where one walk would take 5; in return no sum of a
+// query head crosses CTAs: no atomics, no fp32 dQ in memory, the same result in every call.  Where blocks of keys are few and
+// heads share them, the keys' walk takes one query head per CTA and leaves its dK and dV in the workspace (fp32), and
+// attn_bwd_heads_kernel, the fourth launch, adds a group's in the order of its heads: the same result in every call again.
 //
 // Every tensor core operand lies as TMA left it or as a warpgroup wrote it to TMEM: the keys' walk forms the transposed
 // S^T = K Q^T and dP^T = V dO^T, whose rows are keys, so that P^T and dS^T are A operands from TMEM; Q and dO are K-major B
@@ -16,7 +18,7 @@
 // busy (ncu).  A tile's products take the pipe 2048 and 1536 cycles; a tile takes 2830 and 2160 (clock64): the pipe waits
 // for the warpgroups' exponentials (about 1000 cycles for 64 columns a thread) in the keys' walk, whose next scores need
 // P's place in TMEM, and a unit's end and start cost 4200 cycles beside its 9 tiles in the queries' walk.
-// Widths up to 64 halve the products and not the exponentials: 9 images of 256 to 2048 patches, 16 heads, 182 us in all.
+// Widths up to 64 halve the products and not the exponentials: 9 images of 256 to 2048 patches, 16 heads, 182 to 190 us in all.
 //
 // Errors of dQ and dK (norms, random inputs, 40 to 2000 keys): 1.66e-3 is their own rounding to bf16; dS rounded to bf16, as
 // the tensor core takes it, makes that 2.3e-3 to 2.4e-3, and delta from an O that was rounded 2.4e-3 to 2.6e-3.  The rest of dS
@@ -546,6 +548,9 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
             const uint32_t lead = elect_leader();
             bool ok = true, any = false;
             uint32_t own_par = 0, p_par = 0, ds_par = 0;
+            // The warp stays together: its lanes part in a wait, in clear_rows and where one of them arrives for all (next_unit),
+            // and meet again in the __all_sync of the wait or the __syncwarp of clear_rows that stands between each of these and
+            // the next MMA or commit.  All lanes come to these with the same operands, and the elected one issues them.
             auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
             };
@@ -837,6 +842,7 @@ __global__ void __launch_bounds__(bw::kThreads, 1)
             const uint32_t lead = elect_leader();
             bool ok = true, any = false;
             uint32_t own_par = 0, ds_par = 0, g = 0;  // g: key tiles of this CTA so far
+            // (the warp stays together, as in the keys' walk)
             auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, wait_bounded(bar, parity, ctl.abort_flag, p)) != 0;
             };

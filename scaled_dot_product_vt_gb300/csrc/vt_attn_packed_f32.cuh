@@ -12,7 +12,7 @@
 //   P B (acc): these rows are k = t, t + 4; n = g of four column tiles is column 4 g + m of 32, so a thread's results are
 //   8 consecutive columns 8 t .. 8 t + 7.
 // Both loads fall into different banks (swizzle gives 8 lanes' units different low bits).
-// Measured (widths 72 on rows of 96): five sequences of 100 to 1000 tokens, 8 heads, 127 us (26 TFLOP/s; the SMs that
+// Measured (widths 72 on rows of 96): five sequences of 100 to 1000 tokens, 8 heads, 127 to 134 us (26 TFLOP/s; the SMs that
 // hold two CTAs of the longest one end last); gradients of three of 77 to 500, window 128: 78 us, 56 of them the keys' walk.
 // With 32 rows a CTA and 16-row tiles the forward took 195 us where this took 152 (fewer independent products per warp).
 // Errors (norms, random inputs): O 4e-7, dQ and dK 4.6e-7.

@@ -123,8 +123,9 @@ int64_t ctas_per_sm(const Args &a) { return a.dtype == VT_F32 ? 1 : (a.D_v <= 64
 // full, and a partial result is written and read at 5 bytes per ns.  32 trees of 25 nodes in 4 heads, behind 8192 shared keys
 // and caches of 1024: 221 us in one launch (256 units of 68 steps on 152 SMs, and 100 rows fill one tile of two), 124 us with
 // the prefix in a launch of its own; 16 trees of 64 over up to 8192 keys: 101 us in one launch of 128 units, 94 us in two
-// shares, longest first (114 us in the order of the batch).  (vt_attn_fwd_prefix keeps its plan, and so the rounding of its
-// results.)
+// shares, longest first (114 us in the order of the batch).  Without a cache, one sequence of 64 nodes, 32 heads on 8, behind
+// 8192 keys: 28 us in shares, 94 us in one launch; behind 1024 keys 23 and 19 us; 16 sequences behind 8192 keys 107 and 97 us.
+// (vt_attn_fwd_prefix keeps its plan, and so the rounding of its results.)
 void tree_plan(const Args &a, const Sizes &z, int sms, Plan *p) {
     const double step = 1.6, unit = 5.0;
     const int64_t tp = (a.S_p + q2::kBN - 1) / q2::kBN, tc = (a.S_c / 2 + q2::kBN - 1) / q2::kBN;
